@@ -70,7 +70,8 @@ typedef enum {
     LORA_ERR_WORKSPACE = 6,     /* workspace missing or smaller than lora_workspace_bytes() */
     LORA_ERR_TIMEOUT = 7,       /* device: a bounded wait between thread blocks gave up */
     LORA_ERR_CUDA = 8,          /* a CUDA runtime call failed (e.g. launch) */
-    LORA_ERR_UNSUPPORTED = 9    /* no kernel for this device or configuration */
+    LORA_ERR_UNSUPPORTED = 9,   /* no kernel for this device or configuration */
+    LORA_ERR_NO_PAGES = 10      /* device: lora_kv_step ran out of free cache pages */
 } lora_status_t;
 
 /* Kernel path of lora_apply_ex. */

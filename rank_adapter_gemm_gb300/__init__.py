@@ -28,6 +28,8 @@ __all__ = [
     "lora_build_index", "lora_build_index_seq", "lora_workspace_bytes", "lora_workspace_xa_offset", "lora_shrink", "lora_expand", "lora_apply", "lora_resolve_path",
     "apply", "lora_apply_noalloc", "lora_apply_overlap", "lora_moe_slot_pointers", "lora_build_index_moe", "lora_apply_moe",
     "lora_build_index_activated", "lora_plan_bytes", "lora_build_plan", "lora_apply_plan", "lora_build_plans", "Plan", "apply_with_base", "SlotTable", "TokenIndex", "Workspace",
+    "PagedKV", "KVStep", "Rope", "Attention", "lora_kv_step", "lora_rope_phases", "lora_rope_append", "lora_attend",
+    "lora_attend_workspace_bytes", "lora_attend_resolve_path", "LORA_MAX_SEQS",
 ]
 
 
@@ -484,3 +486,8 @@ class Workspace:
         torch = _torch()
         nbytes = lora_workspace_bytes(T, shape)
         self.buf = torch.zeros((nbytes + 3) // 4, dtype=torch.float32, device=device)
+
+
+from .attention import (Attention, KVStep, LORA_MAX_SEQS, PagedKV, Rope, lora_attend,  # noqa: E402
+                        lora_attend_resolve_path, lora_attend_workspace_bytes, lora_kv_step, lora_rope_append,
+                        lora_rope_phases)

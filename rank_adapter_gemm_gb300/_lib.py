@@ -29,6 +29,7 @@ STATUS = {
     7: "LORA_ERR_TIMEOUT",
     8: "LORA_ERR_CUDA",
     9: "LORA_ERR_UNSUPPORTED",
+    10: "LORA_ERR_NO_PAGES",
 }
 globals().update({name: code for code, name in STATUS.items()})
 
@@ -48,6 +49,17 @@ EXPORTED = (
 )
 
 
+# Every function include/lora_attention.h declares.
+EXPORTED_ATTENTION = (
+    "lora_kv_step", "lora_rope_phases", "lora_rope_append", "lora_attend_workspace_bytes", "lora_attend_resolve_path",
+    "lora_attend",
+)
+
+LORA_MAX_SEQS = 4096
+ATTEND_PATHS = {"auto": 0, "decode": 1, "prompt": 2}
+ROPE_KINDS = {"plain": 0, "linear": 1, "ntk": 2, "llama3": 3, "yarn": 4}
+
+
 class lora_shape_t(ctypes.Structure):
     _fields_ = [
         ("S", ctypes.c_int32),
@@ -56,6 +68,31 @@ class lora_shape_t(ctypes.Structure):
         ("n_slices", ctypes.c_int32),
         ("slice_offsets", ctypes.c_int32 * (LORA_MAX_SLICES + 1)),
     ]
+
+
+class lora_kv_t(ctypes.Structure):
+    _fields_ = [
+        ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+        ("n_pages", ctypes.c_int32), ("page_size", ctypes.c_int32), ("n_kv", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32),
+        ("page_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
+        ("type", ctypes.c_int32), ("k_scale", ctypes.c_float), ("v_scale", ctypes.c_float),
+    ]
+
+
+class lora_rope_scaling_t(ctypes.Structure):
+    _fields_ = [("kind", ctypes.c_int32)] + [(name, ctypes.c_double) for name in (
+        "factor", "low_freq_factor", "high_freq_factor", "beta_fast", "beta_slow", "original")]
+
+
+class lora_rope_t(ctypes.Structure):
+    _fields_ = [("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("mscale", ctypes.c_float),
+                ("phases", ctypes.c_void_p)]
+
+
+class lora_attention_t(ctypes.Structure):
+    _fields_ = [("n_heads", ctypes.c_int32), ("scale", ctypes.c_float), ("softcap", ctypes.c_float),
+                ("window", ctypes.c_int32), ("slopes", ctypes.c_void_p)]
 
 
 class LoraError(RuntimeError):
@@ -118,6 +155,16 @@ def load() -> ctypes.CDLL:
         "lora_set_slot_table_tma": (ST, [P, P, SH, P, P, P, P, P]),
         "lora_apply_moe_ex": (ST, [P, I64, I32, P, I64, I32, I32, SH, P, P, P, P, ST, P, SZ, P, P]),
         "lora_apply_moe_plan_ex": (ST, [P, I64, I32, P, I64, I32, I32, SH, P, SZ, ST, P, SZ, P, P]),
+    }
+    KV, AT = ctypes.POINTER(lora_kv_t), ctypes.POINTER(lora_attention_t)
+    sig |= {
+        "lora_kv_step": (ST, [P, P, I32, I32, P, I32, P, I64, I32, I32, P, P, P, P, P, P, P, P]),
+        "lora_rope_phases": (ST, [I32, ctypes.c_double, ctypes.POINTER(lora_rope_scaling_t), P,
+                                  ctypes.POINTER(ctypes.c_float)]),
+        "lora_rope_append": (ST, [P, I64, I32, I32, ctypes.POINTER(lora_rope_t), P, P, P, I64, KV, P, P]),
+        "lora_attend_workspace_bytes": (ST, [AT, KV, ctypes.POINTER(SZ)]),
+        "lora_attend_resolve_path": (ST, [ST, AT, KV, I32]),
+        "lora_attend": (ST, [P, I64, P, I64, P, I32, I32, P, P, P, I64, I32, KV, AT, I32, ST, P, SZ, P, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)

@@ -1,0 +1,196 @@
+"""Binding of include/lora_attention.h: the attention side of a serving step.
+
+Per step ``KVStep.build`` writes the block tables, slot map and positions from
+the requests' lengths; per layer ``Rope.append`` turns q and k of the packed
+projection and writes k and v into the layer's ``PagedKV``, and
+``Attention.run`` attends over it.  As in the rest of the binding, the
+``lora_*`` functions carry the C names and pass addresses, strides and the
+current stream; the classes only hold the caller-owned buffers.
+"""
+from __future__ import annotations
+
+import ctypes
+from typing import Mapping, Optional
+
+import numpy as np
+
+from . import _dev, _p, _rows, _stream, _torch
+from ._lib import (ATTEND_PATHS, LORA_MAX_SEQS, ROPE_KINDS, check, load, lora_attention_t, lora_kv_t,
+                   lora_rope_scaling_t, lora_rope_t)
+
+
+def _i32(t, name, n=None, dtype=None):
+    _dev(t, name, dtype or _torch().int32)
+    if not t.is_contiguous() or (n is not None and t.numel() != n):
+        raise ValueError(f"{name} must be contiguous" + (f" with {n} elements" if n is not None else ""))
+    return t.data_ptr()
+
+
+def _table(t, n_seq):
+    """(address, row stride, width) of a block table."""
+    _dev(t, "block_table", _torch().int32)
+    if t.dim() != 2 or t.shape[0] != n_seq or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError("block_table must be a 2-D int32 tensor, one row a request, with unit column stride")
+    return t.data_ptr(), max(t.stride(0), t.shape[1]), t.shape[1]
+
+
+def lora_kv_step(ctx_lens, new_lens, page_size, free_pages, block_table, q_offsets, kv_lens, positions, seq_ids,
+                 slot_map, taken, err, stream=None) -> None:
+    n, T = ctx_lens.numel(), positions.numel()
+    table, ld, width = _table(block_table, n)
+    check(load().lora_kv_step(
+        _i32(ctx_lens, "ctx_lens"), _i32(new_lens, "new_lens", n), n, int(page_size), _i32(free_pages, "free_pages"),
+        free_pages.numel(), table, ld, width, T, _i32(q_offsets, "q_offsets", n + 1), _i32(kv_lens, "kv_lens", n),
+        _i32(positions, "positions"), _i32(seq_ids, "seq_ids", T),
+        _i32(slot_map, "slot_map", T, _torch().int64), _i32(taken, "taken", 1), _p(err), _stream(stream)),
+        "lora_kv_step")
+
+
+def lora_rope_phases(rot_dim: int, theta: float, scaling: Optional[Mapping] = None):
+    """(uint64 phases [rot_dim / 2], factor on cos and sin) of a model's rotary
+    frequencies; scaling: {"kind": "linear" | "ntk" | "llama3" | "yarn", "factor": ...}
+    and, by kind, low_freq_factor, high_freq_factor, beta_fast, beta_slow, original."""
+    sc = None
+    if scaling is not None:
+        fields = dict(scaling)
+        kind = fields.pop("kind")
+        if kind not in ROPE_KINDS:
+            raise ValueError(f"unknown rotary scaling {kind!r}")
+        known = {name for name, _ in lora_rope_scaling_t._fields_}
+        if not set(fields) <= known:
+            raise ValueError(f"unknown rotary scaling fields {sorted(set(fields) - known)}")
+        sc = lora_rope_scaling_t(kind=ROPE_KINDS[kind], **{k: float(v) for k, v in fields.items()})
+    phases = np.zeros(max(int(rot_dim) // 2, 1), np.uint64)
+    mscale = ctypes.c_float(0.0)
+    check(load().lora_rope_phases(int(rot_dim), float(theta), ctypes.byref(sc) if sc is not None else None,
+                                  _p(phases), ctypes.byref(mscale)), "lora_rope_phases")
+    return phases, float(mscale.value)
+
+
+def lora_rope_append(qkv, q_out, n_heads, rope: lora_rope_t, positions, slot_map, kv: lora_kv_t, err,
+                     stream=None) -> None:
+    ldqkv, ldq, T = _rows(qkv, "qkv"), _rows(q_out, "q_out"), qkv.shape[0]
+    n_heads = int(n_heads)
+    if (q_out.shape[0] != T or qkv.shape[1] != (n_heads + 2 * kv.n_kv) * kv.head_dim
+            or q_out.shape[1] < n_heads * kv.head_dim):
+        raise ValueError("qkv must have n_heads + 2 n_kv heads and q_out n_heads heads, with the same rows")
+    check(load().lora_rope_append(qkv.data_ptr(), ldqkv, T, n_heads, rope, _i32(positions, "positions", T),
+                                  _i32(slot_map, "slot_map", T, _torch().int64), q_out.data_ptr(), ldq, kv, _p(err),
+                                  _stream(stream)), "lora_rope_append")
+
+
+def lora_attend_workspace_bytes(att: lora_attention_t, kv: lora_kv_t) -> int:
+    out = ctypes.c_size_t(0)
+    check(load().lora_attend_workspace_bytes(att, kv, ctypes.byref(out)), "lora_attend_workspace_bytes")
+    return int(out.value)
+
+
+def lora_attend_resolve_path(path: str, att: lora_attention_t, kv: lora_kv_t, max_q_hint: int) -> str:
+    code = load().lora_attend_resolve_path(ATTEND_PATHS[path], att, kv, int(max_q_hint))
+    return {v: k for k, v in ATTEND_PATHS.items()}[int(code)]
+
+
+def lora_attend(q, out, q_offsets, kv_lens, block_table, kv: lora_kv_t, att: lora_attention_t, ws, err,
+                max_q_hint: int = 0, lse=None, path: str = "auto", stream=None) -> None:
+    ldq, ldo, T, n = _rows(q, "q"), _rows(out, "out"), q.shape[0], kv_lens.numel()
+    cols = att.n_heads * kv.head_dim
+    if out.shape[0] != T or q.shape[1] < cols or out.shape[1] < cols:
+        raise ValueError("q and out must have the same rows and n_heads * head_dim columns")
+    if lse is not None:
+        _dev(lse, "lse", _torch().float32)
+        if lse.shape != (T, att.n_heads) or not lse.is_contiguous():
+            raise ValueError("lse must be a contiguous fp32 [T, n_heads] tensor")
+    table, ld, width = _table(block_table, n)
+    check(load().lora_attend(q.data_ptr(), ldq, out.data_ptr(), ldo, _p(lse), T, n,
+                             _i32(q_offsets, "q_offsets", n + 1), _i32(kv_lens, "kv_lens"), table, ld, width, kv, att,
+                             int(max_q_hint), ATTEND_PATHS[path], ws.data_ptr(), ws.numel() * ws.element_size(),
+                             _p(err), _stream(stream)), "lora_attend")
+
+
+class PagedKV:
+    """A layer's paged cache: k and v are [page, token, head, dim] tensors (any
+    strides with contiguous dims, the same for both), bf16 or float8_e4m3fn (or
+    uint8 codes); an e4m3 value is its code times the scale."""
+
+    def __init__(self, k, v, k_scale: float = 1.0, v_scale: float = 1.0):
+        torch = _torch()
+        for t, name in ((k, "k"), (v, "v")):
+            _dev(t, name)
+            if t.dim() != 4 or t.stride(3) != 1 or t.dtype not in (torch.bfloat16, torch.float8_e4m3fn, torch.uint8):
+                raise TypeError(f"{name} must be a bf16 or e4m3 [page, token, head, dim] tensor with contiguous dims")
+        if k.shape != v.shape or k.stride() != v.stride() or k.dtype != v.dtype:
+            raise ValueError("k and v must have the same shape, strides and type")
+        self.k, self.v = k, v
+        self.c = lora_kv_t(k.data_ptr(), v.data_ptr(), *k.shape, *k.stride()[:3],
+                           0 if k.dtype == torch.bfloat16 else 1, float(k_scale), float(v_scale))
+
+    @classmethod
+    def empty(cls, n_pages: int, page_size: int, n_kv: int, head_dim: int, dtype=None, k_scale: float = 1.0,
+              v_scale: float = 1.0, device="cuda") -> "PagedKV":
+        """A cache in which the tokens of one head of a page are contiguous."""
+        torch = _torch()
+        k, v = (torch.empty(n_pages, n_kv, page_size, head_dim, dtype=dtype or torch.bfloat16,
+                            device=device).transpose(1, 2) for _ in range(2))
+        return cls(k, v, k_scale, v_scale)
+
+
+class KVStep:
+    """Block tables and the per-step arrays of lora_kv_step: room for T rows of
+    n_seq requests of up to max_pages pages.  The block table persists over
+    steps; ``taken`` is the number of pages taken from the front of free_pages."""
+
+    def __init__(self, n_seq: int, T: int, max_pages: int, page_size: int, device="cuda"):
+        torch = _torch()
+        self.page_size = int(page_size)
+
+        def zeros(*shape, dtype=torch.int32):
+            return torch.zeros(*shape, dtype=dtype, device=device)
+        self.block_table = zeros(n_seq, max_pages)
+        self.q_offsets, self.kv_lens = zeros(n_seq + 1), zeros(n_seq)
+        self.positions, self.seq_ids, self.slot_map = zeros(T), zeros(T), zeros(T, dtype=torch.int64)
+        self.taken, self.err = zeros(1), zeros(1)
+
+    def build(self, ctx_lens, new_lens, free_pages, stream=None) -> None:
+        lora_kv_step(ctx_lens, new_lens, self.page_size, free_pages, self.block_table, self.q_offsets, self.kv_lens,
+                     self.positions, self.seq_ids, self.slot_map, self.taken, self.err, stream)
+
+
+class Rope:
+    """Rotary frequencies of one model on the device."""
+
+    def __init__(self, head_dim: int, rot_dim: Optional[int] = None, theta: float = 10000.0, interleaved: bool = False,
+                 scaling: Optional[Mapping] = None, device="cuda"):
+        torch = _torch()
+        self.rot_dim = int(head_dim if rot_dim is None else rot_dim)
+        phases, mscale = lora_rope_phases(self.rot_dim, theta, scaling)
+        self.phases = torch.from_numpy(phases.view(np.int64)).to(device)
+        self.c = lora_rope_t(self.rot_dim, int(bool(interleaved)), mscale, self.phases.data_ptr())
+
+    def append(self, qkv, q_out, n_heads: int, kv: PagedKV, positions, slot_map, err, stream=None) -> None:
+        """q of qkv turned into q_out; k turned, and v, written to kv at slot_map."""
+        lora_rope_append(qkv, q_out, n_heads, self.c, positions, slot_map, kv.c, err, stream)
+
+
+class Attention:
+    """One layer's attention over a PagedKV: its parameters, workspace and error
+    word.  Layers whose calls do not overlap can share one by passing ``kv``."""
+
+    def __init__(self, n_seq: int, T: int, n_heads: int, kv: PagedKV, scale: Optional[float] = None,
+                 softcap: float = 0.0, window: int = 0, slopes=None, device="cuda"):
+        torch = _torch()
+        if not 0 <= n_seq <= LORA_MAX_SEQS:
+            raise ValueError(f"between 0 and {LORA_MAX_SEQS} requests")
+        self.n_seq, self.T, self.kv, self.slopes = int(n_seq), int(T), kv, slopes
+        if slopes is not None:
+            _i32(slopes, "slopes", int(n_heads), torch.float32)
+        scale = float(kv.c.head_dim) ** -0.5 if scale is None else float(scale)
+        self.c = lora_attention_t(int(n_heads), scale, float(softcap or 0.0), int(window or 0),
+                                  slopes.data_ptr() if slopes is not None else None)
+        self.ws = torch.zeros(lora_attend_workspace_bytes(self.c, kv.c), dtype=torch.uint8, device=device)
+        self.err = torch.zeros(1, dtype=torch.int32, device=device)
+
+    def run(self, q, out, q_offsets, kv_lens, block_table, max_q_hint: int = 0, kv: Optional[PagedKV] = None, lse=None,
+            path: str = "auto", stream=None) -> None:
+        """out = attention of q's rows; max_q_hint is an upper bound on a request's rows."""
+        lora_attend(q, out, q_offsets, kv_lens, block_table, (kv or self.kv).c, self.c, self.ws, self.err, max_q_hint,
+                    lse, path, stream)

@@ -140,6 +140,7 @@ const char *lora_status_string(lora_status_t status) {
     case LORA_ERR_TIMEOUT: return "LORA_ERR_TIMEOUT: a bounded wait between thread blocks gave up";
     case LORA_ERR_CUDA: return "LORA_ERR_CUDA: a CUDA runtime call failed";
     case LORA_ERR_UNSUPPORTED: return "LORA_ERR_UNSUPPORTED: no kernel for this device or configuration";
+    case LORA_ERR_NO_PAGES: return "LORA_ERR_NO_PAGES: not enough free cache pages for every request of the step";
     }
     return "LORA_ERR_UNKNOWN";
 }
