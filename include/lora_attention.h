@@ -27,6 +27,7 @@ extern "C" {
 #define LORA_MAX_SEQS 4096
 #define LORA_MAX_PAGE_SIZE 1024
 #define LORA_MAX_HEAD_DIM 256
+#define LORA_MAX_KV_LEN (1 << 30)
 
 /* Element type of the cache. */
 typedef enum {
@@ -175,8 +176,8 @@ lora_status_t lora_rope_append(const void *qkv, int64_t ldqkv, int32_t T, int32_
  * Limits (LORA_ERR_UNSUPPORTED): head_dim 64 or 128.  n_heads a multiple of
  * n_kv, n_seq <= LORA_MAX_SEQS, scale finite, softcap >= 0, window >= 0
  * (LORA_ERR_INVALID_ARG).  Device errors: LORA_ERR_INVALID_ARG (offsets out of
- * order or past T, kv_lens negative or beyond the table row: that request is
- * skipped), LORA_ERR_SLOT_RANGE (a page id outside [0, n_pages): its keys and
+ * order or past T, kv_lens negative, beyond the table row or above
+ * LORA_MAX_KV_LEN: that request is skipped), LORA_ERR_SLOT_RANGE (a page id outside [0, n_pages): its keys and
  * values read as zeros), LORA_ERR_TIMEOUT (a wait inside the kernel gave up).
  */
 typedef struct {

@@ -1,0 +1,696 @@
+// Attention of few rows a request over the paged cache (LORA_ATTEND_DECODE).
+//
+// What it must read is the cache: 2 head_dim elements a key and key head, for
+// group * rows dot products each, so HBM bandwidth bounds it.  The split below
+// therefore spreads the bytes evenly whatever the lengths, and keeps copies in
+// flight at all times:
+//   - A segment is one (request, key head, tile of up to ROWS query rows), a
+//     step 32 of its keys.  All steps of the call, in order, are cut into equal
+//     shares, one a warp: a long request spreads over the whole GPU, many short
+//     ones share a warp.  Every block finds its shares by a prefix sum over the
+//     requests' lengths, so no plan has to be built or kept.
+//   - A warp streams its steps' k and v through a private ring of cp.async
+//     stages with no barrier between warps; the copies run ahead over segment
+//     boundaries.  Rows are gathered key by key through the block table, so any
+//     page size and any strides go the same way.
+//   - The running maximum, sum and output stay in fp32 registers; both products
+//     are warp MMAs (m16n8k16), which at 16 rows a tile need a fraction of the
+//     time of the copies.
+//   - A segment that one warp covers is written at once.  The others leave
+//     (maximum, sum, output) partials: after the last step the block joins those
+//     of its own warps, and the last block to arrive at a segment joins the
+//     blocks', always in the order of the keys, so results do not depend on
+//     timing.  Nothing waits.
+//
+// Weights are rounded for the second product: to f16 (11 bits) against an e4m3
+// cache, scaled by 2^12 so that weights down to 2^-26 of the largest keep them
+// all; against a bf16 cache to two bf16 parts, value and remainder (16 bits).
+// With at most 8 rows the remainder goes into the MMA's unused rows 8..15 and
+// costs nothing.  An e4m3 code is exact in f16; a query row is scaled by a power
+// of two into f16, exact to 2^-24 of its largest element.
+#include <cuda_fp16.h>
+
+#include "attention.cuh"
+#include "tc.cuh"
+
+namespace lora {
+
+namespace {
+
+constexpr int kMaxGrid = 160;
+constexpr int kKeys = 32;                 // keys a step
+constexpr int kSmemMax = 227 * 1024;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+template <int HD, bool E4M3>
+struct Shape32 {
+    static constexpr int kRowB = HD * (E4M3 ? 1 : 2);     // bytes of a key
+    static constexpr int kChunks = kRowB / 16;            // 16-byte pieces of a key
+    static constexpr int kTileB = kKeys * kRowB;
+    static constexpr int kStageB = 2 * kTileB;            // k and v of a step
+    static constexpr int kWarps = kStageB >= 16384 ? 4 : 8;
+};
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// tanh to about 2^-20: from the exponential away from zero, by the series near it.
+__device__ __forceinline__ float tanh_of(float z) {
+    const float far = 1.0f - __fdividef(2.0f, ex2(z * (2.0f * kLog2e)) + 1.0f);
+    const float z2 = z * z;
+    const float near = z * (1.0f + z2 * (-0.33333333f + z2 * (0.13333333f + z2 * (-0.05396825f))));
+    return fabsf(z) < 0.25f ? near : far;
+}
+
+__device__ __forceinline__ void mma_f16_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                              uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+
+__device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+
+// Two e4m3 codes (low 16 bits) to two f16, exact.
+__device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t w) {
+    uint32_t r;
+    asm("{\n\t.reg .b16 l;\n\tcvt.u16.u32 l, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t}" : "=r"(r) : "r"(w));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// Byte offset of a 16-byte piece inside a k or v tile: pieces are XORed with the
+// row so that eight rows at one piece fall in different banks.
+template <int CHUNKS>
+__device__ __forceinline__ uint32_t piece_at(int row, int piece) {
+    if constexpr (CHUNKS == 4) return row * 64 + ((piece ^ ((row >> 1) & 3)) << 4);
+    return row * (CHUNKS * 16) + ((piece ^ (row & 7)) << 4);
+}
+
+// A segment: its request, key head and row tile, and its keys.
+struct Segment {
+    int32_t seq, head, tile;  // tile: first of its rows, rows numbered token * group + head in group
+    int32_t q0, n, len;       // the request's rows and length
+    int32_t lo, base, steps;  // first key that a row sees, the multiple of 32 at or before it, steps from there
+    int32_t begin;            // index of its first step among all of the call
+};
+
+// The first key of a request that any of its rows sees.
+__device__ __forceinline__ int32_t first_key(const AttendArgs &a, const RequestRows &r) {
+    if (a.window <= 0) return 0;
+    return static_cast<int32_t>(max(int64_t(0), int64_t(r.len) - r.n - a.window + 1));
+}
+
+__device__ __forceinline__ int32_t steps_of(const AttendArgs &a, const RequestRows &r) {
+    return r.n > 0 ? (r.len - (first_key(a, r) & ~(kKeys - 1)) + kKeys - 1) / kKeys : 0;
+}
+
+template <int ROWS>
+__device__ __forceinline__ int32_t tiles_of(const AttendArgs &a, int32_t n) {
+    return static_cast<int32_t>((int64_t(n) * a.group + ROWS - 1) / ROWS);
+}
+
+// The segment of request `seq` that step x of the call belongs to.
+template <int ROWS>
+__device__ __forceinline__ Segment segment_at(const AttendArgs &a, const int32_t *s_pref, int32_t seq, int32_t x) {
+    const RequestRows r = load_rows(a, seq);
+    Segment s;
+    s.seq = seq;
+    s.q0 = r.q0;
+    s.n = r.n;
+    s.len = r.len;
+    s.lo = first_key(a, r);
+    s.base = s.lo & ~(kKeys - 1);
+    s.steps = max(1, steps_of(a, r));
+    const int32_t tiles = max(1, tiles_of<ROWS>(a, r.n)), i = (x - s_pref[seq]) / s.steps;
+    s.head = i / tiles;  // tiles of one head are neighbours: they read the same keys
+    s.tile = (i - s.head * tiles) * ROWS;
+    s.begin = s_pref[seq] + i * s.steps;
+    return s;
+}
+
+// The request that step x (below the total) belongs to.
+__device__ __forceinline__ int32_t find_seq(const int32_t *s_pref, int32_t n, int32_t x) {
+    int32_t lo = 0, hi = n - 1;
+    while (lo < hi) {
+        const int32_t mid = (lo + hi + 1) >> 1;
+        if (s_pref[mid] <= x) lo = mid;
+        else hi = mid - 1;
+    }
+    return lo;
+}
+
+// A partial: maxima and sums of ROWS rows, then their outputs, fp32.
+template <int HD, int ROWS>
+constexpr int kPartial = ROWS * (HD + 2);
+
+// Joins partials first..last (slot 2 i, or 2 i + 1 where the segment begins in
+// share i) in order and writes the result: rows of `out`, or one partial.
+template <int HD, int ROWS>
+__device__ void join(const AttendArgs &a, const float *parts, int32_t first, int32_t last, int64_t share,
+                     const Segment &s, float shift, float *to, int lane) {
+    constexpr int V = HD / 32;
+    const int32_t rows = min(ROWS, s.n * a.group - s.tile);
+    const int64_t begin = s.begin;
+    for (int r = 0; r < rows; ++r) {
+        float top = -INFINITY;
+        for (int32_t i = first; i <= last; ++i) {
+            const float *p = parts + (2 * i + (begin >= i * share ? 1 : 0)) * int64_t(kPartial<HD, ROWS>);
+            top = fmaxf(top, __ldcg(p + r));
+        }
+        const float ref = top == -INFINITY ? 0.0f : top;
+        float sum = 0.0f, o[V] = {};
+#pragma unroll 4
+        for (int32_t i = first; i <= last; ++i) {
+            const float *p = parts + (2 * i + (begin >= i * share ? 1 : 0)) * int64_t(kPartial<HD, ROWS>);
+            const float w = ex2(__ldcg(p + r) - ref);
+            sum += w * __ldcg(p + ROWS + r);
+            const float *v = p + 2 * ROWS + r * HD + lane * V;
+            if constexpr (V == 4) {
+                const float4 x = __ldcg(reinterpret_cast<const float4 *>(v));
+                o[0] += w * x.x, o[1] += w * x.y, o[2] += w * x.z, o[3] += w * x.w;
+            } else {
+                const float2 x = __ldcg(reinterpret_cast<const float2 *>(v));
+                o[0] += w * x.x, o[1] += w * x.y;
+            }
+        }
+        if (to != nullptr) {
+            if (lane == 0) {
+                to[r] = top;
+                to[ROWS + r] = sum;
+            }
+#pragma unroll
+            for (int e = 0; e < V; ++e) to[2 * ROWS + r * HD + lane * V + e] = o[e];
+        } else {
+            const int32_t row = s.tile + r, t = s.q0 + row / a.group, h = s.head * a.group + row % a.group;
+            const float inv = sum > 0.0f ? a.kv.v_scale / sum : sum == 0.0f ? 0.0f : sum;
+            uint32_t w[V / 2];
+#pragma unroll
+            for (int e = 0; e < V / 2; ++e) w[e] = pack_bf16x2(o[2 * e] * inv, o[2 * e + 1] * inv);
+            uint16_t *dst = a.out + t * a.ldo + h * HD + lane * V;
+            if constexpr (V == 4) *reinterpret_cast<uint2 *>(dst) = make_uint2(w[0], w[1]);
+            else *reinterpret_cast<uint32_t *>(dst) = w[0];
+            if (a.lse != nullptr && lane == 0)
+                a.lse[int64_t(t) * a.n_heads + h] = sum == 0.0f ? -INFINITY : kLn2 * (ref - shift) + logf(sum);
+        }
+    }
+}
+
+template <int HD, bool E4M3, int ROWS>
+__global__ void __launch_bounds__(Shape32<HD, E4M3>::kWarps * 32, 1)
+attend_decode_kernel(const AttendArgs a, float *parts, int32_t *counters, int stages, int pref_bytes) {
+    using C = Shape32<HD, E4M3>;
+    constexpr int NW = C::kWarps, NT = NW * 32, MB = ROWS == 32 ? 2 : 1, KK = HD / 16, DT = HD / 8;
+    constexpr bool kHalf = ROWS == 8;      // only rows 0..7 of the MMA's 16 hold queries
+    constexpr bool kQShared = ROWS == 32;  // query fragments in shared memory, else in registers
+    constexpr float kShift = E4M3 ? 12.0f : 0.0f;
+    extern __shared__ __align__(128) unsigned char smem[];
+    int32_t *s_pref = reinterpret_cast<int32_t *>(smem);
+    __shared__ int64_t s_warp[NW];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c4 = lane & 3;
+
+    // steps of every request: exclusive prefix in s_pref[0..n_seq], total behind it
+    int32_t total;
+    {
+        const int32_t per = (a.n_seq + NT - 1) / NT, i0 = min(a.n_seq, tid * per), i1 = min(a.n_seq, i0 + per);
+        int64_t mine = 0;
+        for (int32_t i = i0; i < i1; ++i) {
+            const RequestRows r = load_rows(a, i);
+            if (!r.ok && blockIdx.x == 0) report_error(a.err, LORA_ERR_INVALID_ARG);
+            mine += int64_t(steps_of(a, r)) * a.kv.n_kv * tiles_of<ROWS>(a, r.n);
+        }
+        int64_t incl = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t u = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += u;
+        }
+        if (lane == 31) s_warp[warp] = incl;
+        __syncthreads();
+        int64_t run = incl - mine, sum = 0;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) {
+            if (w < warp) run += s_warp[w];
+            sum += s_warp[w];
+        }
+        if (sum > INT32_MAX) {  // the same in every block
+            if (blockIdx.x == 0 && tid == 0) report_error(a.err, LORA_ERR_UNSUPPORTED);
+            return;
+        }
+        for (int32_t i = i0; i < i1; ++i) {
+            const RequestRows r = load_rows(a, i);
+            s_pref[i] = static_cast<int32_t>(run);
+            run += int64_t(steps_of(a, r)) * a.kv.n_kv * tiles_of<ROWS>(a, r.n);
+        }
+        total = static_cast<int32_t>(sum);
+        if (tid == 0) s_pref[a.n_seq] = total;
+        __syncthreads();
+    }
+
+    // rows of requests without cached tokens
+    for (int32_t i = blockIdx.x; i < a.n_seq; i += gridDim.x) {
+        if (s_pref[i + 1] != s_pref[i]) continue;
+        const RequestRows r = load_rows(a, i);
+        for (int64_t e = tid; e < int64_t(r.n) * a.n_heads; e += NT) {
+            const int64_t t = r.q0 + e / a.n_heads, h = e % a.n_heads;
+            for (int d = 0; d < HD; d += 8) stg_u4(a.out + t * a.ldo + h * HD + d, make_uint4(0, 0, 0, 0));
+            if (a.lse != nullptr) a.lse[t * a.n_heads + h] = -INFINITY;
+        }
+    }
+
+    const int32_t shares = gridDim.x * NW;
+    const int64_t share = (int64_t(total) + shares - 1) / shares;  // steps a warp
+    const int32_t me = blockIdx.x * NW + warp;
+    const int32_t x0 = static_cast<int32_t>(min(int64_t(total), me * share));
+    const int32_t x1 = static_cast<int32_t>(min(int64_t(total), x0 + share));
+
+    const uint32_t ring = tc::smem_u32(smem) + pref_bytes + (kQShared ? NW * KK * MB * 512 : 0) +
+                          warp * stages * C::kStageB;
+    uint4 *s_q = reinterpret_cast<uint4 *>(smem + pref_bytes) + warp * KK * MB * 32;
+
+    // ---- the copying side: where its next step is ------------------------------
+    Segment ls{};
+    int32_t lx = x0, lkey = 0, lleft = 0, lpage = -1;
+    const int32_t *ltab = nullptr;
+    // whether this lane's key of the next step is one that a row sees, and its page
+    const auto has_key = [&]() { return lkey + lane >= ls.lo && lkey + lane < ls.len; };
+    const auto look_up = [&]() {
+        if (lx < x1 && has_key()) lpage = __ldg(ltab + ((lkey + lane) >> a.kv.page_shift));
+    };
+    const auto open_load = [&](int32_t seq) {
+        ls = segment_at<ROWS>(a, s_pref, seq, lx);
+        lkey = ls.base + (lx - ls.begin) * kKeys;
+        lleft = ls.steps - (lx - ls.begin);
+        ltab = a.table + ls.seq * a.ld_table;
+    };
+    if (x0 < x1) {
+        open_load(find_seq(s_pref, a.n_seq, x0));
+        look_up();
+    }
+    const auto issue = [&](int stage) {
+        if (lx < x1) {
+            const int32_t key = lkey + lane;
+            const bool has = has_key(), ok = has && lpage >= 0 && lpage < a.kv.n_pages;
+            if (has && !ok) report_error(a.err, LORA_ERR_SLOT_RANGE);
+            const int64_t at = ok ? lpage * a.kv.page_b + (key & a.kv.page_mask) * a.kv.token_b + ls.head * a.kv.head_b
+                                  : -1;
+            const uint32_t dst = ring + stage * C::kStageB;
+            const int piece = lane % C::kChunks;
+#pragma unroll
+            for (int i = 0; i < C::kChunks; ++i) {
+                const int row = i * (32 / C::kChunks) + lane / C::kChunks;
+                const int64_t o = __shfl_sync(0xffffffffu, at, row);
+                const int64_t src = (o >= 0 ? o : 0) + piece * 16;
+                const uint32_t d = dst + piece_at<C::kChunks>(row, piece);
+                tc::cp16(d, a.kv.k + src, o >= 0);
+                tc::cp16(d + C::kTileB, a.kv.v + src, o >= 0);
+            }
+            ++lx;
+            lkey += kKeys;
+            if (--lleft == 0 && lx < x1) {
+                int32_t seq = ls.seq;
+                while (s_pref[seq + 1] <= lx) ++seq;
+                open_load(seq);
+            }
+            look_up();
+        }
+        tc::cp_commit();
+    };
+
+    // ---- the computing side ----------------------------------------------------
+    Segment cs{};
+    int32_t cleft = 0, ckey = 0, pos_lo = 0, pos_hi = 0;
+    int32_t pos[MB][2];
+    uint32_t qf[kQShared ? 1 : KK][4];
+    float m[MB][2], l[MB][2], mult[MB][2], slope[MB][2], acc[MB][DT][4];
+
+    const auto open_compute = [&](int32_t seq, int32_t x) {
+        cs = segment_at<ROWS>(a, s_pref, seq, x);
+        cleft = cs.steps - (x - cs.begin);
+        ckey = cs.base + (x - cs.begin) * kKeys;
+        const int32_t rows = min(ROWS, cs.n * a.group - cs.tile);
+        pos_lo = cs.len - cs.n + cs.tile / a.group;
+        pos_hi = cs.len - cs.n + (cs.tile + rows - 1) / a.group;
+#pragma unroll
+        for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+            for (int i = 0; i < (kHalf ? 1 : 2); ++i) {
+                const int32_t r = mb * 16 + i * 8 + g, row = cs.tile + r;
+                const bool live = r < rows;
+                const int32_t token = row / a.group, h = cs.head * a.group + row % a.group;
+                pos[mb][i] = live ? cs.len - cs.n + token : -1;
+                slope[mb][i] = live && a.slopes != nullptr ? a.slopes[h] * kLog2e : 0.0f;
+                m[mb][i] = -INFINITY;
+                l[mb][i] = 0.0f;
+                mult[mb][i] = a.scale * a.kv.k_scale;
+                const uint16_t *src = a.q + (cs.q0 + token) * a.ldq + h * HD;
+                uint32_t w[KK][2];
+                if constexpr (E4M3) {
+                    // dims 4 c4 .. 4 c4 + 3 of each 16: the order in which a lane gets the codes of k
+                    float top = 0.0f;
+                    float f[KK][4];
+#pragma unroll
+                    for (int kk = 0; kk < KK; ++kk) {
+                        const uint2 u = live ? __ldg(reinterpret_cast<const uint2 *>(src + kk * 16 + 4 * c4))
+                                             : make_uint2(0, 0);
+                        f[kk][0] = bf16lo_to_f32(u.x), f[kk][1] = bf16hi_to_f32(u.x);
+                        f[kk][2] = bf16lo_to_f32(u.y), f[kk][3] = bf16hi_to_f32(u.y);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) top = fmaxf(top, fabsf(f[kk][e]));
+                    }
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                    // 2^e <= top < 2^(e + 1): the row times 2^-e is below 2
+                    const int e = top > 0.0f ? max(-60, min(60, static_cast<int>(__float_as_uint(top) >> 23) - 127)) : 0;
+                    const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+                    mult[mb][i] *= __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+#pragma unroll
+                    for (int kk = 0; kk < KK; ++kk) {
+                        w[kk][0] = pack_f16x2(f[kk][0] * down, f[kk][1] * down);
+                        w[kk][1] = pack_f16x2(f[kk][2] * down, f[kk][3] * down);
+                    }
+                } else {
+#pragma unroll
+                    for (int kk = 0; kk < KK; ++kk) {
+                        w[kk][0] = live ? __ldg(reinterpret_cast<const uint32_t *>(src + kk * 16 + 2 * c4)) : 0u;
+                        w[kk][1] = live ? __ldg(reinterpret_cast<const uint32_t *>(src + kk * 16 + 8 + 2 * c4)) : 0u;
+                    }
+                }
+#pragma unroll
+                for (int kk = 0; kk < KK; ++kk) {
+                    if constexpr (kQShared) {
+                        uint32_t *to = reinterpret_cast<uint32_t *>(s_q + (kk * MB + mb) * 32 + lane);
+                        to[i] = w[kk][0];
+                        to[2 + i] = w[kk][1];
+                    } else {
+                        qf[kk][i] = w[kk][0];
+                        qf[kk][2 + i] = w[kk][1];
+                        if (kHalf) qf[kk][1] = qf[kk][3] = 0u;
+                    }
+                }
+            }
+#pragma unroll
+        for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+            for (int d = 0; d < DT; ++d)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[mb][d][e] = 0.0f;
+    };
+
+    const auto step = [&](int stage) {
+        const uint32_t kt = ring + stage * C::kStageB, vt = kt + C::kTileB;
+        const int mat = lane >> 3, r8 = lane & 7;
+        float s[MB][4][4] = {};
+        // scores: 4 tiles of 8 keys
+#pragma unroll
+        for (int kk = 0; kk < KK; kk += E4M3 ? 4 : 2) {
+            uint32_t b[4][4];
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+                ldsm4(b[t], kt + piece_at<C::kChunks>(8 * t + r8, (E4M3 ? kk : 2 * kk) + mat));
+#pragma unroll
+            for (int u = 0; u < (E4M3 ? 4 : 2); ++u) {
+#pragma unroll
+                for (int mb = 0; mb < MB; ++mb) {
+                    uint4 q;
+                    if constexpr (kQShared) q = s_q[((kk + u) * MB + mb) * 32 + lane];
+                    else q = make_uint4(qf[kk + u][0], qf[kk + u][1], qf[kk + u][2], qf[kk + u][3]);
+#pragma unroll
+                    for (int t = 0; t < 4; ++t) {
+                        if constexpr (E4M3)
+                            mma_f16_16816(s[mb][t], q.x, q.y, q.z, q.w, e4m3x2_f16x2(b[t][u]),
+                                          e4m3x2_f16x2(b[t][u] >> 16));
+                        else
+                            mma_bf16_16816(s[mb][t], q.x, q.y, q.z, q.w, b[t][2 * u], b[t][2 * u + 1]);
+                    }
+                }
+            }
+        }
+        // weights: p = 2^(score log2 e - maximum), and the fragments of the second product
+        const bool masked = ckey + kKeys - 1 > pos_lo || (a.window > 0 && pos_hi - ckey >= a.window);
+        uint32_t hi[MB][2][4], lo[MB][2][4];
+#pragma unroll
+        for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+            for (int i = 0; i < (kHalf ? 1 : 2); ++i) {
+                float top = -INFINITY;
+                const float by = a.softcap > 0.0f ? mult[mb][i] / a.softcap : mult[mb][i] * kLog2e;
+                const float cap = a.softcap * kLog2e;
+#pragma unroll
+                for (int t = 0; t < 4; ++t)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float &x = s[mb][t][2 * i + e];
+                        x *= by;
+                        if (a.softcap > 0.0f) x = cap * tanh_of(x);
+                        const int32_t key = ckey + 8 * t + 2 * c4 + e;
+                        if (a.slopes != nullptr) x += slope[mb][i] * static_cast<float>(key - pos[mb][i]);
+                        if (masked && (key > pos[mb][i] || (a.window > 0 && pos[mb][i] - key >= a.window)))
+                            x = -INFINITY;
+                        top = fmaxf(top, x);
+                    }
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                const float now = fmaxf(m[mb][i], top);
+                const float ref = (now == -INFINITY ? 0.0f : now) - kShift;
+                if (__any_sync(0xffffffffu, now != m[mb][i])) {
+                    const float f = ex2(m[mb][i] - kShift - ref);
+                    l[mb][i] *= f;
+#pragma unroll
+                    for (int d = 0; d < DT; ++d) {
+                        acc[mb][d][2 * i] *= f;
+                        acc[mb][d][2 * i + 1] *= f;
+                        if (kHalf && !E4M3) {  // the remainder's part of the same row
+                            acc[mb][d][2] *= f;
+                            acc[mb][d][3] *= f;
+                        }
+                    }
+                    m[mb][i] = now;
+                }
+                float sum = 0.0f;
+#pragma unroll
+                for (int t = 0; t < 4; ++t) {
+                    const float p0 = ex2(s[mb][t][2 * i] - ref), p1 = ex2(s[mb][t][2 * i + 1] - ref);
+                    sum += p0 + p1;
+                    // keys 8 t + 2 c4, + 1: the A fragment's word of 16-key block t / 2
+                    const int w = (t & 1) * 2 + i;
+                    if constexpr (E4M3) {
+                        hi[mb][t / 2][w] = pack_f16x2(p0, p1);
+                        if (kHalf) hi[mb][t / 2][w + 1] = 0u;
+                    } else {
+                        const uint32_t h = pack_bf16x2(p0, p1);
+                        const uint32_t r = pack_bf16x2(p0 - bf16lo_to_f32(h), p1 - bf16hi_to_f32(h));
+                        hi[mb][t / 2][w] = h;
+                        if (kHalf) hi[mb][t / 2][w + 1] = r;
+                        else lo[mb][t / 2][w] = r;
+                    }
+                }
+                l[mb][i] += sum;
+            }
+        // output: 2 blocks of 16 keys, all dims
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+            for (int c = 0; c < C::kChunks; c += 2) {
+                uint32_t b[4];
+                ldsm4_t(b, vt + piece_at<C::kChunks>(kb * 16 + (mat & 1) * 8 + r8, c + (mat >> 1)));
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    if constexpr (E4M3) {
+                        // piece c + u, 16 dims: even dims in one MMA, odd dims in the next
+                        const uint32_t e0 = e4m3x2_f16x2(__byte_perm(b[2 * u], 0, 0x4420));
+                        const uint32_t e1 = e4m3x2_f16x2(__byte_perm(b[2 * u + 1], 0, 0x4420));
+                        const uint32_t o0 = e4m3x2_f16x2(__byte_perm(b[2 * u], 0, 0x4431));
+                        const uint32_t o1 = e4m3x2_f16x2(__byte_perm(b[2 * u + 1], 0, 0x4431));
+#pragma unroll
+                        for (int mb = 0; mb < MB; ++mb) {
+                            const uint32_t(&p)[4] = hi[mb][kb];
+                            mma_f16_16816(acc[mb][2 * (c + u)], p[0], p[1], p[2], p[3], e0, e1);
+                            mma_f16_16816(acc[mb][2 * (c + u) + 1], p[0], p[1], p[2], p[3], o0, o1);
+                        }
+                    } else {
+#pragma unroll
+                        for (int mb = 0; mb < MB; ++mb) {
+                            const uint32_t(&p)[4] = hi[mb][kb];
+                            mma_bf16_16816(acc[mb][c + u], p[0], p[1], p[2], p[3], b[2 * u], b[2 * u + 1]);
+                            if constexpr (!kHalf) {
+                                const uint32_t(&r)[4] = lo[mb][kb];
+                                mma_bf16_16816(acc[mb][c + u], r[0], r[1], r[2], r[3], b[2 * u], b[2 * u + 1]);
+                            }
+                        }
+                    }
+                }
+            }
+    };
+
+    // ends a segment, or this warp's part of it: rows to `out`, or a partial
+    const auto close = [&](int32_t x_end) {
+        const int32_t rows = min(ROWS, cs.n * a.group - cs.tile);
+        const bool whole = cs.begin >= x0 && cs.begin + cs.steps <= x_end;
+        float *part = parts + (2 * int64_t(me) + (cs.begin >= x0 ? 1 : 0)) * kPartial<HD, ROWS>;
+#pragma unroll
+        for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+            for (int i = 0; i < (kHalf ? 1 : 2); ++i) {
+                float sum = l[mb][i];
+                sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+                sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+                const int32_t r = mb * 16 + i * 8 + g, row = cs.tile + r;
+                if (r >= rows) continue;
+                const int32_t t = cs.q0 + row / a.group, h = cs.head * a.group + row % a.group;
+                const float inv = !whole ? 1.0f : sum > 0.0f ? a.kv.v_scale / sum : sum == 0.0f ? 0.0f : sum;
+                uint16_t *out = a.out + t * a.ldo + h * HD;
+                float *to = part + 2 * ROWS + r * HD;
+                if (c4 == 0) {
+                    if (!whole) {
+                        part[r] = m[mb][i];
+                        part[ROWS + r] = sum;
+                    } else if (a.lse != nullptr) {
+                        a.lse[int64_t(t) * a.n_heads + h] = sum == 0.0f ? -INFINITY
+                                                                        : kLn2 * (m[mb][i] - kShift) + logf(sum);
+                    }
+                }
+                if constexpr (E4M3) {
+#pragma unroll
+                    for (int c = 0; c < DT; c += 2) {  // dims 16 (c / 2) + 4 c4 + {0, 1, 2, 3}
+                        const float4 v = make_float4(acc[mb][c][2 * i] * inv, acc[mb][c + 1][2 * i] * inv,
+                                                     acc[mb][c][2 * i + 1] * inv, acc[mb][c + 1][2 * i + 1] * inv);
+                        const int d = 8 * c + 4 * c4;
+                        if (whole)
+                            *reinterpret_cast<uint2 *>(out + d) = make_uint2(pack_bf16x2(v.x, v.y),
+                                                                             pack_bf16x2(v.z, v.w));
+                        else
+                            *reinterpret_cast<float4 *>(to + d) = v;
+                    }
+                } else {
+#pragma unroll
+                    for (int d8 = 0; d8 < DT; ++d8) {  // dims 8 d8 + 2 c4 + {0, 1}
+                        float v0 = acc[mb][d8][2 * i], v1 = acc[mb][d8][2 * i + 1];
+                        if (kHalf) v0 += acc[mb][d8][2], v1 += acc[mb][d8][3];
+                        const int d = 8 * d8 + 2 * c4;
+                        if (whole) *reinterpret_cast<uint32_t *>(out + d) = pack_bf16x2(v0 * inv, v1 * inv);
+                        else *reinterpret_cast<float2 *>(to + d) = make_float2(v0, v1);
+                    }
+                }
+            }
+    };
+
+    // ---- the stream --------------------------------------------------------------
+    for (int s = 0; s < stages - 1; ++s) issue(s);
+    int stage = 0;
+    if (x0 < x1) open_compute(find_seq(s_pref, a.n_seq, x0), x0);
+    for (int32_t x = x0; x < x1; ++x) {
+        tc::cp_wait_group_n(stages - 2);
+        __syncwarp();
+        issue(stage == 0 ? stages - 1 : stage - 1);
+        step(stage);
+        ckey += kKeys;
+        if (--cleft == 0 || x + 1 == x1) {
+            close(x + 1);
+            if (x + 1 < x1) {
+                int32_t seq = cs.seq;
+                while (s_pref[seq + 1] <= x + 1) ++seq;
+                open_compute(seq, x + 1);
+            }
+        }
+        stage = stage + 1 == stages ? 0 : stage + 1;
+    }
+    tc::cp_wait_all();
+
+    // ---- joining -------------------------------------------------------------------
+    __syncthreads();
+    float *block_parts = parts + 2 * int64_t(gridDim.x) * NW * kPartial<HD, ROWS>;
+    const int64_t block_share = share * NW, b0 = min(int64_t(total), blockIdx.x * block_share);
+    const int64_t b1 = min(int64_t(total), b0 + block_share);
+    for (int i = warp; i <= NW; i += NW) {
+        // the segment that share boundary i of this block cuts, if no earlier boundary cuts it too
+        const int64_t x = min(int64_t(total), b0 + i * share);
+        if (x <= 0 || x >= total) continue;
+        const Segment s = segment_at<ROWS>(a, s_pref, find_seq(s_pref, a.n_seq, static_cast<int32_t>(x)),
+                                           static_cast<int32_t>(x));
+        const int64_t end = int64_t(s.begin) + s.steps;
+        if (s.begin >= x || (i > 0 && s.begin < x - share)) continue;
+        const int64_t lo = max(int64_t(s.begin), b0), hi = min(end, b1);
+        const int32_t w0 = static_cast<int32_t>(lo / share), w1 = static_cast<int32_t>((hi - 1) / share);
+        const int32_t c0 = static_cast<int32_t>(s.begin / block_share);
+        const int32_t c1 = static_cast<int32_t>((end - 1) / block_share);
+        if (c0 == c1) {
+            join<HD, ROWS>(a, parts, w0, w1, share, s, kShift, nullptr, lane);
+            continue;
+        }
+        float *mine = block_parts + (2 * int64_t(blockIdx.x) + (s.begin >= b0 ? 1 : 0)) * kPartial<HD, ROWS>;
+        join<HD, ROWS>(a, parts, w0, w1, share, s, kShift, mine, lane);
+        __threadfence();
+        __syncwarp();
+        int32_t before = 0;
+        if (lane == 0) before = atomicAdd(counters + c0, 1);
+        before = __shfl_sync(0xffffffffu, before, 0);
+        if (before == c1 - c0) {  // the last block of this segment: all others have written theirs
+            __threadfence();
+            if (lane == 0) counters[c0] = 0;
+            join<HD, ROWS>(a, block_parts, c0, c1, block_share, s, kShift, nullptr, lane);
+        }
+    }
+}
+
+template <int HD, bool E4M3, int ROWS>
+cudaError_t launch(const AttendArgs &a, void *ws, cudaStream_t stream) {
+    using C = Shape32<HD, E4M3>;
+    constexpr int kQ = ROWS == 32 ? C::kWarps * (HD / 16) * 2 * 512 : 0;
+    int device = 0, sms = 0;
+    cudaError_t e = cudaGetDevice(&device);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device);
+    if (e != cudaSuccess) return e;
+    const int grid = sms < kMaxGrid ? sms : kMaxGrid;
+    const int pref = ((a.n_seq + 1) * 4 + 127) & ~127;
+    int stages = (kSmemMax - 1024 - pref - kQ) / (C::kWarps * C::kStageB);
+    stages = stages > 8 ? 8 : stages;
+    const int smem = pref + kQ + stages * C::kWarps * C::kStageB;
+    const auto kernel = attend_decode_kernel<HD, E4M3, ROWS>;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    int32_t *counters = static_cast<int32_t *>(ws);
+    float *parts = reinterpret_cast<float *>(static_cast<char *>(ws) + 1024);
+    kernel<<<grid, C::kWarps * 32, smem, stream>>>(a, parts, counters, stages, pref);
+    return cudaGetLastError();
+}
+
+template <int HD, bool E4M3>
+cudaError_t pick(const AttendArgs &a, int64_t rows, void *ws, cudaStream_t stream) {
+    if (rows <= 8) return launch<HD, E4M3, 8>(a, ws, stream);
+    if (rows <= 16) return launch<HD, E4M3, 16>(a, ws, stream);
+    return launch<HD, E4M3, 32>(a, ws, stream);
+}
+
+}  // namespace
+
+// Counters (one a block), then two partials a warp and two a block, of up to 32 rows.
+size_t decode_workspace_bytes(int32_t head_dim, bool e4m3) {
+    const int warps = 2 * kKeys * head_dim * (e4m3 ? 1 : 2) >= 16384 ? 4 : 8;
+    return 1024 + size_t(kMaxGrid) * (warps + 1) * 2 * 32 * (head_dim + 2) * sizeof(float);
+}
+
+cudaError_t launch_attend_decode(const AttendArgs &a, bool e4m3, int32_t max_q, void *ws, cudaStream_t stream) {
+    const int64_t rows = int64_t(max_q) * a.group;
+    if (a.kv.head_dim == 64) return e4m3 ? pick<64, true>(a, rows, ws, stream) : pick<64, false>(a, rows, ws, stream);
+    return e4m3 ? pick<128, true>(a, rows, ws, stream) : pick<128, false>(a, rows, ws, stream);
+}
+
+}  // namespace lora

@@ -41,7 +41,8 @@ struct RequestRows {
 
 __device__ __forceinline__ RequestRows load_rows(const AttendArgs &a, int32_t i) {
     const int32_t q0 = a.q_offsets[i], q1 = a.q_offsets[i + 1], len = a.kv_lens[i];
-    const bool ok = q0 >= 0 && q1 >= q0 && q1 <= a.T && len >= 0 && len <= (int64_t(a.width) << a.kv.page_shift);
+    const bool ok = q0 >= 0 && q1 >= q0 && q1 <= a.T && len >= 0 && len <= LORA_MAX_KV_LEN &&
+                    len <= (int64_t(a.width) << a.kv.page_shift);
     return {q0, ok ? q1 - q0 : 0, ok ? len : 0, ok};
 }
 

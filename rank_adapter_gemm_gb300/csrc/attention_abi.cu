@@ -13,6 +13,8 @@ cudaError_t launch_kv_step(const int32_t *ctx_lens, const int32_t *new_lens, int
 cudaError_t launch_rope_append(const uint16_t *qkv, int64_t ldqkv, int32_t T, int32_t n_heads, const lora_rope_t &rope,
                                const int32_t *positions, const int64_t *slots, uint16_t *q_out, int64_t ldq,
                                const KvView &kv, bool e4m3, int32_t *err, cudaStream_t stream);
+size_t decode_workspace_bytes(int32_t head_dim, bool e4m3);
+cudaError_t launch_attend_decode(const AttendArgs &a, bool e4m3, int32_t max_q, void *ws, cudaStream_t stream);
 cudaError_t launch_attend_rows(const AttendArgs &a, bool e4m3, cudaStream_t stream);
 }  // namespace lora
 
@@ -129,7 +131,7 @@ lora_status_t lora_attend_workspace_bytes(const lora_attention_t *att, const lor
     if (bytes == nullptr) return LORA_ERR_INVALID_ARG;
     if ((st = check_kv(kv, &view)) != LORA_OK) return st;
     if ((st = check_attention(att, view)) != LORA_OK) return st;
-    *bytes = 256;
+    *bytes = lora::decode_workspace_bytes(view.head_dim, kv->type == LORA_KV_E4M3);
     return LORA_OK;
 }
 
@@ -165,7 +167,11 @@ lora_status_t lora_attend(const void *q, int64_t ldq, void *out, int64_t ldo, fl
     const lora::AttendArgs a{static_cast<const uint16_t *>(q), static_cast<uint16_t *>(out), lse, ldq, ldo, ld_table,
                              q_offsets, kv_lens, block_table, att->slopes, err, view, T, n_seq, table_width,
                              att->n_heads, att->n_heads / view.n_kv, att->window, att->scale, att->softcap};
-    return from_cuda(lora::launch_attend_rows(a, kv->type == LORA_KV_E4M3, reinterpret_cast<cudaStream_t>(stream)));
+    const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const bool e4m3 = kv->type == LORA_KV_E4M3;
+    if (lora_attend_resolve_path(path, att, kv, max_q_hint) == LORA_ATTEND_DECODE)
+        return from_cuda(lora::launch_attend_decode(a, e4m3, max_q_hint, ws, s));
+    return from_cuda(lora::launch_attend_rows(a, e4m3, s));
 }
 
 }  // extern "C"
