@@ -38,18 +38,30 @@ namespace lora {
 namespace {
 
 constexpr int kMaxGrid = 160;
-constexpr int kKeys = 32;                 // keys a step
 constexpr int kSmemMax = 227 * 1024;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
-template <int HD, bool E4M3>
-struct Shape32 {
-    static constexpr int kRowB = HD * (E4M3 ? 1 : 2);     // bytes of a key
-    static constexpr int kChunks = kRowB / 16;            // 16-byte pieces of a key
-    static constexpr int kTileB = kKeys * kRowB;
-    static constexpr int kStageB = 2 * kTileB;            // k and v of a step
-    static constexpr int kWarps = kStageB >= 16384 ? 4 : 8;
+constexpr int kWarps = 8;
+constexpr int kPrefixMax = ((LORA_MAX_SEQS + 1) * 4 + 127) & ~127;  // the requests' step prefix
+
+template <int HD, bool E4M3, int ROWS>
+struct Config {
+    static constexpr int kRowB = HD * (E4M3 ? 1 : 2);  // bytes of a key
+    static constexpr int kChunks = kRowB / 16;         // 16-byte pieces of a key
+    // Keys a step: 8 KB of k where the scores' registers allow, so that the work
+    // around the products (maxima, waits, addresses) is spread over more keys.
+    static constexpr int kKeys = ROWS == 32 || kRowB == 256 ? 32 : 64;
+    static constexpr int kTileB = kKeys * kRowB;       // k, or v, of a step
+    // A partial: maxima and sums of ROWS rows, then their outputs, fp32.
+    static constexpr int kPartial = ROWS * (HD + 2);
+    // A warp's query fragments in shared memory: with 32 rows there are no registers for them.
+    static constexpr int kQBytes = ROWS == 32 ? (HD / 16) * 2 * 512 : 0;
+    // Tiles of a warp's ring: all the memory that the longest prefix leaves.
+    static constexpr int kRoom = (kSmemMax - 1024 - kPrefixMax) / kWarps - kQBytes;
+    static constexpr int kTiles = kRoom / kTileB < 9 ? kRoom / kTileB : 9;
+    static constexpr int kWarpB = kQBytes + kTiles * kTileB;
+    static_assert(kTiles >= 2 && kPartial * 4 <= kWarpB, "ring");
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -104,11 +116,11 @@ __device__ __forceinline__ uint32_t piece_at(int row, int piece) {
     return row * (CHUNKS * 16) + ((piece ^ (row & 7)) << 4);
 }
 
-// A segment: its request, key head and row tile, and its keys.
+// A segment: its request, key head and row tile, and its keys (in steps of KEYS).
 struct Segment {
     int32_t seq, head, tile;  // tile: first of its rows, rows numbered token * group + head in group
     int32_t q0, n, len;       // the request's rows and length
-    int32_t lo, base, steps;  // first key that a row sees, the multiple of 32 at or before it, steps from there
+    int32_t lo, base, steps;  // first key that a row sees, the multiple of KEYS at or before it, steps from there
     int32_t begin;            // index of its first step among all of the call
 };
 
@@ -118,8 +130,9 @@ __device__ __forceinline__ int32_t first_key(const AttendArgs &a, const RequestR
     return static_cast<int32_t>(max(int64_t(0), int64_t(r.len) - r.n - a.window + 1));
 }
 
+template <int KEYS>
 __device__ __forceinline__ int32_t steps_of(const AttendArgs &a, const RequestRows &r) {
-    return r.n > 0 ? (r.len - (first_key(a, r) & ~(kKeys - 1)) + kKeys - 1) / kKeys : 0;
+    return r.n > 0 ? (r.len - (first_key(a, r) & ~(KEYS - 1)) + KEYS - 1) / KEYS : 0;
 }
 
 template <int ROWS>
@@ -128,7 +141,7 @@ __device__ __forceinline__ int32_t tiles_of(const AttendArgs &a, int32_t n) {
 }
 
 // The segment of request `seq` that step x of the call belongs to.
-template <int ROWS>
+template <int ROWS, int KEYS>
 __device__ __forceinline__ Segment segment_at(const AttendArgs &a, const int32_t *s_pref, int32_t seq, int32_t x) {
     const RequestRows r = load_rows(a, seq);
     Segment s;
@@ -137,8 +150,8 @@ __device__ __forceinline__ Segment segment_at(const AttendArgs &a, const int32_t
     s.n = r.n;
     s.len = r.len;
     s.lo = first_key(a, r);
-    s.base = s.lo & ~(kKeys - 1);
-    s.steps = max(1, steps_of(a, r));
+    s.base = s.lo & ~(KEYS - 1);
+    s.steps = max(1, steps_of<KEYS>(a, r));
     const int32_t tiles = max(1, tiles_of<ROWS>(a, r.n)), i = (x - s_pref[seq]) / s.steps;
     s.head = i / tiles;  // tiles of one head are neighbours: they read the same keys
     s.tile = (i - s.head * tiles) * ROWS;
@@ -157,67 +170,68 @@ __device__ __forceinline__ int32_t find_seq(const int32_t *s_pref, int32_t n, in
     return lo;
 }
 
-// A partial: maxima and sums of ROWS rows, then their outputs, fp32.
-template <int HD, int ROWS>
-constexpr int kPartial = ROWS * (HD + 2);
-
-// Joins partials first..last (slot 2 i, or 2 i + 1 where the segment begins in
-// share i) in order and writes the result: rows of `out`, or one partial.
-template <int HD, int ROWS>
-__device__ void join(const AttendArgs &a, const float *parts, int32_t first, int32_t last, int64_t share,
-                     const Segment &s, float shift, float *to, int lane) {
+// One row joined over partials first..last, in order: part(i) is partial i's
+// address, shared (a few, read one after the other) or global (many, a lane
+// each for the statistics).  Writes the row of `out`, or of the partial `to`.
+template <int HD, int ROWS, class P>
+__device__ __forceinline__ void join_row(const AttendArgs &a, P part, int32_t first, int32_t last, const Segment &s,
+                                         int r, float shift, float *to, int lane) {
     constexpr int V = HD / 32;
-    const int32_t rows = min(ROWS, s.n * a.group - s.tile);
-    const int64_t begin = s.begin;
-    for (int r = 0; r < rows; ++r) {
-        float top = -INFINITY;
-        for (int32_t i = first; i <= last; ++i) {
-            const float *p = parts + (2 * i + (begin >= i * share ? 1 : 0)) * int64_t(kPartial<HD, ROWS>);
-            top = fmaxf(top, __ldcg(p + r));
-        }
-        const float ref = top == -INFINITY ? 0.0f : top;
-        float sum = 0.0f, o[V] = {};
-#pragma unroll 4
-        for (int32_t i = first; i <= last; ++i) {
-            const float *p = parts + (2 * i + (begin >= i * share ? 1 : 0)) * int64_t(kPartial<HD, ROWS>);
-            const float w = ex2(__ldcg(p + r) - ref);
-            sum += w * __ldcg(p + ROWS + r);
-            const float *v = p + 2 * ROWS + r * HD + lane * V;
+    float top = -INFINITY, sum = 0.0f, o[V] = {};
+    for (int32_t c = first; c <= last; c += 32) {
+        const int32_t n = min(32, last - c + 1);
+        const float *mine = part(c + min(lane, n - 1));
+        const float m = lane < n ? mine[r] : -INFINITY, l = lane < n ? mine[ROWS + r] : 0.0f;
+        float now = m;
+#pragma unroll
+        for (int x = 16; x > 0; x >>= 1) now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, x));
+        now = fmaxf(now, top);
+        const float ref = now == -INFINITY ? 0.0f : now, w = ex2(m - ref), f = ex2(top - ref);
+        sum *= f;
+#pragma unroll
+        for (int e = 0; e < V; ++e) o[e] *= f;
+#pragma unroll 8
+        for (int32_t j = 0; j < n; ++j) {
+            const float wj = __shfl_sync(0xffffffffu, w, j);
+            sum += wj * __shfl_sync(0xffffffffu, l, j);
+            const float *v = part(c + j) + 2 * ROWS + r * HD + lane * V;
             if constexpr (V == 4) {
-                const float4 x = __ldcg(reinterpret_cast<const float4 *>(v));
-                o[0] += w * x.x, o[1] += w * x.y, o[2] += w * x.z, o[3] += w * x.w;
+                const float4 x = *reinterpret_cast<const float4 *>(v);
+                o[0] += wj * x.x, o[1] += wj * x.y, o[2] += wj * x.z, o[3] += wj * x.w;
             } else {
-                const float2 x = __ldcg(reinterpret_cast<const float2 *>(v));
-                o[0] += w * x.x, o[1] += w * x.y;
+                const float2 x = *reinterpret_cast<const float2 *>(v);
+                o[0] += wj * x.x, o[1] += wj * x.y;
             }
         }
-        if (to != nullptr) {
-            if (lane == 0) {
-                to[r] = top;
-                to[ROWS + r] = sum;
-            }
-#pragma unroll
-            for (int e = 0; e < V; ++e) to[2 * ROWS + r * HD + lane * V + e] = o[e];
-        } else {
-            const int32_t row = s.tile + r, t = s.q0 + row / a.group, h = s.head * a.group + row % a.group;
-            const float inv = sum > 0.0f ? a.kv.v_scale / sum : sum == 0.0f ? 0.0f : sum;
-            uint32_t w[V / 2];
-#pragma unroll
-            for (int e = 0; e < V / 2; ++e) w[e] = pack_bf16x2(o[2 * e] * inv, o[2 * e + 1] * inv);
-            uint16_t *dst = a.out + t * a.ldo + h * HD + lane * V;
-            if constexpr (V == 4) *reinterpret_cast<uint2 *>(dst) = make_uint2(w[0], w[1]);
-            else *reinterpret_cast<uint32_t *>(dst) = w[0];
-            if (a.lse != nullptr && lane == 0)
-                a.lse[int64_t(t) * a.n_heads + h] = sum == 0.0f ? -INFINITY : kLn2 * (ref - shift) + logf(sum);
-        }
+        top = now;
     }
+    if (to != nullptr) {
+        if (lane == 0) {
+            to[r] = top;
+            to[ROWS + r] = sum;
+        }
+#pragma unroll
+        for (int e = 0; e < V; ++e) to[2 * ROWS + r * HD + lane * V + e] = o[e];
+        return;
+    }
+    const int32_t row = s.tile + r, t = s.q0 + row / a.group, h = s.head * a.group + row % a.group;
+    const float inv = sum > 0.0f ? a.kv.v_scale / sum : sum == 0.0f ? 0.0f : sum;
+    uint32_t w[V / 2];
+#pragma unroll
+    for (int e = 0; e < V / 2; ++e) w[e] = pack_bf16x2(o[2 * e] * inv, o[2 * e + 1] * inv);
+    uint16_t *dst = a.out + t * a.ldo + h * HD + lane * V;
+    if constexpr (V == 4) *reinterpret_cast<uint2 *>(dst) = make_uint2(w[0], w[1]);
+    else *reinterpret_cast<uint32_t *>(dst) = w[0];
+    if (a.lse != nullptr && lane == 0)
+        a.lse[int64_t(t) * a.n_heads + h] = sum == 0.0f ? -INFINITY : kLn2 * (top - shift) + logf(sum);
 }
 
 template <int HD, bool E4M3, int ROWS>
-__global__ void __launch_bounds__(Shape32<HD, E4M3>::kWarps * 32, 1)
-attend_decode_kernel(const AttendArgs a, float *parts, int32_t *counters, int stages, int pref_bytes) {
-    using C = Shape32<HD, E4M3>;
-    constexpr int NW = C::kWarps, NT = NW * 32, MB = ROWS == 32 ? 2 : 1, KK = HD / 16, DT = HD / 8;
+__global__ void __launch_bounds__(kWarps * 32, 1)
+attend_decode_kernel(const AttendArgs a, float *parts, int32_t *counters, int pref_bytes) {
+    using C = Config<HD, E4M3, ROWS>;
+    constexpr int kKeys = C::kKeys, NK = kKeys / 32, ST = kKeys / 8, KB = kKeys / 16, kTiles = C::kTiles;
+    constexpr int NW = kWarps, NT = NW * 32, MB = ROWS == 32 ? 2 : 1, KK = HD / 16, DT = HD / 8;
     constexpr bool kHalf = ROWS == 8;      // only rows 0..7 of the MMA's 16 hold queries
     constexpr bool kQShared = ROWS == 32;  // query fragments in shared memory, else in registers
     constexpr float kShift = E4M3 ? 12.0f : 0.0f;
@@ -234,7 +248,7 @@ attend_decode_kernel(const AttendArgs a, float *parts, int32_t *counters, int st
         for (int32_t i = i0; i < i1; ++i) {
             const RequestRows r = load_rows(a, i);
             if (!r.ok && blockIdx.x == 0) report_error(a.err, LORA_ERR_INVALID_ARG);
-            mine += int64_t(steps_of(a, r)) * a.kv.n_kv * tiles_of<ROWS>(a, r.n);
+            mine += int64_t(steps_of<kKeys>(a, r)) * a.kv.n_kv * tiles_of<ROWS>(a, r.n);
         }
         int64_t incl = mine;
 #pragma unroll
@@ -257,7 +271,7 @@ attend_decode_kernel(const AttendArgs a, float *parts, int32_t *counters, int st
         for (int32_t i = i0; i < i1; ++i) {
             const RequestRows r = load_rows(a, i);
             s_pref[i] = static_cast<int32_t>(run);
-            run += int64_t(steps_of(a, r)) * a.kv.n_kv * tiles_of<ROWS>(a, r.n);
+            run += int64_t(steps_of<kKeys>(a, r)) * a.kv.n_kv * tiles_of<ROWS>(a, r.n);
         }
         total = static_cast<int32_t>(sum);
         if (tid == 0) s_pref[a.n_seq] = total;
@@ -281,21 +295,27 @@ attend_decode_kernel(const AttendArgs a, float *parts, int32_t *counters, int st
     const int32_t x0 = static_cast<int32_t>(min(int64_t(total), me * share));
     const int32_t x1 = static_cast<int32_t>(min(int64_t(total), x0 + share));
 
-    const uint32_t ring = tc::smem_u32(smem) + pref_bytes + (kQShared ? NW * KK * MB * 512 : 0) +
-                          warp * stages * C::kStageB;
-    uint4 *s_q = reinterpret_cast<uint4 *>(smem + pref_bytes) + warp * KK * MB * 32;
+    // this warp's memory: its query fragments and its ring of k and v tiles; the last
+    // partial of its share takes their place in the end
+    unsigned char *const warp_ptr = smem + pref_bytes + warp * C::kWarpB;
+    const uint32_t ring = tc::smem_u32(warp_ptr) + C::kQBytes;
+    uint4 *s_q = reinterpret_cast<uint4 *>(warp_ptr);
 
     // ---- the copying side: where its next step is ------------------------------
     Segment ls{};
-    int32_t lx = x0, lkey = 0, lleft = 0, lpage = -1;
+    int32_t lx = x0, lkey = 0, lleft = 0, lpage[NK];
     const int32_t *ltab = nullptr;
-    // whether this lane's key of the next step is one that a row sees, and its page
-    const auto has_key = [&]() { return lkey + lane >= ls.lo && lkey + lane < ls.len; };
+    // whether this lane's key 32 i + lane of the next step is one that a row sees, and its page
+    const auto has_key = [&](int i) { return lkey + 32 * i + lane >= ls.lo && lkey + 32 * i + lane < ls.len; };
     const auto look_up = [&]() {
-        if (lx < x1 && has_key()) lpage = __ldg(ltab + ((lkey + lane) >> a.kv.page_shift));
+        if (lx < x1) {
+#pragma unroll
+            for (int i = 0; i < NK; ++i)
+                lpage[i] = has_key(i) ? __ldg(ltab + ((lkey + 32 * i + lane) >> a.kv.page_shift)) : -1;
+        }
     };
     const auto open_load = [&](int32_t seq) {
-        ls = segment_at<ROWS>(a, s_pref, seq, lx);
+        ls = segment_at<ROWS, kKeys>(a, s_pref, seq, lx);
         lkey = ls.base + (lx - ls.begin) * kKeys;
         lleft = ls.steps - (lx - ls.begin);
         ltab = a.table + ls.seq * a.ld_table;
@@ -304,32 +324,59 @@ attend_decode_kernel(const AttendArgs a, float *parts, int32_t *counters, int st
         open_load(find_seq(s_pref, a.n_seq, x0));
         look_up();
     }
-    const auto issue = [&](int stage) {
+    // copies the next tile, k and v of a step in turn
+    constexpr int kRows = 32 / C::kChunks;  // keys a copy instruction
+    const int piece = lane % C::kChunks, row0 = lane / C::kChunks;
+    const int64_t lane_off = row0 * a.kv.token_b + piece * 16, row_stride = kRows * a.kv.token_b;
+    bool lv = false, smooth = false;
+    int64_t at[NK];  // byte offsets of this lane's keys, -1: none
+    const auto issue = [&](int slot) {
         if (lx < x1) {
-            const int32_t key = lkey + lane;
-            const bool has = has_key(), ok = has && lpage >= 0 && lpage < a.kv.n_pages;
-            if (has && !ok) report_error(a.err, LORA_ERR_SLOT_RANGE);
-            const int64_t at = ok ? lpage * a.kv.page_b + (key & a.kv.page_mask) * a.kv.token_b + ls.head * a.kv.head_b
-                                  : -1;
-            const uint32_t dst = ring + stage * C::kStageB;
-            const int piece = lane % C::kChunks;
+            if (!lv) {
+                bool all = a.kv.page_shift >= 4;
 #pragma unroll
-            for (int i = 0; i < C::kChunks; ++i) {
-                const int row = i * (32 / C::kChunks) + lane / C::kChunks;
-                const int64_t o = __shfl_sync(0xffffffffu, at, row);
-                const int64_t src = (o >= 0 ? o : 0) + piece * 16;
-                const uint32_t d = dst + piece_at<C::kChunks>(row, piece);
-                tc::cp16(d, a.kv.k + src, o >= 0);
-                tc::cp16(d + C::kTileB, a.kv.v + src, o >= 0);
+                for (int i = 0; i < NK; ++i) {
+                    const bool ok = lpage[i] >= 0 && lpage[i] < a.kv.n_pages;
+                    if (!ok && has_key(i)) report_error(a.err, LORA_ERR_SLOT_RANGE);
+                    at[i] = ok ? lpage[i] * a.kv.page_b + ((lkey + 32 * i + lane) & a.kv.page_mask) * a.kv.token_b +
+                                     ls.head * a.kv.head_b
+                               : -1;
+                    all = all && ok;
+                }
+                smooth = __all_sync(0xffffffffu, all);
             }
-            ++lx;
-            lkey += kKeys;
-            if (--lleft == 0 && lx < x1) {
-                int32_t seq = ls.seq;
-                while (s_pref[seq + 1] <= lx) ++seq;
-                open_load(seq);
+            const unsigned char *from = lv ? a.kv.v : a.kv.k;
+            const uint32_t dst = ring + slot * C::kTileB;
+            if (smooth) {
+                // 16 neighbouring keys share a page: one address for them
+#pragma unroll
+                for (int half = 0; half < 2 * NK; ++half) {
+                    const unsigned char *src = from + __shfl_sync(0xffffffffu, at[half / 2], 16 * (half & 1)) + lane_off;
+#pragma unroll
+                    for (int i = 0; i < C::kChunks / 2; ++i) {
+                        tc::cp16(dst + piece_at<C::kChunks>(16 * half + i * kRows + row0, piece), src, true);
+                        src += row_stride;
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < NK * C::kChunks; ++i) {
+                    const int row = i * kRows + row0;
+                    const int64_t o = __shfl_sync(0xffffffffu, at[i / C::kChunks], row & 31);
+                    tc::cp16(dst + piece_at<C::kChunks>(row, piece), from + (o >= 0 ? o : 0) + piece * 16, o >= 0);
+                }
             }
-            look_up();
+            if (lv) {
+                ++lx;
+                lkey += kKeys;
+                if (--lleft == 0 && lx < x1) {
+                    int32_t seq = ls.seq;
+                    while (s_pref[seq + 1] <= lx) ++seq;
+                    open_load(seq);
+                }
+                look_up();
+            }
+            lv = !lv;
         }
         tc::cp_commit();
     };
@@ -342,7 +389,7 @@ attend_decode_kernel(const AttendArgs a, float *parts, int32_t *counters, int st
     float m[MB][2], l[MB][2], mult[MB][2], slope[MB][2], acc[MB][DT][4];
 
     const auto open_compute = [&](int32_t seq, int32_t x) {
-        cs = segment_at<ROWS>(a, s_pref, seq, x);
+        cs = segment_at<ROWS, kKeys>(a, s_pref, seq, x);
         cleft = cs.steps - (x - cs.begin);
         ckey = cs.base + (x - cs.begin) * kKeys;
         const int32_t rows = min(ROWS, cs.n * a.group - cs.tile);
@@ -414,58 +461,67 @@ attend_decode_kernel(const AttendArgs a, float *parts, int32_t *counters, int st
                 for (int e = 0; e < 4; ++e) acc[mb][d][e] = 0.0f;
     };
 
-    const auto step = [&](int stage) {
-        const uint32_t kt = ring + stage * C::kStageB, vt = kt + C::kTileB;
-        const int mat = lane >> 3, r8 = lane & 7;
-        float s[MB][4][4] = {};
-        // scores: 4 tiles of 8 keys
+    uint32_t hi[MB][KB][4], lo[MB][KB][4];
+    const int mat = lane >> 3, r8 = lane & 7;
+    const bool plain = a.softcap == 0.0f && a.slopes == nullptr && a.scale > 0.0f;
+    // weights p = 2^(score log2 e - maximum) of the step's keys, as the fragments of the second product
+    const auto scores = [&](int slot) {
+        const uint32_t kt = ring + slot * C::kTileB;
+        float s[MB][ST][4] = {};
 #pragma unroll
         for (int kk = 0; kk < KK; kk += E4M3 ? 4 : 2) {
-            uint32_t b[4][4];
 #pragma unroll
-            for (int t = 0; t < 4; ++t)
-                ldsm4(b[t], kt + piece_at<C::kChunks>(8 * t + r8, (E4M3 ? kk : 2 * kk) + mat));
+            for (int t0 = 0; t0 < ST; t0 += 4) {
+                uint32_t b[4][4];
 #pragma unroll
-            for (int u = 0; u < (E4M3 ? 4 : 2); ++u) {
+                for (int t = 0; t < 4; ++t)
+                    ldsm4(b[t], kt + piece_at<C::kChunks>(8 * (t0 + t) + r8, (E4M3 ? kk : 2 * kk) + mat));
 #pragma unroll
-                for (int mb = 0; mb < MB; ++mb) {
-                    uint4 q;
-                    if constexpr (kQShared) q = s_q[((kk + u) * MB + mb) * 32 + lane];
-                    else q = make_uint4(qf[kk + u][0], qf[kk + u][1], qf[kk + u][2], qf[kk + u][3]);
+                for (int u = 0; u < (E4M3 ? 4 : 2); ++u) {
 #pragma unroll
-                    for (int t = 0; t < 4; ++t) {
-                        if constexpr (E4M3)
-                            mma_f16_16816(s[mb][t], q.x, q.y, q.z, q.w, e4m3x2_f16x2(b[t][u]),
-                                          e4m3x2_f16x2(b[t][u] >> 16));
-                        else
-                            mma_bf16_16816(s[mb][t], q.x, q.y, q.z, q.w, b[t][2 * u], b[t][2 * u + 1]);
+                    for (int mb = 0; mb < MB; ++mb) {
+                        uint4 q;
+                        if constexpr (kQShared) q = s_q[((kk + u) * MB + mb) * 32 + lane];
+                        else q = make_uint4(qf[kk + u][0], qf[kk + u][1], qf[kk + u][2], qf[kk + u][3]);
+#pragma unroll
+                        for (int t = 0; t < 4; ++t) {
+                            if constexpr (E4M3)
+                                mma_f16_16816(s[mb][t0 + t], q.x, q.y, q.z, q.w, e4m3x2_f16x2(b[t][u]),
+                                              e4m3x2_f16x2(b[t][u] >> 16));
+                            else
+                                mma_bf16_16816(s[mb][t0 + t], q.x, q.y, q.z, q.w, b[t][2 * u], b[t][2 * u + 1]);
+                        }
                     }
                 }
             }
         }
-        // weights: p = 2^(score log2 e - maximum), and the fragments of the second product
         const bool masked = ckey + kKeys - 1 > pos_lo || (a.window > 0 && pos_hi - ckey >= a.window);
-        uint32_t hi[MB][2][4], lo[MB][2][4];
+        const bool fast = plain && !masked;
 #pragma unroll
         for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
             for (int i = 0; i < (kHalf ? 1 : 2); ++i) {
-                float top = -INFINITY;
-                const float by = a.softcap > 0.0f ? mult[mb][i] / a.softcap : mult[mb][i] * kLog2e;
-                const float cap = a.softcap * kLog2e;
+                float top = -INFINITY, by = mult[mb][i] * kLog2e;
+                if (fast) {
 #pragma unroll
-                for (int t = 0; t < 4; ++t)
+                    for (int t = 0; t < ST; ++t) top = fmaxf(top, fmaxf(s[mb][t][2 * i], s[mb][t][2 * i + 1]));
+                    top *= by;
+                } else {
+                    const float in = a.softcap > 0.0f ? mult[mb][i] / a.softcap : by, cap = a.softcap * kLog2e;
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        float &x = s[mb][t][2 * i + e];
-                        x *= by;
-                        if (a.softcap > 0.0f) x = cap * tanh_of(x);
-                        const int32_t key = ckey + 8 * t + 2 * c4 + e;
-                        if (a.slopes != nullptr) x += slope[mb][i] * static_cast<float>(key - pos[mb][i]);
-                        if (masked && (key > pos[mb][i] || (a.window > 0 && pos[mb][i] - key >= a.window)))
-                            x = -INFINITY;
-                        top = fmaxf(top, x);
-                    }
+                    for (int t = 0; t < ST; ++t)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            float &x = s[mb][t][2 * i + e];
+                            x *= in;
+                            if (a.softcap > 0.0f) x = cap * tanh_of(x);
+                            const int32_t key = ckey + 8 * t + 2 * c4 + e;
+                            x += slope[mb][i] * static_cast<float>(key - pos[mb][i]);
+                            if (key > pos[mb][i] || (a.window > 0 && pos[mb][i] - key >= a.window)) x = -INFINITY;
+                            top = fmaxf(top, x);
+                        }
+                    by = 1.0f;
+                }
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
                 const float now = fmaxf(m[mb][i], top);
@@ -486,8 +542,8 @@ attend_decode_kernel(const AttendArgs a, float *parts, int32_t *counters, int st
                 }
                 float sum = 0.0f;
 #pragma unroll
-                for (int t = 0; t < 4; ++t) {
-                    const float p0 = ex2(s[mb][t][2 * i] - ref), p1 = ex2(s[mb][t][2 * i + 1] - ref);
+                for (int t = 0; t < ST; ++t) {
+                    const float p0 = ex2(fmaf(s[mb][t][2 * i], by, -ref)), p1 = ex2(fmaf(s[mb][t][2 * i + 1], by, -ref));
                     sum += p0 + p1;
                     // keys 8 t + 2 c4, + 1: the A fragment's word of 16-key block t / 2
                     const int w = (t & 1) * 2 + i;
@@ -504,9 +560,12 @@ attend_decode_kernel(const AttendArgs a, float *parts, int32_t *counters, int st
                 }
                 l[mb][i] += sum;
             }
-        // output: 2 blocks of 16 keys, all dims
+    };
+    // output: 16 keys at a time, all dims
+    const auto outputs = [&](int slot) {
+        const uint32_t vt = ring + slot * C::kTileB;
 #pragma unroll
-        for (int kb = 0; kb < 2; ++kb)
+        for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
             for (int c = 0; c < C::kChunks; c += 2) {
                 uint32_t b[4];
@@ -540,11 +599,12 @@ attend_decode_kernel(const AttendArgs a, float *parts, int32_t *counters, int st
             }
     };
 
-    // ends a segment, or this warp's part of it: rows to `out`, or a partial
+    // ends a segment, or this warp's part of it: rows to `out`, or a partial (the
+    // share's last one into the warp's own memory, which holds no more tiles then)
     const auto close = [&](int32_t x_end) {
         const int32_t rows = min(ROWS, cs.n * a.group - cs.tile);
         const bool whole = cs.begin >= x0 && cs.begin + cs.steps <= x_end;
-        float *part = parts + (2 * int64_t(me) + (cs.begin >= x0 ? 1 : 0)) * kPartial<HD, ROWS>;
+        float *part = x_end == x1 ? reinterpret_cast<float *>(warp_ptr) : parts + int64_t(me) * C::kPartial;
 #pragma unroll
         for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
@@ -593,16 +653,23 @@ attend_decode_kernel(const AttendArgs a, float *parts, int32_t *counters, int st
     };
 
     // ---- the stream --------------------------------------------------------------
-    for (int s = 0; s < stages - 1; ++s) issue(s);
-    int stage = 0;
+    for (int u = 0; u < kTiles - 1; ++u) issue(u);
+    int slot = 0;
+    const auto next = [&]() {
+        tc::cp_wait_group<kTiles - 2>();
+        __syncwarp();
+        issue(slot == 0 ? kTiles - 1 : slot - 1);
+        const int now = slot;
+        slot = slot + 1 == kTiles ? 0 : slot + 1;
+        return now;
+    };
     if (x0 < x1) open_compute(find_seq(s_pref, a.n_seq, x0), x0);
     for (int32_t x = x0; x < x1; ++x) {
-        tc::cp_wait_group_n(stages - 2);
-        __syncwarp();
-        issue(stage == 0 ? stages - 1 : stage - 1);
-        step(stage);
+        scores(next());
+        outputs(next());
         ckey += kKeys;
         if (--cleft == 0 || x + 1 == x1) {
+            __syncwarp();
             close(x + 1);
             if (x + 1 < x1) {
                 int32_t seq = cs.seq;
@@ -610,65 +677,78 @@ attend_decode_kernel(const AttendArgs a, float *parts, int32_t *counters, int st
                 open_compute(seq, x + 1);
             }
         }
-        stage = stage + 1 == stages ? 0 : stage + 1;
     }
     tc::cp_wait_all();
 
     // ---- joining -------------------------------------------------------------------
-    __syncthreads();
-    float *block_parts = parts + 2 * int64_t(gridDim.x) * NW * kPartial<HD, ROWS>;
+    __shared__ int32_t s_last;
+    float *block_parts = parts + int64_t(gridDim.x) * NW * C::kPartial;
     const int64_t block_share = share * NW, b0 = min(int64_t(total), blockIdx.x * block_share);
     const int64_t b1 = min(int64_t(total), b0 + block_share);
-    for (int i = warp; i <= NW; i += NW) {
-        // the segment that share boundary i of this block cuts, if no earlier boundary cuts it too
+    // the segments that the block's share boundaries cut, each at its first boundary
+    __shared__ bool s_cut[NW + 1];
+    const auto at_boundary = [&](int i, Segment &s) {
         const int64_t x = min(int64_t(total), b0 + i * share);
-        if (x <= 0 || x >= total) continue;
-        const Segment s = segment_at<ROWS>(a, s_pref, find_seq(s_pref, a.n_seq, static_cast<int32_t>(x)),
-                                           static_cast<int32_t>(x));
+        if (x <= 0 || x >= total) return false;
+        s = segment_at<ROWS, kKeys>(a, s_pref, find_seq(s_pref, a.n_seq, static_cast<int32_t>(x)),
+                                    static_cast<int32_t>(x));
+        return s.begin < x && (i == 0 || s.begin >= x - share);
+    };
+    if (tid <= NW) {
+        Segment s;
+        s_cut[tid] = at_boundary(tid, s);
+    }
+    __syncthreads();
+    for (int i = 0; i <= NW; ++i) {
+        Segment s;
+        if (!s_cut[i] || !at_boundary(i, s)) continue;
         const int64_t end = int64_t(s.begin) + s.steps;
-        if (s.begin >= x || (i > 0 && s.begin < x - share)) continue;
-        const int64_t lo = max(int64_t(s.begin), b0), hi = min(end, b1);
-        const int32_t w0 = static_cast<int32_t>(lo / share), w1 = static_cast<int32_t>((hi - 1) / share);
+        const int32_t rows = min(ROWS, s.n * a.group - s.tile);
+        const int32_t w0 = static_cast<int32_t>(max(int64_t(s.begin), b0) / share);
+        const int32_t w1 = static_cast<int32_t>((min(end, b1) - 1) / share);
         const int32_t c0 = static_cast<int32_t>(s.begin / block_share);
         const int32_t c1 = static_cast<int32_t>((end - 1) / block_share);
-        if (c0 == c1) {
-            join<HD, ROWS>(a, parts, w0, w1, share, s, kShift, nullptr, lane);
-            continue;
-        }
-        float *mine = block_parts + (2 * int64_t(blockIdx.x) + (s.begin >= b0 ? 1 : 0)) * kPartial<HD, ROWS>;
-        join<HD, ROWS>(a, parts, w0, w1, share, s, kShift, mine, lane);
+        // a warp's partial is in its ring, unless more segments followed in its share
+        const auto of_warp = [&](int32_t w) -> const float * {
+            if (end < min(int64_t(total), (w + 1) * share)) return parts + int64_t(w) * C::kPartial;
+            return reinterpret_cast<const float *>(smem + pref_bytes + (w - blockIdx.x * NW) * C::kWarpB);
+        };
+        // a block's: its first segment begins before it or is its last cut one
+        const auto of_block = [&](int32_t c) -> float * {
+            return block_parts + (2 * int64_t(c) + (s.begin >= c * block_share ? 1 : 0)) * C::kPartial;
+        };
+        float *to = c0 == c1 ? nullptr : of_block(blockIdx.x);
+        for (int r = warp; r < rows; r += NW) join_row<HD, ROWS>(a, of_warp, w0, w1, s, r, kShift, to, lane);
+        if (c0 == c1) continue;
         __threadfence();
-        __syncwarp();
-        int32_t before = 0;
-        if (lane == 0) before = atomicAdd(counters + c0, 1);
-        before = __shfl_sync(0xffffffffu, before, 0);
-        if (before == c1 - c0) {  // the last block of this segment: all others have written theirs
-            __threadfence();
-            if (lane == 0) counters[c0] = 0;
-            join<HD, ROWS>(a, block_parts, c0, c1, block_share, s, kShift, nullptr, lane);
+        __syncthreads();
+        if (tid == 0) {
+            s_last = atomicAdd(counters + c0, 1) == c1 - c0;
+            if (s_last) counters[c0] = 0;
         }
+        __syncthreads();
+        if (!s_last) continue;  // the last block of this segment: all others have written theirs
+        __threadfence();
+        for (int r = warp; r < rows; r += NW) join_row<HD, ROWS>(a, of_block, c0, c1, s, r, kShift, nullptr, lane);
     }
 }
 
 template <int HD, bool E4M3, int ROWS>
 cudaError_t launch(const AttendArgs &a, void *ws, cudaStream_t stream) {
-    using C = Shape32<HD, E4M3>;
-    constexpr int kQ = ROWS == 32 ? C::kWarps * (HD / 16) * 2 * 512 : 0;
+    using C = Config<HD, E4M3, ROWS>;
     int device = 0, sms = 0;
     cudaError_t e = cudaGetDevice(&device);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device);
     if (e != cudaSuccess) return e;
     const int grid = sms < kMaxGrid ? sms : kMaxGrid;
     const int pref = ((a.n_seq + 1) * 4 + 127) & ~127;
-    int stages = (kSmemMax - 1024 - pref - kQ) / (C::kWarps * C::kStageB);
-    stages = stages > 8 ? 8 : stages;
-    const int smem = pref + kQ + stages * C::kWarps * C::kStageB;
+    const int smem = pref + kWarps * C::kWarpB;
     const auto kernel = attend_decode_kernel<HD, E4M3, ROWS>;
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     int32_t *counters = static_cast<int32_t *>(ws);
     float *parts = reinterpret_cast<float *>(static_cast<char *>(ws) + 1024);
-    kernel<<<grid, C::kWarps * 32, smem, stream>>>(a, parts, counters, stages, pref);
+    kernel<<<grid, kWarps * 32, smem, stream>>>(a, parts, counters, pref);
     return cudaGetLastError();
 }
 
@@ -681,10 +761,9 @@ cudaError_t pick(const AttendArgs &a, int64_t rows, void *ws, cudaStream_t strea
 
 }  // namespace
 
-// Counters (one a block), then two partials a warp and two a block, of up to 32 rows.
-size_t decode_workspace_bytes(int32_t head_dim, bool e4m3) {
-    const int warps = 2 * kKeys * head_dim * (e4m3 ? 1 : 2) >= 16384 ? 4 : 8;
-    return 1024 + size_t(kMaxGrid) * (warps + 1) * 2 * 32 * (head_dim + 2) * sizeof(float);
+// Counters (one a block), then a partial a warp and two a block, of up to 32 rows.
+size_t decode_workspace_bytes(int32_t head_dim) {
+    return 1024 + size_t(kMaxGrid) * (kWarps + 2) * 32 * (head_dim + 2) * sizeof(float);
 }
 
 cudaError_t launch_attend_decode(const AttendArgs &a, bool e4m3, int32_t max_q, void *ws, cudaStream_t stream) {

@@ -13,7 +13,7 @@ cudaError_t launch_kv_step(const int32_t *ctx_lens, const int32_t *new_lens, int
 cudaError_t launch_rope_append(const uint16_t *qkv, int64_t ldqkv, int32_t T, int32_t n_heads, const lora_rope_t &rope,
                                const int32_t *positions, const int64_t *slots, uint16_t *q_out, int64_t ldq,
                                const KvView &kv, bool e4m3, int32_t *err, cudaStream_t stream);
-size_t decode_workspace_bytes(int32_t head_dim, bool e4m3);
+size_t decode_workspace_bytes(int32_t head_dim);
 cudaError_t launch_attend_decode(const AttendArgs &a, bool e4m3, int32_t max_q, void *ws, cudaStream_t stream);
 cudaError_t launch_attend_rows(const AttendArgs &a, bool e4m3, cudaStream_t stream);
 }  // namespace lora
@@ -131,7 +131,7 @@ lora_status_t lora_attend_workspace_bytes(const lora_attention_t *att, const lor
     if (bytes == nullptr) return LORA_ERR_INVALID_ARG;
     if ((st = check_kv(kv, &view)) != LORA_OK) return st;
     if ((st = check_attention(att, view)) != LORA_OK) return st;
-    *bytes = lora::decode_workspace_bytes(view.head_dim, kv->type == LORA_KV_E4M3);
+    *bytes = lora::decode_workspace_bytes(view.head_dim);
     return LORA_OK;
 }
 
