@@ -681,55 +681,71 @@ attend_decode_kernel(const AttendArgs a, float *parts, int32_t *counters, int pr
     tc::cp_wait_all();
 
     // ---- joining -------------------------------------------------------------------
-    __shared__ int32_t s_last;
+    // The segments that the block's share boundaries cut, each listed once; a (segment,
+    // row) pair a warp, first over the block's own partials, then, for segments of
+    // several blocks, by the block that arrives last over the blocks'.
+    struct Cut {
+        Segment s;
+        int32_t w0, w1, c0, c1, rows;  // first and last warp of this block and block of the call, rows
+        bool last;
+    };
+    __shared__ Cut s_cut[NW + 1];
     float *block_parts = parts + int64_t(gridDim.x) * NW * C::kPartial;
     const int64_t block_share = share * NW, b0 = min(int64_t(total), blockIdx.x * block_share);
     const int64_t b1 = min(int64_t(total), b0 + block_share);
-    // the segments that the block's share boundaries cut, each at its first boundary
-    __shared__ bool s_cut[NW + 1];
-    const auto at_boundary = [&](int i, Segment &s) {
-        const int64_t x = min(int64_t(total), b0 + i * share);
-        if (x <= 0 || x >= total) return false;
-        s = segment_at<ROWS, kKeys>(a, s_pref, find_seq(s_pref, a.n_seq, static_cast<int32_t>(x)),
-                                    static_cast<int32_t>(x));
-        return s.begin < x && (i == 0 || s.begin >= x - share);
-    };
     if (tid <= NW) {
-        Segment s;
-        s_cut[tid] = at_boundary(tid, s);
+        const int64_t x = min(int64_t(total), b0 + tid * share);
+        Cut c{};
+        if (x > 0 && x < total) {
+            c.s = segment_at<ROWS, kKeys>(a, s_pref, find_seq(s_pref, a.n_seq, static_cast<int32_t>(x)),
+                                          static_cast<int32_t>(x));
+            const int64_t end = int64_t(c.s.begin) + c.s.steps;
+            if (c.s.begin < x && (tid == 0 || c.s.begin >= x - share)) {
+                c.rows = min(ROWS, c.s.n * a.group - c.s.tile);
+                c.w0 = static_cast<int32_t>(max(int64_t(c.s.begin), b0) / share);
+                c.w1 = static_cast<int32_t>((min(end, b1) - 1) / share);
+                c.c0 = static_cast<int32_t>(c.s.begin / block_share);
+                c.c1 = static_cast<int32_t>((end - 1) / block_share);
+            }
+        }
+        s_cut[tid] = c;
     }
     __syncthreads();
-    for (int i = 0; i <= NW; ++i) {
-        Segment s;
-        if (!s_cut[i] || !at_boundary(i, s)) continue;
-        const int64_t end = int64_t(s.begin) + s.steps;
-        const int32_t rows = min(ROWS, s.n * a.group - s.tile);
-        const int32_t w0 = static_cast<int32_t>(max(int64_t(s.begin), b0) / share);
-        const int32_t w1 = static_cast<int32_t>((min(end, b1) - 1) / share);
-        const int32_t c0 = static_cast<int32_t>(s.begin / block_share);
-        const int32_t c1 = static_cast<int32_t>((end - 1) / block_share);
-        // a warp's partial is in its ring, unless more segments followed in its share
+    // a block's partial: its first segment begins before it, its last cut one inside
+    const auto block_part = [&](const Segment &s, int32_t c) -> float * {
+        return block_parts + (2 * int64_t(c) + (s.begin >= c * block_share ? 1 : 0)) * C::kPartial;
+    };
+    bool shared_cut = false;
+    for (int i = 0, at_row = 0; i <= NW; ++i) {
+        const Cut &c = s_cut[i];
+        shared_cut = shared_cut || (c.rows > 0 && c.c0 != c.c1);
+        const int64_t end = int64_t(c.s.begin) + c.s.steps;
+        // a warp's partial is in its own memory, unless more segments followed in its share
         const auto of_warp = [&](int32_t w) -> const float * {
             if (end < min(int64_t(total), (w + 1) * share)) return parts + int64_t(w) * C::kPartial;
             return reinterpret_cast<const float *>(smem + pref_bytes + (w - blockIdx.x * NW) * C::kWarpB);
         };
-        // a block's: its first segment begins before it or is its last cut one
-        const auto of_block = [&](int32_t c) -> float * {
-            return block_parts + (2 * int64_t(c) + (s.begin >= c * block_share ? 1 : 0)) * C::kPartial;
-        };
-        float *to = c0 == c1 ? nullptr : of_block(blockIdx.x);
-        for (int r = warp; r < rows; r += NW) join_row<HD, ROWS>(a, of_warp, w0, w1, s, r, kShift, to, lane);
-        if (c0 == c1) continue;
-        __threadfence();
-        __syncthreads();
-        if (tid == 0) {
-            s_last = atomicAdd(counters + c0, 1) == c1 - c0;
-            if (s_last) counters[c0] = 0;
-        }
-        __syncthreads();
-        if (!s_last) continue;  // the last block of this segment: all others have written theirs
-        __threadfence();
-        for (int r = warp; r < rows; r += NW) join_row<HD, ROWS>(a, of_block, c0, c1, s, r, kShift, nullptr, lane);
+        for (int r = 0; r < c.rows; ++r, ++at_row)
+            if (at_row % NW == warp)
+                join_row<HD, ROWS>(a, of_warp, c.w0, c.w1, c.s, r, kShift,
+                                   c.c0 == c.c1 ? nullptr : block_part(c.s, blockIdx.x), lane);
+    }
+    if (!shared_cut) return;
+    __threadfence();
+    __syncthreads();
+    if (tid <= NW && s_cut[tid].rows > 0 && s_cut[tid].c0 != s_cut[tid].c1) {
+        Cut &c = s_cut[tid];
+        c.last = atomicAdd(counters + c.c0, 1) == c.c1 - c.c0;
+        if (c.last) counters[c.c0] = 0;
+    }
+    __syncthreads();
+    __threadfence();
+    for (int i = 0, at_row = 0; i <= NW; ++i) {
+        const Cut &c = s_cut[i];
+        if (!c.last) continue;
+        const auto of_block = [&](int32_t b) -> const float * { return block_part(c.s, b); };
+        for (int r = 0; r < c.rows; ++r, ++at_row)
+            if (at_row % NW == warp) join_row<HD, ROWS>(a, of_block, c.c0, c.c1, c.s, r, kShift, nullptr, lane);
     }
 }
 
