@@ -28,6 +28,8 @@
 // With at most 8 rows the remainder goes into the MMA's unused rows 8..15 and
 // costs nothing.  An e4m3 code is exact in f16; a query row is scaled by a power
 // of two into f16, exact to 2^-24 of its largest element.
+#include <type_traits>
+
 #include <cuda_fp16.h>
 
 #include "attention.cuh"
@@ -70,9 +72,11 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
-// tanh to about 2^-20: from the exponential away from zero, by the series near it.
+// tanh to 2^-22 absolutely; NEAR: also relatively, by the series near zero.
+template <bool NEAR>
 __device__ __forceinline__ float tanh_of(float z) {
     const float far = 1.0f - __fdividef(2.0f, ex2(z * (2.0f * kLog2e)) + 1.0f);
+    if constexpr (!NEAR) return far;
     const float z2 = z * z;
     const float near = z * (1.0f + z2 * (-0.33333333f + z2 * (0.13333333f + z2 * (-0.05396825f))));
     return fabsf(z) < 0.25f ? near : far;
@@ -124,6 +128,10 @@ struct Segment {
     int32_t begin;            // index of its first step among all of the call
 };
 
+// Opening a segment (its query, its lengths, closing it) costs a warp about as
+// much as kOpen steps: it counts as so many, in front of the real ones.
+constexpr int kOpen = 2;
+
 // The first key of a request that any of its rows sees.
 __device__ __forceinline__ int32_t first_key(const AttendArgs &a, const RequestRows &r) {
     if (a.window <= 0) return 0;
@@ -140,6 +148,13 @@ __device__ __forceinline__ int32_t tiles_of(const AttendArgs &a, int32_t n) {
     return static_cast<int32_t>((int64_t(n) * a.group + ROWS - 1) / ROWS);
 }
 
+// Steps of all segments of a request, their openings included.
+template <int ROWS, int KEYS>
+__device__ __forceinline__ int64_t cost_of(const AttendArgs &a, const RequestRows &r) {
+    const int64_t steps = steps_of<KEYS>(a, r);
+    return steps > 0 ? (steps + kOpen) * a.kv.n_kv * tiles_of<ROWS>(a, r.n) : 0;
+}
+
 // The segment of request `seq` that step x of the call belongs to.
 template <int ROWS, int KEYS>
 __device__ __forceinline__ Segment segment_at(const AttendArgs &a, const int32_t *s_pref, int32_t seq, int32_t x) {
@@ -152,10 +167,10 @@ __device__ __forceinline__ Segment segment_at(const AttendArgs &a, const int32_t
     s.lo = first_key(a, r);
     s.base = s.lo & ~(KEYS - 1);
     s.steps = max(1, steps_of<KEYS>(a, r));
-    const int32_t tiles = max(1, tiles_of<ROWS>(a, r.n)), i = (x - s_pref[seq]) / s.steps;
+    const int32_t tiles = max(1, tiles_of<ROWS>(a, r.n)), i = (x - s_pref[seq]) / (s.steps + kOpen);
     s.head = i / tiles;  // tiles of one head are neighbours: they read the same keys
     s.tile = (i - s.head * tiles) * ROWS;
-    s.begin = s_pref[seq] + i * s.steps;
+    s.begin = s_pref[seq] + i * (s.steps + kOpen) + kOpen;
     return s;
 }
 
@@ -170,60 +185,86 @@ __device__ __forceinline__ int32_t find_seq(const int32_t *s_pref, int32_t n, in
     return lo;
 }
 
-// One row joined over partials first..last, in order: part(i) is partial i's
-// address, shared (a few, read one after the other) or global (many, a lane
-// each for the statistics).  Writes the row of `out`, or of the partial `to`.
-template <int HD, int ROWS, class P>
-__device__ __forceinline__ void join_row(const AttendArgs &a, P part, int32_t first, int32_t last, const Segment &s,
-                                         int r, float shift, float *to, int lane) {
+// Rows r0 .. r0 + R - 1 (below `rows`) joined over partials first..last, in order;
+// part(i) is partial i's address, in shared or global memory.  Writes rows of
+// `out`, or of the partial `to`.
+template <int HD, int ROWS, int R, class P>
+__device__ __forceinline__ void join_rows(const AttendArgs &a, P part, int32_t first, int32_t last, const Segment &s,
+                                          int r0, int rows, float shift, float *to, int lane) {
     constexpr int V = HD / 32;
-    float top = -INFINITY, sum = 0.0f, o[V] = {};
+    float top[R], sum[R], o[R][V];
+#pragma unroll
+    for (int q = 0; q < R; ++q) {
+        top[q] = -INFINITY;
+        sum[q] = 0.0f;
+#pragma unroll
+        for (int e = 0; e < V; ++e) o[q][e] = 0.0f;
+    }
     for (int32_t c = first; c <= last; c += 32) {
         const int32_t n = min(32, last - c + 1);
         const float *mine = part(c + min(lane, n - 1));
-        const float m = lane < n ? mine[r] : -INFINITY, l = lane < n ? mine[ROWS + r] : 0.0f;
-        float now = m;
+        float w[R], l[R];
 #pragma unroll
-        for (int x = 16; x > 0; x >>= 1) now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, x));
-        now = fmaxf(now, top);
-        const float ref = now == -INFINITY ? 0.0f : now, w = ex2(m - ref), f = ex2(top - ref);
-        sum *= f;
+        for (int q = 0; q < R; ++q) {
+            const int r = min(r0 + q, rows - 1);
+            w[q] = lane < n ? mine[r] : -INFINITY;
+            l[q] = lane < n ? mine[ROWS + r] : 0.0f;
+        }
 #pragma unroll
-        for (int e = 0; e < V; ++e) o[e] *= f;
-#pragma unroll 8
+        for (int q = 0; q < R; ++q) {
+            float now = w[q];
+#pragma unroll
+            for (int x = 16; x > 0; x >>= 1) now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, x));
+            now = fmaxf(now, top[q]);
+            const float ref = now == -INFINITY ? 0.0f : now, f = ex2(top[q] - ref);
+            w[q] = ex2(w[q] - ref);
+            sum[q] *= f;
+#pragma unroll
+            for (int e = 0; e < V; ++e) o[q][e] *= f;
+            top[q] = now;
+        }
+#pragma unroll 4
         for (int32_t j = 0; j < n; ++j) {
-            const float wj = __shfl_sync(0xffffffffu, w, j);
-            sum += wj * __shfl_sync(0xffffffffu, l, j);
-            const float *v = part(c + j) + 2 * ROWS + r * HD + lane * V;
-            if constexpr (V == 4) {
-                const float4 x = *reinterpret_cast<const float4 *>(v);
-                o[0] += wj * x.x, o[1] += wj * x.y, o[2] += wj * x.z, o[3] += wj * x.w;
-            } else {
-                const float2 x = *reinterpret_cast<const float2 *>(v);
-                o[0] += wj * x.x, o[1] += wj * x.y;
+            const float *v = part(c + j) + 2 * ROWS + lane * V;
+#pragma unroll
+            for (int q = 0; q < R; ++q) {
+                const float wj = __shfl_sync(0xffffffffu, w[q], j);
+                sum[q] += wj * __shfl_sync(0xffffffffu, l[q], j);
+                const float *x = v + min(r0 + q, rows - 1) * HD;
+                if constexpr (V == 4) {
+                    const float4 y = *reinterpret_cast<const float4 *>(x);
+                    o[q][0] += wj * y.x, o[q][1] += wj * y.y, o[q][2] += wj * y.z, o[q][3] += wj * y.w;
+                } else {
+                    const float2 y = *reinterpret_cast<const float2 *>(x);
+                    o[q][0] += wj * y.x, o[q][1] += wj * y.y;
+                }
             }
         }
-        top = now;
     }
-    if (to != nullptr) {
-        if (lane == 0) {
-            to[r] = top;
-            to[ROWS + r] = sum;
+#pragma unroll
+    for (int q = 0; q < R; ++q) {
+        const int r = r0 + q;
+        if (r >= rows) break;
+        if (to != nullptr) {
+            if (lane == 0) {
+                to[r] = top[q];
+                to[ROWS + r] = sum[q];
+            }
+#pragma unroll
+            for (int e = 0; e < V; ++e) to[2 * ROWS + r * HD + lane * V + e] = o[q][e];
+            continue;
         }
+        const int32_t row = s.tile + r, t = s.q0 + row / a.group, h = s.head * a.group + row % a.group;
+        const float inv = sum[q] > 0.0f ? a.kv.v_scale / sum[q] : sum[q] == 0.0f ? 0.0f : sum[q];
+        uint32_t w[V / 2];
 #pragma unroll
-        for (int e = 0; e < V; ++e) to[2 * ROWS + r * HD + lane * V + e] = o[e];
-        return;
+        for (int e = 0; e < V / 2; ++e) w[e] = pack_bf16x2(o[q][2 * e] * inv, o[q][2 * e + 1] * inv);
+        uint16_t *dst = a.out + t * a.ldo + h * HD + lane * V;
+        if constexpr (V == 4) *reinterpret_cast<uint2 *>(dst) = make_uint2(w[0], w[1]);
+        else *reinterpret_cast<uint32_t *>(dst) = w[0];
+        if (a.lse != nullptr && lane == 0)
+            a.lse[int64_t(t) * a.n_heads + h] = sum[q] == 0.0f ? -INFINITY : kLn2 * (top[q] - shift) + logf(sum[q]);
     }
-    const int32_t row = s.tile + r, t = s.q0 + row / a.group, h = s.head * a.group + row % a.group;
-    const float inv = sum > 0.0f ? a.kv.v_scale / sum : sum == 0.0f ? 0.0f : sum;
-    uint32_t w[V / 2];
-#pragma unroll
-    for (int e = 0; e < V / 2; ++e) w[e] = pack_bf16x2(o[2 * e] * inv, o[2 * e + 1] * inv);
-    uint16_t *dst = a.out + t * a.ldo + h * HD + lane * V;
-    if constexpr (V == 4) *reinterpret_cast<uint2 *>(dst) = make_uint2(w[0], w[1]);
-    else *reinterpret_cast<uint32_t *>(dst) = w[0];
-    if (a.lse != nullptr && lane == 0)
-        a.lse[int64_t(t) * a.n_heads + h] = sum == 0.0f ? -INFINITY : kLn2 * (top - shift) + logf(sum);
 }
 
 template <int HD, bool E4M3, int ROWS>
@@ -248,7 +289,7 @@ attend_decode_kernel(const AttendArgs a, float *parts, int32_t *counters, int pr
         for (int32_t i = i0; i < i1; ++i) {
             const RequestRows r = load_rows(a, i);
             if (!r.ok && blockIdx.x == 0) report_error(a.err, LORA_ERR_INVALID_ARG);
-            mine += int64_t(steps_of<kKeys>(a, r)) * a.kv.n_kv * tiles_of<ROWS>(a, r.n);
+            mine += cost_of<ROWS, kKeys>(a, r);
         }
         int64_t incl = mine;
 #pragma unroll
@@ -271,7 +312,7 @@ attend_decode_kernel(const AttendArgs a, float *parts, int32_t *counters, int pr
         for (int32_t i = i0; i < i1; ++i) {
             const RequestRows r = load_rows(a, i);
             s_pref[i] = static_cast<int32_t>(run);
-            run += int64_t(steps_of<kKeys>(a, r)) * a.kv.n_kv * tiles_of<ROWS>(a, r.n);
+            run += cost_of<ROWS, kKeys>(a, r);
         }
         total = static_cast<int32_t>(sum);
         if (tid == 0) s_pref[a.n_seq] = total;
@@ -303,7 +344,7 @@ attend_decode_kernel(const AttendArgs a, float *parts, int32_t *counters, int pr
 
     // ---- the copying side: where its next step is ------------------------------
     Segment ls{};
-    int32_t lx = x0, lkey = 0, lleft = 0, lpage[NK];
+    int32_t lx = x0, lkey = 0, lend = 0, lpage[NK];
     const int32_t *ltab = nullptr;
     // whether this lane's key 32 i + lane of the next step is one that a row sees, and its page
     const auto has_key = [&](int i) { return lkey + 32 * i + lane >= ls.lo && lkey + 32 * i + lane < ls.len; };
@@ -316,8 +357,9 @@ attend_decode_kernel(const AttendArgs a, float *parts, int32_t *counters, int pr
     };
     const auto open_load = [&](int32_t seq) {
         ls = segment_at<ROWS, kKeys>(a, s_pref, seq, lx);
+        lx = max(lx, ls.begin);
         lkey = ls.base + (lx - ls.begin) * kKeys;
-        lleft = ls.steps - (lx - ls.begin);
+        lend = ls.begin + ls.steps;
         ltab = a.table + ls.seq * a.ld_table;
     };
     if (x0 < x1) {
@@ -369,7 +411,7 @@ attend_decode_kernel(const AttendArgs a, float *parts, int32_t *counters, int pr
             if (lv) {
                 ++lx;
                 lkey += kKeys;
-                if (--lleft == 0 && lx < x1) {
+                if (lx == lend && lx < x1) {
                     int32_t seq = ls.seq;
                     while (s_pref[seq + 1] <= lx) ++seq;
                     open_load(seq);
@@ -383,15 +425,17 @@ attend_decode_kernel(const AttendArgs a, float *parts, int32_t *counters, int pr
 
     // ---- the computing side ----------------------------------------------------
     Segment cs{};
-    int32_t cleft = 0, ckey = 0, pos_lo = 0, pos_hi = 0;
+    int32_t cx = x0, cend = 0, ckey = 0, pos_lo = 0, pos_hi = 0;
     int32_t pos[MB][2];
     uint32_t qf[kQShared ? 1 : KK][4];
     float m[MB][2], l[MB][2], mult[MB][2], slope[MB][2], acc[MB][DT][4];
 
-    const auto open_compute = [&](int32_t seq, int32_t x) {
-        cs = segment_at<ROWS, kKeys>(a, s_pref, seq, x);
-        cleft = cs.steps - (x - cs.begin);
-        ckey = cs.base + (x - cs.begin) * kKeys;
+    const auto open_compute = [&](int32_t seq) {
+        cs = segment_at<ROWS, kKeys>(a, s_pref, seq, cx);
+        cx = max(cx, cs.begin);
+        cend = cs.begin + cs.steps;
+        if (cx >= x1) return;
+        ckey = cs.base + (cx - cs.begin) * kKeys;
         const int32_t rows = min(ROWS, cs.n * a.group - cs.tile);
         pos_lo = cs.len - cs.n + cs.tile / a.group;
         pos_hi = cs.len - cs.n + (cs.tile + rows - 1) / a.group;
@@ -463,6 +507,8 @@ attend_decode_kernel(const AttendArgs a, float *parts, int32_t *counters, int pr
 
     uint32_t hi[MB][KB][4], lo[MB][KB][4];
     const int mat = lane >> 3, r8 = lane & 7;
+    // a capped score is off by softcap * 2^-22: above 64 that asks for the series near zero
+    const bool wide_cap = a.softcap > 64.0f;
     const bool plain = a.softcap == 0.0f && a.slopes == nullptr && a.scale > 0.0f;
     // weights p = 2^(score log2 e - maximum) of the step's keys, as the fragments of the second product
     const auto scores = [&](int slot) {
@@ -507,19 +553,38 @@ attend_decode_kernel(const AttendArgs a, float *parts, int32_t *counters, int pr
                     for (int t = 0; t < ST; ++t) top = fmaxf(top, fmaxf(s[mb][t][2 * i], s[mb][t][2 * i + 1]));
                     top *= by;
                 } else {
-                    const float in = a.softcap > 0.0f ? mult[mb][i] / a.softcap : by, cap = a.softcap * kLog2e;
+                    if (a.softcap > 0.0f) {
+                        const float in = mult[mb][i] / a.softcap;
 #pragma unroll
-                    for (int t = 0; t < ST; ++t)
+                        for (int t = 0; t < ST; ++t)
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            float &x = s[mb][t][2 * i + e];
-                            x *= in;
-                            if (a.softcap > 0.0f) x = cap * tanh_of(x);
-                            const int32_t key = ckey + 8 * t + 2 * c4 + e;
-                            x += slope[mb][i] * static_cast<float>(key - pos[mb][i]);
-                            if (key > pos[mb][i] || (a.window > 0 && pos[mb][i] - key >= a.window)) x = -INFINITY;
-                            top = fmaxf(top, x);
+                            for (int e = 0; e < 2; ++e) {
+                                float &x = s[mb][t][2 * i + e];
+                                x = a.softcap * kLog2e * (wide_cap ? tanh_of<true>(x * in) : tanh_of<false>(x * in));
+                            }
+                    } else {
+#pragma unroll
+                        for (int t = 0; t < ST; ++t) s[mb][t][2 * i] *= by, s[mb][t][2 * i + 1] *= by;
+                    }
+                    const int32_t back = ckey + 2 * c4 - pos[mb][i];  // of this lane's first key
+                    if (a.slopes != nullptr) {
+#pragma unroll
+                        for (int t = 0; t < ST; ++t) {
+                            s[mb][t][2 * i] += slope[mb][i] * static_cast<float>(back + 8 * t);
+                            s[mb][t][2 * i + 1] += slope[mb][i] * static_cast<float>(back + 8 * t + 1);
                         }
+                    }
+                    if (masked) {
+#pragma unroll
+                        for (int t = 0; t < ST; ++t)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                const int32_t b = back + 8 * t + e;
+                                if (b > 0 || (a.window > 0 && -b >= a.window)) s[mb][t][2 * i + e] = -INFINITY;
+                            }
+                    }
+#pragma unroll
+                    for (int t = 0; t < ST; ++t) top = fmaxf(top, fmaxf(s[mb][t][2 * i], s[mb][t][2 * i + 1]));
                     by = 1.0f;
                 }
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
@@ -601,10 +666,10 @@ attend_decode_kernel(const AttendArgs a, float *parts, int32_t *counters, int pr
 
     // ends a segment, or this warp's part of it: rows to `out`, or a partial (the
     // share's last one into the warp's own memory, which holds no more tiles then)
-    const auto close = [&](int32_t x_end) {
+    const auto close = [&]() {
         const int32_t rows = min(ROWS, cs.n * a.group - cs.tile);
-        const bool whole = cs.begin >= x0 && cs.begin + cs.steps <= x_end;
-        float *part = x_end == x1 ? reinterpret_cast<float *>(warp_ptr) : parts + int64_t(me) * C::kPartial;
+        const bool whole = cs.begin >= x0 && cend == cx;
+        float *part = cend + kOpen >= x1 ? reinterpret_cast<float *>(warp_ptr) : parts + int64_t(me) * C::kPartial;
 #pragma unroll
         for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
@@ -663,26 +728,27 @@ attend_decode_kernel(const AttendArgs a, float *parts, int32_t *counters, int pr
         slot = slot + 1 == kTiles ? 0 : slot + 1;
         return now;
     };
-    if (x0 < x1) open_compute(find_seq(s_pref, a.n_seq, x0), x0);
-    for (int32_t x = x0; x < x1; ++x) {
+    if (x0 < x1) open_compute(find_seq(s_pref, a.n_seq, x0));
+    while (cx < x1) {
         scores(next());
         outputs(next());
         ckey += kKeys;
-        if (--cleft == 0 || x + 1 == x1) {
+        ++cx;
+        if (cx == cend || cx == x1) {
             __syncwarp();
-            close(x + 1);
-            if (x + 1 < x1) {
+            close();
+            if (cx < x1) {
                 int32_t seq = cs.seq;
-                while (s_pref[seq + 1] <= x + 1) ++seq;
-                open_compute(seq, x + 1);
+                while (s_pref[seq + 1] <= cx) ++seq;
+                open_compute(seq);
             }
         }
     }
     tc::cp_wait_all();
 
     // ---- joining -------------------------------------------------------------------
-    // The segments that the block's share boundaries cut, each listed once; a (segment,
-    // row) pair a warp, first over the block's own partials, then, for segments of
+    // The segments that the block's share boundaries cut, each listed once; its rows go to
+    // the warps, first over the block's own partials, then, for segments of
     // several blocks, by the block that arrives last over the blocks'.
     struct Cut {
         Segment s;
@@ -715,21 +781,33 @@ attend_decode_kernel(const AttendArgs a, float *parts, int32_t *counters, int pr
     const auto block_part = [&](const Segment &s, int32_t c) -> float * {
         return block_parts + (2 * int64_t(c) + (s.begin >= c * block_share ? 1 : 0)) * C::kPartial;
     };
-    bool shared_cut = false;
-    for (int i = 0, at_row = 0; i <= NW; ++i) {
-        const Cut &c = s_cut[i];
-        shared_cut = shared_cut || (c.rows > 0 && c.c0 != c.c1);
+    // calls f(cut, first row, rows at a time) for this warp's part of the cuts that pick()
+    // takes: four rows at a time hide each other's latency, one at a time where there are
+    // fewer rows than that gives warps
+    const auto each = [&](auto pick, auto f) {
+        int all = 0;
+        for (int i = 0; i <= NW; ++i) all += pick(s_cut[i]) ? s_cut[i].rows : 0;
+        const int by = all > 2 * NW ? 4 : 1;
+        for (int i = 0, turn = 0; i <= NW; ++i)
+            if (pick(s_cut[i]))
+                for (int r = 0; r < s_cut[i].rows; r += by, ++turn)
+                    if (turn % NW == warp) {
+                        if (by == 4) f(s_cut[i], r, std::integral_constant<int, 4>());
+                        else f(s_cut[i], r, std::integral_constant<int, 1>());
+                    }
+    };
+    each([](const Cut &c) { return c.rows > 0; }, [&](const Cut &c, int r, auto by) {
         const int64_t end = int64_t(c.s.begin) + c.s.steps;
         // a warp's partial is in its own memory, unless more segments followed in its share
         const auto of_warp = [&](int32_t w) -> const float * {
-            if (end < min(int64_t(total), (w + 1) * share)) return parts + int64_t(w) * C::kPartial;
+            if (end + kOpen < min(int64_t(total), (w + 1) * share)) return parts + int64_t(w) * C::kPartial;
             return reinterpret_cast<const float *>(smem + pref_bytes + (w - blockIdx.x * NW) * C::kWarpB);
         };
-        for (int r = 0; r < c.rows; ++r, ++at_row)
-            if (at_row % NW == warp)
-                join_row<HD, ROWS>(a, of_warp, c.w0, c.w1, c.s, r, kShift,
-                                   c.c0 == c.c1 ? nullptr : block_part(c.s, blockIdx.x), lane);
-    }
+        join_rows<HD, ROWS, by.value>(a, of_warp, c.w0, c.w1, c.s, r, c.rows, kShift,
+                                      c.c0 == c.c1 ? nullptr : block_part(c.s, blockIdx.x), lane);
+    });
+    bool shared_cut = false;
+    for (int i = 0; i <= NW; ++i) shared_cut = shared_cut || (s_cut[i].rows > 0 && s_cut[i].c0 != s_cut[i].c1);
     if (!shared_cut) return;
     __threadfence();
     __syncthreads();
@@ -740,13 +818,10 @@ attend_decode_kernel(const AttendArgs a, float *parts, int32_t *counters, int pr
     }
     __syncthreads();
     __threadfence();
-    for (int i = 0, at_row = 0; i <= NW; ++i) {
-        const Cut &c = s_cut[i];
-        if (!c.last) continue;
+    each([](const Cut &c) { return c.last; }, [&](const Cut &c, int r, auto by) {
         const auto of_block = [&](int32_t b) -> const float * { return block_part(c.s, b); };
-        for (int r = 0; r < c.rows; ++r, ++at_row)
-            if (at_row % NW == warp) join_row<HD, ROWS>(a, of_block, c.c0, c.c1, c.s, r, kShift, nullptr, lane);
-    }
+        join_rows<HD, ROWS, by.value>(a, of_block, c.c0, c.c1, c.s, r, c.rows, kShift, nullptr, lane);
+    });
 }
 
 template <int HD, bool E4M3, int ROWS>
