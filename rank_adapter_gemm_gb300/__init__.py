@@ -46,11 +46,12 @@ def _p(t) -> Optional[ctypes.c_void_p]:
     return ctypes.c_void_p(t.data_ptr())
 
 
-def _stream(stream) -> ctypes.c_void_p:
-    torch = _torch()
+def _stream(stream):
     if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream)
+        # the current stream's address without building a Stream object (2.8 us on a Grace core)
+        _C = _torch()._C
+        return _C._cuda_getCurrentRawStream(_C._cuda_getDevice())
+    return stream.cuda_stream
 
 
 def _dev(t, name, dtype=None):

@@ -14,36 +14,55 @@ from typing import Mapping, Optional
 
 import numpy as np
 
-from . import _dev, _p, _rows, _stream, _torch
+from . import _dev, _p, _stream, _torch
 from ._lib import (ATTEND_PATHS, LORA_MAX_SEQS, ROPE_KINDS, check, load, lora_attention_t, lora_kv_t,
                    lora_rope_scaling_t, lora_rope_t)
 
 
-def _i32(t, name, n=None, dtype=None):
-    _dev(t, name, dtype or _torch().int32)
-    if not t.is_contiguous() or (n is not None and t.numel() != n):
-        raise ValueError(f"{name} must be contiguous" + (f" with {n} elements" if n is not None else ""))
-    return t.data_ptr()
+# The checks below run on every call of a decode loop: they read each property
+# once and leave the wording of a refusal to the slow path.
+def _flat(t, name, dtype, n=None) -> int:
+    """Address of a contiguous device tensor of n elements (any number: None)."""
+    if (getattr(t, "dtype", None) is dtype and t.is_cuda and t.is_contiguous() and (n is None or t.numel() == n)):
+        return t.data_ptr()
+    _dev(t, name, dtype)
+    raise ValueError(f"{name} must be contiguous" + (f" with {n} elements" if n is not None else ""))
 
 
 def _table(t, n_seq):
     """(address, row stride, width) of a block table."""
+    if getattr(t, "dtype", None) is _torch().int32 and t.is_cuda and t.dim() == 2:
+        rows, width = t.shape
+        ld, one = t.stride()
+        if rows == n_seq and (one == 1 or width <= 1):
+            return t.data_ptr(), ld if ld > width else width, width
     _dev(t, "block_table", _torch().int32)
-    if t.dim() != 2 or t.shape[0] != n_seq or (t.shape[1] > 1 and t.stride(1) != 1):
-        raise ValueError("block_table must be a 2-D int32 tensor, one row a request, with unit column stride")
-    return t.data_ptr(), max(t.stride(0), t.shape[1]), t.shape[1]
+    raise ValueError("block_table must be a 2-D int32 tensor, one row a request, with unit column stride")
+
+
+def _matrix(t, name):
+    """(address, row stride, rows, columns) of bf16 rows."""
+    if getattr(t, "dtype", None) is _torch().bfloat16 and t.is_cuda and t.dim() == 2:
+        rows, cols = t.shape
+        ld, one = t.stride()
+        if one == 1:
+            return t.data_ptr(), ld, rows, cols
+    _dev(t, name, _torch().bfloat16)
+    raise ValueError(f"{name} must be a 2-D bf16 tensor with unit column stride")
 
 
 def lora_kv_step(ctx_lens, new_lens, page_size, free_pages, block_table, q_offsets, kv_lens, positions, seq_ids,
                  slot_map, taken, err, stream=None) -> None:
-    n, T = ctx_lens.numel(), positions.numel()
+    torch = _torch()
+    i32, n, T = torch.int32, ctx_lens.numel(), positions.numel()
     table, ld, width = _table(block_table, n)
     check(load().lora_kv_step(
-        _i32(ctx_lens, "ctx_lens"), _i32(new_lens, "new_lens", n), n, int(page_size), _i32(free_pages, "free_pages"),
-        free_pages.numel(), table, ld, width, T, _i32(q_offsets, "q_offsets", n + 1), _i32(kv_lens, "kv_lens", n),
-        _i32(positions, "positions"), _i32(seq_ids, "seq_ids", T),
-        _i32(slot_map, "slot_map", T, _torch().int64), _i32(taken, "taken", 1), _p(err), _stream(stream)),
-        "lora_kv_step")
+        _flat(ctx_lens, "ctx_lens", i32), _flat(new_lens, "new_lens", i32, n), n, page_size,
+        _flat(free_pages, "free_pages", i32), free_pages.numel(), table, ld, width, T,
+        _flat(q_offsets, "q_offsets", i32, n + 1), _flat(kv_lens, "kv_lens", i32, n),
+        _flat(positions, "positions", i32), _flat(seq_ids, "seq_ids", i32, T),
+        _flat(slot_map, "slot_map", torch.int64, T), _flat(taken, "taken", i32, 1),
+        None if err is None else _flat(err, "err", i32), _stream(stream)), "lora_kv_step")
 
 
 def lora_rope_phases(rot_dim: int, theta: float, scaling: Optional[Mapping] = None):
@@ -69,14 +88,16 @@ def lora_rope_phases(rot_dim: int, theta: float, scaling: Optional[Mapping] = No
 
 def lora_rope_append(qkv, q_out, n_heads, rope: lora_rope_t, positions, slot_map, kv: lora_kv_t, err,
                      stream=None) -> None:
-    ldqkv, ldq, T = _rows(qkv, "qkv"), _rows(q_out, "q_out"), qkv.shape[0]
-    n_heads = int(n_heads)
-    if (q_out.shape[0] != T or qkv.shape[1] != (n_heads + 2 * kv.n_kv) * kv.head_dim
-            or q_out.shape[1] < n_heads * kv.head_dim):
+    torch = _torch()
+    x, ldx, T, cols = _matrix(qkv, "qkv")
+    q, ldq, rows, q_cols = _matrix(q_out, "q_out")
+    hd = kv.head_dim
+    if rows != T or cols != (n_heads + 2 * kv.n_kv) * hd or q_cols < n_heads * hd:
         raise ValueError("qkv must have n_heads + 2 n_kv heads and q_out n_heads heads, with the same rows")
-    check(load().lora_rope_append(qkv.data_ptr(), ldqkv, T, n_heads, rope, _i32(positions, "positions", T),
-                                  _i32(slot_map, "slot_map", T, _torch().int64), q_out.data_ptr(), ldq, kv, _p(err),
-                                  _stream(stream)), "lora_rope_append")
+    check(load().lora_rope_append(
+        x, ldx, T, n_heads, rope, _flat(positions, "positions", torch.int32, T),
+        _flat(slot_map, "slot_map", torch.int64, T), q, ldq, kv,
+        None if err is None else _flat(err, "err", torch.int32), _stream(stream)), "lora_rope_append")
 
 
 def lora_attend_workspace_bytes(att: lora_attention_t, kv: lora_kv_t) -> int:
@@ -92,19 +113,19 @@ def lora_attend_resolve_path(path: str, att: lora_attention_t, kv: lora_kv_t, ma
 
 def lora_attend(q, out, q_offsets, kv_lens, block_table, kv: lora_kv_t, att: lora_attention_t, ws, err,
                 max_q_hint: int = 0, lse=None, path: str = "auto", stream=None) -> None:
-    ldq, ldo, T, n = _rows(q, "q"), _rows(out, "out"), q.shape[0], kv_lens.numel()
+    torch = _torch()
+    i32, n = torch.int32, kv_lens.numel()
+    x, ldq, T, q_cols = _matrix(q, "q")
+    o, ldo, rows, o_cols = _matrix(out, "out")
     cols = att.n_heads * kv.head_dim
-    if out.shape[0] != T or q.shape[1] < cols or out.shape[1] < cols:
+    if rows != T or q_cols < cols or o_cols < cols:
         raise ValueError("q and out must have the same rows and n_heads * head_dim columns")
-    if lse is not None:
-        _dev(lse, "lse", _torch().float32)
-        if lse.shape != (T, att.n_heads) or not lse.is_contiguous():
-            raise ValueError("lse must be a contiguous fp32 [T, n_heads] tensor")
     table, ld, width = _table(block_table, n)
-    check(load().lora_attend(q.data_ptr(), ldq, out.data_ptr(), ldo, _p(lse), T, n,
-                             _i32(q_offsets, "q_offsets", n + 1), _i32(kv_lens, "kv_lens"), table, ld, width, kv, att,
-                             int(max_q_hint), ATTEND_PATHS[path], ws.data_ptr(), ws.numel() * ws.element_size(),
-                             _p(err), _stream(stream)), "lora_attend")
+    check(load().lora_attend(
+        x, ldq, o, ldo, None if lse is None else _flat(lse, "lse", torch.float32, T * att.n_heads), T, n,
+        _flat(q_offsets, "q_offsets", i32, n + 1), _flat(kv_lens, "kv_lens", i32), table, ld, width, kv, att,
+        max_q_hint, ATTEND_PATHS[path], _flat(ws, "ws", torch.uint8), ws.numel(),
+        None if err is None else _flat(err, "err", i32), _stream(stream)), "lora_attend")
 
 
 class PagedKV:
@@ -182,7 +203,7 @@ class Attention:
             raise ValueError(f"between 0 and {LORA_MAX_SEQS} requests")
         self.n_seq, self.T, self.kv, self.slopes = int(n_seq), int(T), kv, slopes
         if slopes is not None:
-            _i32(slopes, "slopes", int(n_heads), torch.float32)
+            _flat(slopes, "slopes", torch.float32, int(n_heads))
         scale = float(kv.c.head_dim) ** -0.5 if scale is None else float(scale)
         self.c = lora_attention_t(int(n_heads), scale, float(softcap or 0.0), int(window or 0),
                                   slopes.data_ptr() if slopes is not None else None)

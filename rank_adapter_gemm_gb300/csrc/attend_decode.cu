@@ -281,6 +281,7 @@ attend_decode_kernel(const AttendArgs a, float *parts, int32_t *counters, int pr
     __shared__ int64_t s_warp[NW];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c4 = lane & 3;
 
+    wait_for_previous();
     // steps of every request: exclusive prefix in s_pref[0..n_seq], total behind it
     int32_t total;
     {
@@ -839,8 +840,7 @@ cudaError_t launch(const AttendArgs &a, void *ws, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     int32_t *counters = static_cast<int32_t *>(ws);
     float *parts = reinterpret_cast<float *>(static_cast<char *>(ws) + 1024);
-    kernel<<<grid, kWarps * 32, smem, stream>>>(a, parts, counters, pref);
-    return cudaGetLastError();
+    return launch_dependent(kernel, grid, kWarps * 32, smem, stream, a, parts, counters, pref);
 }
 
 template <int HD, bool E4M3>

@@ -167,6 +167,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t base = (tc::smem_u32(smem_raw) + 1023) & ~1023u;  // two q tiles, then the ring
 
+    wait_for_previous();
     // ---- this block's item: the requests' row-tile pairs, last ones first --------------
     {
         const int32_t per = (a.n_seq + kThreads - 1) / kThreads, i0 = min(a.n_seq, tid * per),
@@ -579,8 +580,7 @@ cudaError_t launch(const AttendArgs &a, cudaStream_t stream) {
     // every request's rows fill pairs of tiles but for one
     const int64_t pairs = int64_t(a.T) * a.group / (2 * kRows) + a.n_seq;
     if (pairs * a.kv.n_kv > INT32_MAX) return cudaErrorInvalidConfiguration;
-    kernel<<<static_cast<unsigned>(pairs * a.kv.n_kv), kThreads, C::kSmem, stream>>>(a);
-    return cudaGetLastError();
+    return launch_dependent(kernel, static_cast<unsigned>(pairs * a.kv.n_kv), kThreads, C::kSmem, stream, a);
 }
 
 }  // namespace

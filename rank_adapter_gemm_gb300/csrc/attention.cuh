@@ -46,6 +46,32 @@ __device__ __forceinline__ RequestRows load_rows(const AttendArgs &a, int32_t i)
     return {q0, ok ? q1 - q0 : 0, ok ? len : 0, ok};
 }
 
+// The kernels of this file's users are launched as programmatic dependents of the
+// kernel before them on the stream, which hides the launch's latency.  Each first
+// waits until that kernel has finished and its writes are visible, so it may read
+// and write what the kernel before it wrote; only then does it let its own
+// dependent's blocks start.
+__device__ __forceinline__ void wait_for_previous() {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+template <class... P, class... A>
+cudaError_t launch_dependent(void (*kernel)(P...), unsigned grid, unsigned threads, size_t smem, cudaStream_t stream,
+                             A... args) {
+    cudaLaunchAttribute attr[1] = {};
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
+
 inline lora_status_t check_kv(const lora_kv_t *kv, KvView *out) {
     if (kv == nullptr || kv->k == nullptr || kv->v == nullptr) return LORA_ERR_INVALID_ARG;
     if (kv->n_pages < 1 || kv->n_kv < 1 || kv->type < LORA_KV_BF16 || kv->type > LORA_KV_E4M3)

@@ -67,6 +67,7 @@ kv_step_kernel(const int32_t *__restrict__ ctx_lens, const int32_t *__restrict__
     __shared__ int32_t s_ctx[kChunk];
     __shared__ Sums s_warp[kThreads / 32];
     __shared__ unsigned long long s_taken;
+    wait_for_previous();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int64_t w0 = int64_t(blockIdx.x) * kWindow, w1 = min(w0 + kWindow, int64_t(T));
     if (tid == 0) s_taken = 0;
@@ -177,10 +178,9 @@ cudaError_t launch_kv_step(const int32_t *ctx_lens, const int32_t *new_lens, int
                            int32_t T, int32_t *q_offsets, int32_t *kv_lens, int32_t *positions, int32_t *seq_ids,
                            int64_t *slot_map, int32_t *taken, int32_t *err, cudaStream_t stream) {
     const int32_t grid = T > kWindow ? (T - 1) / kWindow + 1 : 1;
-    kv_step_kernel<<<grid, kThreads, 0, stream>>>(ctx_lens, new_lens, n_seq, page_shift, free_pages, n_free, table,
-                                                  ld_table, width, T, q_offsets, kv_lens, positions, seq_ids, slot_map,
-                                                  taken, err);
-    return cudaGetLastError();
+    return launch_dependent(kv_step_kernel, grid, kThreads, 0, stream, ctx_lens, new_lens, n_seq, page_shift,
+                            free_pages, n_free, table, ld_table, width, T, q_offsets, kv_lens, positions, seq_ids,
+                            slot_map, taken, err);
 }
 
 }  // namespace lora

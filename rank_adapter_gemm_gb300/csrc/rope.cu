@@ -69,6 +69,7 @@ __device__ __forceinline__ uint2 pack8_e4m3(const float *f, float scale) {
 
 template <bool E4M3>
 __global__ void __launch_bounds__(kThreads) rope_append_kernel(RopeArgs a) {
+    wait_for_previous();
     const int32_t hd = a.kv.head_dim, units = hd / 16, per_pass = kThreads / units;
     const int32_t u = threadIdx.x % units, h0 = threadIdx.x / units;
     if (h0 >= per_pass) return;
@@ -145,9 +146,7 @@ cudaError_t launch_rope_append(const uint16_t *qkv, int64_t ldqkv, int32_t T, in
                                const KvView &kv, bool e4m3, int32_t *err, cudaStream_t stream) {
     const RopeArgs a{qkv,  q_out,   ldqkv,        ldq,              rope.phases, positions, slots, err, kv,
                      n_heads, rope.rot_dim, rope.interleaved, rope.mscale};
-    if (e4m3) rope_append_kernel<true><<<T, kThreads, 0, stream>>>(a);
-    else rope_append_kernel<false><<<T, kThreads, 0, stream>>>(a);
-    return cudaGetLastError();
+    return launch_dependent(e4m3 ? rope_append_kernel<true> : rope_append_kernel<false>, T, kThreads, 0, stream, a);
 }
 
 }  // namespace lora
