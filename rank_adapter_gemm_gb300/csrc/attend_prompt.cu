@@ -9,11 +9,13 @@
 // all heads of its group.
 //
 //   warps 0-3, 4-7   softmax of tile 0 and 1, one row a thread: the row of S from
-//                    tensor memory, running maximum and sum in fp32, weights back
+//                    tensor memory in chunks of 32, each weight once it is known
+//                    not to pass 2^8: the reference of a row's weights is a whole
+//                    power of two that moves, and the sum, O and the step's earlier
+//                    weights with it (exactly), only when a chunk's maximum passes
+//                    2^8 times it.  So a score is read once, no chunk waits for the
+//                    row's maximum, and most steps never touch O.  Weights go back
 //                    into S's place as the left operand of the second product.
-//                    O is rescaled only when a row's maximum grew by more than
-//                    2^8: weights stay exact in bf16's range, and most tiles skip
-//                    the pass over O.
 //   warps 8-11       copy q rows and k and v tiles of 128 keys, key by key through
 //                    the block table, into the swizzled layout that the tensor
 //                    cores read (e4m3 codes are widened to bf16, exactly, on the way)
@@ -24,6 +26,7 @@
 //
 // Weights are rounded to bf16 for the second product (the cache's type: the
 // instruction takes one type for both operands); sums use them unrounded.
+#include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
 #include "attention.cuh"
@@ -97,13 +100,6 @@ __device__ __forceinline__ void tmem_wait(uint32_t (&r)[32]) {
                  : LORA_R8(r, 0), LORA_R8(r, 8), LORA_R8(r, 16), LORA_R8(r, 24) : : "memory");
 }
 
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};"
-        :: LORA_I8(r, 0), LORA_I8(r, 8), LORA_I8(r, 16), LORA_I8(r, 24), "r"(taddr) : "memory");
-}
-
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};"
@@ -120,6 +116,93 @@ __device__ __forceinline__ float tanh_of(float z) {
     const float z2 = z * z;
     const float near = z * (1.0f + z2 * (-0.33333333f + z2 * (0.13333333f + z2 * (-0.05396825f))));
     return fabsf(z) < 0.25f ? near : far;
+}
+
+// Two fp32 in a 64-bit register, for the packed fp32 instructions.
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+
+__device__ __forceinline__ void unpack2(uint64_t v, float &lo, float &hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+
+__device__ __forceinline__ uint64_t fma2(uint64_t x, uint64_t y, uint64_t z) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(x), "l"(y), "l"(z));
+    return r;
+}
+
+__device__ __forceinline__ uint64_t mul2(uint64_t x, uint64_t y) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+    return r;
+}
+
+__device__ __forceinline__ uint64_t add2(uint64_t x, uint64_t y) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+    return r;
+}
+
+// 32 products of a row in their final form, times log2 e: scaled, capped,
+// biased and masked.  back: the first one's key minus the row's position.
+__device__ __forceinline__ void finish_scores(uint32_t (&s)[32], const AttendArgs &a, float mult, float by, float slope,
+                                              int32_t back, bool masked) {
+    if (a.softcap > 0.0f) {
+        // a capped score is off by softcap * 2^-22: above 64 that asks for the series near zero
+        const float in = mult / a.softcap, cap = a.softcap * kLog2e;
+        if (a.softcap > 64.0f) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) s[e] = __float_as_uint(cap * tanh_of<true>(__uint_as_float(s[e]) * in));
+        } else {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) s[e] = __float_as_uint(cap * tanh_of<false>(__uint_as_float(s[e]) * in));
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 32; ++e) s[e] = __float_as_uint(__uint_as_float(s[e]) * by);
+    }
+    if (a.slopes != nullptr) {
+#pragma unroll
+        for (int e = 0; e < 32; ++e)
+            s[e] = __float_as_uint(fmaf(slope, static_cast<float>(back + e), __uint_as_float(s[e])));
+    }
+    if (masked) {
+#pragma unroll
+        for (int e = 0; e < 32; ++e)
+            if (back + e > 0 || (a.window > 0 && -(back + e) >= a.window)) s[e] = __float_as_uint(-INFINITY);
+    }
+}
+
+// The first c chunks of 32 weights of this step times f, a power of two.
+__device__ __forceinline__ void rescale_weights(uint32_t s_at, int c, float f) {
+    const __nv_bfloat162 f2 = __float2bfloat162_rn(f);
+#pragma unroll 1
+    for (int i = 0; i < c; ++i) {
+        uint32_t p[16];
+        tc::tmem_ld16(s_at + 16 * i, p);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+            const __nv_bfloat162 w = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&p[e]), f2);
+            p[e] = *reinterpret_cast<const uint32_t *>(&w);
+        }
+        tmem_st16(s_at + 16 * i, p);
+    }
+}
+
+template <int HD>
+__device__ __forceinline__ void rescale_output(uint32_t o_at, float f) {
+#pragma unroll 1
+    for (int c = 0; c < HD / 16; ++c) {
+        uint32_t o[16];
+        tc::tmem_ld16(o_at + 16 * c, o);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+        tmem_st16(o_at + 16 * c, o);
+    }
 }
 
 // Sixteen e4m3 codes as bf16, exactly (through f16 and fp32).
@@ -430,108 +513,68 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
             const float mult = a.scale * a.kv.k_scale, by0 = mult * kLog2e;
             const float slope = live && a.slopes != nullptr ? a.slopes[h] * kLog2e : 0.0f;
             const bool plain = a.softcap == 0.0f && a.slopes == nullptr && a.scale > 0.0f;
-            const bool wide_cap = a.softcap > 64.0f;
-            float m = -INFINITY, l = 0.0f;
+            float m = -INFINITY;  // the reference of the row's weights: a whole number, or no key yet
+            uint64_t sum[2] = {0, 0};  // pairs of fp32
             for (int32_t j = 0; j < steps; ++j) {
                 if (!wait(&bar.s_full[i], j & 1)) break;
                 tc::fence_after_sync();
                 const int32_t key = it.key0 + j * kKeys;
                 const bool masked = key + kKeys - 1 > pos_lo || (a.window > 0 && pos_hi - key >= a.window);
+                const bool direct = plain && !masked;
+                const float by = direct ? by0 : 1.0f;
                 uint32_t x[2][32];
-                float top = -INFINITY, by = by0;
                 tmem_ld32(s_at, x[0]);
-                if (plain && !masked) {
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        tmem_wait(x[c & 1]);
-                        tmem_ld32(s_at + (c < 3 ? 32 * (c + 1) : 0), x[(c + 1) & 1]);
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) top = fmaxf(top, __uint_as_float(x[c & 1][e]));
-                    }
-                    top *= by;
-                } else {
-                    // scores in their final form go back to tensor memory
-                    by = 1.0f;
-#pragma unroll 1
-                    for (int c = 0; c < 4; ++c) {
-                        tmem_wait(x[0]);
-                        const int32_t back = key + 32 * c - pos;
-                        if (a.softcap > 0.0f) {
-                            const float in = mult / a.softcap, cap = a.softcap * kLog2e;
-                            if (wide_cap) {
-#pragma unroll
-                                for (int e = 0; e < 32; ++e)
-                                    x[0][e] = __float_as_uint(cap * tanh_of<true>(__uint_as_float(x[0][e]) * in));
-                            } else {
-#pragma unroll
-                                for (int e = 0; e < 32; ++e)
-                                    x[0][e] = __float_as_uint(cap * tanh_of<false>(__uint_as_float(x[0][e]) * in));
-                            }
-                        } else {
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) x[0][e] = __float_as_uint(__uint_as_float(x[0][e]) * by0);
-                        }
-                        if (a.slopes != nullptr) {
-#pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                x[0][e] = __float_as_uint(__uint_as_float(x[0][e]) + slope * static_cast<float>(back + e));
-                        }
-                        if (masked) {
-#pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                if (back + e > 0 || (a.window > 0 && -(back + e) >= a.window))
-                                    x[0][e] = __float_as_uint(-INFINITY);
-                        }
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) top = fmaxf(top, __uint_as_float(x[0][e]));
-                        tmem_st32(s_at + 32 * c, x[0]);
-                        if (c < 3) tmem_ld32(s_at + 32 * (c + 1), x[0]);
-                    }
-                    tmem_wait_st();
-                    tmem_ld32(s_at, x[0]);
-                }
-                // the reference only moves when it must: then O and the sum are rescaled
-                const bool grow = top > m + kGrow || (m == -INFINITY && top > m);
-                if (__any_sync(0xffffffffu, grow)) {
-                    const float now = fmaxf(m, top);
-                    const float f = now == -INFINITY ? 1.0f : ex2(m - now);
-                    l *= f;
-                    m = now;
-                    if (j > 0) {
-#pragma unroll
-                        for (int c = 0; c < HD / 32; ++c) {
-                            tmem_wait(x[0]);  // (also the first scores, loaded ahead)
-                            tmem_ld32(o_at + 32 * c, x[1]);
-                            tmem_wait(x[1]);
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) x[1][e] = __float_as_uint(__uint_as_float(x[1][e]) * f);
-                            tmem_st32(o_at + 32 * c, x[1]);
-                        }
-                    }
-                }
-                const float ref = m == -INFINITY ? 0.0f : m;
-                float sum0 = 0.0f, sum1 = 0.0f;
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
-                    tmem_wait(x[c & 1]);
+                    uint32_t(&s)[32] = x[c & 1];
+                    tmem_wait(s);
                     if (c < 3) tmem_ld32(s_at + 32 * (c + 1), x[(c + 1) & 1]);
+                    if (!direct) finish_scores(s, a, mult, by0, slope, key + 32 * c - pos, masked);
+                    float top4[4];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        top4[q] = fmaxf(__uint_as_float(s[q]), __uint_as_float(s[4 + q]));
+#pragma unroll
+                        for (int e = 8 + q; e < 32; e += 8)
+                            top4[q] = fmaxf(fmaxf(top4[q], __uint_as_float(s[e])), __uint_as_float(s[e + 4]));
+                    }
+                    const float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3])) * by;
+                    // the reference only moves when it must; then the sum, O and this step's earlier weights follow
+                    if (__any_sync(0xffffffffu, top > m + kGrow || (m == -INFINITY && top > m))) {
+                        if (c < 3) tmem_wait(x[(c + 1) & 1]);
+                        const float now = fmaxf(m, ceilf(top));
+                        const float f = m > -INFINITY && now < INFINITY
+                                            ? (m - now < -126.0f ? 0.0f : __int_as_float((127 + static_cast<int>(m - now)) << 23))
+                                            : 1.0f;
+                        m = now;
+                        const uint64_t f2 = pack2(f, f);
+                        sum[0] = mul2(sum[0], f2);
+                        sum[1] = mul2(sum[1], f2);
+                        rescale_weights(s_at, c, f);
+                        if (j > 0) rescale_output<HD>(o_at, f);
+                    }
+                    const float ref = m == -INFINITY ? 0.0f : -m;
+                    const uint64_t by2 = pack2(by, by), ref2 = pack2(ref, ref);
                     uint32_t p[16];
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
-                        const float p0 = ex2(fmaf(__uint_as_float(x[c & 1][2 * e]), by, -ref));
-                        const float p1 = ex2(fmaf(__uint_as_float(x[c & 1][2 * e + 1]), by, -ref));
-                        sum0 += p0;
-                        sum1 += p1;
+                        float p0, p1;
+                        unpack2(fma2(pack2(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1])), by2, ref2), p0, p1);
+                        p0 = ex2(p0);
+                        p1 = ex2(p1);
+                        sum[e & 1] = add2(sum[e & 1], pack2(p0, p1));
                         p[e] = pack_bf16x2(p0, p1);
                     }
                     tmem_st16(s_at + 16 * c, p);
                 }
-                l += sum0 + sum1;
                 tmem_wait_st();
                 tc::fence_before_sync();
                 __syncwarp();
                 if (lane == 0) tc::mbar_arrive(&bar.p_full[i]);
             }
+            float l, l1;
+            unpack2(add2(sum[0], sum[1]), l, l1);
+            l += l1;
             if (fine && wait(&bar.o_full[i], 0)) {
                 tc::fence_after_sync();
                 const float inv = l > 0.0f ? a.kv.v_scale / l : l == 0.0f ? 0.0f : l;
