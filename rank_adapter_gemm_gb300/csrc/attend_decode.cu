@@ -32,7 +32,7 @@
 
 #include <cuda_fp16.h>
 
-#include "attention.cuh"
+#include "attend.cuh"
 #include "tc.cuh"
 
 namespace lora {
@@ -41,9 +41,6 @@ namespace {
 
 constexpr int kMaxGrid = 160;
 constexpr int kSmemMax = 227 * 1024;
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
-
 constexpr int kWarps = 8;
 constexpr int kPrefixMax = ((LORA_MAX_SEQS + 1) * 4 + 127) & ~127;  // the requests' step prefix
 
@@ -65,22 +62,6 @@ struct Config {
     static constexpr int kWarpB = kQBytes + kTiles * kTileB;
     static_assert(kTiles >= 2 && kPartial * 4 <= kWarpB, "ring");
 };
-
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
-// tanh to 2^-22 absolutely; NEAR: also relatively, by the series near zero.
-template <bool NEAR>
-__device__ __forceinline__ float tanh_of(float z) {
-    const float far = 1.0f - __fdividef(2.0f, ex2(z * (2.0f * kLog2e)) + 1.0f);
-    if constexpr (!NEAR) return far;
-    const float z2 = z * z;
-    const float near = z * (1.0f + z2 * (-0.33333333f + z2 * (0.13333333f + z2 * (-0.05396825f))));
-    return fabsf(z) < 0.25f ? near : far;
-}
 
 __device__ __forceinline__ void mma_f16_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                               uint32_t b0, uint32_t b1) {
@@ -508,8 +489,6 @@ attend_decode_kernel(const AttendArgs a, float *parts, int32_t *counters, int pr
 
     uint32_t hi[MB][KB][4], lo[MB][KB][4];
     const int mat = lane >> 3, r8 = lane & 7;
-    // a capped score is off by softcap * 2^-22: above 64 that asks for the series near zero
-    const bool wide_cap = a.softcap > 64.0f;
     const bool plain = a.softcap == 0.0f && a.slopes == nullptr && a.scale > 0.0f;
     // weights p = 2^(score log2 e - maximum) of the step's keys, as the fragments of the second product
     const auto scores = [&](int slot) {
@@ -554,38 +533,15 @@ attend_decode_kernel(const AttendArgs a, float *parts, int32_t *counters, int pr
                     for (int t = 0; t < ST; ++t) top = fmaxf(top, fmaxf(s[mb][t][2 * i], s[mb][t][2 * i + 1]));
                     top *= by;
                 } else {
-                    if (a.softcap > 0.0f) {
-                        const float in = mult[mb][i] / a.softcap;
+                    float f[2 * ST];
 #pragma unroll
-                        for (int t = 0; t < ST; ++t)
+                    for (int t = 0; t < ST; ++t) f[2 * t] = s[mb][t][2 * i], f[2 * t + 1] = s[mb][t][2 * i + 1];
+                    finish_scores<2 * ST, 8>(f, a, mult[mb][i], slope[mb][i], ckey + 2 * c4 - pos[mb][i], masked);
 #pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                float &x = s[mb][t][2 * i + e];
-                                x = a.softcap * kLog2e * (wide_cap ? tanh_of<true>(x * in) : tanh_of<false>(x * in));
-                            }
-                    } else {
-#pragma unroll
-                        for (int t = 0; t < ST; ++t) s[mb][t][2 * i] *= by, s[mb][t][2 * i + 1] *= by;
+                    for (int t = 0; t < ST; ++t) {
+                        s[mb][t][2 * i] = f[2 * t], s[mb][t][2 * i + 1] = f[2 * t + 1];
+                        top = fmaxf(top, fmaxf(f[2 * t], f[2 * t + 1]));
                     }
-                    const int32_t back = ckey + 2 * c4 - pos[mb][i];  // of this lane's first key
-                    if (a.slopes != nullptr) {
-#pragma unroll
-                        for (int t = 0; t < ST; ++t) {
-                            s[mb][t][2 * i] += slope[mb][i] * static_cast<float>(back + 8 * t);
-                            s[mb][t][2 * i + 1] += slope[mb][i] * static_cast<float>(back + 8 * t + 1);
-                        }
-                    }
-                    if (masked) {
-#pragma unroll
-                        for (int t = 0; t < ST; ++t)
-#pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                const int32_t b = back + 8 * t + e;
-                                if (b > 0 || (a.window > 0 && -b >= a.window)) s[mb][t][2 * i + e] = -INFINITY;
-                            }
-                    }
-#pragma unroll
-                    for (int t = 0; t < ST; ++t) top = fmaxf(top, fmaxf(s[mb][t][2 * i], s[mb][t][2 * i + 1]));
                     by = 1.0f;
                 }
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));

@@ -9,27 +9,24 @@
 // all heads of its group.
 //
 //   warps 0-3, 4-7   softmax of tile 0 and 1, one row a thread: the row of S from
-//                    tensor memory in chunks of 32, each weight once it is known
-//                    not to pass 2^8: the reference of a row's weights is a whole
-//                    power of two that moves, and the sum, O and the step's earlier
-//                    weights with it (exactly), only when a chunk's maximum passes
-//                    2^8 times it.  So a score is read once, no chunk waits for the
-//                    row's maximum, and most steps never touch O.  Weights go back
-//                    into S's place as the left operand of the second product.
+//                    tensor memory into registers, weights back into S's place
+//                    as the left operand of the second product, in halves that
+//                    it starts on at once.  Weights are taken against a reference
+//                    that moves, and the sum and O with it, only when a step's
+//                    maximum passes 2^8 times it: most steps never touch O.
 //   warps 8-11       copy q rows and k and v tiles of 128 keys, key by key through
 //                    the block table, into the swizzled layout that the tensor
 //                    cores read (e4m3 codes are widened to bf16, exactly, on the way)
-//   warp 12          one thread issues the products
+//   warps 12-15      one thread issues the products
 // k and v tiles share one ring; every wait is bounded (2 s) and reports
 // LORA_ERR_TIMEOUT.  Blocks take the (request, row tile, key head) items with the
 // most keys of a request first.
 //
 // Weights are rounded to bf16 for the second product (the cache's type: the
 // instruction takes one type for both operands); sums use them unrounded.
-#include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
-#include "attention.cuh"
+#include "attend.cuh"
 #include "tc.cuh"
 
 namespace lora {
@@ -37,10 +34,12 @@ namespace lora {
 namespace {
 
 constexpr int kRows = 128, kKeys = 128;    // a tile
-constexpr int kThreads = 13 * 32;
+constexpr int kThreads = 16 * 32;
+// Registers a thread: 128 at launch, then by role.  The four warpgroups' shares
+// (two of softmax, copies, products) add up to the launch's 4 x 128.
+constexpr int kSoftmaxRegs = 192, kCopyRegs = 64, kMmaRegs = 64;
+static_assert(2 * kSoftmaxRegs + kCopyRegs + kMmaRegs == 4 * 128, "registers of the block");
 constexpr uint64_t kWaitNs = 2000000000ull;
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kGrow = 8.0f;              // log2 by which a row's maximum may grow before O is rescaled
 
 template <int HD>
@@ -52,14 +51,8 @@ struct PromptConfig {
 };
 
 struct Barriers {
-    uint64_t q_full, full[8], empty[8], s_full[2], p_full[2], o_full[2], done;
+    uint64_t q_full, full[8], empty[8], s_full[2], p_full[2][2], o_full[2], done;
 };
-
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 
 // Shared-memory matrix descriptor, 128-byte swizzle: 64 elements of the
 // contiguous dimension a row, 8 rows (1024 bytes) a group `sbo` apart, and for
@@ -69,6 +62,13 @@ __device__ __forceinline__ uint64_t desc128(uint32_t saddr, uint32_t lbo, uint32
     return static_cast<uint64_t>((saddr >> 4) & 0x3FFF) | (static_cast<uint64_t>((lbo >> 4) & 0x3FFF) << 16) |
            (static_cast<uint64_t>((sbo >> 4) & 0x3FFF) << 32) | (static_cast<uint64_t>(1) << 46) |
            (static_cast<uint64_t>(tc::kLayoutSW128) << 61);
+}
+
+// Whole warpgroup: registers a thread from here on.
+template <int N, bool MORE>
+__device__ __forceinline__ void set_registers() {
+    if constexpr (MORE) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(N));
+    else asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(N));
 }
 
 // D[tmem] (+)= A[tmem] * B[smem], issued by one thread.
@@ -107,91 +107,6 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
 }
 
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-
-// tanh to 2^-22 absolutely; NEAR: also relatively, by the series near zero.
-template <bool NEAR>
-__device__ __forceinline__ float tanh_of(float z) {
-    const float far = 1.0f - __fdividef(2.0f, ex2(z * (2.0f * kLog2e)) + 1.0f);
-    if constexpr (!NEAR) return far;
-    const float z2 = z * z;
-    const float near = z * (1.0f + z2 * (-0.33333333f + z2 * (0.13333333f + z2 * (-0.05396825f))));
-    return fabsf(z) < 0.25f ? near : far;
-}
-
-// Two fp32 in a 64-bit register, for the packed fp32 instructions.
-__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-    return r;
-}
-
-__device__ __forceinline__ void unpack2(uint64_t v, float &lo, float &hi) {
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
-}
-
-__device__ __forceinline__ uint64_t fma2(uint64_t x, uint64_t y, uint64_t z) {
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(x), "l"(y), "l"(z));
-    return r;
-}
-
-__device__ __forceinline__ uint64_t mul2(uint64_t x, uint64_t y) {
-    uint64_t r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
-    return r;
-}
-
-__device__ __forceinline__ uint64_t add2(uint64_t x, uint64_t y) {
-    uint64_t r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
-    return r;
-}
-
-// 32 products of a row in their final form, times log2 e: scaled, capped,
-// biased and masked.  back: the first one's key minus the row's position.
-__device__ __forceinline__ void finish_scores(uint32_t (&s)[32], const AttendArgs &a, float mult, float by, float slope,
-                                              int32_t back, bool masked) {
-    if (a.softcap > 0.0f) {
-        // a capped score is off by softcap * 2^-22: above 64 that asks for the series near zero
-        const float in = mult / a.softcap, cap = a.softcap * kLog2e;
-        if (a.softcap > 64.0f) {
-#pragma unroll
-            for (int e = 0; e < 32; ++e) s[e] = __float_as_uint(cap * tanh_of<true>(__uint_as_float(s[e]) * in));
-        } else {
-#pragma unroll
-            for (int e = 0; e < 32; ++e) s[e] = __float_as_uint(cap * tanh_of<false>(__uint_as_float(s[e]) * in));
-        }
-    } else {
-#pragma unroll
-        for (int e = 0; e < 32; ++e) s[e] = __float_as_uint(__uint_as_float(s[e]) * by);
-    }
-    if (a.slopes != nullptr) {
-#pragma unroll
-        for (int e = 0; e < 32; ++e)
-            s[e] = __float_as_uint(fmaf(slope, static_cast<float>(back + e), __uint_as_float(s[e])));
-    }
-    if (masked) {
-#pragma unroll
-        for (int e = 0; e < 32; ++e)
-            if (back + e > 0 || (a.window > 0 && -(back + e) >= a.window)) s[e] = __float_as_uint(-INFINITY);
-    }
-}
-
-// The first c chunks of 32 weights of this step times f, a power of two.
-__device__ __forceinline__ void rescale_weights(uint32_t s_at, int c, float f) {
-    const __nv_bfloat162 f2 = __float2bfloat162_rn(f);
-#pragma unroll 1
-    for (int i = 0; i < c; ++i) {
-        uint32_t p[16];
-        tc::tmem_ld16(s_at + 16 * i, p);
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-            const __nv_bfloat162 w = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&p[e]), f2);
-            p[e] = *reinterpret_cast<const uint32_t *>(&w);
-        }
-        tmem_st16(s_at + 16 * i, p);
-    }
-}
 
 template <int HD>
 __device__ __forceinline__ void rescale_output(uint32_t o_at, float f) {
@@ -244,7 +159,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
     extern __shared__ unsigned char smem_raw[];
     __shared__ Barriers bar;
     __shared__ Item s_item;
-    __shared__ int64_t s_warp[13];
+    __shared__ int64_t s_warp[kThreads / 32];
     __shared__ uint32_t s_tmem;
     __shared__ volatile int32_t s_abort;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -278,7 +193,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
         __syncthreads();
         int64_t run = incl - mine, total = 0;
 #pragma unroll
-        for (int w = 0; w < 13; ++w) {
+        for (int w = 0; w < kThreads / 32; ++w) {
             if (w < warp) run += s_warp[w];
             total += s_warp[w];
         }
@@ -314,7 +229,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
         }
         for (int i = 0; i < 2; ++i) {
             tc::mbar_init(&bar.s_full[i], 1);
-            tc::mbar_init(&bar.p_full[i], 4);
+            tc::mbar_init(&bar.p_full[i][0], 4);
+            tc::mbar_init(&bar.p_full[i][1], 4);
             tc::mbar_init(&bar.o_full[i], 1);
         }
         tc::mbar_init(&bar.done, 1);
@@ -347,22 +263,28 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
     };
 
     if (warp >= 8 && warp < 12) {
+        set_registers<kCopyRegs, false>();
         // ---- copies ---------------------------------------------------------------------
         const int w = warp - 8;
         constexpr int kPieces = HD / 8;  // 16-byte pieces of a bf16 row
-        {
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            // 32 rows: a lane's row's offset, then a few rows a copy instruction
             constexpr int kStep = 32 / kPieces;
-            const int piece = lane % kPieces;
-            for (int r = w * 64 + lane / kPieces; r < w * 64 + 64; r += kStep) {
-                const int32_t row = it.row0 + r;
-                const bool live = r < it.rows;
-                const int64_t t = it.q0 + (live ? row / a.group : 0);
-                const int32_t h = it.head * a.group + (live ? row % a.group : 0);
+            const int piece = lane % kPieces, r0 = w * 64 + half * 32;
+            const int32_t row = it.row0 + r0 + lane;
+            int64_t at = -1;
+            if (r0 + lane < it.rows)
+                at = (it.q0 + row / a.group) * a.ldq + (it.head * a.group + row % a.group) * HD;
+#pragma unroll
+            for (int i = 0; i < kPieces; ++i) {
+                const int r = r0 + i * kStep + lane / kPieces;
+                const int64_t o = __shfl_sync(0xffffffffu, at, i * kStep + lane / kPieces);
                 tc::cp16(q_base + (r / kRows) * C::kTileB + tile_at(r % kRows, piece),
-                         a.q + t * a.ldq + h * HD + piece * 8, live);
+                         a.q + (o >= 0 ? o : 0) + piece * 8, o >= 0);
             }
-            tc::cp_commit();
         }
+        tc::cp_commit();
         const int32_t *table = a.table + it.seq * a.ld_table;
         const int32_t end = min(it.len, it.key1);
         // the byte offset of this lane's key of a step, -1: none
@@ -449,27 +371,34 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
             }
             tc::cp_wait_all();
         }
-    } else if (warp == 12) {
+    } else if (warp >= 12) {
+        set_registers<kMmaRegs, false>();
         // ---- products -------------------------------------------------------------------
-        if (lane == 0) {
+        if (warp == 12 && lane == 0) {
             constexpr uint32_t kS = tc::idesc_bf16(kRows, kKeys);
             constexpr uint32_t kO = tc::idesc_bf16(kRows, HD) | (1u << 16);  // v: keys are the strided dimension
             const auto full = [&](int32_t u) { return wait(&bar.full[u % C::kSlots], (u / C::kSlots) & 1); };
+            // descriptors are a tile's plus a constant: addresses stay below 2^18, so nothing carries
+            const uint64_t q_desc = desc128(q_base, 16, 1024), k_desc = desc128(ring, 16, 1024);
+            const uint64_t v_desc = desc128(ring, C::kHalfB, 1024);
             const auto scores = [&](int i, int32_t u) {
-                const uint32_t q = q_base + i * C::kTileB, k = ring + (u % C::kSlots) * C::kTileB;
+                const uint64_t q = q_desc + ((i * C::kTileB) >> 4), k = k_desc + (((u % C::kSlots) * C::kTileB) >> 4);
 #pragma unroll
                 for (int kk = 0; kk < HD / 16; ++kk) {
-                    const uint32_t off = (kk / 4) * C::kHalfB + (kk % 4) * 32;
-                    tc::mma_bf16(tmem + i * kKeys, desc128(q + off, 16, 1024), desc128(k + off, 16, 1024), kS, kk > 0);
+                    const uint32_t off = ((kk / 4) * C::kHalfB + (kk % 4) * 32) >> 4;
+                    tc::mma_bf16(tmem + i * kKeys, q + off, k + off, kS, kk > 0);
                 }
                 tc::mma_commit(&bar.s_full[i]);
             };
-            const auto outputs = [&](int i, int32_t u, bool first) {
-                const uint32_t v = ring + (u % C::kSlots) * C::kTileB;
+            // half of a step's keys, as soon as their weights are there
+            const auto outputs = [&](int i, int32_t u, int half, bool first) {
+                const uint64_t v = v_desc + (((u % C::kSlots) * C::kTileB) >> 4);
 #pragma unroll
-                for (int ks = 0; ks < kKeys / 16; ++ks)
-                    mma_bf16_ts(tmem + 2 * kKeys + i * 128, tmem + i * kKeys + ks * 8,
-                                desc128(v + ks * 2048, C::kHalfB, 1024), kO, !first || ks > 0);
+                for (int ks = 0; ks < kKeys / 32; ++ks) {
+                    const int k16 = half * (kKeys / 32) + ks;
+                    mma_bf16_ts(tmem + 2 * kKeys + i * 128, tmem + i * kKeys + k16 * 8, v + ((k16 * 2048) >> 4), kO,
+                                !first || k16 > 0);
+                }
             };
             if (wait(&bar.q_full, 0) && full(0)) {
                 tc::fence_after_sync();
@@ -478,10 +407,13 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
             }
             for (int32_t j = 0; j < steps && fine; ++j) {
                 for (int i = 0; i < n_tiles && fine; ++i) {
-                    if (!wait(&bar.p_full[i], j & 1)) break;
                     if (i == 0 && !full(2 * j + 1)) break;
+                    if (!wait(&bar.p_full[i][0], j & 1)) break;
                     tc::fence_after_sync();
-                    outputs(i, 2 * j + 1, j == 0);
+                    outputs(i, 2 * j + 1, 0, j == 0);
+                    if (!wait(&bar.p_full[i][1], j & 1)) break;
+                    tc::fence_after_sync();
+                    outputs(i, 2 * j + 1, 1, j == 0);
                     if (j + 1 == steps) tc::mma_commit(&bar.o_full[i]);
                     if (i == n_tiles - 1) tc::mma_commit(&bar.empty[(2 * j + 1) % C::kSlots]);
                     if (j + 1 < steps) {
@@ -498,6 +430,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
         }
         fine = __all_sync(0xffffffffu, fine);
     } else {
+        set_registers<kSoftmaxRegs, true>();
         // ---- softmax --------------------------------------------------------------------
         const int i = warp >> 2;
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
@@ -513,8 +446,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
             const float mult = a.scale * a.kv.k_scale, by0 = mult * kLog2e;
             const float slope = live && a.slopes != nullptr ? a.slopes[h] * kLog2e : 0.0f;
             const bool plain = a.softcap == 0.0f && a.slopes == nullptr && a.scale > 0.0f;
-            float m = -INFINITY;  // the reference of the row's weights: a whole number, or no key yet
-            uint64_t sum[2] = {0, 0};  // pairs of fp32
+            float m = -INFINITY;  // the reference of the row's weights
+            uint64_t sum[4] = {0, 0, 0, 0};  // pairs of fp32
             for (int32_t j = 0; j < steps; ++j) {
                 if (!wait(&bar.s_full[i], j & 1)) break;
                 tc::fence_after_sync();
@@ -522,58 +455,66 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
                 const bool masked = key + kKeys - 1 > pos_lo || (a.window > 0 && pos_hi - key >= a.window);
                 const bool direct = plain && !masked;
                 const float by = direct ? by0 : 1.0f;
-                uint32_t x[2][32];
-                tmem_ld32(s_at, x[0]);
+                uint32_t x[4][32];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) tmem_ld32(s_at + 32 * c, x[c]);
+                float top8[8];
+#pragma unroll
+                for (int q = 0; q < 8; ++q) top8[q] = -INFINITY;
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
-                    uint32_t(&s)[32] = x[c & 1];
-                    tmem_wait(s);
-                    if (c < 3) tmem_ld32(s_at + 32 * (c + 1), x[(c + 1) & 1]);
-                    if (!direct) finish_scores(s, a, mult, by0, slope, key + 32 * c - pos, masked);
-                    float top4[4];
+                    tmem_wait(x[c]);
+                    if (!direct) {
+                        float s[32];
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        top4[q] = fmaxf(__uint_as_float(s[q]), __uint_as_float(s[4 + q]));
+                        for (int e = 0; e < 32; ++e) s[e] = __uint_as_float(x[c][e]);
+                        finish_scores<32, 2>(s, a, mult, slope, key + 32 * c - pos, masked);
 #pragma unroll
-                        for (int e = 8 + q; e < 32; e += 8)
-                            top4[q] = fmaxf(fmaxf(top4[q], __uint_as_float(s[e])), __uint_as_float(s[e + 4]));
+                        for (int e = 0; e < 32; ++e) x[c][e] = __float_as_uint(s[e]);
                     }
-                    const float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3])) * by;
-                    // the reference only moves when it must; then the sum, O and this step's earlier weights follow
-                    if (__any_sync(0xffffffffu, top > m + kGrow || (m == -INFINITY && top > m))) {
-                        if (c < 3) tmem_wait(x[(c + 1) & 1]);
-                        const float now = fmaxf(m, ceilf(top));
-                        const float f = m > -INFINITY && now < INFINITY
-                                            ? (m - now < -126.0f ? 0.0f : __int_as_float((127 + static_cast<int>(m - now)) << 23))
-                                            : 1.0f;
-                        m = now;
-                        const uint64_t f2 = pack2(f, f);
-                        sum[0] = mul2(sum[0], f2);
-                        sum[1] = mul2(sum[1], f2);
-                        rescale_weights(s_at, c, f);
-                        if (j > 0) rescale_output<HD>(o_at, f);
-                    }
-                    const float ref = m == -INFINITY ? 0.0f : -m;
-                    const uint64_t by2 = pack2(by, by), ref2 = pack2(ref, ref);
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2)
+                        top8[(e / 2) & 7] = fmaxf(fmaxf(top8[(e / 2) & 7], __uint_as_float(x[c][e])),
+                                                  __uint_as_float(x[c][e + 1]));
+                }
+#pragma unroll
+                for (int q = 0; q < 4; ++q) top8[q] = fmaxf(top8[q], top8[q + 4]);
+                const float top = fmaxf(fmaxf(top8[0], top8[1]), fmaxf(top8[2], top8[3])) * by;
+                // the reference only moves when it must; then the sum and O follow
+                if (__any_sync(0xffffffffu, top > m + kGrow || (m == -INFINITY && top > m))) {
+                    const float now = fmaxf(m, top), f = now == -INFINITY ? 1.0f : ex2(m - now);
+                    m = now;
+                    const uint64_t f2 = pack2(f, f);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) sum[q] = mul2(sum[q], f2);
+                    if (j > 0) rescale_output<HD>(o_at, f);
+                }
+                const float ref = m == -INFINITY ? 0.0f : -m;
+                const uint64_t by2 = pack2(by, by), ref2 = pack2(ref, ref);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
                     uint32_t p[16];
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
                         float p0, p1;
-                        unpack2(fma2(pack2(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1])), by2, ref2), p0, p1);
+                        unpack2(fma2(pack2(__uint_as_float(x[c][2 * e]), __uint_as_float(x[c][2 * e + 1])), by2, ref2),
+                                p0, p1);
                         p0 = ex2(p0);
                         p1 = ex2(p1);
-                        sum[e & 1] = add2(sum[e & 1], pack2(p0, p1));
+                        sum[e & 3] = add2(sum[e & 3], pack2(p0, p1));
                         p[e] = pack_bf16x2(p0, p1);
                     }
                     tmem_st16(s_at + 16 * c, p);
+                    if (c & 1) {  // half of the step's weights
+                        tmem_wait_st();
+                        tc::fence_before_sync();
+                        __syncwarp();
+                        if (lane == 0) tc::mbar_arrive(&bar.p_full[i][c >> 1]);
+                    }
                 }
-                tmem_wait_st();
-                tc::fence_before_sync();
-                __syncwarp();
-                if (lane == 0) tc::mbar_arrive(&bar.p_full[i]);
             }
             float l, l1;
-            unpack2(add2(sum[0], sum[1]), l, l1);
+            unpack2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), l, l1);
             l += l1;
             if (fine && wait(&bar.o_full[i], 0)) {
                 tc::fence_after_sync();
