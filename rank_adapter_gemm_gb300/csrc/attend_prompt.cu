@@ -458,13 +458,11 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
                 uint32_t x[4][32];
 #pragma unroll
                 for (int c = 0; c < 4; ++c) tmem_ld32(s_at + 32 * c, x[c]);
-                float top8[8];
 #pragma unroll
-                for (int q = 0; q < 8; ++q) top8[q] = -INFINITY;
+                for (int c = 0; c < 4; ++c) tmem_wait(x[c]);
+                if (!direct) {
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    tmem_wait(x[c]);
-                    if (!direct) {
+                    for (int c = 0; c < 4; ++c) {
                         float s[32];
 #pragma unroll
                         for (int e = 0; e < 32; ++e) s[e] = __uint_as_float(x[c][e]);
@@ -472,10 +470,15 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
 #pragma unroll
                         for (int e = 0; e < 32; ++e) x[c][e] = __float_as_uint(s[e]);
                     }
+                }
+                float top8[8];
 #pragma unroll
-                    for (int e = 0; e < 32; e += 2)
-                        top8[(e / 2) & 7] = fmaxf(fmaxf(top8[(e / 2) & 7], __uint_as_float(x[c][e])),
-                                                  __uint_as_float(x[c][e + 1]));
+                for (int q = 0; q < 8; ++q) {
+                    top8[q] = fmaxf(__uint_as_float(x[0][2 * q]), __uint_as_float(x[0][2 * q + 1]));
+#pragma unroll
+                    for (int e = 16 + 2 * q; e < 128; e += 16)
+                        top8[q] = fmaxf(fmaxf(top8[q], __uint_as_float(x[e / 32][e % 32])),
+                                        __uint_as_float(x[e / 32][e % 32 + 1]));
                 }
 #pragma unroll
                 for (int q = 0; q < 4; ++q) top8[q] = fmaxf(top8[q], top8[q + 4]);
