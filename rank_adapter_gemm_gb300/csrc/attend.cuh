@@ -43,64 +43,71 @@ __device__ __forceinline__ uint64_t add2(uint64_t x, uint64_t y) {
     return r;
 }
 
-// tanh of two numbers up to 1 in size, times `scale`: z (1 + z^2 (c1 + z^2 (c2 + ...))),
-// the coefficients a minimax fit on [-1, 1]: within 2^-24 of tanh, and relatively so.
-// Scores are seldom larger than the cap, and packed products cost a third of
-// the exponential and the reciprocal that the general form needs.
-__device__ __forceinline__ uint64_t tanh2_near(uint64_t z, uint64_t scale) {
-    const uint64_t w = mul2(z, z);
-    uint64_t r = pack2(0.0010059071f, 0.0010059071f);
-    r = fma2(r, w, pack2(-0.0060955156f, -0.0060955156f));
-    r = fma2(r, w, pack2(0.020165906f, 0.020165906f));
-    r = fma2(r, w, pack2(-0.05339197f, -0.05339197f));
-    r = fma2(r, w, pack2(0.13323739f, 0.13323739f));
-    r = fma2(r, w, pack2(-0.33332753f, -0.33332753f));
-    r = fma2(r, w, pack2(1.0f, 1.0f));
-    return mul2(mul2(z, scale), r);
-}
+// tanh z = z (1 + c1 z^2 + ... + c5 z^10) to 2^-21 for |z| <= 1 (a minimax fit with
+// the first coefficient held at 1, so that small z keep their relative accuracy
+// too).  Scores are seldom larger than the cap, and the polynomial costs a third
+// of the exponential and the reciprocal that the general form needs.
+#define LORA_TANH_COEFFICIENTS {1.0f, -0.3332867f, 0.13275616f, -0.05142535f, 0.016532812f, -0.002983080f}
 
-// tanh of any number to 2^-22: good relatively too for |z| >= 1/2.
+// tanh of any number to 2^-22.
 __device__ __forceinline__ float tanh_far(float z) {
     return 1.0f - __fdividef(2.0f, ex2(z * (2.0f * kLog2e)) + 1.0f);
 }
 
-// N products s in their final form, times log2 e, in fp32: scaled, capped,
-// biased by distance, masked.  back: first one's key minus the row's position;
-// consecutive pairs lie STEP keys apart.  by = mult * log2 e, slope alike.
-// Called by whole warps.
+// N products s in their final form, times log2 e, in fp32: scaled by mult, capped,
+// biased by distance (slope: times log2 e), masked.  back: the first one's key minus
+// the row's position; consecutive pairs lie STEP keys apart.  Called by whole warps.
 template <int N, int STEP>
 __device__ __forceinline__ void finish_scores(float (&s)[N], const AttendArgs &a, float mult, float slope, int32_t back,
                                               bool masked) {
-    if (a.softcap > 0.0f) {
-        const float in = mult / a.softcap, cap = a.softcap * kLog2e;
+    constexpr float kTanh[6] = LORA_TANH_COEFFICIENTS;
+    const uint64_t slope2 = pack2(slope, slope), at2 = pack2(slope * back, slope * back);
+    const float by = mult * kLog2e;
+    bool near = a.softcap > 0.0f;
+    if (near) {
         float top = 0.0f;
 #pragma unroll
-        for (int e = 0; e < N; ++e) top = fmaxf(top, fabsf(s[e]));
-        if (__any_sync(0xffffffffu, !(top * fabsf(in) <= 1.0f))) {
+        for (int e = 0; e < N; e += 2) top = fmaxf(fmaxf(top, fabsf(s[e])), fabsf(s[e + 1]));
+        near = __all_sync(0xffffffffu, top * fabsf(mult) <= a.softcap);
+        if (!near) {
+            const float in = mult / a.softcap, cap = a.softcap * kLog2e;
 #pragma unroll
             for (int e = 0; e < N; ++e) {
-                float near, other;
-                unpack2(tanh2_near(pack2(s[e] * in, 0.0f), pack2(cap, cap)), near, other);
-                s[e] = fabsf(s[e] * in) < 0.75f ? near : cap * tanh_far(s[e] * in);
+                const float z = s[e] * in, w = z * z;
+                const float poly = z * (1.0f + w * (kTanh[1] + w * (kTanh[2] + w * (kTanh[3] + w * (kTanh[4] +
+                                                                                                     w * kTanh[5])))));
+                s[e] = cap * (fabsf(z) <= 1.0f ? poly : tanh_far(z));
             }
-        } else {
-            const uint64_t in2 = pack2(in, in), cap2 = pack2(cap, cap);
+        }
+    }
+    if (near) {
+        // by s + by c1 in^2 s^3 + ...: the scales are in the coefficients
+        const float in = mult / a.softcap, in2 = in * in;
+        float c = by;
+        uint64_t k[6];
 #pragma unroll
-            for (int e = 0; e < N; e += 2)
-                unpack2(tanh2_near(mul2(pack2(s[e], s[e + 1]), in2), cap2), s[e], s[e + 1]);
+        for (int i = 0; i < 6; ++i, c *= in2) k[i] = pack2(c * kTanh[i], c * kTanh[i]);
+#pragma unroll
+        for (int e = 0; e < N; e += 2) {
+            const uint64_t x = pack2(s[e], s[e + 1]), w = mul2(x, x);
+            uint64_t r = fma2(k[5], w, k[4]);
+#pragma unroll
+            for (int i = 3; i >= 0; --i) r = fma2(r, w, k[i]);
+            if (a.slopes != nullptr) {
+                const float d = static_cast<float>(e / 2 * STEP);
+                r = fma2(x, r, fma2(slope2, pack2(d, d + 1.0f), at2));
+            } else {
+                r = mul2(x, r);
+            }
+            unpack2(r, s[e], s[e + 1]);
         }
     } else {
-        const uint64_t by2 = pack2(mult * kLog2e, mult * kLog2e);
-#pragma unroll
-        for (int e = 0; e < N; e += 2) unpack2(mul2(pack2(s[e], s[e + 1]), by2), s[e], s[e + 1]);
-    }
-    if (a.slopes != nullptr) {
-        const float at = slope * static_cast<float>(back);
-        const uint64_t at2 = pack2(at, at), slope2 = pack2(slope, slope);
+        const float scale = a.softcap > 0.0f ? 1.0f : by;
+        const uint64_t scale2 = pack2(scale, scale);
 #pragma unroll
         for (int e = 0; e < N; e += 2) {
             const float d = static_cast<float>(e / 2 * STEP);
-            unpack2(add2(pack2(s[e], s[e + 1]), fma2(slope2, pack2(d, d + 1.0f), at2)), s[e], s[e + 1]);
+            unpack2(fma2(pack2(s[e], s[e + 1]), scale2, fma2(slope2, pack2(d, d + 1.0f), at2)), s[e], s[e + 1]);
         }
     }
     if (masked) {

@@ -37,7 +37,7 @@ constexpr int kRows = 128, kKeys = 128;    // a tile
 constexpr int kThreads = 16 * 32;
 // Registers a thread: 128 at launch, then by role.  The four warpgroups' shares
 // (two of softmax, copies, products) add up to the launch's 4 x 128.
-constexpr int kSoftmaxRegs = 192, kCopyRegs = 64, kMmaRegs = 64;
+constexpr int kSoftmaxRegs = 200, kCopyRegs = 56, kMmaRegs = 56;
 static_assert(2 * kSoftmaxRegs + kCopyRegs + kMmaRegs == 4 * 128, "registers of the block");
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr float kGrow = 8.0f;              // log2 by which a row's maximum may grow before O is rescaled
@@ -92,6 +92,23 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
         "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
         "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
         : LORA_W8(r, 0), LORA_W8(r, 8), LORA_W8(r, 16), LORA_W8(r, 24) : "r"(taddr));
+}
+
+// Whole warp: 64 columns of the warp's lanes into r[0..63], without waiting.
+__device__ __forceinline__ void tmem_ld64(uint32_t taddr, uint32_t *r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%64];"
+        : LORA_W8(r, 0), LORA_W8(r, 8), LORA_W8(r, 16), LORA_W8(r, 24), LORA_W8(r, 32), LORA_W8(r, 40), LORA_W8(r, 48),
+          LORA_W8(r, 56)
+        : "r"(taddr));
+}
+
+__device__ __forceinline__ void tmem_wait128(uint32_t (&r)[128]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : LORA_R8(r, 0), LORA_R8(r, 8), LORA_R8(r, 16), LORA_R8(r, 24), LORA_R8(r, 32), LORA_R8(r, 40),
+                   LORA_R8(r, 48), LORA_R8(r, 56), LORA_R8(r, 64), LORA_R8(r, 72), LORA_R8(r, 80), LORA_R8(r, 88),
+                   LORA_R8(r, 96), LORA_R8(r, 104), LORA_R8(r, 112), LORA_R8(r, 120)
+                 : : "memory");
 }
 
 // Waits for this thread's loads; names the registers they fill.
@@ -436,10 +453,17 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t s_at = tmem + lanes + i * kKeys, o_at = tmem + lanes + 2 * kKeys + i * 128;
         if (i < n_tiles) {
-            const int32_t r = i * kRows + (warp & 3) * 32 + lane, row = it.row0 + r;
-            const bool live = r < it.rows;
-            const int32_t token = live ? row / a.group : 0, h = it.head * a.group + (live ? row % a.group : 0);
-            const int32_t first_pos = it.len - it.n;
+            // the row's place is worked out again for the output: registers are scarce between
+            const auto place = [&](bool &live, int32_t &token, int32_t &h) {
+                const int32_t r = i * kRows + (warp & 3) * 32 + lane, row = s_item.row0 + r;
+                live = r < s_item.rows;
+                token = live ? row / a.group : 0;
+                h = s_item.head * a.group + (live ? row % a.group : 0);
+            };
+            bool live;
+            int32_t token, h;
+            place(live, token, h);
+            const int32_t first_pos = it.len - it.n, key0 = it.key0;
             const int32_t pos = live ? first_pos + token : -1;
             const int32_t pos_lo = first_pos + (it.row0 + i * kRows) / a.group;
             const int32_t pos_hi = first_pos + (it.row0 + min(it.rows, (i + 1) * kRows) - 1) / a.group;
@@ -447,38 +471,36 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
             const float slope = live && a.slopes != nullptr ? a.slopes[h] * kLog2e : 0.0f;
             const bool plain = a.softcap == 0.0f && a.slopes == nullptr && a.scale > 0.0f;
             float m = -INFINITY;  // the reference of the row's weights
-            uint64_t sum[4] = {0, 0, 0, 0};  // pairs of fp32
+            uint64_t sum[2] = {0, 0};  // pairs of fp32
             for (int32_t j = 0; j < steps; ++j) {
                 if (!wait(&bar.s_full[i], j & 1)) break;
                 tc::fence_after_sync();
-                const int32_t key = it.key0 + j * kKeys;
+                const int32_t key = key0 + j * kKeys;
                 const bool masked = key + kKeys - 1 > pos_lo || (a.window > 0 && pos_hi - key >= a.window);
                 const bool direct = plain && !masked;
                 const float by = direct ? by0 : 1.0f;
-                uint32_t x[4][32];
-#pragma unroll
-                for (int c = 0; c < 4; ++c) tmem_ld32(s_at + 32 * c, x[c]);
-#pragma unroll
-                for (int c = 0; c < 4; ++c) tmem_wait(x[c]);
+                uint32_t x[128];
+                tmem_ld64(s_at, x);
+                tmem_ld64(s_at + 64, x + 64);
+                tmem_wait128(x);
                 if (!direct) {
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
                         float s[32];
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) s[e] = __uint_as_float(x[c][e]);
+                        for (int e = 0; e < 32; ++e) s[e] = __uint_as_float(x[32 * c + e]);
                         finish_scores<32, 2>(s, a, mult, slope, key + 32 * c - pos, masked);
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) x[c][e] = __float_as_uint(s[e]);
+                        for (int e = 0; e < 32; ++e) x[32 * c + e] = __float_as_uint(s[e]);
                     }
                 }
                 float top8[8];
 #pragma unroll
                 for (int q = 0; q < 8; ++q) {
-                    top8[q] = fmaxf(__uint_as_float(x[0][2 * q]), __uint_as_float(x[0][2 * q + 1]));
+                    top8[q] = fmaxf(__uint_as_float(x[2 * q]), __uint_as_float(x[2 * q + 1]));
 #pragma unroll
                     for (int e = 16 + 2 * q; e < 128; e += 16)
-                        top8[q] = fmaxf(fmaxf(top8[q], __uint_as_float(x[e / 32][e % 32])),
-                                        __uint_as_float(x[e / 32][e % 32 + 1]));
+                        top8[q] = fmaxf(fmaxf(top8[q], __uint_as_float(x[e])), __uint_as_float(x[e + 1]));
                 }
 #pragma unroll
                 for (int q = 0; q < 4; ++q) top8[q] = fmaxf(top8[q], top8[q + 4]);
@@ -489,7 +511,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
                     m = now;
                     const uint64_t f2 = pack2(f, f);
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) sum[q] = mul2(sum[q], f2);
+                    for (int q = 0; q < 2; ++q) sum[q] = mul2(sum[q], f2);
                     if (j > 0) rescale_output<HD>(o_at, f);
                 }
                 const float ref = m == -INFINITY ? 0.0f : -m;
@@ -500,11 +522,11 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
                         float p0, p1;
-                        unpack2(fma2(pack2(__uint_as_float(x[c][2 * e]), __uint_as_float(x[c][2 * e + 1])), by2, ref2),
-                                p0, p1);
+                        const int k = 32 * c + 2 * e;
+                        unpack2(fma2(pack2(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), by2, ref2), p0, p1);
                         p0 = ex2(p0);
                         p1 = ex2(p1);
-                        sum[e & 3] = add2(sum[e & 3], pack2(p0, p1));
+                        sum[e & 1] = add2(sum[e & 1], pack2(p0, p1));
                         p[e] = pack_bf16x2(p0, p1);
                     }
                     tmem_st16(s_at + 16 * c, p);
@@ -517,12 +539,13 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
                 }
             }
             float l, l1;
-            unpack2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), l, l1);
+            unpack2(add2(sum[0], sum[1]), l, l1);
             l += l1;
             if (fine && wait(&bar.o_full[i], 0)) {
                 tc::fence_after_sync();
                 const float inv = l > 0.0f ? a.kv.v_scale / l : l == 0.0f ? 0.0f : l;
-                const int64_t t = it.q0 + token;
+                place(live, token, h);
+                const int64_t t = s_item.q0 + token;
                 uint16_t *dst = a.out + t * a.ldo + h * HD;
                 uint32_t x[32];
 #pragma unroll
