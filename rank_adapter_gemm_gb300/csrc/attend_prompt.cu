@@ -71,6 +71,13 @@ __device__ __forceinline__ void set_registers() {
     else asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(N));
 }
 
+// True in one thread of the (whole) warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t one;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
+    return one != 0;
+}
+
 // D[tmem] (+)= A[tmem] * B[smem], issued by one thread.
 __device__ __forceinline__ void mma_bf16_ts(uint32_t d, uint32_t a, uint64_t b_desc, uint32_t idesc, bool accumulate) {
     asm volatile(
@@ -391,39 +398,53 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
     } else if (warp >= 12) {
         set_registers<kMmaRegs, false>();
         // ---- products -------------------------------------------------------------------
-        if (warp == 12 && lane == 0) {
+        if (warp == 12) {
+            // The warp stays together and one elected thread issues: the products' operands
+            // then stay in uniform registers.
             constexpr uint32_t kS = tc::idesc_bf16(kRows, kKeys);
             constexpr uint32_t kO = tc::idesc_bf16(kRows, HD) | (1u << 16);  // v: keys are the strided dimension
-            const auto full = [&](int32_t u) { return wait(&bar.full[u % C::kSlots], (u / C::kSlots) & 1); };
             // descriptors are a tile's plus a constant: addresses stay below 2^18, so nothing carries
             const uint64_t q_desc = desc128(q_base, 16, 1024), k_desc = desc128(ring, 16, 1024);
             const uint64_t v_desc = desc128(ring, C::kHalfB, 1024);
-            const auto scores = [&](int i, int32_t u) {
+            const auto full = [&](int32_t u) { return wait(&bar.full[u % C::kSlots], (u / C::kSlots) & 1); };
+            const auto scores = [&](int i, int32_t u, bool last) {
                 const uint64_t q = q_desc + ((i * C::kTileB) >> 4), k = k_desc + (((u % C::kSlots) * C::kTileB) >> 4);
+                if (elect_one()) {
 #pragma unroll
-                for (int kk = 0; kk < HD / 16; ++kk) {
-                    const uint32_t off = ((kk / 4) * C::kHalfB + (kk % 4) * 32) >> 4;
-                    tc::mma_bf16(tmem + i * kKeys, q + off, k + off, kS, kk > 0);
+                    for (int kk = 0; kk < HD / 16; ++kk) {
+                        const uint32_t off = ((kk / 4) * C::kHalfB + (kk % 4) * 32) >> 4;
+                        tc::mma_bf16(tmem + i * kKeys, q + off, k + off, kS, kk > 0);
+                    }
+                    tc::mma_commit(&bar.s_full[i]);
+                    if (last) tc::mma_commit(&bar.empty[u % C::kSlots]);
                 }
-                tc::mma_commit(&bar.s_full[i]);
+                __syncwarp();
             };
             // half of a step's keys, as soon as their weights are there
             const auto outputs = [&](int i, int32_t u, int half, bool first) {
                 const uint64_t v = v_desc + (((u % C::kSlots) * C::kTileB) >> 4);
+                if (elect_one()) {
 #pragma unroll
-                for (int ks = 0; ks < kKeys / 32; ++ks) {
-                    const int k16 = half * (kKeys / 32) + ks;
-                    mma_bf16_ts(tmem + 2 * kKeys + i * 128, tmem + i * kKeys + k16 * 8, v + ((k16 * 2048) >> 4), kO,
-                                !first || k16 > 0);
+                    for (int ks = 0; ks < kKeys / 32; ++ks) {
+                        const int k16 = half * (kKeys / 32) + ks;
+                        mma_bf16_ts(tmem + 2 * kKeys + i * 128, tmem + i * kKeys + k16 * 8, v + ((k16 * 2048) >> 4),
+                                    kO, !first || k16 > 0);
+                    }
                 }
+                __syncwarp();
+            };
+            const auto commit = [&](uint64_t *b) {
+                if (elect_one()) tc::mma_commit(b);
+                __syncwarp();
             };
             if (wait(&bar.q_full, 0) && full(0)) {
                 tc::fence_after_sync();
-                for (int i = 0; i < n_tiles; ++i) scores(i, 0);
-                tc::mma_commit(&bar.empty[0]);
+                for (int i = 0; i < n_tiles; ++i) scores(i, 0, i == n_tiles - 1);
             }
             for (int32_t j = 0; j < steps && fine; ++j) {
+                const bool more = j + 1 < steps;
                 for (int i = 0; i < n_tiles && fine; ++i) {
+                    const bool last = i == n_tiles - 1;
                     if (i == 0 && !full(2 * j + 1)) break;
                     if (!wait(&bar.p_full[i][0], j & 1)) break;
                     tc::fence_after_sync();
@@ -431,18 +452,17 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
                     if (!wait(&bar.p_full[i][1], j & 1)) break;
                     tc::fence_after_sync();
                     outputs(i, 2 * j + 1, 1, j == 0);
-                    if (j + 1 == steps) tc::mma_commit(&bar.o_full[i]);
-                    if (i == n_tiles - 1) tc::mma_commit(&bar.empty[(2 * j + 1) % C::kSlots]);
-                    if (j + 1 < steps) {
+                    if (!more) commit(&bar.o_full[i]);
+                    if (last) commit(&bar.empty[(2 * j + 1) % C::kSlots]);
+                    if (more) {
                         if (i == 0 && !full(2 * j + 2)) break;
                         tc::fence_after_sync();
-                        scores(i, 2 * j + 2);
-                        if (i == n_tiles - 1) tc::mma_commit(&bar.empty[(2 * j + 2) % C::kSlots]);
+                        scores(i, 2 * j + 2, last);
                     }
                 }
             }
             // every product has finished, and every arrival landed, before the block ends
-            tc::mma_commit(&bar.done);
+            commit(&bar.done);
             if (!tc::mbar_wait_timed(&bar.done, 0, kWaitNs)) fine = false;
         }
         fine = __all_sync(0xffffffffu, fine);
