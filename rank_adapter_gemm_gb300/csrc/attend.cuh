@@ -43,11 +43,13 @@ __device__ __forceinline__ uint64_t add2(uint64_t x, uint64_t y) {
     return r;
 }
 
-// tanh z = z (1 + c1 z^2 + ... + c5 z^10) to 2^-21 for |z| <= 1 (a minimax fit with
-// the first coefficient held at 1, so that small z keep their relative accuracy
-// too).  Scores are seldom larger than the cap, and the polynomial costs a third
-// of the exponential and the reciprocal that the general form needs.
-#define LORA_TANH_COEFFICIENTS {1.0f, -0.3332867f, 0.13275616f, -0.05142535f, 0.016532812f, -0.002983080f}
+// tanh z = z (1 + c1 z^2 + c2 z^4 + ...): minimax fits with the first coefficient
+// held at 1 (so that small z keep their relative accuracy too), within 2^-22 for
+// |z| <= 1/2 and 2^-21 for |z| <= 1.  Scores seldom reach half their cap, and the
+// short polynomial costs a fifth of the exponential and the reciprocal that the
+// general form needs.
+#define LORA_TANH_HALF {1.0f, -0.33326461f, 0.13185862f, -0.04422929f}
+#define LORA_TANH_ONE {1.0f, -0.3332867f, 0.13275616f, -0.05142535f, 0.016532812f, -0.002983080f}
 
 // tanh of any number to 2^-22.
 __device__ __forceinline__ float tanh_far(float z) {
@@ -60,7 +62,6 @@ __device__ __forceinline__ float tanh_far(float z) {
 template <int N, int STEP>
 __device__ __forceinline__ void finish_scores(float (&s)[N], const AttendArgs &a, float mult, float slope, int32_t back,
                                               bool masked) {
-    constexpr float kTanh[6] = LORA_TANH_COEFFICIENTS;
     const uint64_t slope2 = pack2(slope, slope), at2 = pack2(slope * back, slope * back);
     const float by = mult * kLog2e;
     bool near = a.softcap > 0.0f;
@@ -68,9 +69,10 @@ __device__ __forceinline__ void finish_scores(float (&s)[N], const AttendArgs &a
         float top = 0.0f;
 #pragma unroll
         for (int e = 0; e < N; e += 2) top = fmaxf(fmaxf(top, fabsf(s[e])), fabsf(s[e + 1]));
-        near = __all_sync(0xffffffffu, top * fabsf(mult) <= a.softcap);
+        near = __all_sync(0xffffffffu, top * fabsf(mult) <= 0.5f * a.softcap);
         if (!near) {
-            const float in = mult / a.softcap, cap = a.softcap * kLog2e;
+            constexpr float kTanh[6] = LORA_TANH_ONE;
+            const float in = mult * a.inv_softcap, cap = a.softcap * kLog2e;
 #pragma unroll
             for (int e = 0; e < N; ++e) {
                 const float z = s[e] * in, w = z * z;
@@ -82,17 +84,18 @@ __device__ __forceinline__ void finish_scores(float (&s)[N], const AttendArgs &a
     }
     if (near) {
         // by s + by c1 in^2 s^3 + ...: the scales are in the coefficients
-        const float in = mult / a.softcap, in2 = in * in;
+        const float in = mult * a.inv_softcap, in2 = in * in;
         float c = by;
-        uint64_t k[6];
+        constexpr float kTanh[4] = LORA_TANH_HALF;
+        uint64_t k[4];
 #pragma unroll
-        for (int i = 0; i < 6; ++i, c *= in2) k[i] = pack2(c * kTanh[i], c * kTanh[i]);
+        for (int i = 0; i < 4; ++i, c *= in2) k[i] = pack2(c * kTanh[i], c * kTanh[i]);
 #pragma unroll
         for (int e = 0; e < N; e += 2) {
             const uint64_t x = pack2(s[e], s[e + 1]), w = mul2(x, x);
-            uint64_t r = fma2(k[5], w, k[4]);
+            uint64_t r = fma2(k[3], w, k[2]);
 #pragma unroll
-            for (int i = 3; i >= 0; --i) r = fma2(r, w, k[i]);
+            for (int i = 1; i >= 0; --i) r = fma2(r, w, k[i]);
             if (a.slopes != nullptr) {
                 const float d = static_cast<float>(e / 2 * STEP);
                 r = fma2(x, r, fma2(slope2, pack2(d, d + 1.0f), at2));
@@ -112,9 +115,13 @@ __device__ __forceinline__ void finish_scores(float (&s)[N], const AttendArgs &a
     }
     if (masked) {
 #pragma unroll
-        for (int e = 0; e < N; ++e) {
-            const int32_t b = back + e / 2 * STEP + (e & 1);
-            if (b > 0 || (a.window > 0 && -b >= a.window)) s[e] = -INFINITY;
+        for (int e = 0; e < N; ++e)
+            if (back > -(e / 2 * STEP + (e & 1))) s[e] = -INFINITY;
+        if (a.window > 0) {
+            const int32_t first = -back - a.window;  // keys up to this one's index are out of the window
+#pragma unroll
+            for (int e = 0; e < N; ++e)
+                if (first >= e / 2 * STEP + (e & 1)) s[e] = -INFINITY;
         }
     }
 }

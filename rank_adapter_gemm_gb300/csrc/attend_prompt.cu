@@ -20,7 +20,9 @@
 //   warps 12-15      one thread issues the products
 // k and v tiles share one ring; every wait is bounded (2 s) and reports
 // LORA_ERR_TIMEOUT.  Blocks take the (request, row tile, key head) items with the
-// most keys of a request first.
+// most keys of a request first, and an item's keys from the last tile down: with a
+// bias that falls with distance the largest scores come first and O is not rescaled
+// step after step.
 //
 // Weights are rounded to bf16 for the second product (the cache's type: the
 // instruction takes one type for both operands); sums use them unrounded.
@@ -110,6 +112,13 @@ __device__ __forceinline__ void tmem_ld64(uint32_t taddr, uint32_t *r) {
         : "r"(taddr));
 }
 
+__device__ __forceinline__ void tmem_wait64(uint32_t (&r)[64]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : LORA_R8(r, 0), LORA_R8(r, 8), LORA_R8(r, 16), LORA_R8(r, 24), LORA_R8(r, 32), LORA_R8(r, 40),
+                   LORA_R8(r, 48), LORA_R8(r, 56)
+                 : : "memory");
+}
+
 __device__ __forceinline__ void tmem_wait128(uint32_t (&r)[128]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;"
                  : LORA_R8(r, 0), LORA_R8(r, 8), LORA_R8(r, 16), LORA_R8(r, 24), LORA_R8(r, 32), LORA_R8(r, 40),
@@ -122,6 +131,13 @@ __device__ __forceinline__ void tmem_wait128(uint32_t (&r)[128]) {
 __device__ __forceinline__ void tmem_wait(uint32_t (&r)[32]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;"
                  : LORA_R8(r, 0), LORA_R8(r, 8), LORA_R8(r, 16), LORA_R8(r, 24) : : "memory");
+}
+
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t *r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};"
+        :: LORA_I8(r, 0), LORA_I8(r, 8), LORA_I8(r, 16), LORA_I8(r, 24), "r"(taddr) : "memory");
 }
 
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
@@ -313,7 +329,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
         const int32_t end = min(it.len, it.key1);
         // the byte offset of this lane's key of a step, -1: none
         const auto offset_of = [&](int32_t step) -> int64_t {
-            const int32_t key = it.key0 + step * kKeys + w * 32 + lane;
+            const int32_t key = it.key0 + (steps - 1 - step) * kKeys + w * 32 + lane;  // last keys first
             if (key < it.lo || key >= end) return -1;
             const int32_t page = __ldg(table + (key >> a.kv.page_shift));
             if (page < 0 || page >= a.kv.n_pages) {
@@ -495,25 +511,32 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
             for (int32_t j = 0; j < steps; ++j) {
                 if (!wait(&bar.s_full[i], j & 1)) break;
                 tc::fence_after_sync();
-                const int32_t key = key0 + j * kKeys;
+                const int32_t key = key0 + (steps - 1 - j) * kKeys;
                 const bool masked = key + kKeys - 1 > pos_lo || (a.window > 0 && pos_hi - key >= a.window);
                 const bool direct = plain && !masked;
                 const float by = direct ? by0 : 1.0f;
+                if (!direct) {
+                    // the final form of the scores, in place, 64 at a time (one copy of the code)
+#pragma unroll 1
+                    for (int c = 0; c < 2; ++c) {
+                        uint32_t r[64];
+                        float s[64];
+                        tmem_ld64(s_at + 64 * c, r);
+                        tmem_wait64(r);
+#pragma unroll
+                        for (int e = 0; e < 64; ++e) s[e] = __uint_as_float(r[e]);
+                        finish_scores<64, 2>(s, a, mult, slope, key + 64 * c - pos, masked);
+#pragma unroll
+                        for (int e = 0; e < 64; ++e) r[e] = __float_as_uint(s[e]);
+                        tmem_st32(s_at + 64 * c, r);
+                        tmem_st32(s_at + 64 * c + 32, r + 32);
+                    }
+                    tmem_wait_st();
+                }
                 uint32_t x[128];
                 tmem_ld64(s_at, x);
                 tmem_ld64(s_at + 64, x + 64);
                 tmem_wait128(x);
-                if (!direct) {
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        float s[32];
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) s[e] = __uint_as_float(x[32 * c + e]);
-                        finish_scores<32, 2>(s, a, mult, slope, key + 32 * c - pos, masked);
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) x[32 * c + e] = __float_as_uint(s[e]);
-                    }
-                }
                 float top8[8];
 #pragma unroll
                 for (int q = 0; q < 8; ++q) {

@@ -29,7 +29,7 @@ struct AttendArgs {
     int32_t *err;
     KvView kv;
     int32_t T, n_seq, width, n_heads, group, window;
-    float scale, softcap;
+    float scale, softcap, inv_softcap;  // inv_softcap: 0 without a cap
 };
 
 // Rows [q0, q0 + n) of request i, its last n of len positions; not ok (and

@@ -166,7 +166,8 @@ lora_status_t lora_attend(const void *q, int64_t ldq, void *out, int64_t ldo, fl
     if (max_q_hint <= 0 || max_q_hint > T) max_q_hint = T;
     const lora::AttendArgs a{static_cast<const uint16_t *>(q), static_cast<uint16_t *>(out), lse, ldq, ldo, ld_table,
                              q_offsets, kv_lens, block_table, att->slopes, err, view, T, n_seq, table_width,
-                             att->n_heads, att->n_heads / view.n_kv, att->window, att->scale, att->softcap};
+                             att->n_heads, att->n_heads / view.n_kv, att->window, att->scale, att->softcap,
+                             att->softcap > 0.0f ? 1.0f / att->softcap : 0.0f};
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const bool e4m3 = kv->type == LORA_KV_E4M3;
     if (lora_attend_resolve_path(path, att, kv, max_q_hint) == LORA_ATTEND_DECODE)
