@@ -171,7 +171,8 @@ lora_status_t lora_rope_append(const void *qkv, int64_t ldqkv, int32_t T, int32_
  *   max_q_hint   host-known upper bound on a request's rows (0: T); it picks the
  *                path, results do not depend on it
  *   ws           lora_attend_workspace_bytes() bytes, 16-byte aligned, zeroed once
- *                before the first call; every call leaves it as it found it.
+ *                before the first call; every call leaves it as it found it (but
+ *                zero it again after a call that reports LORA_ERR_TIMEOUT).
  *                Calls that may overlap need a workspace each
  * Limits (LORA_ERR_UNSUPPORTED): head_dim 64 or 128.  n_heads a multiple of
  * n_kv, n_seq <= LORA_MAX_SEQS, scale finite, softcap >= 0, window >= 0

@@ -69,7 +69,8 @@ __device__ __forceinline__ void finish_scores(float (&s)[N], const AttendArgs &a
         float top = 0.0f;
 #pragma unroll
         for (int e = 0; e < N; e += 2) top = fmaxf(fmaxf(top, fabsf(s[e])), fabsf(s[e + 1]));
-        near = __all_sync(0xffffffffu, top * fabsf(mult) <= 0.5f * a.softcap);
+        // (a cap below 1e-6 of mult would overflow the coefficients)
+        near = __all_sync(0xffffffffu, top * fabsf(mult) <= 0.5f * a.softcap && fabsf(mult) <= 1e6f * a.softcap);
         if (!near) {
             constexpr float kTanh[6] = LORA_TANH_ONE;
             const float in = mult * a.inv_softcap, cap = a.softcap * kLog2e;

@@ -16,16 +16,22 @@
 //                    maximum passes 2^8 times it: most steps never touch O.
 //   warps 8-11       copy q rows and k and v tiles of 128 keys, key by key through
 //                    the block table, into the swizzled layout that the tensor
-//                    cores read (e4m3 codes are widened to bf16, exactly, on the way)
-//   warps 12-15      one thread issues the products
-// k and v tiles share one ring; every wait is bounded (2 s) and reports
-// LORA_ERR_TIMEOUT.  Blocks take the (request, row tile, key head) items with the
-// most keys of a request first, and an item's keys from the last tile down: with a
-// bias that falls with distance the largest scores come first and O is not rescaled
-// step after step.
+//                    cores read (e4m3 codes are widened to f16 on the way)
+//   warp 12          issues the products
+//   warp 13          hands out the work
+// One block an SM stays for the whole call.  The (request, row tiles, key head)
+// items go to whichever block is free, those with the most keys of a request
+// first, and a block's copies and products begin its next item while the softmax
+// warps still write the last one's output.  An item's keys are taken from the last
+// tile down: with a bias that falls with distance the largest scores come first
+// and O is not rescaled step after step.  k and v tiles share one ring; every wait
+// is bounded (2 s) and reports LORA_ERR_TIMEOUT.
 //
-// Weights are rounded to bf16 for the second product (the cache's type: the
-// instruction takes one type for both operands); sums use them unrounded.
+// The instruction takes one type for both operands.  Over a bf16 cache weights
+// are rounded to bf16 (sums use them unrounded).  Over an e4m3 cache everything is
+// f16: codes are exact in it, a query row is scaled by a power of two to keep
+// 2^-24 of its largest element, and weights, times 2^7, keep 11 bits down to 2^-21
+// of the row's reference.
 #include <cuda_fp16.h>
 
 #include "attend.cuh"
@@ -39,7 +45,7 @@ constexpr int kRows = 128, kKeys = 128;    // a tile
 constexpr int kThreads = 16 * 32;
 // Registers a thread: 128 at launch, then by role.  The four warpgroups' shares
 // (two of softmax, copies, products) add up to the launch's 4 x 128.
-constexpr int kSoftmaxRegs = 200, kCopyRegs = 56, kMmaRegs = 56;
+constexpr int kSoftmaxRegs = 184, kCopyRegs = 80, kMmaRegs = 64;
 static_assert(2 * kSoftmaxRegs + kCopyRegs + kMmaRegs == 4 * 128, "registers of the block");
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr float kGrow = 8.0f;              // log2 by which a row's maximum may grow before O is rescaled
@@ -53,7 +59,8 @@ struct PromptConfig {
 };
 
 struct Barriers {
-    uint64_t q_full, full[8], empty[8], s_full[2], p_full[2][2], o_full[2], done;
+    uint64_t q_full, q_empty, full[8], empty[8], s_full[2], p_full[2][2], o_full[2], o_empty[2], item_full[2],
+        item_empty[2], exp_full[2], claim, done;
 };
 
 // Shared-memory matrix descriptor, 128-byte swizzle: 64 elements of the
@@ -160,20 +167,22 @@ __device__ __forceinline__ void rescale_output(uint32_t o_at, float f) {
     }
 }
 
-// Sixteen e4m3 codes as bf16, exactly (through f16 and fp32).
+// Sixteen e4m3 codes as f16, exactly.
 __device__ __forceinline__ void widen16(uint4 w, uint4 &lo, uint4 &hi) {
     const uint32_t u[4] = {w.x, w.y, w.z, w.w};
     uint32_t o[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const uint32_t pair = u[i >> 1] >> (16 * (i & 1));
-        uint32_t h;
-        asm("{\n\t.reg .b16 l;\n\tcvt.u16.u32 l, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t}" : "=r"(h) : "r"(pair));
-        const __half2 h2 = *reinterpret_cast<const __half2 *>(&h);
-        o[i] = pack_bf16x2(__low2float(h2), __high2float(h2));
-    }
+    for (int i = 0; i < 8; ++i)
+        asm("{\n\t.reg .b16 l;\n\tcvt.u16.u32 l, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t}"
+            : "=r"(o[i]) : "r"(u[i >> 1] >> (16 * (i & 1))));
     lo = make_uint4(o[0], o[1], o[2], o[3]);
     hi = make_uint4(o[4], o[5], o[6], o[7]);
+}
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
 }
 
 __device__ __forceinline__ void sts16(uint32_t addr, uint4 v) {
@@ -186,83 +195,54 @@ __device__ __forceinline__ uint32_t tile_at(int row, int piece) {
     return (piece >> 3) * (kRows * 128) + row * 128 + (((piece & 7) ^ (row & 7)) << 4);
 }
 
-// A block's item: 256 rows (two tiles) of a request and key head, keys [key0, key1).
+// 256 rows (two tiles) of a request and key head, and their keys [key0, key1).
 struct Item {
     int32_t seq, head, row0, rows;  // first row and rows (of the request's n * group)
-    int32_t q0, n, len, lo, key0, key1;
-    bool any;
+    int32_t q0, n, len, lo, key0, steps;
+    bool any;                       // none: the work is done
+};
+
+// Claims on the call's items, zero between calls: items given out past the first
+// one of each block, and blocks that are done.
+struct Claims {
+    int32_t given, done;
 };
 
 template <int HD, bool E4M3>
-__global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const AttendArgs a) {
+__global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const AttendArgs a, Claims *claims) {
     using C = PromptConfig<HD>;
+    constexpr float kShift = E4M3 ? 7.0f : 0.0f;
     extern __shared__ unsigned char smem_raw[];
     __shared__ Barriers bar;
-    __shared__ Item s_item;
+    __shared__ Item s_item[2];
     __shared__ int64_t s_warp[kThreads / 32];
     __shared__ uint32_t s_tmem;
     __shared__ volatile int32_t s_abort;
+    __shared__ int8_t s_qexp[2][E4M3 ? 2 * kRows : 1];  // of this and the next item: q rows' powers of two
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const uint32_t base = (tc::smem_u32(smem_raw) + 1023) & ~1023u;  // two q tiles, then the ring
+    const uint32_t q_base = (tc::smem_u32(smem_raw) + 1023) & ~1023u;  // two q tiles, then the ring
+    const uint32_t ring = q_base + 2 * C::kTileB;
 
     wait_for_previous();
-    // ---- this block's item: the requests' row-tile pairs, last ones first --------------
+    const auto pairs_of = [&](const RequestRows &r) {
+        return (int64_t(r.n) * a.group + 2 * kRows - 1) / (2 * kRows);
+    };
+    int64_t total = 0;  // pairs of row tiles
     {
-        const int32_t per = (a.n_seq + kThreads - 1) / kThreads, i0 = min(a.n_seq, tid * per),
-                      i1 = min(a.n_seq, i0 + per);
-        const auto pairs_of = [&](const RequestRows &r) {
-            return (int64_t(r.n) * a.group + 2 * kRows - 1) / (2 * kRows);
-        };
         int64_t mine = 0;
-        for (int32_t i = i0; i < i1; ++i) {
+        for (int32_t i = tid; i < a.n_seq; i += kThreads) {
             const RequestRows r = load_rows(a, i);
             if (!r.ok && blockIdx.x == 0) report_error(a.err, LORA_ERR_INVALID_ARG);
             mine += pairs_of(r);
         }
-        int64_t incl = mine;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int64_t u = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += u;
-        }
-        if (lane == 31) s_warp[warp] = incl;
-        if (tid == 0) {
-            s_item.any = false;
-            s_abort = 0;
-        }
-        __syncthreads();
-        int64_t run = incl - mine, total = 0;
-#pragma unroll
-        for (int w = 0; w < kThreads / 32; ++w) {
-            if (w < warp) run += s_warp[w];
-            total += s_warp[w];
-        }
-        const int64_t want = total - 1 - blockIdx.x / a.kv.n_kv;
-        for (int32_t i = i0; i < i1 && want >= run; ++i) {
-            const RequestRows r = load_rows(a, i);
-            const int64_t pairs = pairs_of(r);
-            if (want < run + pairs) {
-                Item it;
-                it.seq = i;
-                it.head = blockIdx.x % a.kv.n_kv;
-                it.row0 = static_cast<int32_t>(want - run) * 2 * kRows;
-                it.rows = min(2 * kRows, r.n * a.group - it.row0);
-                it.q0 = r.q0;
-                it.n = r.n;
-                it.len = r.len;
-                const int32_t first = r.len - r.n + it.row0 / a.group;
-                const int32_t last = r.len - r.n + (it.row0 + it.rows - 1) / a.group;
-                it.lo = a.window > 0 ? static_cast<int32_t>(max(int64_t(0), int64_t(first) - a.window + 1)) : 0;
-                it.key0 = it.lo & ~(kKeys - 1);
-                it.key1 = last + 1;
-                it.any = true;
-                s_item = it;
-            }
-            run += pairs;
-        }
+        for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+        if (lane == 0) s_warp[warp] = mine;
     }
     if (tid == 0) {
+        s_abort = 0;
         tc::mbar_init(&bar.q_full, 4);
+        tc::mbar_init(&bar.q_empty, 1);
         for (int i = 0; i < C::kSlots; ++i) {
             tc::mbar_init(&bar.full[i], 4);
             tc::mbar_init(&bar.empty[i], 1);
@@ -272,158 +252,213 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
             tc::mbar_init(&bar.p_full[i][0], 4);
             tc::mbar_init(&bar.p_full[i][1], 4);
             tc::mbar_init(&bar.o_full[i], 1);
+            tc::mbar_init(&bar.o_empty[i], 4);
+            tc::mbar_init(&bar.item_full[i], 1);
+            tc::mbar_init(&bar.exp_full[i], 4);
+            tc::mbar_init(&bar.item_empty[i], 13);  // the copying, multiplying and softmax warps
         }
+        tc::mbar_init(&bar.claim, 1);
         tc::mbar_init(&bar.done, 1);
         tc::mbar_init_fence();
-    }
-    __syncthreads();
-    const Item it = s_item;
-    if (!it.any) return;
-    if (it.key1 <= 0) {  // no row sees a key
-        for (int32_t e = tid; e < it.rows * (HD / 8); e += kThreads) {
-            const int32_t row = it.row0 + e / (HD / 8), t = it.q0 + row / a.group;
-            const int32_t h = it.head * a.group + row % a.group;
-            stg_u4(a.out + t * a.ldo + h * HD + e % (HD / 8) * 8, make_uint4(0, 0, 0, 0));
-            if (a.lse != nullptr && e % (HD / 8) == 0) a.lse[int64_t(t) * a.n_heads + h] = -INFINITY;
-        }
-        return;
     }
     if (warp == 12) tc::tmem_alloc(&s_tmem, 512);
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) total += s_warp[w];
     const uint32_t tmem = s_tmem;
-    const int n_tiles = it.rows > kRows ? 2 : 1;
-    const int32_t steps = (it.key1 - it.key0 + kKeys - 1) / kKeys;
-    const uint32_t q_base = base, ring = base + 2 * C::kTileB;
     bool fine = true;
     const auto wait = [&](uint64_t *b, uint32_t parity) {
         fine = fine && tc::mbar_wait(b, parity, &s_abort, kWaitNs);
         return fine;
+    };
+    // a warp lets go of the block's k-th item
+    const auto release = [&](int32_t k) {
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&bar.item_empty[k & 1]);
     };
 
     if (warp >= 8 && warp < 12) {
         set_registers<kCopyRegs, false>();
         // ---- copies ---------------------------------------------------------------------
         const int w = warp - 8;
-        constexpr int kPieces = HD / 8;  // 16-byte pieces of a bf16 row
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            // 32 rows: a lane's row's offset, then a few rows a copy instruction
-            constexpr int kStep = 32 / kPieces;
-            const int piece = lane % kPieces, r0 = w * 64 + half * 32;
-            const int32_t row = it.row0 + r0 + lane;
-            int64_t at = -1;
-            if (r0 + lane < it.rows)
-                at = (it.q0 + row / a.group) * a.ldq + (it.head * a.group + row % a.group) * HD;
-#pragma unroll
-            for (int i = 0; i < kPieces; ++i) {
-                const int r = r0 + i * kStep + lane / kPieces;
-                const int64_t o = __shfl_sync(0xffffffffu, at, i * kStep + lane / kPieces);
-                tc::cp16(q_base + (r / kRows) * C::kTileB + tile_at(r % kRows, piece),
-                         a.q + (o >= 0 ? o : 0) + piece * 8, o >= 0);
-            }
-        }
-        tc::cp_commit();
-        const int32_t *table = a.table + it.seq * a.ld_table;
-        const int32_t end = min(it.len, it.key1);
-        // the byte offset of this lane's key of a step, -1: none
-        const auto offset_of = [&](int32_t step) -> int64_t {
-            const int32_t key = it.key0 + (steps - 1 - step) * kKeys + w * 32 + lane;  // last keys first
-            if (key < it.lo || key >= end) return -1;
-            const int32_t page = __ldg(table + (key >> a.kv.page_shift));
-            if (page < 0 || page >= a.kv.n_pages) {
-                report_error(a.err, LORA_ERR_SLOT_RANGE);
-                return -1;
-            }
-            return page * a.kv.page_b + (key & a.kv.page_mask) * a.kv.token_b + it.head * a.kv.head_b;
-        };
-        const int32_t tiles = 2 * steps;
-        const auto slot_free = [&](int32_t u) {
-            return u < C::kSlots || wait(&bar.empty[u % C::kSlots], (u / C::kSlots - 1) & 1);
-        };
+        constexpr int kPieces = HD / 8;                          // 16-byte pieces of a 16-bit row
+        constexpr int kStep = 32 / kPieces;                      // rows a q (or bf16) instruction
+        constexpr int kKvPieces = E4M3 ? HD / 16 : kPieces;      // pieces of a cache row
+        constexpr int kKvStep = 32 / kKvPieces;
+        const int piece = lane % kPieces, row_in = lane / kPieces;
+        const auto q_piece = [&](int r) { return q_base + (r / kRows) * C::kTileB + tile_at(r % kRows, piece); };
+        const int kv_piece = lane % kKvPieces, kv_row = lane / kKvPieces;
         const auto publish = [&](uint64_t *b) {
             tc::fence_async_smem();
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(b);
         };
-        if constexpr (E4M3) {
-            constexpr int kCodes = HD / 16;        // 16-byte pieces of a row of codes
-            constexpr int kStep = 32 / kCodes;     // keys a load instruction
-            const int piece = lane % kCodes;
-            uint4 v[kCodes];
-            int64_t at = offset_of(0), next_at = -1;
-            const auto load = [&](int32_t u) {
-                const unsigned char *from = (u & 1) ? a.kv.v : a.kv.k;
+        int32_t u = 0, q_round = 0;  // tiles and items so far
+        for (int32_t k = 0;; ++k) {
+            if (!wait(&bar.item_full[k & 1], (k >> 1) & 1) || !s_item[k & 1].any) break;
+            const Item &it = s_item[k & 1];
+            const int32_t steps = it.steps, lo = it.lo;
+            const int32_t last = it.len - it.n + (it.row0 + it.rows - 1) / a.group;
+            const int32_t *table = a.table + it.seq * a.ld_table;
+            const int64_t head = it.head * a.kv.head_b;
+            // this lane's key of the step to copy (the last keys first) and, ahead of it, its page
+            int32_t key = it.key0 + (steps - 1) * kKeys + w * 32 + lane, page = -1;
+            const auto has_key = [&]() { return key >= lo && key <= last; };
+            if (has_key()) page = __ldg(table + (key >> a.kv.page_shift));
+            if (steps > 0 && (q_round == 0 || wait(&bar.q_empty, (q_round - 1) & 1))) {
+                ++q_round;
+#pragma unroll 1
+                for (int half = 0; half < 2; ++half) {
+                    // 32 rows of q: a lane's row's offset, then a few rows an instruction
+                    const int r0 = w * 64 + half * 32, row = it.row0 + r0 + lane;
+                    int64_t q_at = -1;
+                    if (r0 + lane < it.rows)
+                        q_at = (it.q0 + row / a.group) * a.ldq + (it.head * a.group + row % a.group) * HD;
 #pragma unroll
-                for (int i = 0; i < kCodes; ++i) {
-                    const int64_t o = __shfl_sync(0xffffffffu, at, i * kStep + lane / kCodes);
-                    v[i] = o >= 0 ? ldg_stream(from + o + piece * 16) : make_uint4(0, 0, 0, 0);
+                    for (int i = 0; i < kPieces; ++i) {
+                        const int64_t o = __shfl_sync(0xffffffffu, q_at, i * kStep + row_in);
+                        tc::cp16(q_piece(r0 + i * kStep + row_in), a.q + (o >= 0 ? o : 0) + piece * 8, o >= 0);
+                    }
+                }
+                if constexpr (E4M3) {
+                    // each lane turns the pieces that it copied into f16, in place
+                    tc::cp_wait_all();
+#pragma unroll 2
+                    for (int i = 0; i < 2 * kPieces; ++i) {
+                        const int r = w * 64 + i * kStep + row_in;
+                        uint32_t x[4];
+                        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                                     : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]) : "r"(q_piece(r)) : "memory");
+                        float top = 0.0f;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            top = fmaxf(fmaxf(top, fabsf(bf16lo_to_f32(x[e]))), fabsf(bf16hi_to_f32(x[e])));
+#pragma unroll
+                        for (int s = kPieces / 2; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
+                        // 2^e <= top < 2^(e + 1): the row times 2^-e is below 2
+                        const int e2 = top > 0.0f ? max(-60, min(60, static_cast<int>(__float_as_uint(top) >> 23) - 127))
+                                                  : 0;
+                        const float down = __uint_as_float(static_cast<uint32_t>(127 - e2) << 23);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            x[e] = pack_f16x2(bf16lo_to_f32(x[e]) * down, bf16hi_to_f32(x[e]) * down);
+                        sts16(q_piece(r), make_uint4(x[0], x[1], x[2], x[3]));
+                        if (piece == 0) s_qexp[k & 1][r] = static_cast<int8_t>(e2);
+                    }
+                }
+                if (E4M3) publish(&bar.q_full);
+                else tc::cp_commit();
+            }
+            if (E4M3 && lane == 0) tc::mbar_arrive(&bar.exp_full[k & 1]);
+            release(k);  // nothing below reads the item
+            if (!fine) break;
+
+            int64_t at = -1;      // byte offset of this lane's key, -1: none
+            bool smooth = false;  // all keys there, and 16 neighbours always in one page
+            const auto next_keys = [&]() {
+                const bool ok = page >= 0 && page < a.kv.n_pages, has = has_key();
+                if (has && !ok) report_error(a.err, LORA_ERR_SLOT_RANGE);
+                at = has && ok ? page * a.kv.page_b + (key & a.kv.page_mask) * a.kv.token_b + head : -1;
+                smooth = __all_sync(0xffffffffu, at >= 0) && a.kv.page_shift >= 4;
+                key -= kKeys;
+                if (has_key()) page = __ldg(table + (key >> a.kv.page_shift));
+            };
+            // calls f(instruction, address or null) for this warp's 32 keys of k or v
+            const auto each = [&](const unsigned char *from, auto f) {
+                from += kv_piece * 16;
+                if (smooth) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const unsigned char *src = from + __shfl_sync(0xffffffffu, at, 16 * h) + kv_row * a.kv.token_b;
+#pragma unroll
+                        for (int i = 0; i < kKvPieces / 2; ++i) {
+                            f(h * (kKvPieces / 2) + i, src);
+                            src += kKvStep * a.kv.token_b;
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < kKvPieces; ++i) {
+                        const int64_t o = __shfl_sync(0xffffffffu, at, i * kKvStep + kv_row);
+                        f(i, o >= 0 ? from + o : nullptr);
+                    }
                 }
             };
-            load(0);
-            tc::cp_wait_all();
-            publish(&bar.q_full);
-            for (int32_t u = 0; u < tiles; ++u) {
-                if ((u & 1) == 0 && u + 2 < tiles) next_at = offset_of(u / 2 + 1);
-                if (!slot_free(u)) break;
-                const uint32_t dst = ring + (u % C::kSlots) * C::kTileB;
+            const auto slot_free = [&]() {
+                return u < C::kSlots || wait(&bar.empty[u % C::kSlots], (u / C::kSlots - 1) & 1);
+            };
+            const int32_t tiles = 2 * steps;
+            if constexpr (E4M3) {
+                uint4 v[kKvPieces];
+                const auto load = [&](int32_t t) {
+                    if ((t & 1) == 0) next_keys();
+                    each((t & 1) ? a.kv.v : a.kv.k, [&](int i, const unsigned char *src) {
+                        v[i] = src != nullptr ? ldg_stream(src) : make_uint4(0, 0, 0, 0);
+                    });
+                };
+                if (tiles > 0) load(0);
+                for (int32_t t = 0; t < tiles; ++t, ++u) {
+                    if (t == tiles - 2 && w == 0 && lane == 0) tc::mbar_arrive(&bar.claim);
+                    if (!slot_free()) break;
+                    const uint32_t dst = ring + (u % C::kSlots) * C::kTileB;
 #pragma unroll
-                for (int i = 0; i < kCodes; ++i) {
-                    const int row = w * 32 + i * kStep + lane / kCodes;
-                    uint4 lo, hi;
-                    widen16(v[i], lo, hi);
-                    sts16(dst + tile_at(row, 2 * piece), lo);
-                    sts16(dst + tile_at(row, 2 * piece + 1), hi);
+                    for (int i = 0; i < kKvPieces; ++i) {
+                        const int row = w * 32 + i * kKvStep + kv_row;
+                        uint4 x, y;
+                        widen16(v[i], x, y);
+                        sts16(dst + tile_at(row, 2 * kv_piece), x);
+                        sts16(dst + tile_at(row, 2 * kv_piece + 1), y);
+                    }
+                    if (t + 1 < tiles) load(t + 1);
+                    publish(&bar.full[u % C::kSlots]);
                 }
-                if (u & 1) at = next_at;
-                if (u + 1 < tiles) load(u + 1);
-                publish(&bar.full[u % C::kSlots]);
-            }
-        } else {
-            constexpr int kStep = 32 / kPieces;    // keys a copy instruction
-            const int piece = lane % kPieces, row0 = lane / kPieces;
-            int64_t at = offset_of(0), next_at = -1;
-            int32_t u = 0;
-            for (; u < tiles; ++u) {
-                if ((u & 1) == 0 && u + 2 < tiles) next_at = offset_of(u / 2 + 1);
-                if (!slot_free(u)) break;
-                const unsigned char *from = (u & 1) ? a.kv.v : a.kv.k;
-                const uint32_t dst = ring + (u % C::kSlots) * C::kTileB;
-#pragma unroll
-                for (int i = 0; i < kPieces; ++i) {
-                    const int row = i * kStep + row0;
-                    const int64_t o = __shfl_sync(0xffffffffu, at, row);
-                    tc::cp16(dst + tile_at(w * 32 + row, piece), from + (o >= 0 ? o : 0) + piece * 16, o >= 0);
+            } else {
+                for (int32_t t = 0; t < tiles; ++t, ++u) {
+                    if (t == tiles - 2 && w == 0 && lane == 0) tc::mbar_arrive(&bar.claim);
+                    if ((t & 1) == 0) next_keys();
+                    if (!slot_free()) break;
+                    const uint32_t dst = ring + (u % C::kSlots) * C::kTileB;
+                    each((t & 1) ? a.kv.v : a.kv.k, [&](int i, const unsigned char *src) {
+                        tc::cp16(dst + tile_at(w * 32 + i * kKvStep + kv_row, kv_piece), src != nullptr ? src : a.kv.k,
+                                 src != nullptr);
+                    });
+                    tc::cp_commit();
+                    // the tile two before this one (and q before all) has landed
+                    tc::cp_wait_group<2>();
+                    if (t == 1) publish(&bar.q_full);
+                    if (t >= 2) publish(&bar.full[(u - 2) % C::kSlots]);
                 }
-                tc::cp_commit();
-                if (u & 1) at = next_at;
-                // the tile two before this one (and q before all) has landed
-                tc::cp_wait_group<2>();
-                if (u == 1) publish(&bar.q_full);
-                if (u >= 2) publish(&bar.full[(u - 2) % C::kSlots]);
+                if (fine && tiles > 0) {
+                    tc::cp_wait_group<1>();
+                    publish(&bar.full[(u - 2) % C::kSlots]);
+                    tc::cp_wait_group<0>();
+                    publish(&bar.full[(u - 1) % C::kSlots]);
+                }
             }
-            if (fine) {
-                tc::cp_wait_group<1>();
-                publish(&bar.full[(tiles - 2) % C::kSlots]);
-                tc::cp_wait_group<0>();
-                publish(&bar.full[(tiles - 1) % C::kSlots]);
-            }
-            tc::cp_wait_all();
+            if (steps == 0 && w == 0 && lane == 0) tc::mbar_arrive(&bar.claim);
+            if (!fine) break;
         }
+        tc::cp_wait_all();
     } else if (warp >= 12) {
         set_registers<kMmaRegs, false>();
-        // ---- products -------------------------------------------------------------------
         if (warp == 12) {
+            // ---- products ---------------------------------------------------------------
             // The warp stays together and one elected thread issues: the products' operands
             // then stay in uniform registers.
-            constexpr uint32_t kS = tc::idesc_bf16(kRows, kKeys);
-            constexpr uint32_t kO = tc::idesc_bf16(kRows, HD) | (1u << 16);  // v: keys are the strided dimension
+            constexpr uint32_t kType = E4M3 ? (1u << 7) | (1u << 10) : 0u;  // f16 has 0 where bf16 has 1
+            constexpr uint32_t kS = tc::idesc_bf16(kRows, kKeys) ^ kType;
+            constexpr uint32_t kO = (tc::idesc_bf16(kRows, HD) ^ kType) | (1u << 16);  // v: keys are strided
             // descriptors are a tile's plus a constant: addresses stay below 2^18, so nothing carries
             const uint64_t q_desc = desc128(q_base, 16, 1024), k_desc = desc128(ring, 16, 1024);
             const uint64_t v_desc = desc128(ring, C::kHalfB, 1024);
             const auto full = [&](int32_t u) { return wait(&bar.full[u % C::kSlots], (u / C::kSlots) & 1); };
-            const auto scores = [&](int i, int32_t u, bool last) {
+            const auto commit = [&](uint64_t *b) {
+                if (elect_one()) tc::mma_commit(b);
+                __syncwarp();
+            };
+            const auto scores = [&](int i, int32_t u) {
                 const uint64_t q = q_desc + ((i * C::kTileB) >> 4), k = k_desc + (((u % C::kSlots) * C::kTileB) >> 4);
                 if (elect_one()) {
 #pragma unroll
@@ -432,7 +467,6 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
                         tc::mma_bf16(tmem + i * kKeys, q + off, k + off, kS, kk > 0);
                     }
                     tc::mma_commit(&bar.s_full[i]);
-                    if (last) tc::mma_commit(&bar.empty[u % C::kSlots]);
                 }
                 __syncwarp();
             };
@@ -449,67 +483,168 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
                 }
                 __syncwarp();
             };
-            const auto commit = [&](uint64_t *b) {
-                if (elect_one()) tc::mma_commit(b);
-                __syncwarp();
-            };
-            if (wait(&bar.q_full, 0) && full(0)) {
+            int32_t u = 0, q_round = 0;
+            uint32_t p_parity = 0, o_parity = 0, o_used = 0;  // a bit a tile
+            for (int32_t k = 0;; ++k) {
+                if (!wait(&bar.item_full[k & 1], (k >> 1) & 1) || !s_item[k & 1].any) break;
+                const int32_t steps = s_item[k & 1].steps;
+                const int n_tiles = s_item[k & 1].rows > kRows ? 2 : 1;
+                release(k);
+                if (steps == 0) continue;
+                if (!wait(&bar.q_full, q_round & 1) || !full(u)) break;
+                ++q_round;
                 tc::fence_after_sync();
-                for (int i = 0; i < n_tiles; ++i) scores(i, 0, i == n_tiles - 1);
-            }
-            for (int32_t j = 0; j < steps && fine; ++j) {
-                const bool more = j + 1 < steps;
-                for (int i = 0; i < n_tiles && fine; ++i) {
-                    const bool last = i == n_tiles - 1;
-                    if (i == 0 && !full(2 * j + 1)) break;
-                    if (!wait(&bar.p_full[i][0], j & 1)) break;
-                    tc::fence_after_sync();
-                    outputs(i, 2 * j + 1, 0, j == 0);
-                    if (!wait(&bar.p_full[i][1], j & 1)) break;
-                    tc::fence_after_sync();
-                    outputs(i, 2 * j + 1, 1, j == 0);
-                    if (!more) commit(&bar.o_full[i]);
-                    if (last) commit(&bar.empty[(2 * j + 1) % C::kSlots]);
-                    if (more) {
-                        if (i == 0 && !full(2 * j + 2)) break;
+                for (int i = 0; i < n_tiles; ++i) scores(i, u);
+                commit(&bar.empty[u % C::kSlots]);
+                if (steps == 1) commit(&bar.q_empty);
+                for (int32_t j = 0; j < steps && fine; ++j, u += 2) {
+                    const bool more = j + 1 < steps;
+                    for (int i = 0; i < n_tiles && fine; ++i) {
+                        const bool last = i == n_tiles - 1;
+                        if (i == 0 && !full(u + 1)) break;
+                        // the last item's output has been read
+                        if (j == 0 && ((o_used >> i) & 1) && !wait(&bar.o_empty[i], ((o_parity >> i) & 1) ^ 1)) break;
+                        if (!wait(&bar.p_full[i][0], (p_parity >> i) & 1)) break;
                         tc::fence_after_sync();
-                        scores(i, 2 * j + 2, last);
+                        outputs(i, u + 1, 0, j == 0);
+                        if (!wait(&bar.p_full[i][1], (p_parity >> i) & 1)) break;
+                        tc::fence_after_sync();
+                        outputs(i, u + 1, 1, j == 0);
+                        p_parity ^= 1u << i;
+                        if (!more) {
+                            commit(&bar.o_full[i]);
+                            o_parity ^= 1u << i;
+                            o_used |= 1u << i;
+                        }
+                        if (last) commit(&bar.empty[(u + 1) % C::kSlots]);
+                        if (more) {
+                            if (i == 0 && !full(u + 2)) break;
+                            tc::fence_after_sync();
+                            scores(i, u + 2);
+                            if (last) {
+                                commit(&bar.empty[(u + 2) % C::kSlots]);
+                                if (j + 2 == steps) commit(&bar.q_empty);
+                            }
+                        }
                     }
                 }
+                if (!fine) break;
             }
             // every product has finished, and every arrival landed, before the block ends
             commit(&bar.done);
             if (!tc::mbar_wait_timed(&bar.done, 0, kWaitNs)) fine = false;
+        } else if (warp == 13) {
+            // ---- work -------------------------------------------------------------------
+            // Items in order: pairs of row tiles from the last request's last one down, key
+            // heads innermost.  The pairs above the walk's request are `above`.
+            const int64_t items = total * a.kv.n_kv;
+            int64_t above = total;
+            int32_t seq = a.n_seq;  // requests from here on have been passed
+            int64_t idx = blockIdx.x;
+            for (int32_t k = 0;; ++k) {
+                Item it{};
+                if (idx < items) {
+                    const int64_t want = total - 1 - idx / a.kv.n_kv;
+                    // 32 requests at a time: lane l holds request seq - 1 - l
+                    while (seq > 0) {
+                        const int32_t i = seq - 1 - lane;
+                        RequestRows r{0, 0, 0, false};
+                        if (i >= 0) r = load_rows(a, i);
+                        const int64_t pairs = i >= 0 ? pairs_of(r) : 0;
+                        int64_t incl = pairs;
+#pragma unroll
+                        for (int o = 1; o < 32; o <<= 1) {
+                            const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
+                            if (lane >= o) incl += v;
+                        }
+                        const bool mine = i >= 0 && pairs > 0 && want >= above - incl && want < above - incl + pairs;
+                        const uint32_t who = __ballot_sync(0xffffffffu, mine);
+                        if (who != 0) {
+                            if (mine) {
+                                it.seq = i;
+                                it.head = static_cast<int32_t>(idx % a.kv.n_kv);
+                                it.row0 = static_cast<int32_t>(want - (above - incl)) * 2 * kRows;
+                                it.rows = min(2 * kRows, r.n * a.group - it.row0);
+                                it.q0 = r.q0;
+                                it.n = r.n;
+                                it.len = r.len;
+                                const int32_t first = r.len - r.n + it.row0 / a.group;
+                                const int32_t last = r.len - r.n + (it.row0 + it.rows - 1) / a.group;
+                                it.lo = a.window > 0
+                                            ? static_cast<int32_t>(max(int64_t(0), int64_t(first) - a.window + 1))
+                                            : 0;
+                                it.key0 = it.lo & ~(kKeys - 1);
+                                it.steps = last < 0 ? 0 : (last - it.key0) / kKeys + 1;
+                                it.any = true;
+                            }
+                            // the requests before the one found stay passed over
+                            const int l = __ffs(who) - 1;
+                            above -= __shfl_sync(0xffffffffu, incl - pairs, l);
+                            seq -= l;
+                            break;
+                        }
+                        above -= __shfl_sync(0xffffffffu, incl, 31);
+                        seq -= 32;
+                    }
+                }
+                if (k >= 2 && !wait(&bar.item_empty[k & 1], ((k >> 1) - 1) & 1)) break;
+                const bool any = __any_sync(0xffffffffu, it.any);
+                if (it.any || (!any && lane == 0)) {
+                    s_item[k & 1] = it;
+                    tc::mbar_arrive(&bar.item_full[k & 1]);
+                }
+                __syncwarp();
+                if (!any) {
+                    // the last block to come to the end leaves the claims as they were
+                    if (lane == 0 && atomicAdd(&claims->done, 1) == static_cast<int32_t>(gridDim.x) - 1) {
+                        claims->given = 0;
+                        claims->done = 0;
+                    }
+                    break;
+                }
+                // the next item is claimed when the copies come to this one's last step: late
+                // enough that blocks with short items take more, early enough to hide the claim
+                if (!wait(&bar.claim, k & 1)) break;
+                int32_t next = 0;
+                if (lane == 0) next = atomicAdd(&claims->given, 1);
+                idx = int64_t(gridDim.x) + __shfl_sync(0xffffffffu, next, 0);
+            }
         }
         fine = __all_sync(0xffffffffu, fine);
     } else {
         set_registers<kSoftmaxRegs, true>();
         // ---- softmax --------------------------------------------------------------------
-        const int i = warp >> 2;
+        const int i = warp >> 2, r = i * kRows + (warp & 3) * 32 + lane;
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t s_at = tmem + lanes + i * kKeys, o_at = tmem + lanes + 2 * kKeys + i * 128;
-        if (i < n_tiles) {
-            // the row's place is worked out again for the output: registers are scarce between
-            const auto place = [&](bool &live, int32_t &token, int32_t &h) {
-                const int32_t r = i * kRows + (warp & 3) * 32 + lane, row = s_item.row0 + r;
-                live = r < s_item.rows;
-                token = live ? row / a.group : 0;
-                h = s_item.head * a.group + (live ? row % a.group : 0);
-            };
-            bool live;
-            int32_t token, h;
-            place(live, token, h);
-            const int32_t first_pos = it.len - it.n, key0 = it.key0;
-            const int32_t pos = live ? first_pos + token : -1;
+        const bool plain = a.softcap == 0.0f && a.slopes == nullptr && a.scale > 0.0f;
+        int32_t round = 0, o_round = 0;
+        for (int32_t k = 0;; ++k) {
+            if (!wait(&bar.item_full[k & 1], (k >> 1) & 1) || !s_item[k & 1].any) break;
+            // the item stays in shared memory: registers are scarce in the loop below
+            const Item &it = s_item[k & 1];
+            const int32_t steps = it.steps, key0 = it.key0, first_pos = it.len - it.n;
+            const bool live = r < it.rows;
+            if (it.rows <= i * kRows) {  // this tile has no rows
+                release(k);
+                continue;
+            }
+            const int32_t row = it.row0 + r;
+            const int32_t pos = live ? first_pos + row / a.group : -1;
             const int32_t pos_lo = first_pos + (it.row0 + i * kRows) / a.group;
             const int32_t pos_hi = first_pos + (it.row0 + min(it.rows, (i + 1) * kRows) - 1) / a.group;
-            const float mult = a.scale * a.kv.k_scale, by0 = mult * kLog2e;
-            const float slope = live && a.slopes != nullptr ? a.slopes[h] * kLog2e : 0.0f;
-            const bool plain = a.softcap == 0.0f && a.slopes == nullptr && a.scale > 0.0f;
+            const float slope = live && a.slopes != nullptr ? a.slopes[it.head * a.group + row % a.group] * kLog2e : 0.0f;
+            float mult = a.scale * a.kv.k_scale;
+            if constexpr (E4M3) {
+                // (an item's exponents stay until the item is released)
+                if (!wait(&bar.exp_full[k & 1], (k >> 1) & 1)) break;
+                if (steps > 0) mult *= __uint_as_float(static_cast<uint32_t>(127 + s_qexp[k & 1][r]) << 23);
+            }
+            const float by0 = mult * kLog2e;
             float m = -INFINITY;  // the reference of the row's weights
             uint64_t sum[2] = {0, 0};  // pairs of fp32
-            for (int32_t j = 0; j < steps; ++j) {
-                if (!wait(&bar.s_full[i], j & 1)) break;
+            for (int32_t j = 0; j < steps; ++j, ++round) {
+                if (!wait(&bar.s_full[i], round & 1)) break;
                 tc::fence_after_sync();
                 const int32_t key = key0 + (steps - 1 - j) * kKeys;
                 const bool masked = key + kKeys - 1 > pos_lo || (a.window > 0 && pos_hi - key >= a.window);
@@ -519,17 +654,17 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
                     // the final form of the scores, in place, 64 at a time (one copy of the code)
 #pragma unroll 1
                     for (int c = 0; c < 2; ++c) {
-                        uint32_t r[64];
+                        uint32_t x[64];
                         float s[64];
-                        tmem_ld64(s_at + 64 * c, r);
-                        tmem_wait64(r);
+                        tmem_ld64(s_at + 64 * c, x);
+                        tmem_wait64(x);
 #pragma unroll
-                        for (int e = 0; e < 64; ++e) s[e] = __uint_as_float(r[e]);
+                        for (int e = 0; e < 64; ++e) s[e] = __uint_as_float(x[e]);
                         finish_scores<64, 2>(s, a, mult, slope, key + 64 * c - pos, masked);
 #pragma unroll
-                        for (int e = 0; e < 64; ++e) r[e] = __float_as_uint(s[e]);
-                        tmem_st32(s_at + 64 * c, r);
-                        tmem_st32(s_at + 64 * c + 32, r + 32);
+                        for (int e = 0; e < 64; ++e) x[e] = __float_as_uint(s[e]);
+                        tmem_st32(s_at + 64 * c, x);
+                        tmem_st32(s_at + 64 * c + 32, x + 32);
                     }
                     tmem_wait_st();
                 }
@@ -557,7 +692,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
                     for (int q = 0; q < 2; ++q) sum[q] = mul2(sum[q], f2);
                     if (j > 0) rescale_output<HD>(o_at, f);
                 }
-                const float ref = m == -INFINITY ? 0.0f : -m;
+                const float ref = kShift - (m == -INFINITY ? 0.0f : m);
                 const uint64_t by2 = pack2(by, by), ref2 = pack2(ref, ref);
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
@@ -565,12 +700,12 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
                         float p0, p1;
-                        const int k = 32 * c + 2 * e;
-                        unpack2(fma2(pack2(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), by2, ref2), p0, p1);
+                        const int k2 = 32 * c + 2 * e;
+                        unpack2(fma2(pack2(__uint_as_float(x[k2]), __uint_as_float(x[k2 + 1])), by2, ref2), p0, p1);
                         p0 = ex2(p0);
                         p1 = ex2(p1);
                         sum[e & 1] = add2(sum[e & 1], pack2(p0, p1));
-                        p[e] = pack_bf16x2(p0, p1);
+                        p[e] = E4M3 ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
                     }
                     tmem_st16(s_at + 16 * c, p);
                     if (c & 1) {  // half of the step's weights
@@ -581,32 +716,43 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
                     }
                 }
             }
+            if (!fine || (steps > 0 && !wait(&bar.o_full[i], o_round & 1))) break;
+            tc::fence_after_sync();
             float l, l1;
             unpack2(add2(sum[0], sum[1]), l, l1);
             l += l1;
-            if (fine && wait(&bar.o_full[i], 0)) {
-                tc::fence_after_sync();
-                const float inv = l > 0.0f ? a.kv.v_scale / l : l == 0.0f ? 0.0f : l;
-                place(live, token, h);
-                const int64_t t = s_item.q0 + token;
-                uint16_t *dst = a.out + t * a.ldo + h * HD;
-                uint32_t x[32];
+            const float inv = l > 0.0f ? a.kv.v_scale / l : l == 0.0f ? 0.0f : l;
+            const int32_t out_row = it.row0 + r, h = it.head * a.group + out_row % a.group;
+            const int64_t t = it.q0 + (live ? out_row / a.group : 0);
+            uint16_t *dst = a.out + t * a.ldo + h * HD;
 #pragma unroll
-                for (int c = 0; c < HD / 32; ++c) {
+            for (int c = 0; c < HD / 32; ++c) {
+                uint32_t x[32], o[16];
+                if (steps > 0) {
                     tmem_ld32(o_at + 32 * c, x);
                     tmem_wait(x);
-                    uint32_t o[16];
+                } else {
 #pragma unroll
-                    for (int e = 0; e < 16; ++e)
-                        o[e] = pack_bf16x2(__uint_as_float(x[2 * e]) * inv, __uint_as_float(x[2 * e + 1]) * inv);
-                    if (live) {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            stg_u4(dst + 32 * c + 8 * e, make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]));
-                    }
+                    for (int e = 0; e < 32; ++e) x[e] = 0u;
                 }
-                if (live && a.lse != nullptr) a.lse[t * a.n_heads + h] = l == 0.0f ? -INFINITY : kLn2 * m + logf(l);
+                if (c == HD / 32 - 1 && steps > 0) {  // all of O is in registers
+                    tc::fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) tc::mbar_arrive(&bar.o_empty[i]);
+                }
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                    o[e] = pack_bf16x2(__uint_as_float(x[2 * e]) * inv, __uint_as_float(x[2 * e + 1]) * inv);
+                if (live) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        stg_u4(dst + 32 * c + 8 * e, make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]));
+                }
             }
+            if (steps > 0) ++o_round;
+            if (live && a.lse != nullptr)
+                a.lse[t * a.n_heads + h] = l == 0.0f ? -INFINITY : kLn2 * (m - kShift) + logf(l);
+            release(k);
         }
     }
     // a wait that gave up stops the block's other roles; what is in flight lands before
@@ -625,22 +771,25 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
 }
 
 template <int HD, bool E4M3>
-cudaError_t launch(const AttendArgs &a, cudaStream_t stream) {
+cudaError_t launch(const AttendArgs &a, void *claims, cudaStream_t stream) {
     using C = PromptConfig<HD>;
     const auto kernel = attend_prompt_kernel<HD, E4M3>;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    int device = 0, sms = 0;
+    cudaError_t e = cudaGetDevice(&device);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
     // every request's rows fill pairs of tiles but for one
-    const int64_t pairs = int64_t(a.T) * a.group / (2 * kRows) + a.n_seq;
-    if (pairs * a.kv.n_kv > INT32_MAX) return cudaErrorInvalidConfiguration;
-    return launch_dependent(kernel, static_cast<unsigned>(pairs * a.kv.n_kv), kThreads, C::kSmem, stream, a);
+    const int64_t items = (int64_t(a.T) * a.group / (2 * kRows) + a.n_seq) * a.kv.n_kv;
+    const unsigned grid = static_cast<unsigned>(items < sms ? items : sms);
+    return launch_dependent(kernel, grid, kThreads, C::kSmem, stream, a, static_cast<Claims *>(claims));
 }
 
 }  // namespace
 
-cudaError_t launch_attend_prompt(const AttendArgs &a, bool e4m3, cudaStream_t stream) {
-    if (a.kv.head_dim == 64) return e4m3 ? launch<64, true>(a, stream) : launch<64, false>(a, stream);
-    return e4m3 ? launch<128, true>(a, stream) : launch<128, false>(a, stream);
+cudaError_t launch_attend_prompt(const AttendArgs &a, bool e4m3, void *claims, cudaStream_t stream) {
+    if (a.kv.head_dim == 64) return e4m3 ? launch<64, true>(a, claims, stream) : launch<64, false>(a, claims, stream);
+    return e4m3 ? launch<128, true>(a, claims, stream) : launch<128, false>(a, claims, stream);
 }
 
 }  // namespace lora

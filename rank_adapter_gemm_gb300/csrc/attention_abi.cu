@@ -15,7 +15,7 @@ cudaError_t launch_rope_append(const uint16_t *qkv, int64_t ldqkv, int32_t T, in
                                const KvView &kv, bool e4m3, int32_t *err, cudaStream_t stream);
 size_t decode_workspace_bytes(int32_t head_dim);
 cudaError_t launch_attend_decode(const AttendArgs &a, bool e4m3, int32_t max_q, void *ws, cudaStream_t stream);
-cudaError_t launch_attend_prompt(const AttendArgs &a, bool e4m3, cudaStream_t stream);
+cudaError_t launch_attend_prompt(const AttendArgs &a, bool e4m3, void *claims, cudaStream_t stream);
 }  // namespace lora
 
 using lora::aligned16;
@@ -172,7 +172,8 @@ lora_status_t lora_attend(const void *q, int64_t ldq, void *out, int64_t ldo, fl
     const bool e4m3 = kv->type == LORA_KV_E4M3;
     if (lora_attend_resolve_path(path, att, kv, max_q_hint) == LORA_ATTEND_DECODE)
         return from_cuda(lora::launch_attend_decode(a, e4m3, max_q_hint, ws, s));
-    return from_cuda(lora::launch_attend_prompt(a, e4m3, s));
+    // the decode path's counters and the prompt path's claims share the first kilobyte
+    return from_cuda(lora::launch_attend_prompt(a, e4m3, static_cast<char *>(ws) + 768, s));
 }
 
 }  // extern "C"
