@@ -190,6 +190,13 @@ __device__ __forceinline__ void sts16(uint32_t addr, uint4 v) {
                  : "memory");
 }
 
+__device__ __forceinline__ uint4 lds16(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr)
+                 : "memory");
+    return v;
+}
+
 // Byte offset of the 8-element piece of a row in a tile: 64 dims a 128-byte row.
 __device__ __forceinline__ uint32_t tile_at(int row, int piece) {
     return (piece >> 3) * (kRows * 128) + row * 128 + (((piece & 7) ^ (row & 7)) << 4);
@@ -323,29 +330,35 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
                     }
                 }
                 if constexpr (E4M3) {
-                    // each lane turns the pieces that it copied into f16, in place
+                    // a lane turns a row into f16, in place, scaled to lie below 2
                     tc::cp_wait_all();
-#pragma unroll 2
-                    for (int i = 0; i < 2 * kPieces; ++i) {
-                        const int r = w * 64 + i * kStep + row_in;
-                        uint32_t x[4];
-                        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
-                                     : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]) : "r"(q_piece(r)) : "memory");
-                        float top = 0.0f;
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            top = fmaxf(fmaxf(top, fabsf(bf16lo_to_f32(x[e]))), fabsf(bf16hi_to_f32(x[e])));
-#pragma unroll
-                        for (int s = kPieces / 2; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
-                        // 2^e <= top < 2^(e + 1): the row times 2^-e is below 2
-                        const int e2 = top > 0.0f ? max(-60, min(60, static_cast<int>(__float_as_uint(top) >> 23) - 127))
-                                                  : 0;
+                    __syncwarp();
+#pragma unroll 1
+                    for (int half = 0; half < 2; ++half) {
+                        const int r = w * 64 + half * 32 + lane;
+                        const uint32_t tile = q_base + (r / kRows) * C::kTileB;
+                        uint32_t top2 = 0;  // the row's largest size, as a pair of bf16 bit patterns
+#pragma unroll 4
+                        for (int p = 0; p < kPieces; ++p) {
+                            const uint4 v = lds16(tile + tile_at(r % kRows, p));
+                            top2 = __vmaxu2(top2, __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu),
+                                                           __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu)));
+                        }
+                        const uint32_t top = max(top2 & 0xffffu, top2 >> 16);  // (bf16 sizes order like integers)
+                        // 2^e <= top < 2^(e + 1)
+                        const int e2 = top > 0 ? max(-60, min(60, static_cast<int>(top >> 7) - 127)) : 0;
                         const float down = __uint_as_float(static_cast<uint32_t>(127 - e2) << 23);
+                        s_qexp[k & 1][r] = static_cast<int8_t>(e2);
+#pragma unroll 4
+                        for (int p = 0; p < kPieces; ++p) {
+                            const uint32_t at = tile + tile_at(r % kRows, p);
+                            const uint4 v = lds16(at);
+                            uint32_t x[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            x[e] = pack_f16x2(bf16lo_to_f32(x[e]) * down, bf16hi_to_f32(x[e]) * down);
-                        sts16(q_piece(r), make_uint4(x[0], x[1], x[2], x[3]));
-                        if (piece == 0) s_qexp[k & 1][r] = static_cast<int8_t>(e2);
+                            for (int e = 0; e < 4; ++e)
+                                x[e] = pack_f16x2(bf16lo_to_f32(x[e]) * down, bf16hi_to_f32(x[e]) * down);
+                            sts16(at, make_uint4(x[0], x[1], x[2], x[3]));
+                        }
                     }
                 }
                 if (E4M3) publish(&bar.q_full);
