@@ -14,16 +14,26 @@ from typing import Mapping, Optional
 
 import numpy as np
 
-from . import _dev, _p, _stream, _torch
+from . import _dev, _p, _torch
 from ._lib import (ATTEND_PATHS, LORA_MAX_SEQS, ROPE_KINDS, check, load, lora_attention_t, lora_kv_t,
                    lora_rope_scaling_t, lora_rope_t)
 
 
 # The checks below run on every call of a decode loop: they read each property
-# once and leave the wording of a refusal to the slow path.
+# once and leave the wording of a refusal to the slow path.  torch is loaded with
+# the first call, as in the rest of the binding.
+_I32 = _I64 = _F32 = _BF16 = _C = None
+
+
+def _types():
+    global _I32, _I64, _F32, _BF16, _C
+    torch = _torch()
+    _I32, _I64, _F32, _BF16, _C = torch.int32, torch.int64, torch.float32, torch.bfloat16, torch._C
+
+
 def _flat(t, name, dtype, n=None) -> int:
     """Address of a contiguous device tensor of n elements (any number: None)."""
-    if (getattr(t, "dtype", None) is dtype and t.is_cuda and t.is_contiguous() and (n is None or t.numel() == n)):
+    if getattr(t, "dtype", None) is dtype and t.is_cuda and t.is_contiguous() and (n is None or t.numel() == n):
         return t.data_ptr()
     _dev(t, name, dtype)
     raise ValueError(f"{name} must be contiguous" + (f" with {n} elements" if n is not None else ""))
@@ -31,38 +41,45 @@ def _flat(t, name, dtype, n=None) -> int:
 
 def _table(t, n_seq):
     """(address, row stride, width) of a block table."""
-    if getattr(t, "dtype", None) is _torch().int32 and t.is_cuda and t.dim() == 2:
+    if getattr(t, "dtype", None) is _I32 and t.is_cuda and t.dim() == 2:
         rows, width = t.shape
         ld, one = t.stride()
         if rows == n_seq and (one == 1 or width <= 1):
             return t.data_ptr(), ld if ld > width else width, width
-    _dev(t, "block_table", _torch().int32)
+    _dev(t, "block_table", _I32)
     raise ValueError("block_table must be a 2-D int32 tensor, one row a request, with unit column stride")
 
 
 def _matrix(t, name):
     """(address, row stride, rows, columns) of bf16 rows."""
-    if getattr(t, "dtype", None) is _torch().bfloat16 and t.is_cuda and t.dim() == 2:
+    if getattr(t, "dtype", None) is _BF16 and t.is_cuda and t.dim() == 2:
         rows, cols = t.shape
         ld, one = t.stride()
         if one == 1:
             return t.data_ptr(), ld, rows, cols
-    _dev(t, name, _torch().bfloat16)
+    _dev(t, name, _BF16)
     raise ValueError(f"{name} must be a 2-D bf16 tensor with unit column stride")
+
+
+def _on(stream) -> int:
+    """A stream's address; the current one's without building a Stream object (2.8 us on a Grace core)."""
+    return _C._cuda_getCurrentRawStream(_C._cuda_getDevice()) if stream is None else stream.cuda_stream
 
 
 def lora_kv_step(ctx_lens, new_lens, page_size, free_pages, block_table, q_offsets, kv_lens, positions, seq_ids,
                  slot_map, taken, err, stream=None) -> None:
-    torch = _torch()
-    i32, n, T = torch.int32, ctx_lens.numel(), positions.numel()
+    if _C is None:
+        _types()
+    n, T = ctx_lens.numel(), positions.numel()
     table, ld, width = _table(block_table, n)
-    check(load().lora_kv_step(
-        _flat(ctx_lens, "ctx_lens", i32), _flat(new_lens, "new_lens", i32, n), n, page_size,
-        _flat(free_pages, "free_pages", i32), free_pages.numel(), table, ld, width, T,
-        _flat(q_offsets, "q_offsets", i32, n + 1), _flat(kv_lens, "kv_lens", i32, n),
-        _flat(positions, "positions", i32), _flat(seq_ids, "seq_ids", i32, T),
-        _flat(slot_map, "slot_map", torch.int64, T), _flat(taken, "taken", i32, 1),
-        None if err is None else _flat(err, "err", i32), _stream(stream)), "lora_kv_step")
+    status = load().lora_kv_step(
+        _flat(ctx_lens, "ctx_lens", _I32), _flat(new_lens, "new_lens", _I32, n), n, page_size,
+        _flat(free_pages, "free_pages", _I32), free_pages.numel(), table, ld, width, T,
+        _flat(q_offsets, "q_offsets", _I32, n + 1), _flat(kv_lens, "kv_lens", _I32, n),
+        _flat(positions, "positions", _I32), _flat(seq_ids, "seq_ids", _I32, T), _flat(slot_map, "slot_map", _I64, T),
+        _flat(taken, "taken", _I32, 1), None if err is None else _flat(err, "err", _I32), _on(stream))
+    if status:
+        check(status, "lora_kv_step")
 
 
 def lora_rope_phases(rot_dim: int, theta: float, scaling: Optional[Mapping] = None):
@@ -88,16 +105,18 @@ def lora_rope_phases(rot_dim: int, theta: float, scaling: Optional[Mapping] = No
 
 def lora_rope_append(qkv, q_out, n_heads, rope: lora_rope_t, positions, slot_map, kv: lora_kv_t, err,
                      stream=None) -> None:
-    torch = _torch()
+    if _C is None:
+        _types()
     x, ldx, T, cols = _matrix(qkv, "qkv")
     q, ldq, rows, q_cols = _matrix(q_out, "q_out")
     hd = kv.head_dim
     if rows != T or cols != (n_heads + 2 * kv.n_kv) * hd or q_cols < n_heads * hd:
         raise ValueError("qkv must have n_heads + 2 n_kv heads and q_out n_heads heads, with the same rows")
-    check(load().lora_rope_append(
-        x, ldx, T, n_heads, rope, _flat(positions, "positions", torch.int32, T),
-        _flat(slot_map, "slot_map", torch.int64, T), q, ldq, kv,
-        None if err is None else _flat(err, "err", torch.int32), _stream(stream)), "lora_rope_append")
+    status = load().lora_rope_append(
+        x, ldx, T, n_heads, rope, _flat(positions, "positions", _I32, T), _flat(slot_map, "slot_map", _I64, T), q, ldq,
+        kv, None if err is None else _flat(err, "err", _I32), _on(stream))
+    if status:
+        check(status, "lora_rope_append")
 
 
 def lora_attend_workspace_bytes(att: lora_attention_t, kv: lora_kv_t) -> int:
@@ -113,19 +132,22 @@ def lora_attend_resolve_path(path: str, att: lora_attention_t, kv: lora_kv_t, ma
 
 def lora_attend(q, out, q_offsets, kv_lens, block_table, kv: lora_kv_t, att: lora_attention_t, ws, err,
                 max_q_hint: int = 0, lse=None, path: str = "auto", stream=None) -> None:
-    torch = _torch()
-    i32, n = torch.int32, kv_lens.numel()
+    if _C is None:
+        _types()
+    n = kv_lens.numel()
     x, ldq, T, q_cols = _matrix(q, "q")
     o, ldo, rows, o_cols = _matrix(out, "out")
     cols = att.n_heads * kv.head_dim
     if rows != T or q_cols < cols or o_cols < cols:
         raise ValueError("q and out must have the same rows and n_heads * head_dim columns")
     table, ld, width = _table(block_table, n)
-    check(load().lora_attend(
-        x, ldq, o, ldo, None if lse is None else _flat(lse, "lse", torch.float32, T * att.n_heads), T, n,
-        _flat(q_offsets, "q_offsets", i32, n + 1), _flat(kv_lens, "kv_lens", i32), table, ld, width, kv, att,
-        max_q_hint, ATTEND_PATHS[path], _flat(ws, "ws", torch.uint8), ws.numel(),
-        None if err is None else _flat(err, "err", i32), _stream(stream)), "lora_attend")
+    status = load().lora_attend(
+        x, ldq, o, ldo, None if lse is None else _flat(lse, "lse", _F32, T * att.n_heads), T, n,
+        _flat(q_offsets, "q_offsets", _I32, n + 1), _flat(kv_lens, "kv_lens", _I32), table, ld, width, kv, att,
+        max_q_hint, ATTEND_PATHS[path], ws.data_ptr(), ws.numel() * ws.element_size(),
+        None if err is None else _flat(err, "err", _I32), _on(stream))
+    if status:
+        check(status, "lora_attend")
 
 
 class PagedKV:
@@ -158,22 +180,34 @@ class PagedKV:
 class KVStep:
     """Block tables and the per-step arrays of lora_kv_step: room for T rows of
     n_seq requests of up to max_pages pages.  The block table persists over
-    steps; ``taken`` is the number of pages taken from the front of free_pages."""
+    steps (it may be replaced by another [n_seq, pages] tensor); ``taken`` is the
+    number of pages taken from the front of free_pages.  The other arrays are
+    the step's own for its lifetime."""
+
+    _OWN = ("q_offsets", "kv_lens", "positions", "seq_ids", "slot_map", "taken", "err")
 
     def __init__(self, n_seq: int, T: int, max_pages: int, page_size: int, device="cuda"):
         torch = _torch()
-        self.page_size = int(page_size)
-
-        def zeros(*shape, dtype=torch.int32):
-            return torch.zeros(*shape, dtype=dtype, device=device)
-        self.block_table = zeros(n_seq, max_pages)
-        self.q_offsets, self.kv_lens = zeros(n_seq + 1), zeros(n_seq)
-        self.positions, self.seq_ids, self.slot_map = zeros(T), zeros(T), zeros(T, dtype=torch.int64)
-        self.taken, self.err = zeros(1), zeros(1)
+        _types()
+        self.page_size, self.n_seq, self.T = int(page_size), int(n_seq), int(T)
+        self.block_table = torch.zeros(n_seq, max_pages, dtype=_I32, device=device)
+        sizes = dict(q_offsets=n_seq + 1, kv_lens=n_seq, positions=T, seq_ids=T, slot_map=T, taken=1, err=1)
+        self._own = tuple(torch.zeros(sizes[k], dtype=_I64 if k == "slot_map" else _I32, device=device)
+                          for k in self._OWN)
+        self._at = tuple(t.data_ptr() for t in self._own)
 
     def build(self, ctx_lens, new_lens, free_pages, stream=None) -> None:
-        lora_kv_step(ctx_lens, new_lens, self.page_size, free_pages, self.block_table, self.q_offsets, self.kv_lens,
-                     self.positions, self.seq_ids, self.slot_map, self.taken, self.err, stream)
+        n = self.n_seq
+        table, ld, width = _table(self.block_table, n)
+        status = load().lora_kv_step(
+            _flat(ctx_lens, "ctx_lens", _I32, n), _flat(new_lens, "new_lens", _I32, n), n, self.page_size,
+            _flat(free_pages, "free_pages", _I32), free_pages.numel(), table, ld, width, self.T, *self._at, _on(stream))
+        if status:
+            check(status, "lora_kv_step")
+
+
+for _i, _name in enumerate(KVStep._OWN):
+    setattr(KVStep, _name, property(lambda self, i=_i: self._own[i]))
 
 
 class Rope:

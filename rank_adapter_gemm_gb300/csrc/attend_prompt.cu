@@ -787,10 +787,9 @@ template <int HD, bool E4M3>
 cudaError_t launch(const AttendArgs &a, void *claims, cudaStream_t stream) {
     using C = PromptConfig<HD>;
     const auto kernel = attend_prompt_kernel<HD, E4M3>;
-    int device = 0, sms = 0;
-    cudaError_t e = cudaGetDevice(&device);
-    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    static std::atomic<uint64_t> seen{0};
+    int sms = 0;
+    const cudaError_t e = prepare_kernel(kernel, C::kSmem, seen, &sms);
     if (e != cudaSuccess) return e;
     // every request's rows fill pairs of tiles but for one
     const int64_t items = (int64_t(a.T) * a.group / (2 * kRows) + a.n_seq) * a.kv.n_kv;

@@ -2,6 +2,7 @@
 // (lora_attention.h) and their C entry points.
 #pragma once
 
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 
@@ -54,6 +55,28 @@ __device__ __forceinline__ RequestRows load_rows(const AttendArgs &a, int32_t i)
 __device__ __forceinline__ void wait_for_previous() {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+// The current device's SM count, after raising `kernel`'s shared memory limit to
+// smem there: both looked up once a device (`seen`: one word a kernel, a bit a device).
+template <class K>
+cudaError_t prepare_kernel(K kernel, int smem, std::atomic<uint64_t> &seen, int *sms) {
+    static std::atomic<int> counts[64];
+    int device = 0;
+    cudaError_t e = cudaGetDevice(&device);
+    if (e != cudaSuccess) return e;
+    const bool known = device < 64 && ((seen.load(std::memory_order_acquire) >> device) & 1);
+    if (known) {
+        *sms = counts[device].load(std::memory_order_relaxed);
+        return cudaSuccess;
+    }
+    e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, device);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e == cudaSuccess && device < 64) {
+        counts[device].store(*sms, std::memory_order_relaxed);
+        seen.fetch_or(uint64_t(1) << device, std::memory_order_release);
+    }
+    return e;
 }
 
 template <class... P, class... A>
