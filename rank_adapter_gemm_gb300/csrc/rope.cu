@@ -81,6 +81,13 @@ __global__ void __launch_bounds__(kThreads) rope_append_kernel(RopeArgs a) {
     const bool turned = 16 * u < a.rot;
     const bool half = turned && !a.interleaved;
     const int32_t c0 = half ? 8 * u : 16 * u, c1 = half ? 8 * u + a.rot / 2 : 16 * u + 8;
+    const uint16_t *row = a.qkv + t * a.ldqkv;
+    // a head's loads are issued one head ahead, the first before the angles are known
+    uint4 w0 = make_uint4(0, 0, 0, 0), w1 = w0;
+    if (h0 < total) {
+        w0 = ldg_stream(row + h0 * hd + c0);
+        w1 = ldg_stream(row + h0 * hd + c1);
+    }
     float cs[8], sn[8];
     if (turned) {
 #pragma unroll
@@ -94,12 +101,14 @@ __global__ void __launch_bounds__(kThreads) rope_append_kernel(RopeArgs a) {
     const bool slot_ok = slot >= 0 && slot < (int64_t(a.kv.n_pages) << a.kv.page_shift);
     if (!slot_ok && slot != -1 && threadIdx.x == 0) report_error(a.err, LORA_ERR_SLOT_RANGE);
     const int64_t at = slot_ok ? (slot >> a.kv.page_shift) * a.kv.page_b + (slot & a.kv.page_mask) * a.kv.token_b : 0;
-    const uint16_t *row = a.qkv + t * a.ldqkv;
     for (int32_t h = h0; h < total; h += per_pass) {
-        const uint4 w0 = ldg_stream(row + h * hd + c0), w1 = ldg_stream(row + h * hd + c1);
         float x[8], y[8];
         unpack8(w0, x);
         unpack8(w1, y);
+        if (h + per_pass < total) {
+            w0 = ldg_stream(row + (h + per_pass) * hd + c0);
+            w1 = ldg_stream(row + (h + per_pass) * hd + c1);
+        }
         if (turned && h < H + nk) {
             if (a.interleaved) {
 #pragma unroll
