@@ -9,11 +9,16 @@
 // 2^-20 of the true ones, far inside the 2^-9 of the bf16 result, and no table
 // of cosines is read from memory.
 //
-// One block a token.  A unit is 16 elements of a head that are rotated among
-// themselves: two 8-element (16-byte) pieces j and j + rot / 16 of the half
-// layout, or two adjacent pieces (interleaved pairs, and the dims past rot).
-// A thread keeps one unit index for all its heads, so its eight sines and
-// cosines are computed once a token.
+// A unit is 16 elements of a head that are rotated among themselves: two
+// 8-element (16-byte) pieces j and j + rot / 16 of the half layout, or two
+// adjacent pieces (interleaved pairs, and the dims past rot).  A thread keeps one
+// unit index for all its heads, so its eight sines and cosines are computed once
+// a token: with many tokens a token gets only as many threads as leave each about
+// six heads, so that the angles cost less than the bytes (16,384 tokens of 32/8
+// heads of 128: 128 threads a token 65.4 us, 64 threads 63.4; of 8/1 heads of 64:
+// a block a token 22.8 us, several tokens a block 10.4); with few tokens each gets
+// a whole block, for latency (256 tokens 3.3 us, with 64 threads 3.9).
+// Bound by HBM: 402 MB of q, k and v in and out at 16,384 tokens.
 #include <cuda_fp8.h>
 
 #include "attention.cuh"
@@ -23,6 +28,7 @@ namespace lora {
 namespace {
 
 constexpr int kThreads = 128;
+constexpr int kManyTokens = 2048;  // from here on blocks fill the GPU several times over
 
 struct RopeArgs {
     const uint16_t *qkv;
@@ -33,8 +39,9 @@ struct RopeArgs {
     const int64_t *slots;
     int32_t *err;
     KvView kv;
-    int32_t n_heads, rot, interleaved;
+    int32_t T, n_heads, rot, interleaved;
     float mscale;
+    int32_t per_pass, tokens;  // heads that a token's threads take at a time, tokens a block
 };
 
 __device__ __forceinline__ void unpack8(uint4 w, float *f) {
@@ -68,12 +75,19 @@ __device__ __forceinline__ uint2 pack8_e4m3(const float *f, float scale) {
 }
 
 template <bool E4M3>
-__global__ void __launch_bounds__(kThreads) rope_append_kernel(RopeArgs a) {
+__global__ void __launch_bounds__(kThreads, 8) rope_append_kernel(RopeArgs a) {
     wait_for_previous();
-    const int32_t hd = a.kv.head_dim, units = hd / 16, per_pass = kThreads / units;
-    const int32_t u = threadIdx.x % units, h0 = threadIdx.x / units;
-    if (h0 >= per_pass) return;
-    const int64_t t = blockIdx.x;
+    const int32_t hd = a.kv.head_dim, units = hd / 16, per_pass = a.per_pass, group = units * per_pass;
+    int32_t r = threadIdx.x;
+    int64_t t = blockIdx.x;
+    if (a.tokens > 1) {
+        const int32_t i = r / group;
+        r -= i * group;
+        t = t * a.tokens + i;
+        if (i >= a.tokens || t >= a.T) return;
+    }
+    if (r >= group) return;
+    const int32_t h0 = r / units, u = r - h0 * units;
     const int32_t pos = a.positions[t];
     const int64_t slot = a.slots[t];
     const int32_t nk = a.kv.n_kv, H = a.n_heads, total = H + 2 * nk;
@@ -99,7 +113,7 @@ __global__ void __launch_bounds__(kThreads) rope_append_kernel(RopeArgs a) {
         }
     }
     const bool slot_ok = slot >= 0 && slot < (int64_t(a.kv.n_pages) << a.kv.page_shift);
-    if (!slot_ok && slot != -1 && threadIdx.x == 0) report_error(a.err, LORA_ERR_SLOT_RANGE);
+    if (!slot_ok && slot != -1 && r == 0) report_error(a.err, LORA_ERR_SLOT_RANGE);
     const int64_t at = slot_ok ? (slot >> a.kv.page_shift) * a.kv.page_b + (slot & a.kv.page_mask) * a.kv.token_b : 0;
     for (int32_t h = h0; h < total; h += per_pass) {
         float x[8], y[8];
@@ -153,9 +167,16 @@ __global__ void __launch_bounds__(kThreads) rope_append_kernel(RopeArgs a) {
 cudaError_t launch_rope_append(const uint16_t *qkv, int64_t ldqkv, int32_t T, int32_t n_heads, const lora_rope_t &rope,
                                const int32_t *positions, const int64_t *slots, uint16_t *q_out, int64_t ldq,
                                const KvView &kv, bool e4m3, int32_t *err, cudaStream_t stream) {
-    const RopeArgs a{qkv,  q_out,   ldqkv,        ldq,              rope.phases, positions, slots, err, kv,
-                     n_heads, rope.rot_dim, rope.interleaved, rope.mscale};
-    return launch_dependent(e4m3 ? rope_append_kernel<true> : rope_append_kernel<false>, T, kThreads, 0, stream, a);
+    const int32_t units = kv.head_dim / 16, total = n_heads + 2 * kv.n_kv, most = kThreads / units;
+    int32_t per_pass = total < most ? total : most;
+    if (T >= kManyTokens && per_pass > total / 6) per_pass = total / 6 > 1 ? total / 6 : 1;
+    // a token of 64 threads or more has its own block: half a wide block would wait for the other half
+    const int32_t group = units * per_pass, threads = group >= 64 ? (group + 31) & ~31 : kThreads;
+    const int32_t tokens = threads < 2 * group ? 1 : threads / group;
+    const RopeArgs a{qkv, q_out, ldqkv, ldq, rope.phases, positions, slots, err, kv, T, n_heads, rope.rot_dim,
+                     rope.interleaved, rope.mscale, per_pass, tokens};
+    return launch_dependent(e4m3 ? rope_append_kernel<true> : rope_append_kernel<false>, (T - 1) / tokens + 1, threads,
+                            0, stream, a);
 }
 
 }  // namespace lora
