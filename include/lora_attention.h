@@ -196,9 +196,9 @@ typedef enum {
 
 lora_status_t lora_attend_workspace_bytes(const lora_attention_t *att, const lora_kv_t *kv, size_t *bytes);
 
-/* The path lora_attend takes for `requested`, this shape and max_q_hint rows a request. */
+/* The path lora_attend takes for `requested`, this shape and n_seq requests of at most max_q_hint rows (host only). */
 lora_attend_path_t lora_attend_resolve_path(lora_attend_path_t requested, const lora_attention_t *att,
-                                            const lora_kv_t *kv, int32_t max_q_hint);
+                                            const lora_kv_t *kv, int32_t n_seq, int32_t max_q_hint);
 
 lora_status_t lora_attend(const void *q, int64_t ldq, void *out, int64_t ldo, float *lse, int32_t T, int32_t n_seq,
                           const int32_t *q_offsets, const int32_t *kv_lens, const int32_t *block_table,

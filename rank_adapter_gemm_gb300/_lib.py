@@ -163,7 +163,7 @@ def load() -> ctypes.CDLL:
                                   ctypes.POINTER(ctypes.c_float)]),
         "lora_rope_append": (ST, [P, I64, I32, I32, ctypes.POINTER(lora_rope_t), P, P, P, I64, KV, P, P]),
         "lora_attend_workspace_bytes": (ST, [AT, KV, ctypes.POINTER(SZ)]),
-        "lora_attend_resolve_path": (ST, [ST, AT, KV, I32]),
+        "lora_attend_resolve_path": (ST, [ST, AT, KV, I32, I32]),
         "lora_attend": (ST, [P, I64, P, I64, P, I32, I32, P, P, P, I64, I32, KV, AT, I32, ST, P, SZ, P, P]),
     }
     for name, (res, args) in sig.items():

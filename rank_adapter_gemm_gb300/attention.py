@@ -125,8 +125,9 @@ def lora_attend_workspace_bytes(att: lora_attention_t, kv: lora_kv_t) -> int:
     return int(out.value)
 
 
-def lora_attend_resolve_path(path: str, att: lora_attention_t, kv: lora_kv_t, max_q_hint: int) -> str:
-    code = load().lora_attend_resolve_path(ATTEND_PATHS[path], att, kv, int(max_q_hint))
+def lora_attend_resolve_path(path: str, att: lora_attention_t, kv: lora_kv_t, n_seq: int, max_q_hint: int) -> str:
+    """The path lora_attend takes for n_seq requests of at most max_q_hint rows."""
+    code = load().lora_attend_resolve_path(ATTEND_PATHS[path], att, kv, int(n_seq), int(max_q_hint))
     return {v: k for k, v in ATTEND_PATHS.items()}[int(code)]
 
 

@@ -135,10 +135,21 @@ lora_status_t lora_attend_workspace_bytes(const lora_attention_t *att, const lor
     return LORA_OK;
 }
 
+// The decode path reads a request's cache once for every 32 of its rows, spread over
+// the whole GPU; the prompt path gives 256 rows of a key head to one block, so its
+// time does not grow with rows but steps with the waves of such blocks on 152 SMs.
+// Measured a key: 16 rows of a key head on the decode path cost about 1/256 of a
+// wave on the prompt path.  Both sides, us (decode / prompt, 32/8 heads of 128):
+// 64 requests of 100 to 8,000 tokens, 4 rows 87 / 111, 8 rows 117 / 113, 16 rows
+// 183 / 115; 8 requests of 4,096, 8 rows 48 / 51, 16 rows 66 / 52; one request of
+// 16,384, 32 rows 66 / 179, 96 rows 137 / 231.
 lora_attend_path_t lora_attend_resolve_path(lora_attend_path_t requested, const lora_attention_t *att,
-                                            const lora_kv_t *kv, int32_t max_q_hint) {
+                                            const lora_kv_t *kv, int32_t n_seq, int32_t max_q_hint) {
     if (requested != LORA_ATTEND_AUTO || att == nullptr || kv == nullptr || kv->n_kv < 1) return requested;
-    return int64_t(max_q_hint) * (att->n_heads / kv->n_kv) <= 32 ? LORA_ATTEND_DECODE : LORA_ATTEND_PROMPT;
+    const int64_t rows = int64_t(max_q_hint) * (att->n_heads / kv->n_kv), pairs = int64_t(n_seq) * kv->n_kv;
+    const int64_t half_tiles = rows <= 16 ? 1 : 2 * ((rows + 31) / 32);
+    const int64_t waves = (pairs * ((rows + 255) / 256) + 151) / 152;
+    return pairs * half_tiles < 256 * waves ? LORA_ATTEND_DECODE : LORA_ATTEND_PROMPT;
 }
 
 lora_status_t lora_attend(const void *q, int64_t ldq, void *out, int64_t ldo, float *lse, int32_t T, int32_t n_seq,
@@ -170,7 +181,7 @@ lora_status_t lora_attend(const void *q, int64_t ldq, void *out, int64_t ldo, fl
                              att->softcap > 0.0f ? 1.0f / att->softcap : 0.0f};
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const bool e4m3 = kv->type == LORA_KV_E4M3;
-    if (lora_attend_resolve_path(path, att, kv, max_q_hint) == LORA_ATTEND_DECODE)
+    if (lora_attend_resolve_path(path, att, kv, n_seq, max_q_hint) == LORA_ATTEND_DECODE)
         return from_cuda(lora::launch_attend_decode(a, e4m3, max_q_hint, ws, s));
     // the decode path's counters and the prompt path's claims share the first kilobyte
     return from_cuda(lora::launch_attend_prompt(a, e4m3, static_cast<char *>(ws) + 768, s));

@@ -182,11 +182,15 @@ def test_host_refusals(L):
 
 def test_attend_path_choice(L):
     from rank_adapter_gemm_gb300._lib import lora_attention_t
-    att, kv = lora_attention_t(8, 0.1, 0.0, 0, None), _kv()
-    assert L.lora_attend_resolve_path("auto", att, kv, 1) == "decode"
-    assert L.lora_attend_resolve_path("auto", att, kv, 1000) == "prompt"
-    assert L.lora_attend_resolve_path("decode", att, kv, 1000) == "decode"
-    assert L.lora_attend_resolve_path("prompt", att, kv, 1) == "prompt"
+    att, kv = lora_attention_t(8, 0.1, 0.0, 0, None), _kv()  # 4 query heads a key head
+
+    def path(n_seq, max_q, asked="auto"):
+        return L.lora_attend_resolve_path(asked, att, kv, n_seq, max_q)
+    assert path(1, 1) == path(4096, 1) == path(4096, 4) == "decode"
+    assert path(1, 1000) == path(300, 8) == path(2, 1 << 30) == "prompt"
+    # few requests: the decode path splits the cache, the prompt path would leave SMs idle
+    assert path(1, 64) == "decode" and path(64, 64) == "prompt"
+    assert path(1, 1000, "decode") == "decode" and path(1, 1, "prompt") == "prompt"
 
 
 def test_binding_refuses_host_tensors_and_wrong_types(L):
@@ -797,3 +801,53 @@ def test_two_steps_through_one_cache(L):
             tol = 2.0 ** -8 * np.abs(ref) + (2.0 ** -8 * 1.01 + 2.0 ** -8 * (1 + big[..., None])) * size
             assert (np.abs(got - ref) <= tol).all()
             at += new[i]
+
+
+@gpu
+@pytest.mark.parametrize("kw", [dict(), dict(cache_type="e4m3", softcap=30.0, window=40)])
+def test_layer_example(L, kw):
+    """The example's layer: LoRA projections, rotary append and attention on one
+    cache over a prompt step and decode steps, each call against a plain fp32 form.
+    Every output is rounded to bf16 once by each side (relative rms about 2^-9.3
+    each), the attention's weights once more: below 2^-7 together."""
+    torch = _torch()
+    import importlib.util
+    spec = importlib.util.spec_from_file_location("attention_layer", os.path.join(ROOT, "examples",
+                                                                                  "attention_layer.py"))
+    ex = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(ex)
+    kw = dict(kw)
+    if kw.get("cache_type") == "e4m3":
+        kw["cache_type"] = torch.float8_e4m3fn
+    layer = ex.Layer(512, 8, 2, 64, 3, 16, 6, 16, 16, **kw)
+    worst, _ = ex.serve(layer, [33, 1, 70, 128, 5, 16], 3, 512, check=True)
+    assert worst < 2.0 ** -7
+
+
+# ---------------------------------------------------------------------------
+# Over the range
+# ---------------------------------------------------------------------------
+@gpu
+@pytest.mark.parametrize("seed", range(24))
+def test_attend_drawn(L, seed):
+    """Drawn head layouts, lengths, page sizes, strides, types and score forms on
+    both paths: requests without rows or cached tokens, rows before the first key,
+    one request or many, few keys or enough to be split."""
+    rng = np.random.default_rng(1000 + seed)
+    path = PATHS[seed % 2]
+    KV, G, hd = int(rng.choice([1, 2, 3, 8])), int(rng.choice([1, 2, 3, 5, 8, 16])), int(rng.choice([64, 128]))
+    n = int(rng.choice([1, 2, 5, 40]))
+    q_hi = int(rng.choice([1, 2, 6])) if path == "decode" else int(rng.choice([1, 30, 150]))
+    top = 4000 // (n * max(1, q_hi // 8)) + 1
+    lens = [int(x) for x in np.exp(rng.uniform(0, math.log(top), n))]
+    q_lens = [int(rng.integers(0, q_hi + 1)) for _ in range(n)]
+    for i in range(n):
+        if rng.random() < 0.1:
+            lens[i] = 0
+    c = Case(L, lens, q_lens, KV * G, KV, hd, ps=int(2 ** rng.integers(0, 8)), fp8=bool(rng.random() < 0.5),
+             layout=str(rng.choice(["head", "token", "both", "slot"])), seed=seed, pad=int(rng.integers(0, 3)),
+             v_shift=float(rng.choice([0.0, 0.5])))
+    kw = dict(softcap=float(rng.choice([0.0, 0.0, 8.0, 50.0])), window=int(rng.choice([0, 0, 3, 100, 1000])))
+    if rng.random() < 0.4:
+        kw["slopes"] = [float(2.0 ** -rng.uniform(0, 8)) for _ in range(KV * G)]
+    c.run(path, **kw).check(path, **kw)
