@@ -27,7 +27,7 @@ extern "C" {
 #define LORA_MAX_SEQS 4096
 #define LORA_MAX_PAGE_SIZE 1024
 #define LORA_MAX_HEAD_DIM 256
-#define LORA_MAX_KV_LEN (1 << 30)
+#define LORA_MAX_KV_LEN (1 << 25)
 
 /* Element type of the cache. */
 typedef enum {

@@ -353,7 +353,7 @@ attend_decode_kernel(const AttendArgs a, float *parts, int32_t *counters, int pr
         if (lx < x1) {
 #pragma unroll
             for (int i = 0; i < NK; ++i)
-                lpage[i] = has_key(i) ? __ldg(ltab + ((lkey + 32 * i + lane) >> a.kv.page_shift)) : -1;
+                lpage[i] = has_key(i) ? ltab[(lkey + 32 * i + lane) >> a.kv.page_shift] : -1;
         }
     };
     const auto open_load = [&](int32_t seq) {
@@ -462,7 +462,7 @@ attend_decode_kernel(const AttendArgs a, float *parts, int32_t *counters, int pr
                     float f[KK][4];
 #pragma unroll
                     for (int kk = 0; kk < KK; ++kk) {
-                        const uint2 u = live ? __ldg(reinterpret_cast<const uint2 *>(src + kk * 16 + 4 * c4))
+                        const uint2 u = live ? *reinterpret_cast<const uint2 *>(src + kk * 16 + 4 * c4)
                                              : make_uint2(0, 0);
                         f[kk][0] = bf16lo_to_f32(u.x), f[kk][1] = bf16hi_to_f32(u.x);
                         f[kk][2] = bf16lo_to_f32(u.y), f[kk][3] = bf16hi_to_f32(u.y);
@@ -472,7 +472,7 @@ attend_decode_kernel(const AttendArgs a, float *parts, int32_t *counters, int pr
                     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
                     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
                     // 2^e <= top < 2^(e + 1): the row times 2^-e is below 2
-                    const int e = top > 0.0f ? max(-60, min(60, static_cast<int>(__float_as_uint(top) >> 23) - 127)) : 0;
+                    const int e = top > 0.0f ? max(-126, min(126, static_cast<int>(__float_as_uint(top) >> 23) - 127)) : 0;
                     const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
                     mult[mb][i] *= __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
 #pragma unroll
@@ -483,8 +483,8 @@ attend_decode_kernel(const AttendArgs a, float *parts, int32_t *counters, int pr
                 } else {
 #pragma unroll
                     for (int kk = 0; kk < KK; ++kk) {
-                        w[kk][0] = live ? __ldg(reinterpret_cast<const uint32_t *>(src + kk * 16 + 2 * c4)) : 0u;
-                        w[kk][1] = live ? __ldg(reinterpret_cast<const uint32_t *>(src + kk * 16 + 8 + 2 * c4)) : 0u;
+                        w[kk][0] = live ? *reinterpret_cast<const uint32_t *>(src + kk * 16 + 2 * c4) : 0u;
+                        w[kk][1] = live ? *reinterpret_cast<const uint32_t *>(src + kk * 16 + 8 + 2 * c4) : 0u;
                     }
                 }
 #pragma unroll

@@ -317,7 +317,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
             // this lane's key of the step to copy (the last keys first) and, ahead of it, its page
             int32_t key = it.key0 + (steps - 1) * kKeys + w * 32 + lane, page = -1;
             const auto has_key = [&]() { return key >= lo && key <= last; };
-            if (has_key()) page = __ldg(table + (key >> a.kv.page_shift));
+            if (has_key()) page = table[key >> a.kv.page_shift];
             if (steps > 0 && (q_round == 0 || wait(&bar.q_empty, (q_round - 1) & 1))) {
                 ++q_round;
 #pragma unroll 1
@@ -350,7 +350,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
                         }
                         const uint32_t top = max(top2 & 0xffffu, top2 >> 16);  // (bf16 sizes order like integers)
                         // 2^e <= top < 2^(e + 1)
-                        const int e2 = top > 0 ? max(-60, min(60, static_cast<int>(top >> 7) - 127)) : 0;
+                        const int e2 = top > 0 ? max(-126, min(126, static_cast<int>(top >> 7) - 127)) : 0;
                         const float down = __uint_as_float(static_cast<uint32_t>(127 - e2) << 23);
                         s_qexp[k & 1][r] = static_cast<int8_t>(e2);
 #pragma unroll 4
@@ -380,7 +380,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
                 at = has && ok ? page * a.kv.page_b + (key & a.kv.page_mask) * a.kv.token_b + head : -1;
                 smooth = __all_sync(0xffffffffu, at >= 0) && a.kv.page_shift >= 4;
                 key -= kKeys;
-                if (has_key()) page = __ldg(table + (key >> a.kv.page_shift));
+                if (has_key()) page = table[key >> a.kv.page_shift];
             };
             // calls f(instruction, address or null) for this warp's 32 keys of k or v
             const auto each = [&](const unsigned char *from, auto f) {
@@ -412,7 +412,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
                 const auto load = [&](int32_t t) {
                     if ((t & 1) == 0) next_keys();
                     each((t & 1) ? a.kv.v : a.kv.k, [&](int i, const unsigned char *src) {
-                        v[i] = src != nullptr ? ldg_stream(src) : make_uint4(0, 0, 0, 0);
+                        v[i] = src != nullptr ? ldg_cg(src) : make_uint4(0, 0, 0, 0);
                     });
                 };
                 if (tiles > 0) load(0);

@@ -50,8 +50,9 @@ __device__ __forceinline__ RequestRows load_rows(const AttendArgs &a, int32_t i)
 // The kernels of this file's users are launched as programmatic dependents of the
 // kernel before them on the stream, which hides the launch's latency.  Each first
 // waits until that kernel has finished and its writes are visible, so it may read
-// and write what the kernel before it wrote; only then does it let its own
-// dependent's blocks start.
+// and write what the kernel before it wrote (through coherent loads: the read-only
+// path is for data that no one writes while a kernel's blocks are there); only then
+// does it let its own dependent's blocks start.
 __device__ __forceinline__ void wait_for_previous() {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");

@@ -58,8 +58,8 @@ __device__ __forceinline__ Request load_request(const int32_t *ctx_lens, const i
 }
 
 __global__ void __launch_bounds__(kThreads)
-kv_step_kernel(const int32_t *__restrict__ ctx_lens, const int32_t *__restrict__ new_lens, int32_t n, int32_t shift,
-               const int32_t *__restrict__ free_pages, int32_t n_free, int32_t *table, int64_t ld_table, int32_t width,
+kv_step_kernel(const int32_t *ctx_lens, const int32_t *new_lens, int32_t n, int32_t shift,
+               const int32_t *free_pages, int32_t n_free, int32_t *table, int64_t ld_table, int32_t width,
                int32_t T, int32_t *q_offsets, int32_t *kv_lens, int32_t *positions, int32_t *seq_ids, int64_t *slot_map,
                int32_t *taken, int32_t *err) {
     __shared__ int64_t s_row[kChunk + 1];  // first row of the chunk's requests, and of the next chunk

@@ -99,8 +99,8 @@ __global__ void __launch_bounds__(kThreads, 8) rope_append_kernel(RopeArgs a) {
     // a head's loads are issued one head ahead, the first before the angles are known
     uint4 w0 = make_uint4(0, 0, 0, 0), w1 = w0;
     if (h0 < total) {
-        w0 = ldg_stream(row + h0 * hd + c0);
-        w1 = ldg_stream(row + h0 * hd + c1);
+        w0 = ldg_cg(row + h0 * hd + c0);
+        w1 = ldg_cg(row + h0 * hd + c1);
     }
     float cs[8], sn[8];
     if (turned) {
@@ -120,8 +120,8 @@ __global__ void __launch_bounds__(kThreads, 8) rope_append_kernel(RopeArgs a) {
         unpack8(w0, x);
         unpack8(w1, y);
         if (h + per_pass < total) {
-            w0 = ldg_stream(row + (h + per_pass) * hd + c0);
-            w1 = ldg_stream(row + (h + per_pass) * hd + c1);
+            w0 = ldg_cg(row + (h + per_pass) * hd + c0);
+            w1 = ldg_cg(row + (h + per_pass) * hd + c1);
         }
         if (turned && h < H + nk) {
             if (a.interleaved) {

@@ -221,7 +221,7 @@ def ref_step(ctx, new, ps, free, table, T):
         for u in range(need if served else 0):
             table[i][-(-c // ps) + u] = free[at + u]
             taken = at + need
-        for p in range(c0, c0 + m0):
+        for p in range(c0, c0 + min(m0, max(0, T + 1 - len(pos)))):  # (one past T tells of the rest)
             page = table[i][p // ps] if served else -1
             if served and page < 0:
                 errors.add(4)
@@ -633,6 +633,21 @@ def test_attend_large_scores(L, path):
     c.run(path, scale=1.0).check(path, scale=1.0)
     c = Case(L, [200, 70], [2, 70], 4, 2, 64, seed=5, fp8=True, q_scale=3000.0)
     c.run(path).check(path)
+
+
+@gpu
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("path", PATHS)
+@pytest.mark.parametrize("power", [90, -90])
+def test_attend_query_magnitudes(L, power, path, fp8):
+    """Queries far from 1 with a scale that brings the scores back: powers of two
+    change nothing but exponents."""
+    c = Case(L, [77, 150], [1, 60], 4, 2, 64, seed=13, fp8=fp8)
+    scale = 64 ** -0.5
+    want = c.run(path, scale=scale).out.clone()
+    c.q_big.mul_(2.0 ** power)
+    c.run(path, scale=scale * 2.0 ** -power).check(path, scale=scale * 2.0 ** -power)
+    assert _torch().equal(c.out, want)
 
 
 @gpu
