@@ -20,8 +20,8 @@
 //   warp 12          issues the products
 //   warp 13          hands out the work
 // One block an SM stays for the whole call.  The (request, row tiles, key head)
-// items go to whichever block is free, those with the most keys of a request
-// first, and a block's copies and products begin its next item while the softmax
+// items go to whichever block is free, those with the most keys first (of each
+// request, where there are more than 32), and a block's copies and products begin its next item while the softmax
 // warps still write the last one's output.  An item's keys are taken from the last
 // tile down: with a bias that falls with distance the largest scores come first
 // and O is not rescaled step after step.  k and v tiles share one ring; every wait
@@ -50,7 +50,8 @@ template <int HD>
 struct PromptConfig {
     static constexpr int kTileB = kRows * HD * 2;
     static constexpr int kSlots = HD == 128 ? 5 : 8;  // k and v tiles in the ring
-    static constexpr int kSmem = (2 + kSlots) * kTileB + 1024;
+    static constexpr int kQ = HD == 128 ? 1 : 2;      // items whose q rows fit
+    static constexpr int kSmem = (2 * kQ + kSlots) * kTileB + 1024;
     static constexpr uint32_t kHalfB = kRows * 128;   // 64 dims of all rows
     // Registers a thread: 128 at launch, then by role.  The four warpgroups' shares (two
     // of softmax, copies, products) add up to the launch's 4 x 128.  Measured on 8,192
@@ -63,7 +64,7 @@ struct PromptConfig {
 };
 
 struct Barriers {
-    uint64_t q_full, q_empty, full[8], empty[8], s_full[2], p_full[2][2], o_full[2], o_empty[2], item_full[2],
+    uint64_t q_full[2], q_empty[2], full[8], empty[8], s_full[2], p_full[2][2], o_full[2], o_empty[2], item_full[2],
         item_empty[2], exp_full[2], claim, done;
 };
 
@@ -231,8 +232,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
     __shared__ volatile int32_t s_abort;
     __shared__ int8_t s_qexp[2][E4M3 ? 2 * kRows : 1];  // of this and the next item: q rows' powers of two
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const uint32_t q_base = (tc::smem_u32(smem_raw) + 1023) & ~1023u;  // two q tiles, then the ring
-    const uint32_t ring = q_base + 2 * C::kTileB;
+    const uint32_t q_base = (tc::smem_u32(smem_raw) + 1023) & ~1023u;  // q tiles of kQ items, then the ring
+    const uint32_t ring = q_base + 2 * C::kQ * C::kTileB;
 
     wait_for_previous();
     const auto pairs_of = [&](const RequestRows &r) {
@@ -252,8 +253,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
     }
     if (tid == 0) {
         s_abort = 0;
-        tc::mbar_init(&bar.q_full, 4);
-        tc::mbar_init(&bar.q_empty, 1);
+        for (int i = 0; i < C::kQ; ++i) {
+            tc::mbar_init(&bar.q_full[i], 4);
+            tc::mbar_init(&bar.q_empty[i], 1);
+        }
         for (int i = 0; i < C::kSlots; ++i) {
             tc::mbar_init(&bar.full[i], 4);
             tc::mbar_init(&bar.empty[i], 1);
@@ -299,7 +302,6 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
         constexpr int kKvPieces = E4M3 ? HD / 16 : kPieces;      // pieces of a cache row
         constexpr int kKvStep = 32 / kKvPieces;
         const int piece = lane % kPieces, row_in = lane / kPieces;
-        const auto q_piece = [&](int r) { return q_base + (r / kRows) * C::kTileB + tile_at(r % kRows, piece); };
         const int kv_piece = lane % kKvPieces, kv_row = lane / kKvPieces;
         const auto publish = [&](uint64_t *b) {
             tc::fence_async_smem();
@@ -318,7 +320,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
             int32_t key = it.key0 + (steps - 1) * kKeys + w * 32 + lane, page = -1;
             const auto has_key = [&]() { return key >= lo && key <= last; };
             if (has_key()) page = table[key >> a.kv.page_shift];
-            if (steps > 0 && (q_round == 0 || wait(&bar.q_empty, (q_round - 1) & 1))) {
+            const int qb = q_round % C::kQ;
+            const uint32_t q_at_base = q_base + qb * 2 * C::kTileB;
+            const auto q_piece = [&](int r) { return q_at_base + (r / kRows) * C::kTileB + tile_at(r % kRows, piece); };
+            if (steps > 0 && (q_round < C::kQ || wait(&bar.q_empty[qb], (q_round / C::kQ - 1) & 1))) {
                 ++q_round;
 #pragma unroll 1
                 for (int half = 0; half < 2; ++half) {
@@ -340,7 +345,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
 #pragma unroll 1
                     for (int half = 0; half < 2; ++half) {
                         const int r = w * 64 + half * 32 + lane;
-                        const uint32_t tile = q_base + (r / kRows) * C::kTileB;
+                        const uint32_t tile = q_at_base + (r / kRows) * C::kTileB;
                         uint32_t top2 = 0;  // the row's largest size, as a pair of bf16 bit patterns
 #pragma unroll 4
                         for (int p = 0; p < kPieces; ++p) {
@@ -365,7 +370,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
                         }
                     }
                 }
-                if (E4M3) publish(&bar.q_full);
+                if (E4M3) publish(&bar.q_full[qb]);
                 else tc::cp_commit();
             }
             if (E4M3 && lane == 0) tc::mbar_arrive(&bar.exp_full[k & 1]);
@@ -444,7 +449,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
                     tc::cp_commit();
                     // the tile two before this one (and q before all) has landed
                     tc::cp_wait_group<2>();
-                    if (t == 1) publish(&bar.q_full);
+                    if (t == 1) publish(&bar.q_full[qb]);
                     if (t >= 2) publish(&bar.full[(u - 2) % C::kSlots]);
                 }
                 if (fine && tiles > 0) {
@@ -475,8 +480,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
                 if (elect_one()) tc::mma_commit(b);
                 __syncwarp();
             };
-            const auto scores = [&](int i, int32_t u) {
-                const uint64_t q = q_desc + ((i * C::kTileB) >> 4), k = k_desc + (((u % C::kSlots) * C::kTileB) >> 4);
+            const auto scores = [&](int qb, int i, int32_t u) {
+                const uint64_t q = q_desc + (((2 * qb + i) * C::kTileB) >> 4), k = k_desc + (((u % C::kSlots) * C::kTileB) >> 4);
                 if (elect_one()) {
 #pragma unroll
                     for (int kk = 0; kk < HD / 16; ++kk) {
@@ -508,12 +513,13 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
                 const int n_tiles = s_item[k & 1].rows > kRows ? 2 : 1;
                 release(k);
                 if (steps == 0) continue;
-                if (!wait(&bar.q_full, q_round & 1) || !full(u)) break;
+                const int qb = q_round % C::kQ;
+                if (!wait(&bar.q_full[qb], (q_round / C::kQ) & 1) || !full(u)) break;
                 ++q_round;
                 tc::fence_after_sync();
-                for (int i = 0; i < n_tiles; ++i) scores(i, u);
+                for (int i = 0; i < n_tiles; ++i) scores(qb, i, u);
                 commit(&bar.empty[u % C::kSlots]);
-                if (steps == 1) commit(&bar.q_empty);
+                if (steps == 1) commit(&bar.q_empty[qb]);
                 for (int32_t j = 0; j < steps && fine; ++j, u += 2) {
                     const bool more = j + 1 < steps;
                     for (int i = 0; i < n_tiles && fine; ++i) {
@@ -537,10 +543,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
                         if (more) {
                             if (i == 0 && !full(u + 2)) break;
                             tc::fence_after_sync();
-                            scores(i, u + 2);
+                            scores(qb, i, u + 2);
                             if (last) {
                                 commit(&bar.empty[(u + 2) % C::kSlots]);
-                                if (j + 2 == steps) commit(&bar.q_empty);
+                                if (j + 2 == steps) commit(&bar.q_empty[qb]);
                             }
                         }
                     }
@@ -552,15 +558,75 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
             if (!tc::mbar_wait_timed(&bar.done, 0, kWaitNs)) fine = false;
         } else if (warp == 13) {
             // ---- work -------------------------------------------------------------------
-            // Items in order: pairs of row tiles from the last request's last one down, key
-            // heads innermost.  The pairs above the walk's request are `above`.
+            // Items in order, key heads innermost.  Up to 32 requests, a lane each: the pairs of
+            // row tiles with the most keys first, of any request, so that what is left at the
+            // end is small (8 ragged chunks of 6,546 tokens: 96 us in the requests' order, 82 us so).
+            // More requests: pairs from the last request's last one down; the many items even
+            // out by themselves.
             const int64_t items = total * a.kv.n_kv;
+            const bool by_size = a.n_seq <= 32;
+            // by size: this lane's request
+            RequestRows rows{0, 0, 0, false};
+            int32_t pairs_here = 0;
+            const auto item_of = [&](int32_t seq, const RequestRows &r, int32_t pair) {
+                Item it;
+                it.seq = seq;
+                it.head = 0;
+                it.row0 = pair * 2 * kRows;
+                it.rows = min(2 * kRows, r.n * a.group - it.row0);
+                it.q0 = r.q0;
+                it.n = r.n;
+                it.len = r.len;
+                const int32_t first = r.len - r.n + it.row0 / a.group;
+                const int32_t last = r.len - r.n + (it.row0 + it.rows - 1) / a.group;
+                it.lo = a.window > 0 ? static_cast<int32_t>(max(int64_t(0), int64_t(first) - a.window + 1)) : 0;
+                it.key0 = it.lo & ~(kKeys - 1);
+                it.steps = last < 0 ? 0 : (last - it.key0) / kKeys + 1;
+                it.any = true;
+                return it;
+            };
+            if (by_size && lane < a.n_seq) {
+                rows = load_rows(a, lane);
+                pairs_here = static_cast<int32_t>(pairs_of(rows));
+            }
+            const int32_t longest = static_cast<int32_t>(
+                __reduce_max_sync(0xffffffffu, static_cast<uint32_t>(rows.len) / kKeys));
+            // this lane's pairs whose last row's position is at least 128 b: it grows with the pair
+            const auto at_least = [&](int32_t b) -> uint32_t {
+                const int64_t x = (int64_t(b) * kKeys - (rows.len - rows.n)) * a.group;  // rows before it
+                if (b <= 0 || x <= 0) return pairs_here;
+                if (x >= int64_t(rows.n) * a.group) return 0;
+                return pairs_here - min(pairs_here, static_cast<int32_t>(x / (2 * kRows)));
+            };
+            // in order: the pairs above the walk's request are `above`
             int64_t above = total;
             int32_t seq = a.n_seq;  // requests from here on have been passed
             int64_t idx = blockIdx.x;
             for (int32_t k = 0;; ++k) {
                 Item it{};
-                if (idx < items) {
+                if (idx < items && by_size) {
+                    // the largest b with more than `want` pairs at or above it, by bisection
+                    const uint32_t want = static_cast<uint32_t>(idx / a.kv.n_kv);
+                    int32_t lo = 0, hi = longest;
+                    while (lo < hi) {
+                        const int32_t mid = (lo + hi + 1) >> 1;
+                        if (__reduce_add_sync(0xffffffffu, at_least(mid)) > want) lo = mid;
+                        else hi = mid - 1;
+                    }
+                    // among the pairs of that size: by request, then from the last down
+                    const uint32_t beyond = at_least(lo + 1), same = at_least(lo) - beyond;
+                    const uint32_t r = want - __reduce_add_sync(0xffffffffu, beyond);
+                    uint32_t incl = same;
+#pragma unroll
+                    for (int o = 1; o < 32; o <<= 1) {
+                        const uint32_t v = __shfl_up_sync(0xffffffffu, incl, o);
+                        if (lane >= o) incl += v;
+                    }
+                    if (r >= incl - same && r < incl) {
+                        it = item_of(lane, rows, pairs_here - 1 - static_cast<int32_t>(beyond + (r - (incl - same))));
+                        it.head = static_cast<int32_t>(idx % a.kv.n_kv);
+                    }
+                } else if (idx < items) {
                     const int64_t want = total - 1 - idx / a.kv.n_kv;
                     // 32 requests at a time: lane l holds request seq - 1 - l
                     while (seq > 0) {
@@ -574,25 +640,12 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
                             const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
                             if (lane >= o) incl += v;
                         }
-                        const bool mine = i >= 0 && pairs > 0 && want >= above - incl && want < above - incl + pairs;
-                        const uint32_t who = __ballot_sync(0xffffffffu, mine);
+                        const bool ours = i >= 0 && pairs > 0 && want >= above - incl && want < above - incl + pairs;
+                        const uint32_t who = __ballot_sync(0xffffffffu, ours);
                         if (who != 0) {
-                            if (mine) {
-                                it.seq = i;
+                            if (ours) {
+                                it = item_of(i, r, static_cast<int32_t>(want - (above - incl)));
                                 it.head = static_cast<int32_t>(idx % a.kv.n_kv);
-                                it.row0 = static_cast<int32_t>(want - (above - incl)) * 2 * kRows;
-                                it.rows = min(2 * kRows, r.n * a.group - it.row0);
-                                it.q0 = r.q0;
-                                it.n = r.n;
-                                it.len = r.len;
-                                const int32_t first = r.len - r.n + it.row0 / a.group;
-                                const int32_t last = r.len - r.n + (it.row0 + it.rows - 1) / a.group;
-                                it.lo = a.window > 0
-                                            ? static_cast<int32_t>(max(int64_t(0), int64_t(first) - a.window + 1))
-                                            : 0;
-                                it.key0 = it.lo & ~(kKeys - 1);
-                                it.steps = last < 0 ? 0 : (last - it.key0) / kKeys + 1;
-                                it.any = true;
                             }
                             // the requests before the one found stay passed over
                             const int l = __ffs(who) - 1;
