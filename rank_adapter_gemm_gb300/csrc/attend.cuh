@@ -56,62 +56,70 @@ __device__ __forceinline__ float tanh_far(float z) {
     return 1.0f - __fdividef(2.0f, ex2(z * (2.0f * kLog2e)) + 1.0f);
 }
 
+// Whether products of size `top` lie within half the cap, or there is none.  (A cap
+// below 1e-6 of mult would overflow the coefficients.)
+__device__ __forceinline__ bool near_cap(const AttendArgs &a, float mult, float top) {
+    return a.softcap == 0.0f || (top * fabsf(mult) <= 0.5f * a.softcap && fabsf(mult) <= 1e6f * a.softcap);
+}
+
+// A pair of such products in their final form (finish_scores), the scales in the
+// coefficients: x (k0 + k1 x^2 + k2 x^4 + k3 x^6) + bias.
+struct NearForm {
+    uint64_t k[4], slope2, at2;
+
+    __device__ __forceinline__ NearForm(const AttendArgs &a, float mult, float slope, int32_t back) {
+        constexpr float kTanh[4] = LORA_TANH_HALF;
+        const float in = mult * a.inv_softcap, in2 = in * in;  // 0 without a cap
+        float c = mult * kLog2e;
+#pragma unroll
+        for (int i = 0; i < 4; ++i, c *= in2) k[i] = pack2(c * kTanh[i], c * kTanh[i]);
+        slope2 = pack2(slope, slope);
+        at2 = pack2(slope * back, slope * back);
+    }
+
+    // keys d and d + 1 after the first
+    __device__ __forceinline__ uint64_t operator()(uint64_t x, float d) const {
+        const uint64_t w = mul2(x, x), bias = fma2(slope2, pack2(d, d + 1.0f), at2);
+        return fma2(x, fma2(fma2(fma2(k[3], w, k[2]), w, k[1]), w, k[0]), bias);
+    }
+};
+
 // N products s in their final form, times log2 e, in fp32: scaled by mult, capped,
 // biased by distance (slope: times log2 e), masked.  back: the first one's key minus
 // the row's position; consecutive pairs lie STEP keys apart.  Called by whole warps.
 template <int N, int STEP>
 __device__ __forceinline__ void finish_scores(float (&s)[N], const AttendArgs &a, float mult, float slope, int32_t back,
                                               bool masked) {
-    const uint64_t slope2 = pack2(slope, slope), at2 = pack2(slope * back, slope * back);
-    const float by = mult * kLog2e;
-    bool near = a.softcap > 0.0f;
-    if (near) {
+    bool capped = a.softcap > 0.0f;
+    if (capped) {
         float top = 0.0f;
 #pragma unroll
         for (int e = 0; e < N; e += 2) top = fmaxf(fmaxf(top, fabsf(s[e])), fabsf(s[e + 1]));
-        // (a cap below 1e-6 of mult would overflow the coefficients)
-        near = __all_sync(0xffffffffu, top * fabsf(mult) <= 0.5f * a.softcap && fabsf(mult) <= 1e6f * a.softcap);
-        if (!near) {
+        if (!__all_sync(0xffffffffu, near_cap(a, mult, top))) {
             constexpr float kTanh[6] = LORA_TANH_ONE;
-            const float in = mult * a.inv_softcap, cap = a.softcap * kLog2e;
+            const float in = mult * a.inv_softcap;
 #pragma unroll
             for (int e = 0; e < N; ++e) {
                 const float z = s[e] * in, w = z * z;
                 const float poly = z * (1.0f + w * (kTanh[1] + w * (kTanh[2] + w * (kTanh[3] + w * (kTanh[4] +
                                                                                                      w * kTanh[5])))));
-                s[e] = cap * (fabsf(z) <= 1.0f ? poly : tanh_far(z));
+                s[e] = a.softcap * (fabsf(z) <= 1.0f ? poly : tanh_far(z));
             }
+            capped = false;
+            mult = 1.0f;
         }
     }
-    if (near) {
-        // by s + by c1 in^2 s^3 + ...: the scales are in the coefficients
-        const float in = mult * a.inv_softcap, in2 = in * in;
-        float c = by;
-        constexpr float kTanh[4] = LORA_TANH_HALF;
-        uint64_t k[4];
+    const NearForm form(a, mult, slope, back);
+    if (capped) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i, c *= in2) k[i] = pack2(c * kTanh[i], c * kTanh[i]);
-#pragma unroll
-        for (int e = 0; e < N; e += 2) {
-            const uint64_t x = pack2(s[e], s[e + 1]), w = mul2(x, x);
-            uint64_t r = fma2(k[3], w, k[2]);
-#pragma unroll
-            for (int i = 1; i >= 0; --i) r = fma2(r, w, k[i]);
-            if (a.slopes != nullptr) {
-                const float d = static_cast<float>(e / 2 * STEP);
-                r = fma2(x, r, fma2(slope2, pack2(d, d + 1.0f), at2));
-            } else {
-                r = mul2(x, r);
-            }
-            unpack2(r, s[e], s[e + 1]);
-        }
+        for (int e = 0; e < N; e += 2)
+            unpack2(form(pack2(s[e], s[e + 1]), static_cast<float>(e / 2 * STEP)), s[e], s[e + 1]);
     } else {
-        const float scale = a.softcap > 0.0f ? 1.0f : by;
-        const uint64_t scale2 = pack2(scale, scale);
 #pragma unroll
         for (int e = 0; e < N; e += 2) {
             const float d = static_cast<float>(e / 2 * STEP);
-            unpack2(fma2(pack2(s[e], s[e + 1]), scale2, fma2(slope2, pack2(d, d + 1.0f), at2)), s[e], s[e + 1]);
+            unpack2(fma2(pack2(s[e], s[e + 1]), form.k[0], fma2(form.slope2, pack2(d, d + 1.0f), form.at2)), s[e],
+                    s[e + 1]);
         }
     }
     if (masked) {

@@ -720,28 +720,55 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
                 const bool masked = key + kKeys - 1 > pos_lo || (a.window > 0 && pos_hi - key >= a.window);
                 const bool direct = plain && !masked;
                 const float by = direct ? by0 : 1.0f;
-                if (!direct) {
-                    // the final form of the scores, in place, 64 at a time (one copy of the code)
+                uint32_t x[128];
+                const auto load_scores = [&]() {
+                    tmem_ld64(s_at, x);
+                    tmem_ld64(s_at + 64, x + 64);
+                    tmem_wait128(x);
+                };
+                load_scores();
+                bool final_form = direct;
+                if (!masked && !direct) {
+                    float far4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                    if (a.softcap > 0.0f) {
+#pragma unroll
+                        for (int e = 0; e < 128; e += 2)
+                            far4[(e / 2) & 3] = fmaxf(fmaxf(far4[(e / 2) & 3], fabsf(__uint_as_float(x[e]))),
+                                                      fabsf(__uint_as_float(x[e + 1])));
+                    }
+                    final_form = __all_sync(0xffffffffu, near_cap(a, mult, fmaxf(fmaxf(far4[0], far4[1]),
+                                                                                 fmaxf(far4[2], far4[3]))));
+                    if (final_form) {
+                        const NearForm form(a, mult, slope, key - pos);
+#pragma unroll
+                        for (int e = 0; e < 128; e += 2) {
+                            float s0, s1;
+                            unpack2(form(pack2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])),
+                                         static_cast<float>(e)), s0, s1);
+                            x[e] = __float_as_uint(s0);
+                            x[e + 1] = __float_as_uint(s1);
+                        }
+                    }
+                }
+                if (!final_form) {
+                    // masks, and scores beyond half their cap: in place, 64 at a time (one copy of the code)
 #pragma unroll 1
                     for (int c = 0; c < 2; ++c) {
-                        uint32_t x[64];
+                        uint32_t y[64];
                         float s[64];
-                        tmem_ld64(s_at + 64 * c, x);
-                        tmem_wait64(x);
+                        tmem_ld64(s_at + 64 * c, y);
+                        tmem_wait64(y);
 #pragma unroll
-                        for (int e = 0; e < 64; ++e) s[e] = __uint_as_float(x[e]);
+                        for (int e = 0; e < 64; ++e) s[e] = __uint_as_float(y[e]);
                         finish_scores<64, 2>(s, a, mult, slope, key + 64 * c - pos, masked);
 #pragma unroll
-                        for (int e = 0; e < 64; ++e) x[e] = __float_as_uint(s[e]);
-                        tmem_st32(s_at + 64 * c, x);
-                        tmem_st32(s_at + 64 * c + 32, x + 32);
+                        for (int e = 0; e < 64; ++e) y[e] = __float_as_uint(s[e]);
+                        tmem_st32(s_at + 64 * c, y);
+                        tmem_st32(s_at + 64 * c + 32, y + 32);
                     }
                     tmem_wait_st();
+                    load_scores();
                 }
-                uint32_t x[128];
-                tmem_ld64(s_at, x);
-                tmem_ld64(s_at + 64, x + 64);
-                tmem_wait128(x);
                 float top8[8];
 #pragma unroll
                 for (int q = 0; q < 8; ++q) {
