@@ -176,9 +176,10 @@ __device__ __forceinline__ int32_t find_seq(const int32_t *s_pref, int32_t n, in
 }
 
 // Rows r0 .. r0 + R - 1 (below `rows`) joined over partials first..last, in order;
-// part(i) is partial i's address, in shared or global memory.  Writes rows of
-// `out`, or of the partial `to`.
-template <int HD, int ROWS, int R, class P>
+// part(i) is partial i's address, in shared or global memory; B of them are loaded at
+// a time, the first while the weights are computed (one request of 4,096 tokens: 16 at
+// a time 14.6 us, 4 after the weights 16.1).  Writes rows of `out`, or of the partial `to`.
+template <int HD, int ROWS, int R, int B, class P>
 __device__ __forceinline__ void join_rows(const AttendArgs &a, P part, int32_t first, int32_t last, const Segment &s,
                                           int r0, int rows, float shift, float *to, int lane) {
     constexpr int V = HD / 32;
@@ -193,18 +194,37 @@ __device__ __forceinline__ void join_rows(const AttendArgs &a, P part, int32_t f
     for (int32_t c = first; c <= last; c += 32) {
         const int32_t n = min(32, last - c + 1);
         const float *mine = part(c + min(lane, n - 1));
-        float w[R], l[R];
+        float w[R], l[R], x[B][R][V];
+        const auto fetch = [&](int32_t j0) {
+#pragma unroll
+            for (int b = 0; b < B; ++b) {
+                if (j0 + b >= n) break;
+                const float *v = part(c + j0 + b) + 2 * ROWS + lane * V;
+#pragma unroll
+                for (int q = 0; q < R; ++q) {
+                    const float *from = v + min(r0 + q, rows - 1) * HD;
+                    if constexpr (V == 4) {
+                        const float4 y = *reinterpret_cast<const float4 *>(from);
+                        x[b][q][0] = y.x, x[b][q][1] = y.y, x[b][q][2] = y.z, x[b][q][3] = y.w;
+                    } else {
+                        const float2 y = *reinterpret_cast<const float2 *>(from);
+                        x[b][q][0] = y.x, x[b][q][1] = y.y;
+                    }
+                }
+            }
+        };
 #pragma unroll
         for (int q = 0; q < R; ++q) {
             const int r = min(r0 + q, rows - 1);
             w[q] = lane < n ? mine[r] : -INFINITY;
             l[q] = lane < n ? mine[ROWS + r] : 0.0f;
         }
+        fetch(0);
 #pragma unroll
         for (int q = 0; q < R; ++q) {
             float now = w[q];
 #pragma unroll
-            for (int x = 16; x > 0; x >>= 1) now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, x));
+            for (int d = 16; d > 0; d >>= 1) now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, d));
             now = fmaxf(now, top[q]);
             const float ref = now == -INFINITY ? 0.0f : now, f = ex2(top[q] - ref);
             w[q] = ex2(w[q] - ref);
@@ -213,20 +233,18 @@ __device__ __forceinline__ void join_rows(const AttendArgs &a, P part, int32_t f
             for (int e = 0; e < V; ++e) o[q][e] *= f;
             top[q] = now;
         }
-#pragma unroll 4
-        for (int32_t j = 0; j < n; ++j) {
-            const float *v = part(c + j) + 2 * ROWS + lane * V;
+#pragma unroll 1
+        for (int32_t j0 = 0; j0 < n; j0 += B) {
+            if (j0 > 0) fetch(j0);
 #pragma unroll
-            for (int q = 0; q < R; ++q) {
-                const float wj = __shfl_sync(0xffffffffu, w[q], j);
-                sum[q] += wj * __shfl_sync(0xffffffffu, l[q], j);
-                const float *x = v + min(r0 + q, rows - 1) * HD;
-                if constexpr (V == 4) {
-                    const float4 y = *reinterpret_cast<const float4 *>(x);
-                    o[q][0] += wj * y.x, o[q][1] += wj * y.y, o[q][2] += wj * y.z, o[q][3] += wj * y.w;
-                } else {
-                    const float2 y = *reinterpret_cast<const float2 *>(x);
-                    o[q][0] += wj * y.x, o[q][1] += wj * y.y;
+            for (int b = 0; b < B; ++b) {
+                if (j0 + b >= n) break;
+#pragma unroll
+                for (int q = 0; q < R; ++q) {
+                    const float wj = __shfl_sync(0xffffffffu, w[q], j0 + b);
+                    sum[q] += wj * __shfl_sync(0xffffffffu, l[q], j0 + b);
+#pragma unroll
+                    for (int e = 0; e < V; ++e) o[q][e] += wj * x[b][q][e];
                 }
             }
         }
@@ -781,8 +799,8 @@ attend_decode_kernel(const AttendArgs a, float *parts, int32_t *counters, int pr
             if (end + kOpen < min(int64_t(total), (w + 1) * share)) return parts + int64_t(w) * C::kPartial;
             return reinterpret_cast<const float *>(smem + pref_bytes + (w - blockIdx.x * NW) * C::kWarpB);
         };
-        join_rows<HD, ROWS, by.value>(a, of_warp, c.w0, c.w1, c.s, r, c.rows, kShift,
-                                      c.c0 == c.c1 ? nullptr : block_part(c.s, blockIdx.x), lane);
+        join_rows<HD, ROWS, by.value, ROWS == 32 ? 2 : 4>(a, of_warp, c.w0, c.w1, c.s, r, c.rows, kShift,
+                                                          c.c0 == c.c1 ? nullptr : block_part(c.s, blockIdx.x), lane);
     });
     bool shared_cut = false;
     for (int i = 0; i <= NW; ++i) shared_cut = shared_cut || (s_cut[i].rows > 0 && s_cut[i].c0 != s_cut[i].c1);
@@ -798,7 +816,8 @@ attend_decode_kernel(const AttendArgs a, float *parts, int32_t *counters, int pr
     __threadfence();
     each([](const Cut &c) { return c.last; }, [&](const Cut &c, int r, auto by) {
         const auto of_block = [&](int32_t b) -> const float * { return block_part(c.s, b); };
-        join_rows<HD, ROWS, by.value>(a, of_block, c.c0, c.c1, c.s, r, c.rows, kShift, nullptr, lane);
+        join_rows<HD, ROWS, by.value, ROWS == 32 ? 2 : by.value == 1 ? 16 : 4>(a, of_block, c.c0, c.c1, c.s, r, c.rows,
+                                                                               kShift, nullptr, lane);
     });
 }
 
