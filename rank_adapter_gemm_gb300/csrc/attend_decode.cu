@@ -28,6 +28,14 @@
 // With at most 8 rows the remainder goes into the MMA's unused rows 8..15 and
 // costs nothing.  An e4m3 code is exact in f16; a query row is scaled by a power
 // of two into f16, exact to 2^-24 of its largest element.
+//
+// Measured, 32 / 8 heads of 128, one row a request, graph replay: 256 requests of
+// 4,096 tokens over bf16 623 us, 6.9 TB/s (a plain copy: 6.8), over e4m3 330 us, 6.5;
+// one request of 131,071 tokens 87 us, 6.2; 64 requests of 108,700 tokens together
+// 77 us, 5.8: about 5 us pass until every SM streams and as many in the joins.  One
+// request of 100 tokens 7.7 us: a chain of dependent loads.  With 16 rows a tile over
+// e4m3 the work between the copies bounds it instead: 64 requests of 4 rows and
+// 108,700 tokens 62 us, 3.6 TB/s.
 #include <type_traits>
 
 #include <cuda_fp16.h>

