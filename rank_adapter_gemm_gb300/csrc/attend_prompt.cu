@@ -21,11 +21,13 @@
 //   warp 13          hands out the work
 // One block an SM stays for the whole call.  The (request, row tiles, key head)
 // items go to whichever block is free, those with the most keys first (of each
-// request, where there are more than 32), and a block's copies and products begin its next item while the softmax
-// warps still write the last one's output.  An item's keys are taken from the last
-// tile down: with a bias that falls with distance the largest scores come first
-// and O is not rescaled step after step.  k and v tiles share one ring; every wait
-// is bounded (2 s) and reports LORA_ERR_TIMEOUT.
+// request, where there are more than 32), and a block's copies and products begin
+// its next item while the softmax warps still write the last one's output.  With
+// few items a block takes one part of an item's keys, and the parts are joined pair
+// by pair.  An item's keys are taken from the last tile down: with a bias that falls
+// with distance the largest scores come first and O is not rescaled step after step.
+// k and v tiles share one ring; every wait is bounded (2 s) and reports
+// LORA_ERR_TIMEOUT.
 //
 // The instruction takes one type for both operands.  Over a bf16 cache weights
 // are rounded to bf16 (sums use them unrounded).  Over an e4m3 cache everything is
@@ -217,8 +219,95 @@ __device__ __forceinline__ uint32_t tile_at(int row, int piece) {
 struct Item {
     int32_t seq, head, row0, rows;  // first row and rows (of the request's n * group)
     int32_t q0, n, len, lo, key0, steps;
+    int32_t part, parts;            // of the item's keys; the fields above are the part's
     bool any;                       // none: the work is done
 };
+
+// Few items leave SMs idle: their keys are cut into up to kMaxParts parts, of at least
+// kMinSteps steps each, a block each.  64 rows over 16,384 tokens: 38 us, whole items 179;
+// 16 rows over 2,000 tokens: 21.8 us, in parts of at least 2 steps 23.2, of 1 25.5.
+constexpr int kMaxParts = 16, kMinSteps = 4, kMaxGrid = 160;
+
+// A part's partial result: references and sums of its 256 rows, then their outputs,
+// four dims of all rows together, fp32.
+template <int HD>
+constexpr int64_t kPartial = int64_t(2 * kRows) * (HD + 2);
+
+// A warp's 32 rows (a lane each: reference m, sum l, outputs in tensor memory) joined
+// with those of the item's other parts, two neighbouring groups of parts at a time:
+// of two warps that meet, the one that comes first leaves its rows and ends, the
+// other goes on with both.  The lower part stands on the left whoever comes first,
+// so results do not depend on timing, and nothing waits.  True in the warp that
+// has all parts.  flags: of an item a bit for every warp and pair of groups (8 or 16 a
+// warp: 4 + 2 + 1, or 8 + 4 + 2 + 1), zero between calls.
+template <int HD>
+__device__ __forceinline__ bool join_parts(float *slots, uint32_t *flags, int32_t part, int32_t parts, int r,
+                                           uint32_t o_at, float &m, float &l, int warp, int lane) {
+    const int bits = parts > 8 ? 16 : 8;
+    flags += warp * bits / 32;
+#pragma unroll 1
+    for (int level = 0; (1 << level) < parts; ++level) {
+        const int32_t group = part >> level, other = group ^ 1;
+        if ((other << level) >= parts) continue;
+        const uint32_t bit = 1u << (warp * bits % 32 + (bits - (bits >> level)) + (group >> 1));
+        bool second = *static_cast<volatile uint32_t *>(flags) & bit;
+        second = __shfl_sync(0xffffffffu, static_cast<int>(second), 0);
+        if (!second) {
+            float *mine = slots + (group << level) * kPartial<HD>;
+            mine[r] = m;
+            mine[2 * kRows + r] = l;
+            mine += 4 * kRows + r * 4;
+#pragma unroll 1
+            for (int c = 0; c < HD / 32; ++c) {
+                uint32_t x[32];
+                tmem_ld32(o_at + 32 * c, x);
+                tmem_wait(x);
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    stg_u4(mine + (8 * c + e) * 8 * kRows, make_uint4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]));
+            }
+            __threadfence();
+            __syncwarp();
+        }
+        uint32_t before = 0;
+        if (lane == 0) before = atomicXor(flags, bit);
+        if ((__shfl_sync(0xffffffffu, before, 0) & bit) == 0) return false;
+        __threadfence();
+        const float *theirs = slots + (other << level) * kPartial<HD>;
+        const float m2 = __ldcg(theirs + r), l2 = __ldcg(theirs + 2 * kRows + r);
+        theirs += 4 * kRows + r * 4;
+        const float top = fmaxf(m, m2), ref = top == -INFINITY ? 0.0f : top, w = ex2(m - ref), w2 = ex2(m2 - ref);
+        const bool left = group < other;
+        const auto joined = [&](float v, float v2) {
+            return left ? fmaf(w2, v2, w * v) : fmaf(w, v, w2 * v2);
+        };
+        m = top;
+        l = joined(l, l2);
+#pragma unroll 1
+        for (int c = 0; c < HD / 64; ++c) {
+            float4 y[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) y[e] = ldg_cg_f4(theirs + (16 * c + e) * 8 * kRows);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                uint32_t x[32];
+                tmem_ld32(o_at + 64 * c + 32 * h, x);
+                tmem_wait(x);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float4 v = y[8 * h + e];
+                    x[4 * e] = __float_as_uint(joined(__uint_as_float(x[4 * e]), v.x));
+                    x[4 * e + 1] = __float_as_uint(joined(__uint_as_float(x[4 * e + 1]), v.y));
+                    x[4 * e + 2] = __float_as_uint(joined(__uint_as_float(x[4 * e + 2]), v.z));
+                    x[4 * e + 3] = __float_as_uint(joined(__uint_as_float(x[4 * e + 3]), v.w));
+                }
+                tmem_st32(o_at + 64 * c + 32 * h, x);
+            }
+        }
+        tmem_wait_st();
+    }
+    return true;
+}
 
 // Claims on the call's items, zero between calls: items given out past the first
 // one of each block, and blocks that are done.
@@ -226,8 +315,9 @@ struct Claims {
     int32_t given, done;
 };
 
-template <int HD, bool E4M3>
-__global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const AttendArgs a, Claims *claims) {
+template <int HD, bool E4M3, bool SPLIT>
+__global__ void __launch_bounds__(kThreads, 1)
+attend_prompt_kernel(const AttendArgs a, Claims *claims, uint32_t *flags, float *partials) {
     using C = PromptConfig<HD>;
     constexpr float kShift = E4M3 ? 7.0f : 0.0f;
     extern __shared__ unsigned char smem_raw[];
@@ -588,6 +678,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
                 it.lo = a.window > 0 ? static_cast<int32_t>(max(int64_t(0), int64_t(first) - a.window + 1)) : 0;
                 it.key0 = it.lo & ~(kKeys - 1);
                 it.steps = last < 0 ? 0 : (last - it.key0) / kKeys + 1;
+                it.part = 0;
+                it.parts = 1;
                 it.any = true;
                 return it;
             };
@@ -608,6 +700,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
             int64_t above = total;
             int32_t seq = a.n_seq;  // requests from here on have been passed
             int64_t idx = blockIdx.x;
+            // where items are split: neighbouring blocks take an item's parts
+            const int32_t most = SPLIT && items > 0 ? static_cast<int32_t>(min(int64_t(kMaxParts), gridDim.x / items)) : 1;
+            if (SPLIT) idx = blockIdx.x / most;
             for (int32_t k = 0;; ++k) {
                 Item it{};
                 if (idx < items && by_size) {
@@ -663,6 +758,14 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
                         seq -= 32;
                     }
                 }
+                if (SPLIT && it.any) {
+                    it.parts = max(1, min(most, it.steps / kMinSteps));
+                    it.part = blockIdx.x % most;
+                    it.any = it.part < it.parts;
+                    const int32_t from = it.steps * it.part / it.parts;
+                    it.steps = it.steps * (it.part + 1) / it.parts - from;
+                    it.key0 += from * kKeys;
+                }
                 if (k >= 2 && !wait(&bar.item_empty[k & 1], ((k >> 1) - 1) & 1)) break;
                 const bool any = __any_sync(0xffffffffu, it.any);
                 if (it.any || (!any && lane == 0)) {
@@ -677,6 +780,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
                         claims->done = 0;
                     }
                     break;
+                }
+                if (SPLIT) {
+                    idx = items;
+                    continue;
                 }
                 // the next item is claimed when the copies come to this one's last step: late
                 // enough that blocks with short items take more, early enough to hide the claim
@@ -824,6 +931,13 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
             float l, l1;
             unpack2(add2(sum[0], sum[1]), l, l1);
             l += l1;
+            // (a block has one item where items are split, and its parts are neighbouring blocks)
+            if (SPLIT && it.parts > 1 &&
+                !join_parts<HD>(partials + (blockIdx.x - it.part) * kPartial<HD>,
+                                flags + (blockIdx.x - it.part), it.part, it.parts, r, o_at, m, l, warp, lane)) {
+                release(k);
+                continue;
+            }
             const float inv = l > 0.0f ? a.kv.v_scale / l : l == 0.0f ? 0.0f : l;
             const int32_t out_row = it.row0 + r, h = it.head * a.group + out_row % a.group;
             const int64_t t = it.q0 + (live ? out_row / a.group : 0);
@@ -873,25 +987,37 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prompt_kernel(const Attend
     }
 }
 
-template <int HD, bool E4M3>
-cudaError_t launch(const AttendArgs &a, void *claims, cudaStream_t stream) {
+template <int HD, bool E4M3, bool SPLIT>
+cudaError_t launch_kernel(const AttendArgs &a, unsigned grid, void *ws, cudaStream_t stream) {
     using C = PromptConfig<HD>;
-    const auto kernel = attend_prompt_kernel<HD, E4M3>;
+    const auto kernel = attend_prompt_kernel<HD, E4M3, SPLIT>;
     static std::atomic<uint64_t> seen{0};
     int sms = 0;
     const cudaError_t e = prepare_kernel(kernel, C::kSmem, seen, &sms);
     if (e != cudaSuccess) return e;
+    sms = sms < kMaxGrid ? sms : kMaxGrid;
+    // flags (a word a block: an item has as many words as blocks, and needs 2, or 4 for more than
+    // 8 parts) and partials take the places of the decode path's counters and partials
+    char *bytes = static_cast<char *>(ws);
+    return launch_dependent(kernel, grid < unsigned(sms) ? grid : unsigned(sms), kThreads, C::kSmem, stream, a,
+                            reinterpret_cast<Claims *>(bytes + 768), reinterpret_cast<uint32_t *>(bytes),
+                            reinterpret_cast<float *>(bytes + 1024));
+}
+
+template <int HD, bool E4M3>
+cudaError_t launch(const AttendArgs &a, void *ws, cudaStream_t stream) {
     // every request's rows fill pairs of tiles but for one
     const int64_t items = (int64_t(a.T) * a.group / (2 * kRows) + a.n_seq) * a.kv.n_kv;
-    const unsigned grid = static_cast<unsigned>(items < sms ? items : sms);
-    return launch_dependent(kernel, grid, kThreads, C::kSmem, stream, a, static_cast<Claims *>(claims));
+    // with no more than half of the SMs busy, parts of items for the others
+    if (2 * items <= 152) return launch_kernel<HD, E4M3, true>(a, kMaxGrid, ws, stream);
+    return launch_kernel<HD, E4M3, false>(a, static_cast<unsigned>(items < kMaxGrid ? items : kMaxGrid), ws, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_attend_prompt(const AttendArgs &a, bool e4m3, void *claims, cudaStream_t stream) {
-    if (a.kv.head_dim == 64) return e4m3 ? launch<64, true>(a, claims, stream) : launch<64, false>(a, claims, stream);
-    return e4m3 ? launch<128, true>(a, claims, stream) : launch<128, false>(a, claims, stream);
+cudaError_t launch_attend_prompt(const AttendArgs &a, bool e4m3, void *ws, cudaStream_t stream) {
+    if (a.kv.head_dim == 64) return e4m3 ? launch<64, true>(a, ws, stream) : launch<64, false>(a, ws, stream);
+    return e4m3 ? launch<128, true>(a, ws, stream) : launch<128, false>(a, ws, stream);
 }
 
 }  // namespace lora

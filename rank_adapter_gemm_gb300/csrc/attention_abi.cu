@@ -15,7 +15,7 @@ cudaError_t launch_rope_append(const uint16_t *qkv, int64_t ldqkv, int32_t T, in
                                const KvView &kv, bool e4m3, int32_t *err, cudaStream_t stream);
 size_t decode_workspace_bytes(int32_t head_dim);
 cudaError_t launch_attend_decode(const AttendArgs &a, bool e4m3, int32_t max_q, void *ws, cudaStream_t stream);
-cudaError_t launch_attend_prompt(const AttendArgs &a, bool e4m3, void *claims, cudaStream_t stream);
+cudaError_t launch_attend_prompt(const AttendArgs &a, bool e4m3, void *ws, cudaStream_t stream);
 }  // namespace lora
 
 using lora::aligned16;
@@ -136,20 +136,23 @@ lora_status_t lora_attend_workspace_bytes(const lora_attention_t *att, const lor
 }
 
 // The decode path reads a request's cache once for every 32 of its rows, spread over
-// the whole GPU; the prompt path gives 256 rows of a key head to one block, so its
-// time does not grow with rows but steps with the waves of such blocks on 152 SMs.
-// Measured a key: 16 rows of a key head on the decode path cost about 1/256 of a
-// wave on the prompt path.  Both sides, us (decode / prompt, 32/8 heads of 128):
-// 64 requests of 100 to 8,000 tokens, 4 rows 87 / 111, 8 rows 117 / 113, 16 rows
-// 183 / 115; 8 requests of 4,096, 8 rows 48 / 51, 16 rows 66 / 52; one request of
-// 16,384, 32 rows 66 / 179, 96 rows 137 / 231.
+// the whole GPU; the prompt path gives 256 rows of a key head to one block, or with
+// few such items up to 16 parts of their keys to a block each.  Its time does not grow
+// with rows but steps with the waves of such blocks on 152 SMs.  Measured a key: 16 rows
+// of a key head on the decode path cost about 1/256 of a wave on the prompt path.
+// Both sides, us (decode / prompt, 32/8 heads of 128): 64 requests of 100 to 8,000 tokens,
+// 4 rows 84 / 111, 8 rows 114 / 113; 8 requests of 4,096, 4 rows 38 / 38, 8 rows 47 / 38,
+// 32 rows 104 / 54; one request of 16,384, 4 rows 29 / 37, 8 rows 41 / 37, 32 rows 64 / 38,
+// 128 rows 172 / 55; one of 2,000, 4 rows 18 / 22, 16 rows 22 / 22; one of 131,071, 4 rows
+// 97 / 113, 64 rows 601 / 143.
 lora_attend_path_t lora_attend_resolve_path(lora_attend_path_t requested, const lora_attention_t *att,
                                             const lora_kv_t *kv, int32_t n_seq, int32_t max_q_hint) {
     if (requested != LORA_ATTEND_AUTO || att == nullptr || kv == nullptr || kv->n_kv < 1) return requested;
     const int64_t rows = int64_t(max_q_hint) * (att->n_heads / kv->n_kv), pairs = int64_t(n_seq) * kv->n_kv;
     const int64_t half_tiles = rows <= 16 ? 1 : 2 * ((rows + 31) / 32);
-    const int64_t waves = (pairs * ((rows + 255) / 256) + 151) / 152;
-    return pairs * half_tiles < 256 * waves ? LORA_ATTEND_DECODE : LORA_ATTEND_PROMPT;
+    const int64_t items = pairs * ((rows + 255) / 256), waves = (items + 151) / 152;
+    const int64_t parts = std::min<int64_t>(16, std::max<int64_t>(1, 152 / std::max<int64_t>(1, items)));
+    return pairs * half_tiles * parts < 256 * waves ? LORA_ATTEND_DECODE : LORA_ATTEND_PROMPT;
 }
 
 lora_status_t lora_attend(const void *q, int64_t ldq, void *out, int64_t ldo, float *lse, int32_t T, int32_t n_seq,
@@ -183,8 +186,7 @@ lora_status_t lora_attend(const void *q, int64_t ldq, void *out, int64_t ldo, fl
     const bool e4m3 = kv->type == LORA_KV_E4M3;
     if (lora_attend_resolve_path(path, att, kv, n_seq, max_q_hint) == LORA_ATTEND_DECODE)
         return from_cuda(lora::launch_attend_decode(a, e4m3, max_q_hint, ws, s));
-    // the decode path's counters and the prompt path's claims share the first kilobyte
-    return from_cuda(lora::launch_attend_prompt(a, e4m3, static_cast<char *>(ws) + 768, s));
+    return from_cuda(lora::launch_attend_prompt(a, e4m3, ws, s));
 }
 
 }  // extern "C"

@@ -188,8 +188,8 @@ def test_attend_path_choice(L):
         return L.lora_attend_resolve_path(asked, att, kv, n_seq, max_q)
     assert path(1, 1) == path(4096, 1) == path(4096, 4) == "decode"
     assert path(1, 1000) == path(300, 8) == path(2, 1 << 30) == "prompt"
-    # few requests: the decode path splits the cache, the prompt path would leave SMs idle
-    assert path(1, 64) == "decode" and path(64, 64) == "prompt"
+    # few requests: both paths split the cache, the prompt path into fewer and larger pieces
+    assert path(1, 4) == "decode" and path(1, 64) == path(64, 64) == "prompt"
     assert path(1, 1000, "decode") == "decode" and path(1, 1, "prompt") == "prompt"
 
 
@@ -623,6 +623,36 @@ def test_attend_long_ragged_batches(L, path):
     else:
         Case(L, [1100], [1100], 2, 1, 128, seed=9).run(path).check(path)
         Case(L, [900], [600], 4, 2, 64, seed=10, fp8=True).run(path, window=333).check(path, window=333)
+
+
+@gpu
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("hd,rows", [(128, 9), (64, 40), (128, 64)])
+def test_attend_keys_in_parts(L, hd, rows, fp8):
+    """Few rows over caches of 1 to 71 key steps: every number of parts from 1 to 16, with
+    a request of each in one call too."""
+    lens = [500, 900, 1100, 1700, 2200, 2700, 3300, 4000, 4500, 5200, 9000]
+    for i, n in enumerate(lens[::3] if rows > 9 else lens):
+        Case(L, [n], [min(n, rows)], 4, 1, hd, ps=64, fp8=fp8, seed=20 + i).run("prompt").check("prompt")
+    c = Case(L, [2200, 90, 0, 1300, 4000], [rows, 3, 2, 1, rows], 8, 2, hd, ps=32, fp8=fp8, seed=40)
+    c.run("prompt").check("prompt")
+    kw = dict(softcap=20.0, window=1500, slopes=[2.0 ** -(h + 4) for h in range(8)])
+    c.run("prompt", **kw).check("prompt", **kw)
+
+
+@gpu
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("hd", [64, 128])
+def test_attend_many_prompts(L, hd, fp8):
+    """More items than half of the SMs: whole ones, of up to and of more than 32 requests."""
+    rng = np.random.default_rng(hd)
+    for n in (13, 40):
+        q = [int(x) for x in rng.integers(0, 150, n)]
+        lens = [x + int(y) for x, y in zip(q, rng.integers(0, 300, n))]
+        c = Case(L, lens, q, 16, 8, hd, fp8=fp8, seed=60 + n)
+        c.run("prompt").check("prompt")
+        kw = dict(softcap=20.0, window=100, slopes=[2.0 ** -(h / 2 + 1) for h in range(16)])
+        c.run("prompt", **kw).check("prompt", **kw)
 
 
 @gpu
