@@ -35,8 +35,8 @@
 // 2^-24 of its largest element, and weights, times 2^7, keep 11 bits down to 2^-21
 // of the row's reference.
 //
-// Measured, causal, 32 / 8 heads of 128, graph replay: 8,192 tokens 430 us, 1.28 PFLOP/s
-// (over e4m3 461), 16,384 tokens 1,580 us, 1.39 PFLOP/s; cuBLAS reaches 1.92 on a large
+// Measured, causal, 32 / 8 heads of 128, graph replay: 8,192 tokens 432 us, 1.27 PFLOP/s
+// (over e4m3 463), 16,384 tokens 1,600 us, 1.38 PFLOP/s; cuBLAS reaches 1.92 on a large
 // bf16 product.  64-wide heads: 8,192 tokens 364 us; there a product does half the
 // operations in nearly the time.  With caps and a bias the softmax bounds it: 2,711
 // ragged tokens over e4m3 60 us, without them 44.
@@ -63,8 +63,8 @@ struct PromptConfig {
     static constexpr uint32_t kHalfB = kRows * 128;   // 64 dims of all rows
     // Registers a thread: 128 at launch, then by role.  The four warpgroups' shares (two
     // of softmax, copies, products) add up to the launch's 4 x 128.  Measured on 8,192
-    // tokens (184, 80, 64 against 168, 104, 72): 128-wide heads 436 against 428 us, over
-    // e4m3 571 against 514; 8 ragged chunks of 64-wide heads 69.5 against 71.4.
+    // tokens (184, 80, 64 against 168, 104, 72): 128-wide heads 440 against 432 us, over
+    // e4m3 506 against 463; 64-wide heads 364 against 367, 8 ragged chunks 72 against 76.
     static constexpr int kSoftmaxRegs = HD == 128 ? 168 : 184;
     static constexpr int kCopyRegs = HD == 128 ? 104 : 80;
     static constexpr int kMmaRegs = HD == 128 ? 72 : 64;
@@ -656,7 +656,8 @@ attend_prompt_kernel(const AttendArgs a, Claims *claims, uint32_t *flags, float 
             // ---- work -------------------------------------------------------------------
             // Items in order, key heads innermost.  Up to 32 requests, a lane each: the pairs of
             // row tiles with the most keys first, of any request, so that what is left at the
-            // end is small (8 ragged chunks of 6,546 tokens: 96 us in the requests' order, 82 us so).
+            // end is small (8 ragged chunks of 6,546 tokens: 83 us in the requests' order, 72 us so;
+            // one of 8,192: 445 and 432).
             // More requests: pairs from the last request's last one down; the many items even
             // out by themselves.
             const int64_t items = total * a.kv.n_kv;
