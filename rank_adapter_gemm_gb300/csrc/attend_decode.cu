@@ -854,7 +854,8 @@ cudaError_t pick(const AttendArgs &a, int64_t rows, void *ws, cudaStream_t strea
 
 }  // namespace
 
-// Counters (one a block), then a partial a warp and two a block, of up to 32 rows.
+// Counters (one a block), then a partial a warp and two a block, of up to 32 rows: 320
+// rows a block, of which the prompt path takes 256.
 size_t decode_workspace_bytes(int32_t head_dim) {
     return 1024 + size_t(kMaxGrid) * (kWarps + 2) * 32 * (head_dim + 2) * sizeof(float);
 }
