@@ -56,14 +56,16 @@ __device__ __forceinline__ float tanh_far(float z) {
     return 1.0f - __fdividef(2.0f, ex2(z * (2.0f * kLog2e)) + 1.0f);
 }
 
-// Whether products of size `top` lie within half the cap, or there is none.  (A cap
-// below 1e-6 of mult would overflow the coefficients.)
+// Whether products of size `top` lie within half the cap, and NearForm's coefficients in
+// fp32's range: its last one is about |mult| (mult / cap)^6 and is wanted with all its
+// bits.  (A product's square is finite then too.)  Other scales take the general form.
 __device__ __forceinline__ bool near_cap(const AttendArgs &a, float mult, float top) {
-    return a.softcap == 0.0f || (top * fabsf(mult) <= 0.5f * a.softcap && fabsf(mult) <= 1e6f * a.softcap);
+    const float in = mult * a.inv_softcap, in2 = in * in, last = fabsf(mult) * in2 * in2 * in2;
+    return top * fabsf(mult) <= 0.5f * a.softcap && last >= 0x1p-120f && last <= 0x1p120f;
 }
 
-// A pair of such products in their final form (finish_scores), the scales in the
-// coefficients: x (k0 + k1 x^2 + k2 x^4 + k3 x^6) + bias.
+// A pair of products in their final form (finish_scores), the scales in the coefficients:
+// under a near cap, x (k0 + k1 x^2 + k2 x^4 + k3 x^6) + bias; without one x k0 + bias.
 struct NearForm {
     uint64_t k[4], slope2, at2;
 
@@ -77,11 +79,15 @@ struct NearForm {
         at2 = pack2(slope * back, slope * back);
     }
 
+    __device__ __forceinline__ uint64_t bias(float d) const { return fma2(slope2, pack2(d, d + 1.0f), at2); }
+
     // keys d and d + 1 after the first
-    __device__ __forceinline__ uint64_t operator()(uint64_t x, float d) const {
-        const uint64_t w = mul2(x, x), bias = fma2(slope2, pack2(d, d + 1.0f), at2);
-        return fma2(x, fma2(fma2(fma2(k[3], w, k[2]), w, k[1]), w, k[0]), bias);
+    __device__ __forceinline__ uint64_t capped(uint64_t x, float d) const {
+        const uint64_t w = mul2(x, x);
+        return fma2(x, fma2(fma2(fma2(k[3], w, k[2]), w, k[1]), w, k[0]), bias(d));
     }
+
+    __device__ __forceinline__ uint64_t linear(uint64_t x, float d) const { return fma2(x, k[0], bias(d)); }
 };
 
 // N products s in their final form, times log2 e, in fp32: scaled by mult, capped,
@@ -97,30 +103,26 @@ __device__ __forceinline__ void finish_scores(float (&s)[N], const AttendArgs &a
         for (int e = 0; e < N; e += 2) top = fmaxf(fmaxf(top, fabsf(s[e])), fabsf(s[e + 1]));
         if (!__all_sync(0xffffffffu, near_cap(a, mult, top))) {
             constexpr float kTanh[6] = LORA_TANH_ONE;
-            const float in = mult * a.inv_softcap;
 #pragma unroll
             for (int e = 0; e < N; ++e) {
-                const float z = s[e] * in, w = z * z;
+                const float z = s[e] * mult * a.inv_softcap, w = z * z;
                 const float poly = z * (1.0f + w * (kTanh[1] + w * (kTanh[2] + w * (kTanh[3] + w * (kTanh[4] +
                                                                                                      w * kTanh[5])))));
-                s[e] = a.softcap * (fabsf(z) <= 1.0f ? poly : tanh_far(z));
+                s[e] = fabsf(z) <= 1.0f ? poly : tanh_far(z);
             }
             capped = false;
-            mult = 1.0f;
+            mult = a.softcap;
         }
     }
     const NearForm form(a, mult, slope, back);
     if (capped) {
 #pragma unroll
         for (int e = 0; e < N; e += 2)
-            unpack2(form(pack2(s[e], s[e + 1]), static_cast<float>(e / 2 * STEP)), s[e], s[e + 1]);
+            unpack2(form.capped(pack2(s[e], s[e + 1]), static_cast<float>(e / 2 * STEP)), s[e], s[e + 1]);
     } else {
 #pragma unroll
-        for (int e = 0; e < N; e += 2) {
-            const float d = static_cast<float>(e / 2 * STEP);
-            unpack2(fma2(pack2(s[e], s[e + 1]), form.k[0], fma2(form.slope2, pack2(d, d + 1.0f), form.at2)), s[e],
-                    s[e + 1]);
-        }
+        for (int e = 0; e < N; e += 2)
+            unpack2(form.linear(pack2(s[e], s[e + 1]), static_cast<float>(e / 2 * STEP)), s[e], s[e + 1]);
     }
     if (masked) {
 #pragma unroll

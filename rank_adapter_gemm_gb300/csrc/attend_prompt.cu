@@ -842,14 +842,12 @@ attend_prompt_kernel(const AttendArgs a, Claims *claims, uint32_t *flags, float 
                 };
                 load_scores();
                 bool final_form = direct;
-                if (!masked && !direct) {
+                if (!masked && a.softcap > 0.0f) {
                     float far4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                    if (a.softcap > 0.0f) {
 #pragma unroll
-                        for (int e = 0; e < 128; e += 2)
-                            far4[(e / 2) & 3] = fmaxf(fmaxf(far4[(e / 2) & 3], fabsf(__uint_as_float(x[e]))),
-                                                      fabsf(__uint_as_float(x[e + 1])));
-                    }
+                    for (int e = 0; e < 128; e += 2)
+                        far4[(e / 2) & 3] = fmaxf(fmaxf(far4[(e / 2) & 3], fabsf(__uint_as_float(x[e]))),
+                                                  fabsf(__uint_as_float(x[e + 1])));
                     final_form = __all_sync(0xffffffffu, near_cap(a, mult, fmaxf(fmaxf(far4[0], far4[1]),
                                                                                  fmaxf(far4[2], far4[3]))));
                     if (final_form) {
@@ -857,15 +855,16 @@ attend_prompt_kernel(const AttendArgs a, Claims *claims, uint32_t *flags, float 
 #pragma unroll
                         for (int e = 0; e < 128; e += 2) {
                             float s0, s1;
-                            unpack2(form(pack2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])),
-                                         static_cast<float>(e)), s0, s1);
+                            unpack2(form.capped(pack2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])),
+                                                static_cast<float>(e)), s0, s1);
                             x[e] = __float_as_uint(s0);
                             x[e + 1] = __float_as_uint(s1);
                         }
                     }
                 }
                 if (!final_form) {
-                    // masks, and scores beyond half their cap: in place, 64 at a time (one copy of the code)
+                    // masks, biases without a cap, scores beyond half their cap: in place, 64 at a time (one
+                    // copy of the code)
 #pragma unroll 1
                     for (int c = 0; c < 2; ++c) {
                         uint32_t y[64];

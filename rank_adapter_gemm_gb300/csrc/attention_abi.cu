@@ -1,6 +1,7 @@
 // extern "C" entry points of lora_attention.h: argument checks, the rotary
 // frequencies and kernel dispatch.
 #include <algorithm>
+#include <cfloat>
 #include <cmath>
 
 #include "attention.cuh"
@@ -178,10 +179,12 @@ lora_status_t lora_attend(const void *q, int64_t ldq, void *out, int64_t ldo, fl
     if (!aligned16(ws)) return LORA_ERR_ALIGNMENT;
     if (T == 0 || n_seq == 0) return LORA_OK;
     if (max_q_hint <= 0 || max_q_hint > T) max_q_hint = T;
+    // a cap from 1e30 on changes no score below 1e25 by an fp32 rounding: none
+    const float cap = att->softcap < 1e30f ? att->softcap : 0.0f;
     const lora::AttendArgs a{static_cast<const uint16_t *>(q), static_cast<uint16_t *>(out), lse, ldq, ldo, ld_table,
                              q_offsets, kv_lens, block_table, att->slopes, err, view, T, n_seq, table_width,
-                             att->n_heads, att->n_heads / view.n_kv, att->window, att->scale, att->softcap,
-                             att->softcap > 0.0f ? 1.0f / att->softcap : 0.0f};
+                             att->n_heads, att->n_heads / view.n_kv, att->window, att->scale, cap,
+                             cap > 0.0f ? std::min(1.0f / cap, FLT_MAX) : 0.0f};
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const bool e4m3 = kv->type == LORA_KV_E4M3;
     if (lora_attend_resolve_path(path, att, kv, n_seq, max_q_hint) == LORA_ATTEND_DECODE)

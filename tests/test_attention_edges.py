@@ -1,0 +1,65 @@
+"""The attention side of a serving step at the edges of its range: magnitudes of
+queries and scales, calls whose arguments or device data do not fit together.
+References and tolerances are those of test_attention.py.
+"""
+import numpy as np
+import pytest
+
+from test_attention import PATHS, Case, L, _torch, ref_attend  # noqa: F401  (L: the library fixture)
+
+gpu = pytest.mark.gpu
+SLOPES = [2.0 ** -(h + 1) for h in range(4)]
+
+
+# ---------------------------------------------------------------------------
+# Scores far from 1
+# ---------------------------------------------------------------------------
+@gpu
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("path", PATHS)
+@pytest.mark.parametrize("kw", [dict(slopes=SLOPES), dict(softcap=30.0), dict(softcap=30.0, slopes=SLOPES),
+                                dict(softcap=1e-5), dict(softcap=1e6), dict(softcap=3e38)], ids=str)
+@pytest.mark.parametrize("power", [90, 70, 40, 20, 0, -20, -40, -90])
+def test_scores_at_query_magnitudes(L, power, kw, path, fp8):  # noqa: F811
+    """Queries times a power of two and the scale divided by it: scores, biases and
+    caps stay what they were, in tiles that a mask cuts and in tiles that none does."""
+    c = Case(L, [700, 150], [2, 60], 4, 2, 64, seed=14, fp8=fp8)
+    c.q_big.mul_(2.0 ** power)
+    scale = 64 ** -0.5 * 2.0 ** -power
+    c.run(path, scale=scale, **kw).check(path, scale=scale, **kw)
+
+
+@gpu
+@pytest.mark.parametrize("path", PATHS)
+@pytest.mark.parametrize("kw", [dict(scale=-0.125), dict(scale=-0.125, slopes=SLOPES), dict(scale=-0.125, softcap=4.0),
+                                dict(scale=0.0, softcap=4.0, slopes=SLOPES)], ids=str)
+def test_scale_not_positive(L, kw, path):  # noqa: F811
+    c = Case(L, [700, 150], [2, 60], 4, 2, 128, seed=15)
+    c.run(path, **kw).check(path, **kw)
+
+
+@gpu
+@pytest.mark.parametrize("path", PATHS)
+@pytest.mark.parametrize("kw", [dict(), dict(slopes=SLOPES), dict(softcap=20.0), dict(softcap=20.0, slopes=SLOPES)],
+                         ids=str)
+def test_score_of_minus_infinity(L, kw, path):  # noqa: F811
+    """A key with an infinity whose score is -inf has weight 0 (under a cap: the cap's
+    weight), in a tile that no mask cuts; everything else is as without it."""
+    torch = _torch()
+    c = Case(L, [700], [60 if path == "prompt" else 2], 4, 2, 64, seed=16)
+    heads = c.q_big[:, 8:8 + 4 * 64].view(c.T, 4, 64)
+    heads[:, :, 0] = heads[:, :, 0].abs() + 0.5
+    c.kv.k[c.table[0, 0].item(), 5, :, 0] = float("-inf")
+    c.run(path, **kw)
+    assert c.att.err.item() == 0
+    q = c.q.double().cpu().numpy().reshape(c.T, 4, 64)
+    got = c.out.double().cpu().numpy().reshape(c.T, 4, 64)
+    slopes, cap = kw.get("slopes"), kw.get("softcap", 0.0)
+    big = ref_attend(q, c.k[0], c.v[0], 64 ** -0.5, cap, 0, slopes, 700)[3]  # the other keys' largest score
+    c.k[0][5, :, 0] = -np.inf
+    ref, lse, size, _ = ref_attend(q, c.k[0], c.v[0], 64 ** -0.5, cap, 0, slopes, 700)
+    weights = 2.0 ** -8 if path == "prompt" else 2.0 ** -11
+    tol = 2.0 ** -8 * np.abs(ref) + (weights * 1.01 + 2.0 ** -18 * (1 + max(big.max(), cap))) * size
+    assert (np.abs(got - ref) <= tol).all()
+    assert (np.abs(c.lse.double().cpu().numpy() - lse) <= 2.0 ** -18 * (1 + big)).all()
+    assert torch.isfinite(c.out).all()
