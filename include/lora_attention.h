@@ -79,7 +79,7 @@ typedef struct {
  * Device errors: LORA_ERR_NO_PAGES (a request was not served for want of
  * pages), LORA_ERR_INVALID_ARG (a negative length, a request longer than its
  * table row - neither is served - or more tokens than T: the ones past T are
- * dropped), LORA_ERR_SLOT_RANGE (a negative page id; its tokens get slot -1).
+ * dropped, their requests' pages, kv_lens and q_offsets stand), LORA_ERR_SLOT_RANGE (a negative page id; its tokens get slot -1).
  * n_seq, n_free and T may be 0.  One launch.
  */
 lora_status_t lora_kv_step(const int32_t *ctx_lens, const int32_t *new_lens, int32_t n_seq, int32_t page_size,

@@ -7,7 +7,8 @@
 // the table already (position below the cached pages) or is
 // free_pages[e_i + position / page_size - pages(c_i)]; the token at a page's
 // first position writes that page's table entry, so no thread reads an entry
-// that this launch writes.
+// that this launch writes.  Entries of pages that begin past the step's last row, which
+// have no such token, are written with their request's outputs.
 //
 // The work is a few bytes a token and a request, so chains of dependent loads
 // bound it at every size; one launch therefore, with no second pass that waits
@@ -128,6 +129,12 @@ kv_step_kernel(const int32_t *ctx_lens, const int32_t *new_lens, int32_t n, int3
                 kv_lens[i] = served ? r[e].ctx + r[e].fresh : r[e].ctx;
                 if (!r[e].ok) report_error(err, LORA_ERR_INVALID_ARG);
                 else if (!fits) report_error(err, LORA_ERR_NO_PAGES);
+                if (served && r[e].need > 0 && at.tokens + r[e].fresh > T) {
+                    // page have + u begins at the request's token ((have + u) << shift) - ctx
+                    const int64_t have = pages_of(r[e].ctx, shift), cut = max(int64_t(0), T - at.tokens) + r[e].ctx;
+                    for (int64_t p = max(have, pages_of(cut, shift)); p < have + r[e].need; ++p)
+                        table[i * ld_table + p] = free_pages[at.pages + p - have];
+                }
             }
             if (served && r[e].need > 0) end = at.pages + r[e].need;
             at.tokens += r[e].fresh;

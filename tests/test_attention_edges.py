@@ -5,7 +5,8 @@ References and tolerances are those of test_attention.py.
 import numpy as np
 import pytest
 
-from test_attention import PATHS, Case, L, _torch, ref_attend  # noqa: F401  (L: the library fixture)
+from test_attention import (PATHS, Case, L, _run_step, _step_case, _torch, ref_attend,  # noqa: F401  (L: a fixture)
+                            ref_step)
 
 gpu = pytest.mark.gpu
 SLOPES = [2.0 ** -(h + 1) for h in range(4)]
@@ -63,3 +64,27 @@ def test_score_of_minus_infinity(L, kw, path):  # noqa: F811
     assert (np.abs(got - ref) <= tol).all()
     assert (np.abs(c.lse.double().cpu().numpy() - lse) <= 2.0 ** -18 * (1 + big)).all()
     assert torch.isfinite(c.out).all()
+
+
+# ---------------------------------------------------------------------------
+# Steps with more tokens than rows
+# ---------------------------------------------------------------------------
+@gpu
+@pytest.mark.parametrize("n,ps,ctx_hi,new_hi,part", [
+    (1, 16, 40, 4000, 0.0), (1, 16, 40, 4000, 0.3), (1, 1, 9, 3000, 0.5), (37, 16, 200, 60, 0.5), (37, 128, 500, 300, 0.9),
+    (1500, 16, 50, 40, 0.02), (1500, 16, 50, 40, 0.6), (2100, 64, 10, 200, 0.999), (5, 1024, 5000, 3000, 0.2)])
+@pytest.mark.parametrize("short", [False, True])
+def test_step_tables_of_tokens_past_the_rows(L, n, ps, ctx_hi, new_hi, part, short):  # noqa: F811
+    """The tokens past T are dropped; the table holds all pages of the requests that were
+    served, as `taken` and kv_lens count them."""
+    torch = _torch()
+    ctx, new, table, free = _step_case(3 * n + ps, n, ps, ctx_hi, new_hi, zero=0.1 if n > 1 else 0.0)
+    T = int(part * sum(new))
+    if short:
+        free = free[:2 * len(free) // 3]
+    st = _run_step(L, ctx, new, ps, free, table, T, ld_pad=2)
+    q_off, kv, pos, seq, slots, taken, want, errors = ref_step(ctx, new, ps, free, table, T)
+    assert sum(new) > T and st.err.item() in errors
+    assert torch.equal(st.block_table.cpu(), torch.tensor(want, dtype=torch.int32))
+    assert st.taken.item() == taken and st.kv_lens.tolist() == kv and st.q_offsets.tolist() == q_off
+    assert (st.positions.tolist(), st.seq_ids.tolist(), st.slot_map.tolist()) == (pos, seq, slots)
