@@ -45,9 +45,13 @@ def _table(t, n_seq):
         rows, width = t.shape
         ld, one = t.stride()
         if rows == n_seq and (one == 1 or width <= 1):
-            return t.data_ptr(), ld if ld > width else width, width
+            if ld >= width:
+                return t.data_ptr(), ld, width
+            if rows <= 1:  # the stride of a single row means nothing
+                return t.data_ptr(), width, width
     _dev(t, "block_table", _I32)
-    raise ValueError("block_table must be a 2-D int32 tensor, one row a request, with unit column stride")
+    raise ValueError("block_table must be a 2-D int32 tensor, one row a request, with unit column stride and rows "
+                     "that do not overlap")
 
 
 def _matrix(t, name):

@@ -88,3 +88,73 @@ def test_step_tables_of_tokens_past_the_rows(L, n, ps, ctx_hi, new_hi, part, sho
     assert torch.equal(st.block_table.cpu(), torch.tensor(want, dtype=torch.int32))
     assert st.taken.item() == taken and st.kv_lens.tolist() == kv and st.q_offsets.tolist() == q_off
     assert (st.positions.tolist(), st.seq_ids.tolist(), st.slot_map.tolist()) == (pos, seq, slots)
+
+
+# ---------------------------------------------------------------------------
+# What the binding hands over (host tensors that say they are on the device, and a
+# library that only records)
+# ---------------------------------------------------------------------------
+class OnDevice:
+    """Wraps a host tensor for the binding's checks; no kernel sees it."""
+
+    def __new__(cls, t):
+        torch = _torch()
+        kind = type("OnDeviceTensor", (torch.Tensor,), {"is_cuda": True})
+        return t.as_subclass(kind)
+
+
+@pytest.fixture
+def recorded(L, monkeypatch):  # noqa: F811
+    calls = []
+
+    class Library:
+        def __getattr__(self, name):
+            return lambda *args: calls.append((name, args)) or 0
+    from rank_adapter_gemm_gb300 import attention
+    attention._types()
+    monkeypatch.setattr(attention, "load", Library)
+    monkeypatch.setattr(attention, "_on", lambda stream: 0)
+    return calls
+
+
+def _attend_args(table, n, T=4, width=2 * 16):
+    from rank_adapter_gemm_gb300._lib import lora_attention_t, lora_kv_t
+    torch = _torch()
+    q, out = (OnDevice(torch.zeros(T, width, dtype=torch.bfloat16)) for _ in range(2))
+    off, lens = (OnDevice(torch.zeros(m, dtype=torch.int32)) for m in (n + 1, n))
+    kv = lora_kv_t(1 << 20, 1 << 21, 8, 16, 1, 16, 256, 16, 16, 0, 1.0, 1.0)
+    ws = OnDevice(torch.zeros(64, dtype=torch.uint8))
+    return dict(q=q, out=out, q_offsets=off, kv_lens=lens, block_table=table, kv=kv,
+                att=lora_attention_t(2, 0.1, 0.0, 0, None), ws=ws, err=None)
+
+
+def _tables():
+    torch = _torch()
+    row = torch.arange(6, dtype=torch.int32)
+    return {"shared": row.expand(4, 6), "overlapping": torch.arange(20, dtype=torch.int32).as_strided((4, 6), (3, 1)),
+            "one a request": torch.zeros(4, 6, dtype=torch.int32), "part of wider rows": torch.zeros(
+                4, 9, dtype=torch.int32)[:, :6], "a single expanded row": row.expand(1, 6)}
+
+
+@pytest.mark.parametrize("name,ld", [("shared", None), ("overlapping", None), ("one a request", 6),
+                                     ("part of wider rows", 9), ("a single expanded row", 6)])
+def test_tables_whose_rows_overlap_are_refused(L, recorded, name, ld):  # noqa: F811
+    """A row stride below the width is not replaced by the width: the kernels would read,
+    and the step tables write, past such a table's memory."""
+    torch = _torch()
+    t = OnDevice(_tables()[name])
+    n = t.shape[0]
+    step = L.KVStep(n, 8, 6, 16, device="cpu")
+    step.block_table = t
+    i = OnDevice(torch.zeros(n, dtype=torch.int32))
+    if ld is None:
+        with pytest.raises(ValueError):
+            L.lora_attend(**_attend_args(t, n))
+        with pytest.raises(ValueError):
+            step.build(i, i, i)
+        assert not recorded
+    else:
+        L.lora_attend(**_attend_args(t, n))
+        step.build(i, i, i)
+        (_, a), (_, b) = recorded
+        assert (a[10], a[11]) == (ld, 6) and (b[7], b[8]) == (ld, 6)
