@@ -146,6 +146,9 @@ def lora_attend(q, out, q_offsets, kv_lens, block_table, kv: lora_kv_t, att: lor
     if rows != T or q_cols < cols or o_cols < cols:
         raise ValueError("q and out must have the same rows and n_heads * head_dim columns")
     table, ld, width = _table(block_table, n)
+    if not (ws.is_cuda and ws.is_contiguous()):
+        _dev(ws, "ws")
+        raise ValueError("ws must be contiguous")
     status = load().lora_attend(
         x, ldq, o, ldo, None if lse is None else _flat(lse, "lse", _F32, T * att.n_heads), T, n,
         _flat(q_offsets, "q_offsets", _I32, n + 1), _flat(kv_lens, "kv_lens", _I32), table, ld, width, kv, att,

@@ -158,3 +158,16 @@ def test_tables_whose_rows_overlap_are_refused(L, recorded, name, ld):  # noqa: 
         step.build(i, i, i)
         (_, a), (_, b) = recorded
         assert (a[10], a[11]) == (ld, 6) and (b[7], b[8]) == (ld, 6)
+
+
+def test_workspaces_off_the_device_are_refused(L, recorded):  # noqa: F811
+    torch = _torch()
+    table = OnDevice(torch.zeros(4, 6, dtype=torch.int32))
+    kw = _attend_args(table, 4)
+    with pytest.raises(TypeError):
+        L.lora_attend(**dict(kw, ws=torch.zeros(1 << 20, dtype=torch.uint8)))
+    with pytest.raises(ValueError):
+        L.lora_attend(**dict(kw, ws=OnDevice(torch.zeros(1 << 10, dtype=torch.uint8))[::2]))
+    assert not recorded
+    L.lora_attend(**kw)
+    assert len(recorded) == 1
