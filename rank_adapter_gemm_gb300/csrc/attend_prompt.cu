@@ -701,8 +701,11 @@ attend_prompt_kernel(const AttendArgs a, Claims *claims, uint32_t *flags, float 
             int64_t above = total;
             int32_t seq = a.n_seq;  // requests from here on have been passed
             int64_t idx = blockIdx.x;
-            // where items are split: neighbouring blocks take an item's parts
-            const int32_t most = SPLIT && items > 0 ? static_cast<int32_t>(min(int64_t(kMaxParts), gridDim.x / items)) : 1;
+            // where items are split: neighbouring blocks take an item's parts.  (Offsets out of
+            // order, which are reported, can make more items than the rows of the call: then
+            // whole ones, in turn.)
+            const int32_t most = SPLIT ? static_cast<int32_t>(max(int64_t(1), min(int64_t(kMaxParts),
+                                                                                  gridDim.x / max(items, int64_t(1))))) : 1;
             if (SPLIT) idx = blockIdx.x / most;
             for (int32_t k = 0;; ++k) {
                 Item it{};
@@ -782,8 +785,8 @@ attend_prompt_kernel(const AttendArgs a, Claims *claims, uint32_t *flags, float 
                     }
                     break;
                 }
-                if (SPLIT) {
-                    idx = items;
+                if (SPLIT) {  // a block has one item, unless there are more items than blocks
+                    idx = most == 1 ? idx + gridDim.x : items;
                     continue;
                 }
                 // the next item is claimed when the copies come to this one's last step: late
@@ -931,7 +934,7 @@ attend_prompt_kernel(const AttendArgs a, Claims *claims, uint32_t *flags, float 
             float l, l1;
             unpack2(add2(sum[0], sum[1]), l, l1);
             l += l1;
-            // (a block has one item where items are split, and its parts are neighbouring blocks)
+            // (a block has one item where items are in parts, and the parts are neighbouring blocks')
             if (SPLIT && it.parts > 1 &&
                 !join_parts<HD>(partials + (blockIdx.x - it.part) * kPartial<HD>,
                                 flags + (blockIdx.x - it.part), it.part, it.parts, r, o_at, m, l, warp, lane)) {
@@ -988,29 +991,34 @@ attend_prompt_kernel(const AttendArgs a, Claims *claims, uint32_t *flags, float 
 }
 
 template <int HD, bool E4M3, bool SPLIT>
-cudaError_t launch_kernel(const AttendArgs &a, unsigned grid, void *ws, cudaStream_t stream) {
-    using C = PromptConfig<HD>;
-    const auto kernel = attend_prompt_kernel<HD, E4M3, SPLIT>;
+cudaError_t prepare(int *sms) {
     static std::atomic<uint64_t> seen{0};
-    int sms = 0;
-    const cudaError_t e = prepare_kernel(kernel, C::kSmem, seen, &sms);
-    if (e != cudaSuccess) return e;
-    sms = sms < kMaxGrid ? sms : kMaxGrid;
-    // flags (a word a block: an item has as many words as blocks, and needs 2, or 4 for more than
-    // 8 parts) and partials take the places of the decode path's counters and partials
-    char *bytes = static_cast<char *>(ws);
-    return launch_dependent(kernel, grid < unsigned(sms) ? grid : unsigned(sms), kThreads, C::kSmem, stream, a,
-                            reinterpret_cast<Claims *>(bytes + 768), reinterpret_cast<uint32_t *>(bytes),
-                            reinterpret_cast<float *>(bytes + 1024));
+    const cudaError_t e = prepare_kernel(attend_prompt_kernel<HD, E4M3, SPLIT>, PromptConfig<HD>::kSmem, seen, sms);
+    if (*sms > kMaxGrid) *sms = kMaxGrid;
+    return e;
 }
 
 template <int HD, bool E4M3>
 cudaError_t launch(const AttendArgs &a, void *ws, cudaStream_t stream) {
+    // flags (a word a block: an item has as many words as blocks, and needs 2, or 4 for more than
+    // 8 parts) and partials take the places of the decode path's counters and partials
+    char *bytes = static_cast<char *>(ws);
+    Claims *claims = reinterpret_cast<Claims *>(bytes + 768);
+    uint32_t *flags = reinterpret_cast<uint32_t *>(bytes);
+    float *partials = reinterpret_cast<float *>(bytes + 1024);
     // every request's rows fill pairs of tiles but for one
     const int64_t items = (int64_t(a.T) * a.group / (2 * kRows) + a.n_seq) * a.kv.n_kv;
+    constexpr int kSmem = PromptConfig<HD>::kSmem;
+    int sms = 0;
+    cudaError_t e = prepare<HD, E4M3, true>(&sms);
+    if (e != cudaSuccess) return e;
     // with no more than half of the SMs busy, parts of items for the others
-    if (2 * items <= 152) return launch_kernel<HD, E4M3, true>(a, kMaxGrid, ws, stream);
-    return launch_kernel<HD, E4M3, false>(a, static_cast<unsigned>(items < kMaxGrid ? items : kMaxGrid), ws, stream);
+    if (2 * items <= sms)
+        return launch_dependent(attend_prompt_kernel<HD, E4M3, true>, sms, kThreads, kSmem, stream, a, claims, flags,
+                                partials);
+    if ((e = prepare<HD, E4M3, false>(&sms)) != cudaSuccess) return e;
+    return launch_dependent(attend_prompt_kernel<HD, E4M3, false>, static_cast<unsigned>(items < sms ? items : sms),
+                            kThreads, kSmem, stream, a, claims, flags, partials);
 }
 
 }  // namespace

@@ -171,3 +171,38 @@ def test_workspaces_off_the_device_are_refused(L, recorded):  # noqa: F811
     assert not recorded
     L.lora_attend(**kw)
     assert len(recorded) == 1
+
+
+# ---------------------------------------------------------------------------
+# Offsets out of order
+# ---------------------------------------------------------------------------
+@gpu
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("path", PATHS)
+@pytest.mark.parametrize("n", [3, 31, 39])
+def test_offsets_that_go_back(L, n, path, fp8):  # noqa: F811
+    """[0, T, 0, T, ...]: every other request ends before it begins and is skipped, the rest
+    all own the same rows: more work than T rows stand for.  They are alike here, so their
+    rows come out whole whoever writes them, and the workspace stays usable."""
+    torch = _torch()
+    T = 1000 if path == "prompt" else 10
+    c = Case(L, [1000], [T], 4, 1, 64, seed=17, fp8=fp8)
+    c.run(path)
+    att = L.Attention(n, T, 4, c.kv)
+    off = torch.tensor([0, T] * ((n + 1) // 2), dtype=torch.int32, device="cuda")
+    lens, table = c.lens_dev.repeat(n), c.table.repeat(n, 1)
+    c.out.fill_(float("nan"))
+    att.run(c.q, c.out, off, lens, table, T, path=path, lse=c.lse)
+    torch.cuda.synchronize()
+    assert att.err.item() == 1
+    # the rows that this call wrote
+    q, got = (t.double().cpu().numpy().reshape(T, 4, 64) for t in (c.q, c.out))
+    ref, lse, size, big = ref_attend(q, c.k[0], c.v[0], 64 ** -0.5, 0.0, 0, None, 1000)
+    weights = 2.0 ** -8 if path == "prompt" else 2.0 ** -11
+    tol = 2.0 ** -8 * np.abs(ref) + (weights * 1.01 + 2.0 ** -18 * (1 + big[..., None])) * size
+    assert (np.abs(got - ref) <= tol).all()
+    assert (np.abs(c.lse.double().cpu().numpy() - lse) <= 2.0 ** -18 * (1 + big)).all()
+    c.out.fill_(float("nan"))
+    c.att.ws = att.ws  # a call in the other's workspace gives what the first one did
+    c.att.run(c.q, c.out, c.off, c.lens_dev, c.table, T, path=path, lse=c.lse)
+    c.check(path)
