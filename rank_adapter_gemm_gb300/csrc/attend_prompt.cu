@@ -378,10 +378,25 @@ attend_prompt_kernel(const AttendArgs a, Claims *claims, uint32_t *flags, float 
 #pragma unroll
     for (int w = 0; w < kThreads / 32; ++w) total += s_warp[w];
     const uint32_t tmem = s_tmem;
+    // Waits of a whole warp.  Their outcome is a lane's own, and the instructions around them
+    // want all lanes, so it steers the warp by votes only.  wait() votes at once.  After follow()
+    // a lane that gave up remembers it, ends the block's other waits and goes on - every
+    // address stays in bounds, values no longer matter - until go_on() is asked: at an item's
+    // start and end, and every kVote steps of the products, whose chain of waits has no time
+    // for votes (8,192 tokens: 470 us with one in every wait, 433 so).
+    constexpr int32_t kVote = 64;
     bool fine = true;
+    const auto follow = [&](uint64_t *b, uint32_t parity) {
+        if (!tc::mbar_wait(b, parity, &s_abort, kWaitNs)) {
+            fine = false;
+            s_abort = 1;
+        }
+    };
+    const auto go_on = [&]() { return __all_sync(0xffffffffu, fine) != 0; };
     const auto wait = [&](uint64_t *b, uint32_t parity) {
-        fine = fine && tc::mbar_wait(b, parity, &s_abort, kWaitNs);
-        return fine;
+        const bool there = __all_sync(0xffffffffu, tc::mbar_wait(b, parity, &s_abort, kWaitNs));
+        fine = fine && there;
+        return there;
     };
     // a warp lets go of the block's k-th item
     const auto release = [&](int32_t k) {
@@ -406,7 +421,8 @@ attend_prompt_kernel(const AttendArgs a, Claims *claims, uint32_t *flags, float 
         };
         int32_t u = 0, q_round = 0;  // tiles and items so far
         for (int32_t k = 0;; ++k) {
-            if (!wait(&bar.item_full[k & 1], (k >> 1) & 1) || !s_item[k & 1].any) break;
+            follow(&bar.item_full[k & 1], (k >> 1) & 1);
+            if (!go_on() || !s_item[k & 1].any) break;
             const Item &it = s_item[k & 1];
             const int32_t steps = it.steps, lo = it.lo;
             const int32_t last = it.len - it.n + (it.row0 + it.rows - 1) / a.group;
@@ -419,7 +435,8 @@ attend_prompt_kernel(const AttendArgs a, Claims *claims, uint32_t *flags, float 
             const int qb = q_round % C::kQ;
             const uint32_t q_at_base = q_base + qb * 2 * C::kTileB;
             const auto q_piece = [&](int r) { return q_at_base + (r / kRows) * C::kTileB + tile_at(r % kRows, piece); };
-            if (steps > 0 && (q_round < C::kQ || wait(&bar.q_empty[qb], (q_round / C::kQ - 1) & 1))) {
+            if (steps > 0) {
+                if (q_round >= C::kQ) follow(&bar.q_empty[qb], (q_round / C::kQ - 1) & 1);
                 ++q_round;
 #pragma unroll 1
                 for (int half = 0; half < 2; ++half) {
@@ -471,7 +488,6 @@ attend_prompt_kernel(const AttendArgs a, Claims *claims, uint32_t *flags, float 
             }
             if (E4M3 && lane == 0) tc::mbar_arrive(&bar.exp_full[k & 1]);
             release(k);  // nothing below reads the item
-            if (!fine) break;
 
             int64_t at = -1;      // byte offset of this lane's key, -1: none
             bool smooth = false;  // all keys there, and 16 neighbours always in one page
@@ -548,7 +564,7 @@ attend_prompt_kernel(const AttendArgs a, Claims *claims, uint32_t *flags, float 
                     if (t == 1) publish(&bar.q_full[qb]);
                     if (t >= 2) publish(&bar.full[(u - 2) % C::kSlots]);
                 }
-                if (fine && tiles > 0) {
+                if (tiles > 0) {
                     tc::cp_wait_group<1>();
                     publish(&bar.full[(u - 2) % C::kSlots]);
                     tc::cp_wait_group<0>();
@@ -556,7 +572,6 @@ attend_prompt_kernel(const AttendArgs a, Claims *claims, uint32_t *flags, float 
                 }
             }
             if (steps == 0 && w == 0 && lane == 0) tc::mbar_arrive(&bar.claim);
-            if (!fine) break;
         }
         tc::cp_wait_all();
     } else if (warp >= 12) {
@@ -571,7 +586,8 @@ attend_prompt_kernel(const AttendArgs a, Claims *claims, uint32_t *flags, float 
             // descriptors are a tile's plus a constant: addresses stay below 2^18, so nothing carries
             const uint64_t q_desc = desc128(q_base, 16, 1024), k_desc = desc128(ring, 16, 1024);
             const uint64_t v_desc = desc128(ring, C::kHalfB, 1024);
-            const auto full = [&](int32_t u) { return wait(&bar.full[u % C::kSlots], (u / C::kSlots) & 1); };
+            // (elect_one brings the warp together after a wait)
+            const auto full = [&](int32_t u) { follow(&bar.full[u % C::kSlots], (u / C::kSlots) & 1); };
             const auto commit = [&](uint64_t *b) {
                 if (elect_one()) tc::mma_commit(b);
                 __syncwarp();
@@ -604,50 +620,54 @@ attend_prompt_kernel(const AttendArgs a, Claims *claims, uint32_t *flags, float 
             int32_t u = 0, q_round = 0;
             uint32_t p_parity = 0, o_parity = 0, o_used = 0;  // a bit a tile
             for (int32_t k = 0;; ++k) {
-                if (!wait(&bar.item_full[k & 1], (k >> 1) & 1) || !s_item[k & 1].any) break;
+                follow(&bar.item_full[k & 1], (k >> 1) & 1);
+                if (!go_on() || !s_item[k & 1].any) break;
                 const int32_t steps = s_item[k & 1].steps;
                 const int n_tiles = s_item[k & 1].rows > kRows ? 2 : 1;
                 release(k);
                 if (steps == 0) continue;
                 const int qb = q_round % C::kQ;
-                if (!wait(&bar.q_full[qb], (q_round / C::kQ) & 1) || !full(u)) break;
+                follow(&bar.q_full[qb], (q_round / C::kQ) & 1);
+                full(u);
                 ++q_round;
                 tc::fence_after_sync();
                 for (int i = 0; i < n_tiles; ++i) scores(qb, i, u);
                 commit(&bar.empty[u % C::kSlots]);
                 if (steps == 1) commit(&bar.q_empty[qb]);
-                for (int32_t j = 0; j < steps && fine; ++j, u += 2) {
-                    const bool more = j + 1 < steps;
-                    for (int i = 0; i < n_tiles && fine; ++i) {
-                        const bool last = i == n_tiles - 1;
-                        if (i == 0 && !full(u + 1)) break;
-                        // the last item's output has been read
-                        if (j == 0 && ((o_used >> i) & 1) && !wait(&bar.o_empty[i], ((o_parity >> i) & 1) ^ 1)) break;
-                        if (!wait(&bar.p_full[i][0], (p_parity >> i) & 1)) break;
-                        tc::fence_after_sync();
-                        outputs(i, u + 1, 0, j == 0);
-                        if (!wait(&bar.p_full[i][1], (p_parity >> i) & 1)) break;
-                        tc::fence_after_sync();
-                        outputs(i, u + 1, 1, j == 0);
-                        p_parity ^= 1u << i;
-                        if (!more) {
-                            commit(&bar.o_full[i]);
-                            o_parity ^= 1u << i;
-                            o_used |= 1u << i;
-                        }
-                        if (last) commit(&bar.empty[(u + 1) % C::kSlots]);
-                        if (more) {
-                            if (i == 0 && !full(u + 2)) break;
+                int32_t j = 0;
+                for (int32_t stop = min(steps, kVote); j < steps && go_on(); stop = min(steps, stop + kVote)) {
+                    for (; j < stop; ++j, u += 2) {
+                        const bool more = j + 1 < steps;
+                        for (int i = 0; i < n_tiles; ++i) {
+                            const bool last = i == n_tiles - 1;
+                            if (i == 0) full(u + 1);
+                            // the last item's output has been read
+                            if (j == 0 && ((o_used >> i) & 1)) follow(&bar.o_empty[i], ((o_parity >> i) & 1) ^ 1);
+                            follow(&bar.p_full[i][0], (p_parity >> i) & 1);
                             tc::fence_after_sync();
-                            scores(qb, i, u + 2);
-                            if (last) {
-                                commit(&bar.empty[(u + 2) % C::kSlots]);
-                                if (j + 2 == steps) commit(&bar.q_empty[qb]);
+                            outputs(i, u + 1, 0, j == 0);
+                            follow(&bar.p_full[i][1], (p_parity >> i) & 1);
+                            tc::fence_after_sync();
+                            outputs(i, u + 1, 1, j == 0);
+                            p_parity ^= 1u << i;
+                            if (!more) {
+                                commit(&bar.o_full[i]);
+                                o_parity ^= 1u << i;
+                                o_used |= 1u << i;
+                            }
+                            if (last) commit(&bar.empty[(u + 1) % C::kSlots]);
+                            if (more) {
+                                if (i == 0) full(u + 2);
+                                tc::fence_after_sync();
+                                scores(qb, i, u + 2);
+                                if (last) {
+                                    commit(&bar.empty[(u + 2) % C::kSlots]);
+                                    if (j + 2 == steps) commit(&bar.q_empty[qb]);
+                                }
                             }
                         }
                     }
                 }
-                if (!fine) break;
             }
             // every product has finished, and every arrival landed, before the block ends
             commit(&bar.done);
@@ -797,7 +817,6 @@ attend_prompt_kernel(const AttendArgs a, Claims *claims, uint32_t *flags, float 
                 idx = int64_t(gridDim.x) + __shfl_sync(0xffffffffu, next, 0);
             }
         }
-        fine = __all_sync(0xffffffffu, fine);
     } else {
         set_registers<C::kSoftmaxRegs, true>();
         // ---- softmax --------------------------------------------------------------------
@@ -807,7 +826,8 @@ attend_prompt_kernel(const AttendArgs a, Claims *claims, uint32_t *flags, float 
         const bool plain = a.softcap == 0.0f && a.slopes == nullptr && a.scale > 0.0f;
         int32_t round = 0, o_round = 0;
         for (int32_t k = 0;; ++k) {
-            if (!wait(&bar.item_full[k & 1], (k >> 1) & 1) || !s_item[k & 1].any) break;
+            follow(&bar.item_full[k & 1], (k >> 1) & 1);
+            if (!go_on() || !s_item[k & 1].any) break;
             // the item stays in shared memory: registers are scarce in the loop below
             const Item &it = s_item[k & 1];
             const int32_t steps = it.steps, key0 = it.key0, first_pos = it.len - it.n;
@@ -824,7 +844,7 @@ attend_prompt_kernel(const AttendArgs a, Claims *claims, uint32_t *flags, float 
             float mult = a.scale * a.kv.k_scale;
             if constexpr (E4M3) {
                 // (an item's exponents stay until the item is released)
-                if (!wait(&bar.exp_full[k & 1], (k >> 1) & 1)) break;
+                follow(&bar.exp_full[k & 1], (k >> 1) & 1);
                 if (steps > 0) mult *= __uint_as_float(static_cast<uint32_t>(127 + s_qexp[k & 1][r]) << 23);
             }
             const float by0 = mult * kLog2e;
@@ -929,7 +949,8 @@ attend_prompt_kernel(const AttendArgs a, Claims *claims, uint32_t *flags, float 
                     }
                 }
             }
-            if (!fine || (steps > 0 && !wait(&bar.o_full[i], o_round & 1))) break;
+            if (steps > 0) follow(&bar.o_full[i], o_round & 1);
+            if (!go_on()) break;
             tc::fence_after_sync();
             float l, l1;
             unpack2(add2(sum[0], sum[1]), l, l1);
@@ -977,7 +998,7 @@ attend_prompt_kernel(const AttendArgs a, Claims *claims, uint32_t *flags, float 
     }
     // a wait that gave up stops the block's other roles; what is in flight lands before
     // the tensor memory goes
-    if (!fine) {
+    if (!__all_sync(0xffffffffu, fine)) {
         s_abort = 1;
         report_error(a.err, LORA_ERR_TIMEOUT);
         __nanosleep(1000000);

@@ -206,3 +206,42 @@ def test_offsets_that_go_back(L, n, path, fp8):  # noqa: F811
     c.att.ws = att.ws  # a call in the other's workspace gives what the first one did
     c.att.run(c.q, c.out, c.off, c.lens_dev, c.table, T, path=path, lse=c.lse)
     c.check(path)
+
+
+# ---------------------------------------------------------------------------
+# Waits that give up (by reading: a stalled block is not run)
+# ---------------------------------------------------------------------------
+def _prompt_source():
+    import os
+    import re
+    here = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    text = open(os.path.join(here, "rank_adapter_gemm_gb300", "csrc", "attend_prompt.cu")).read()
+    return re.sub(r"//[^\n]*", "", text)
+
+
+def test_waits_that_give_up_take_the_whole_warp():
+    """A wait's outcome is a lane's own: the phase, the stop flag and the clock are read lane
+    by lane.  It may steer a warp only through a vote of all its lanes, as what follows
+    (votes, shuffles, elections, tensor-memory loads) wants the whole warp."""
+    import re
+    text = _prompt_source()
+    kernel = text[text.index("attend_prompt_kernel(const AttendArgs a"):]
+    # one form votes at once, the other is a helper that returns nothing and stops the block's
+    # other waits ...
+    voted = "__all_sync(0xffffffffu, tc::mbar_wait("
+    assert text.count("tc::mbar_wait(") == 2 and text.count(voted) == 1
+    at = text.replace(voted, "".ljust(len(voted))).index("tc::mbar_wait(")
+    helper = text[text.rindex("const auto", 0, at):]
+    helper = helper[:helper.index("};")]
+    name = re.match(r"const auto (\w+)", helper)[1]
+    assert "return" not in helper and "break" not in helper and "s_abort = 1;" in helper
+    # ... which is called as a statement, in a condition's body at most, also through a shorthand
+    shorthands = re.findall(r"const auto (\w+) = \[&\]\([^)]*\) \{ %s\([^;{}]*\); \};" % name, text)
+    for h in [name] + shorthands:
+        for m in re.finditer(r"[^\n]*\b%s\(&?[^\n]*" % h, text):
+            line = m[0].strip()
+            assert re.match(r"(const auto \w+ = .*|%s\(.*\);|if \((?:(?!%s).)*\) %s\(.*\);)$" % (h, h, h), line), line
+    # what the lanes remember is asked for by votes alone
+    for m in re.finditer(r"[^\n]*\bfine\b[^\n]*", kernel):
+        line = m[0].strip()
+        assert re.search(r"bool fine = true;|fine = false;|fine = fine && there;|__all_sync\(0xffffffffu, fine\)", line), line
