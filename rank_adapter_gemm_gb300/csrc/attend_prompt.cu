@@ -220,8 +220,16 @@ struct Item {
     int32_t seq, head, row0, rows;  // first row and rows (of the request's n * group)
     int32_t q0, n, len, lo, key0, steps;
     int32_t part, parts;            // of the item's keys; the fields above are the part's
+    bool first, last;               // of the part's segments (kSegment)
     bool any;                       // none: the work is done
 };
+
+// The tensor cores cut off what does not fit when they add to O, so that O loses about
+// 2^-24 of itself with every 16 keys: 0.5 % at a million keys, 2 % at four.  More steps than
+// these (65,536 keys) are handed out as segments, whose rows are added up in fp32 in the block's
+// partial result: 0.03 % at any length.  No wait then spans more than a segment either (3 ms
+// with scores far beyond a cap).
+constexpr int32_t kSegment = 512;
 
 // Few items leave SMs idle: their keys are cut into up to kMaxParts parts, of at least
 // kMinSteps steps each, a block each.  64 rows over 16,384 tokens: 38 us, whole items 179;
@@ -307,6 +315,47 @@ __device__ __forceinline__ bool join_parts(float *slots, uint32_t *flags, int32_
         tmem_wait_st();
     }
     return true;
+}
+
+// A warp's rows between the segments of an item: the lane's reference, sum and outputs left
+// in the block's partial result, and joined with it again.  (16 dims at a time: registers.)
+template <int HD>
+__device__ __forceinline__ void leave_segments(float *carried, int r, uint32_t o_at, float m, float l) {
+    carried[r] = m;
+    carried[2 * kRows + r] = l;
+    carried += 4 * kRows + r * 4;
+#pragma unroll 1
+    for (int c = 0; c < HD / 16; ++c) {
+        uint32_t x[16];
+        tc::tmem_ld16(o_at + 16 * c, x);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            stg_u4(carried + (4 * c + e) * 8 * kRows, make_uint4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]));
+    }
+}
+
+template <int HD>
+__device__ __forceinline__ void add_segments(const float *carried, int r, uint32_t o_at, float &m, float &l) {
+    const float m2 = __ldcg(carried + r), l2 = __ldcg(carried + 2 * kRows + r);
+    carried += 4 * kRows + r * 4;
+    const float top = fmaxf(m, m2), ref = top == -INFINITY ? 0.0f : top, w = ex2(m - ref), w2 = ex2(m2 - ref);
+    m = top;
+    l = fmaf(w2, l2, w * l);
+#pragma unroll 1
+    for (int c = 0; c < HD / 16; ++c) {
+        uint32_t x[16];
+        tc::tmem_ld16(o_at + 16 * c, x);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float4 v = ldg_cg_f4(carried + (4 * c + e) * 8 * kRows);
+            x[4 * e] = __float_as_uint(fmaf(w2, v.x, w * __uint_as_float(x[4 * e])));
+            x[4 * e + 1] = __float_as_uint(fmaf(w2, v.y, w * __uint_as_float(x[4 * e + 1])));
+            x[4 * e + 2] = __float_as_uint(fmaf(w2, v.z, w * __uint_as_float(x[4 * e + 2])));
+            x[4 * e + 3] = __float_as_uint(fmaf(w2, v.w, w * __uint_as_float(x[4 * e + 3])));
+        }
+        tmem_st16(o_at + 16 * c, x);
+    }
+    tmem_wait_st();
 }
 
 // Claims on the call's items, zero between calls: items given out past the first
@@ -727,9 +776,18 @@ attend_prompt_kernel(const AttendArgs a, Claims *claims, uint32_t *flags, float 
             const int32_t most = SPLIT ? static_cast<int32_t>(max(int64_t(1), min(int64_t(kMaxParts),
                                                                                   gridDim.x / max(items, int64_t(1))))) : 1;
             if (SPLIT) idx = blockIdx.x / most;
+            int32_t rest = 0;  // steps of the last item still to be handed out, in the lane that found it
             for (int32_t k = 0;; ++k) {
                 Item it{};
-                if (idx < items && by_size) {
+                const bool more = __any_sync(0xffffffffu, rest > 0);
+                if (more) {
+                    if (rest > 0) {
+                        it = s_item[(k - 1) & 1];
+                        it.steps = min(rest, kSegment);
+                        it.key0 -= it.steps * kKeys;
+                        it.first = false;
+                    }
+                } else if (idx < items && by_size) {
                     // the largest b with more than `want` pairs at or above it, by bisection
                     const uint32_t want = static_cast<uint32_t>(idx / a.kv.n_kv);
                     int32_t lo = 0, hi = longest;
@@ -782,13 +840,23 @@ attend_prompt_kernel(const AttendArgs a, Claims *claims, uint32_t *flags, float 
                         seq -= 32;
                     }
                 }
-                if (SPLIT && it.any) {
+                if (SPLIT && it.any && !more) {
                     it.parts = max(1, min(most, it.steps / kMinSteps));
                     it.part = blockIdx.x % most;
                     it.any = it.part < it.parts;
                     const int32_t from = it.steps * it.part / it.parts;
                     it.steps = it.steps * (it.part + 1) / it.parts - from;
                     it.key0 += from * kKeys;
+                }
+                if (it.any) {
+                    if (!more) {
+                        rest = it.steps;
+                        it.steps = min(rest, kSegment);
+                        it.key0 += (rest - it.steps) * kKeys;
+                        it.first = true;
+                    }
+                    rest -= it.steps;
+                    it.last = rest == 0;
                 }
                 if (k >= 2 && !wait(&bar.item_empty[k & 1], ((k >> 1) - 1) & 1)) break;
                 const bool any = __any_sync(0xffffffffu, it.any);
@@ -805,13 +873,15 @@ attend_prompt_kernel(const AttendArgs a, Claims *claims, uint32_t *flags, float 
                     }
                     break;
                 }
+                const bool done = !__any_sync(0xffffffffu, rest > 0);
                 if (SPLIT) {  // a block has one item, unless there are more items than blocks
-                    idx = most == 1 ? idx + gridDim.x : items;
+                    if (done) idx = most == 1 ? idx + gridDim.x : items;
                     continue;
                 }
                 // the next item is claimed when the copies come to this one's last step: late
                 // enough that blocks with short items take more, early enough to hide the claim
                 if (!wait(&bar.claim, k & 1)) break;
+                if (!done) continue;
                 int32_t next = 0;
                 if (lane == 0) next = atomicAdd(&claims->given, 1);
                 idx = int64_t(gridDim.x) + __shfl_sync(0xffffffffu, next, 0);
@@ -848,8 +918,7 @@ attend_prompt_kernel(const AttendArgs a, Claims *claims, uint32_t *flags, float 
                 if (steps > 0) mult *= __uint_as_float(static_cast<uint32_t>(127 + s_qexp[k & 1][r]) << 23);
             }
             const float by0 = mult * kLog2e;
-            float m = -INFINITY;  // the reference of the row's weights
-            uint64_t sum[2] = {0, 0};  // pairs of fp32
+            float m = -INFINITY, l = 0.0f;  // the reference of the row's weights, and their sum
             for (int32_t j = 0; j < steps; ++j, ++round) {
                 if (!wait(&bar.s_full[i], round & 1)) break;
                 tc::fence_after_sync();
@@ -920,13 +989,12 @@ attend_prompt_kernel(const AttendArgs a, Claims *claims, uint32_t *flags, float 
                 if (__any_sync(0xffffffffu, top > m + kGrow || (m == -INFINITY && top > m))) {
                     const float now = fmaxf(m, top), f = now == -INFINITY ? 1.0f : ex2(m - now);
                     m = now;
-                    const uint64_t f2 = pack2(f, f);
-#pragma unroll
-                    for (int q = 0; q < 2; ++q) sum[q] = mul2(sum[q], f2);
+                    l *= f;
                     if (j > 0) rescale_output<HD>(o_at, f);
                 }
                 const float ref = kShift - (m == -INFINITY ? 0.0f : m);
                 const uint64_t by2 = pack2(by, by), ref2 = pack2(ref, ref);
+                uint64_t sum[2] = {0, 0};  // of the step, pairs of fp32: a long row's sum has no room for single weights
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     uint32_t p[16];
@@ -948,13 +1016,25 @@ attend_prompt_kernel(const AttendArgs a, Claims *claims, uint32_t *flags, float 
                         if (lane == 0) tc::mbar_arrive(&bar.p_full[i][c >> 1]);
                     }
                 }
+                float even, odd;
+                unpack2(add2(sum[0], sum[1]), even, odd);
+                l += even + odd;
             }
             if (steps > 0) follow(&bar.o_full[i], o_round & 1);
             if (!go_on()) break;
             tc::fence_after_sync();
-            float l, l1;
-            unpack2(add2(sum[0], sum[1]), l, l1);
-            l += l1;
+            // the segments before this one, and for the one after it
+            float *const carried = partials + blockIdx.x * kPartial<HD>;
+            if (!it.first) add_segments<HD>(carried, r, o_at, m, l);
+            if (!it.last) {
+                leave_segments<HD>(carried, r, o_at, m, l);
+                tc::fence_before_sync();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(&bar.o_empty[i]);
+                ++o_round;
+                release(k);
+                continue;
+            }
             // (a block has one item where items are in parts, and the parts are neighbouring blocks')
             if (SPLIT && it.parts > 1 &&
                 !join_parts<HD>(partials + (blockIdx.x - it.part) * kPartial<HD>,

@@ -245,3 +245,53 @@ def test_waits_that_give_up_take_the_whole_warp():
     for m in re.finditer(r"[^\n]*\bfine\b[^\n]*", kernel):
         line = m[0].strip()
         assert re.search(r"bool fine = true;|fine = false;|fine = fine && there;|__all_sync\(0xffffffffu, fine\)", line), line
+
+
+# ---------------------------------------------------------------------------
+# Sums over very long caches
+# ---------------------------------------------------------------------------
+@gpu
+@pytest.mark.parametrize("fp8,hd,T,kw", [
+    (False, 128, 1301, dict()), (True, 64, 1301, dict(softcap=5.0, window=3000001)), (True, 128, 21, dict()),
+    (False, 64, 21, dict(slopes=[-1e-9] * 16)), (False, 64, 200, dict(window=70001))], ids=str)
+@pytest.mark.parametrize("power", [16, 17, 20, 22])
+def test_sums_over_very_long_caches(L, power, fp8, hd, T, kw):  # noqa: F811
+    """Prompt rows over up to 2^22 keys: eight pages again and again, so that every sum has
+    few terms in the reference and all of them on the device.  Values of one sign and
+    saturated caps leave no error to cancel."""
+    torch = _torch()
+    n, H, ps, P = 2 ** power, 16, 1024, 8
+    rng = np.random.default_rng(power + hd)
+    dtype = torch.float8_e4m3fn if fp8 else torch.bfloat16
+    kv = L.PagedKV.empty(P, ps, 1, hd, dtype)
+    for t, shift in ((kv.k, 0.0), (kv.v, 1.0)):
+        t.copy_(torch.from_numpy((rng.standard_normal((P, ps, 1, hd)) + shift).astype(np.float32)).cuda().to(dtype))
+    k, v = (t.double().cpu().numpy().reshape(P * ps, hd) for t in (kv.k, kv.v))
+    table = (torch.arange(n // ps, dtype=torch.int32, device="cuda") % P)[None].contiguous()
+    scale = 20 * hd ** -0.5 if kw.get("softcap") else hd ** -0.5
+    q = torch.from_numpy(rng.standard_normal((T, H * hd)).astype(np.float32)).cuda().bfloat16()
+    out, lse = torch.empty_like(q), torch.empty(T, H, device="cuda")
+    slopes = None if "slopes" not in kw else torch.tensor(kw["slopes"], device="cuda")
+    att = L.Attention(1, T, H, kv, scale, kw.get("softcap", 0.0), kw.get("window", 0), slopes)
+    att.run(q, out, torch.tensor([0, T], dtype=torch.int32, device="cuda"),
+            torch.tensor([n], dtype=torch.int32, device="cuda"), table, T, lse=lse, path="prompt")
+    torch.cuda.synchronize()
+    assert att.err.item() == 0
+    for t in {0, T // 2, T - 1}:
+        p = n - T + t
+        lo = max(0, p - kw["window"] + 1) if "window" in kw else 0
+        # how often the row sees each of the P * ps keys
+        times = np.bincount(np.arange(lo, p + 1) % (P * ps), minlength=P * ps)
+        s = q[t].double().cpu().numpy().reshape(H, hd) @ k.T * scale
+        if kw.get("softcap"):
+            s = kw["softcap"] * np.tanh(s / kw["softcap"])
+        w = np.where(times > 0, times * np.exp(s - s.max()), 0.0)
+        ref, size = w @ v / w.sum(1, keepdims=True), w @ np.abs(v) / w.sum(1, keepdims=True)
+        big = np.abs(s).max() + (0 if slopes is None else 1e-9 * n)
+        tol = 2.0 ** -8 * np.abs(ref) + (2.0 ** -8 * 1.01 + 2.0 ** -18 * (1 + big)) * size
+        if slopes is not None:  # the bias moves a weight by 1e-9 a key at most; it is not in ref
+            tol = tol + 2 * (np.exp(1e-9 * n) - 1) * size
+        assert (np.abs(out[t].double().cpu().numpy().reshape(H, hd) - ref) <= tol).all()
+        if slopes is None:
+            assert (np.abs(lse[t].double().cpu().numpy() - (np.log(w.sum(1)) + s.max()))
+                    <= 2.0 ** -18 * (1 + big)).all()
