@@ -168,8 +168,9 @@ lora_status_t lora_rope_append(const void *qkv, int64_t ldqkv, int32_t T, int32_
  *   kv_lens      int32 [n_seq]
  *   block_table  int32 [n_seq] rows of ld_table elements, table_width used
  *   slopes       device fp32 [n_heads] (distance bias), or null
- *   max_q_hint   host-known upper bound on a request's rows (0: T); it picks the
- *                path, results do not depend on it
+ *   max_q_hint   host-known upper bound on a request's rows (0: not known; the rows
+ *                are taken as shared out evenly, T / n_seq rounded up).  It picks the
+ *                path and the decode path's tile, no row depends on its being right
  *   ws           lora_attend_workspace_bytes() bytes, 16-byte aligned, zeroed once
  *                before the first call; every call leaves it as it found it (but
  *                zero it again after a call that reports LORA_ERR_TIMEOUT).
@@ -196,7 +197,8 @@ typedef enum {
 
 lora_status_t lora_attend_workspace_bytes(const lora_attention_t *att, const lora_kv_t *kv, size_t *bytes);
 
-/* The path lora_attend takes for `requested`, this shape and n_seq requests of at most max_q_hint rows (host only). */
+/* The path lora_attend takes for `requested`, this shape and n_seq requests of at most max_q_hint >= 1 rows (host
+ * only; without a hint lora_attend asks for T / n_seq rounded up). */
 lora_attend_path_t lora_attend_resolve_path(lora_attend_path_t requested, const lora_attention_t *att,
                                             const lora_kv_t *kv, int32_t n_seq, int32_t max_q_hint);
 

@@ -254,6 +254,6 @@ class Attention:
 
     def run(self, q, out, q_offsets, kv_lens, block_table, max_q_hint: int = 0, kv: Optional[PagedKV] = None, lse=None,
             path: str = "auto", stream=None) -> None:
-        """out = attention of q's rows; max_q_hint is an upper bound on a request's rows."""
+        """out = attention of q's rows; max_q_hint is an upper bound on a request's rows (0: taken as T / n_seq)."""
         lora_attend(q, out, q_offsets, kv_lens, block_table, (kv or self.kv).c, self.c, self.ws, self.err, max_q_hint,
                     lse, path, stream)

@@ -178,7 +178,8 @@ lora_status_t lora_attend(const void *q, int64_t ldq, void *out, int64_t ldo, fl
     if (ws == nullptr || ws_bytes < need) return LORA_ERR_WORKSPACE;
     if (!aligned16(ws)) return LORA_ERR_ALIGNMENT;
     if (T == 0 || n_seq == 0) return LORA_OK;
-    if (max_q_hint <= 0 || max_q_hint > T) max_q_hint = T;
+    if (max_q_hint <= 0) max_q_hint = (T - 1) / n_seq + 1;
+    if (max_q_hint > T) max_q_hint = T;
     // a cap from 1e30 on changes no score below 1e25 by an fp32 rounding: none
     const float cap = att->softcap < 1e30f ? att->softcap : 0.0f;
     const lora::AttendArgs a{static_cast<const uint16_t *>(q), static_cast<uint16_t *>(out), lse, ldq, ldo, ld_table,

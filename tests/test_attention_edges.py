@@ -295,3 +295,21 @@ def test_sums_over_very_long_caches(L, power, fp8, hd, T, kw):  # noqa: F811
         if slopes is None:
             assert (np.abs(lse[t].double().cpu().numpy() - (np.log(w.sum(1)) + s.max()))
                     <= 2.0 ** -18 * (1 + big)).all()
+
+
+# ---------------------------------------------------------------------------
+# Calls without a hint
+# ---------------------------------------------------------------------------
+@gpu
+@pytest.mark.parametrize("rows,n,want", [(1, 64, "decode"), (1, 300, "decode"), (4, 40, "decode"), (600, 2, "prompt"),
+                                         (40, 1, "prompt")])
+def test_without_a_hint_rows_count_as_shared_evenly(L, rows, n, want):  # noqa: F811
+    """The path is the one that a hint of T / n_seq takes: same bits (the paths round weights
+    differently, so that the other path's differ)."""
+    torch = _torch()
+    c = Case(L, [max(rows, 300)] * n, [rows] * n, 8, 2, 64, seed=18)
+    assert L.lora_attend_resolve_path("auto", c.run(want).att.c, c.kv.c, n, rows) == want
+    outs = {p: c.run(p).out.clone() for p in PATHS}
+    assert not torch.equal(*outs.values())
+    assert torch.equal(c.run("auto", hint=0).out, outs[want])
+    assert torch.equal(c.run("auto", hint=rows).out, outs[want])
