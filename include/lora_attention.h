@@ -179,8 +179,10 @@ lora_status_t lora_rope_append(const void *qkv, int64_t ldqkv, int32_t T, int32_
  * n_kv, n_seq <= LORA_MAX_SEQS, scale finite, softcap >= 0, window >= 0
  * (LORA_ERR_INVALID_ARG).  Device errors: LORA_ERR_INVALID_ARG (offsets out of
  * order or past T, kv_lens negative, beyond the table row or above
- * LORA_MAX_KV_LEN: that request is skipped), LORA_ERR_SLOT_RANGE (a page id outside [0, n_pages): its keys and
- * values read as zeros), LORA_ERR_TIMEOUT (a wait inside the kernel gave up).
+ * LORA_MAX_KV_LEN: that request is skipped), LORA_ERR_SLOT_RANGE (a page id outside
+ * [0, n_pages): its keys and values read as zeros), LORA_ERR_TIMEOUT (a wait inside
+ * the kernel gave up), LORA_ERR_UNSUPPORTED (decode path: more than 2^31 steps of 32 or
+ * 64 keys over all requests, key heads and tiles of rows; nothing is written).
  */
 typedef struct {
     int32_t n_heads;

@@ -313,3 +313,27 @@ def test_without_a_hint_rows_count_as_shared_evenly(L, rows, n, want):  # noqa: 
     assert not torch.equal(*outs.values())
     assert torch.equal(c.run("auto", hint=0).out, outs[want])
     assert torch.equal(c.run("auto", hint=rows).out, outs[want])
+
+
+@gpu
+def test_more_decode_steps_than_32_bits_count(L):  # noqa: F811
+    """2^12 requests of 2^25 tokens, all of them the same page: 2^32 steps.  The call reports
+    it and writes nothing."""
+    torch = _torch()
+    n = L.LORA_MAX_SEQS
+    kv = L.PagedKV.empty(1, 1024, 1, 128)
+    for t in (kv.k, kv.v):
+        t.zero_()
+    table = torch.zeros(n, 2 ** 15, dtype=torch.int32, device="cuda")
+    q = torch.zeros(n, 128, dtype=torch.bfloat16, device="cuda")
+    out = torch.full_like(q, 7.0)
+    att = L.Attention(n, n, 1, kv)
+    lens = torch.full((n,), 2 ** 25, dtype=torch.int32, device="cuda")
+    off = torch.arange(n + 1, dtype=torch.int32, device="cuda")
+    att.run(q, out, off, lens, table, 1, path="decode")
+    assert att.err.item() == 9 and bool((out == 7.0).all())
+    assert not bool(att.ws.any())
+    # the same call with shorter requests is served in the same workspace
+    att.err.zero_()
+    att.run(q, out, off, lens // 2 ** 18, table, 1, path="decode")
+    assert att.err.item() == 0 and bool((out == 0.0).all())
