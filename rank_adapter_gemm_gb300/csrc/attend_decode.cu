@@ -30,10 +30,10 @@
 // of two into f16, exact to 2^-24 of its largest element.
 //
 // Measured, 32 / 8 heads of 128, one row a request, graph replay: 256 requests of
-// 4,096 tokens over bf16 623 us, 6.9 TB/s (a plain copy: 6.8), over e4m3 330 us, 6.5;
-// one request of 131,071 tokens 87 us, 6.2; 64 requests of 108,700 tokens together
-// 77 us, 5.8: about 5 us pass until every SM streams and as many in the joins.  One
-// request of 100 tokens 7.7 us: a chain of dependent loads.  With 16 rows a tile over
+// 4,096 tokens over bf16 629 us, 6.8 TB/s (a plain copy: 6.8), over e4m3 335 us, 6.4;
+// one request of 131,071 tokens 88 us, 6.1; 64 requests of 108,700 tokens together
+// 76 us, 5.8: about 5 us pass until every SM streams and as many in the joins.  One
+// request of 100 tokens 7.6 us: a chain of dependent loads.  With 16 rows a tile over
 // e4m3 the work between the copies bounds it instead: 64 requests of 4 rows and
 // 108,700 tokens 62 us, 3.6 TB/s.
 #include <type_traits>
@@ -139,7 +139,7 @@ __device__ __forceinline__ int32_t tiles_of(const AttendArgs &a, int32_t n) {
 
 // Where every warp gets at most one step, a segment takes whole blocks instead (its
 // steps rounded up to the warps of a block, no opening): up to 8 steps then need
-// no join between blocks.  One request of 100 tokens: 7.3 us so, 10.5 with openings and shares across blocks.
+// no join between blocks.  One request of 100 tokens: 7.6 us so, 10.5 with openings and shares across blocks.
 __device__ __forceinline__ int32_t units_of(int32_t steps, bool whole_blocks) {
     return whole_blocks ? (steps + kWarps - 1) / kWarps * kWarps : steps + kOpen;
 }

@@ -35,11 +35,12 @@
 // 2^-24 of its largest element, and weights, times 2^7, keep 11 bits down to 2^-21
 // of the row's reference.
 //
-// Measured, causal, 32 / 8 heads of 128, graph replay: 8,192 tokens 432 us, 1.27 PFLOP/s
-// (over e4m3 463), 16,384 tokens 1,600 us, 1.38 PFLOP/s; cuBLAS reaches 1.92 on a large
-// bf16 product.  64-wide heads: 8,192 tokens 364 us; there a product does half the
-// operations in nearly the time.  With caps and a bias the softmax bounds it: 2,711
-// ragged tokens over e4m3 60 us, without them 44.
+// Measured, causal, 32 / 8 heads of 128, back to back: 8,192 tokens 431 us, 1.28 PFLOP/s
+// (over e4m3 453), 16,384 tokens 1,600 us, 1.37 PFLOP/s; cuBLAS reaches 1.92 on a large
+// bf16 product.  64-wide heads: 8,192 tokens 357 us; there a product does half the
+// operations in nearly the time.  With caps and a bias the softmax bounds it: 16 / 4 heads of
+// 64, 6,546 ragged tokens over e4m3 74 us, without them 54.  A step of a long item takes
+// 1.75 us (131,072 to 4,194,304 keys), 1.5 with 64-wide heads.
 #include <cuda_fp16.h>
 
 #include "attend.cuh"
@@ -63,8 +64,8 @@ struct PromptConfig {
     static constexpr uint32_t kHalfB = kRows * 128;   // 64 dims of all rows
     // Registers a thread: 128 at launch, then by role.  The four warpgroups' shares (two
     // of softmax, copies, products) add up to the launch's 4 x 128.  Measured on 8,192
-    // tokens (184, 80, 64 against 168, 104, 72): 128-wide heads 440 against 432 us, over
-    // e4m3 506 against 463; 64-wide heads 364 against 367, 8 ragged chunks 72 against 76.
+    // tokens (184, 80, 64 against 168, 104, 72): 128-wide heads 450 against 431 us, over
+    // e4m3 482 against 453; 64-wide heads 357 against 365, 8 ragged chunks 74 against 77.
     static constexpr int kSoftmaxRegs = HD == 128 ? 168 : 184;
     static constexpr int kCopyRegs = HD == 128 ? 104 : 80;
     static constexpr int kMmaRegs = HD == 128 ? 72 : 64;
@@ -232,8 +233,9 @@ struct Item {
 constexpr int32_t kSegment = 512;
 
 // Few items leave SMs idle: their keys are cut into up to kMaxParts parts, of at least
-// kMinSteps steps each, a block each.  64 rows over 16,384 tokens: 38 us, whole items 179;
-// 16 rows over 2,000 tokens: 21.8 us, in parts of at least 2 steps 23.2, of 1 25.5.
+// kMinSteps steps each, a block each.  32 rows over 16,384 tokens: 38 us, whole items 187; 64
+// rows 45 and 234; 16 rows over 2,000 tokens 23.6 us, in parts of at least 2 steps 24.8, of 1
+// 26.9, whole 31.
 constexpr int kMaxParts = 16, kMinSteps = 4, kMaxGrid = 160;
 
 // A part's partial result: references and sums of its 256 rows, then their outputs,
@@ -725,8 +727,8 @@ attend_prompt_kernel(const AttendArgs a, Claims *claims, uint32_t *flags, float 
             // ---- work -------------------------------------------------------------------
             // Items in order, key heads innermost.  Up to 32 requests, a lane each: the pairs of
             // row tiles with the most keys first, of any request, so that what is left at the
-            // end is small (8 ragged chunks of 6,546 tokens: 83 us in the requests' order, 72 us so;
-            // one of 8,192: 445 and 432).
+            // end is small (8 ragged chunks of 6,546 tokens: 83 us in the requests' order, 74 us so;
+            // one of 8,192: 437 and 431).
             // More requests: pairs from the last request's last one down; the many items even
             // out by themselves.
             const int64_t items = total * a.kv.n_kv;

@@ -139,20 +139,22 @@ lora_status_t lora_attend_workspace_bytes(const lora_attention_t *att, const lor
 // The decode path reads a request's cache once for every 32 of its rows, spread over
 // the whole GPU; the prompt path gives 256 rows of a key head to one block, or with
 // few such items up to 16 parts of their keys to a block each.  Its time does not grow
-// with rows but steps with the waves of such blocks on 152 SMs.  Measured a key: 16 rows
-// of a key head on the decode path cost about 1/256 of a wave on the prompt path.
-// Both sides, us (decode / prompt, 32/8 heads of 128): 64 requests of 100 to 8,000 tokens,
-// 4 rows 84 / 111, 8 rows 114 / 113; 8 requests of 4,096, 4 rows 38 / 38, 8 rows 47 / 38,
-// 32 rows 104 / 54; one request of 16,384, 4 rows 29 / 37, 8 rows 41 / 37, 32 rows 64 / 38,
-// 128 rows 172 / 55; one of 2,000, 4 rows 18 / 22, 16 rows 22 / 22; one of 131,071, 4 rows
-// 97 / 113, 64 rows 601 / 143.
+// with rows but steps with the waves of such blocks on the SMs (kSms, a GB300's: the choice
+// is made without a device).  Measured a key: 16 rows of a key head on the decode path cost
+// about 1/256 of a wave on the prompt path.  Both sides, us (decode / prompt, 32/8 heads of
+// 128, graph replay): 64 requests of 100 to 8,000 tokens, 4 rows 86 / 114, 8 rows 113 / 115; 8
+// requests of 4,096, 4 rows 38 / 38, 8 rows 47 / 38, 32 rows 104 / 54; one request of 16,384,
+// 4 rows 29 / 37, 8 rows 41 / 38, 32 rows 64 / 38, 128 rows 171 / 55; one of 2,000, 4 rows
+// 18 / 22, 16 rows 22 / 23; one of 131,071, 4 rows 99 / 115, 64 rows 597 / 145.
+constexpr int64_t kSms = 152;
+
 lora_attend_path_t lora_attend_resolve_path(lora_attend_path_t requested, const lora_attention_t *att,
                                             const lora_kv_t *kv, int32_t n_seq, int32_t max_q_hint) {
     if (requested != LORA_ATTEND_AUTO || att == nullptr || kv == nullptr || kv->n_kv < 1) return requested;
     const int64_t rows = int64_t(max_q_hint) * (att->n_heads / kv->n_kv), pairs = int64_t(n_seq) * kv->n_kv;
     const int64_t half_tiles = rows <= 16 ? 1 : 2 * ((rows + 31) / 32);
-    const int64_t items = pairs * ((rows + 255) / 256), waves = (items + 151) / 152;
-    const int64_t parts = std::min<int64_t>(16, std::max<int64_t>(1, 152 / std::max<int64_t>(1, items)));
+    const int64_t items = pairs * ((rows + 255) / 256), waves = (items + kSms - 1) / kSms;
+    const int64_t parts = std::min<int64_t>(16, std::max<int64_t>(1, kSms / std::max<int64_t>(1, items)));
     return pairs * half_tiles * parts < 256 * waves ? LORA_ATTEND_DECODE : LORA_ATTEND_PROMPT;
 }
 

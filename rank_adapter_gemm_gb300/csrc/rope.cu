@@ -18,7 +18,8 @@
 // a whole block, for latency.  Measured, graph replay, heads of 128 dims, 32 of q and 8
 // of k and of v (in brackets the other choice): one token 2.2 us (2.7), 256 into e4m3
 // 3.4 (4.2), 2,048 10.4 (10.4), 16,384 61.5 (64.3).
-// Bound by HBM: 402.9 MB of q, k and v in and out at 16,384 tokens, 6.55 TB/s.
+// Bound by HBM: 402.9 MB of q, k and v in and out at 16,384 tokens, 6.55 TB/s; into e4m3 (369.3 MB,
+// and a rounded division an element) 61.6 us, 6.0.
 #include <cuda_fp8.h>
 
 #include "attention.cuh"
