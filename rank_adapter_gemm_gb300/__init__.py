@@ -30,6 +30,8 @@ __all__ = [
     "lora_build_index_activated", "lora_plan_bytes", "lora_build_plan", "lora_apply_plan", "lora_build_plans", "Plan", "apply_with_base", "SlotTable", "TokenIndex", "Workspace",
     "PagedKV", "KVStep", "Rope", "Attention", "lora_kv_step", "lora_rope_phases", "lora_rope_append", "lora_attend",
     "lora_attend_workspace_bytes", "lora_attend_resolve_path", "LORA_MAX_SEQS",
+    "BeamSelect", "KVLayers", "PageTables", "SharedAttention", "lora_beam_select", "lora_beam_select_workspace_bytes",
+    "lora_kv_fork", "lora_kv_compact", "lora_kv_copy", "lora_attend_shared", "lora_attend_shared_workspace_bytes",
 ]
 
 
@@ -492,3 +494,6 @@ class Workspace:
 from .attention import (Attention, KVStep, LORA_MAX_SEQS, PagedKV, Rope, lora_attend,  # noqa: E402
                         lora_attend_resolve_path, lora_attend_workspace_bytes, lora_kv_step, lora_rope_append,
                         lora_rope_phases)
+from .sharing import (BeamSelect, KVLayers, PageTables, SharedAttention, lora_attend_shared,  # noqa: E402
+                      lora_attend_shared_workspace_bytes, lora_beam_select, lora_beam_select_workspace_bytes,
+                      lora_kv_compact, lora_kv_copy, lora_kv_fork)

@@ -55,7 +55,18 @@ EXPORTED_ATTENTION = (
     "lora_attend",
 )
 
+# Every function include/lora_sharing.h declares.
+EXPORTED_SHARING = (
+    "lora_beam_select_workspace_bytes", "lora_beam_select", "lora_kv_fork", "lora_kv_compact", "lora_kv_copy",
+    "lora_attend_shared_workspace_bytes", "lora_attend_shared",
+)
+
 LORA_MAX_SEQS = 4096
+LORA_MAX_BEAMS = 64
+LORA_MAX_VOCAB = 1 << 24
+LORA_MAX_PAGES = 1 << 20
+LORA_MAX_KV_LAYERS = 128
+LOGITS_TYPES = {"bf16": 0, "fp32": 1}
 ATTEND_PATHS = {"auto": 0, "decode": 1, "prompt": 2}
 ROPE_KINDS = {"plain": 0, "linear": 1, "ntk": 2, "llama3": 3, "yarn": 4}
 
@@ -93,6 +104,10 @@ class lora_rope_t(ctypes.Structure):
 class lora_attention_t(ctypes.Structure):
     _fields_ = [("n_heads", ctypes.c_int32), ("scale", ctypes.c_float), ("softcap", ctypes.c_float),
                 ("window", ctypes.c_int32), ("slopes", ctypes.c_void_p)]
+
+
+class lora_prefix_t(ctypes.Structure):
+    _fields_ = [("group_offsets", ctypes.c_void_p), ("prefix_lens", ctypes.c_void_p), ("n_groups", ctypes.c_int32)]
 
 
 class LoraError(RuntimeError):
@@ -165,6 +180,16 @@ def load() -> ctypes.CDLL:
         "lora_attend_workspace_bytes": (ST, [AT, KV, ctypes.POINTER(SZ)]),
         "lora_attend_resolve_path": (ST, [ST, AT, KV, I32, I32]),
         "lora_attend": (ST, [P, I64, P, I64, P, I32, I32, P, P, P, I64, I32, KV, AT, I32, ST, P, SZ, P, P]),
+    }
+    sig |= {
+        "lora_beam_select_workspace_bytes": (ST, [I32, I32, I32, I32, ctypes.POINTER(SZ)]),
+        "lora_beam_select": (ST, [P, I64, ST, I32, I32, I32, I32, P, P, I32, P, P, P, P, P, SZ, P]),
+        "lora_kv_fork": (ST, [P, I64, I32, P, I32, P, I32, I32, I32, P, I32, P, I64, I32, P, P, P, P, P, P]),
+        "lora_kv_compact": (ST, [P, I64, I32, P, I32, I32, I32, P, I32, P, I64, P, P, P, P, P, P, P]),
+        "lora_kv_copy": (ST, [P, I32, P, I32, P, P, P]),
+        "lora_attend_shared_workspace_bytes": (ST, [AT, KV, I32, I32, ctypes.POINTER(SZ)]),
+        "lora_attend_shared": (ST, [P, I64, P, I64, P, I32, I32, P, P, P, I64, I32, ctypes.POINTER(lora_prefix_t), KV,
+                                    AT, I32, P, SZ, P, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)

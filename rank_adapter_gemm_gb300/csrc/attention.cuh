@@ -1,12 +1,14 @@
 // Structures and host checks shared by the attention-side kernels
-// (lora_attention.h) and their C entry points.
+// (lora_attention.h, lora_sharing.h) and their C entry points.
 #pragma once
 
+#include <algorithm>
 #include <atomic>
+#include <cfloat>
 #include <cmath>
 #include <cstdint>
 
-#include "../../include/lora_attention.h"
+#include "../../include/lora_sharing.h"
 #include "checks.cuh"
 
 namespace lora {
@@ -125,6 +127,44 @@ inline lora_status_t check_kv(const lora_kv_t *kv, KvView *out) {
     out->k_scale = kv->type == LORA_KV_E4M3 ? kv->k_scale : 1.0f;
     out->v_scale = kv->type == LORA_KV_E4M3 ? kv->v_scale : 1.0f;
     return LORA_OK;
+}
+
+inline lora_status_t check_attention(const lora_attention_t *att, const KvView &kv) {
+    if (att == nullptr || att->n_heads < 1 || att->n_heads % kv.n_kv != 0) return LORA_ERR_INVALID_ARG;
+    if (!std::isfinite(att->scale) || !(att->softcap >= 0.0f) || !std::isfinite(att->softcap) || att->window < 0)
+        return LORA_ERR_INVALID_ARG;
+    if (kv.head_dim != 64 && kv.head_dim != 128) return LORA_ERR_UNSUPPORTED;
+    return LORA_OK;
+}
+
+// The checks of an attention call, in lora_attend's order, and its arguments for the kernels.
+inline lora_status_t check_attend(const void *q, int64_t ldq, void *out, int64_t ldo, float *lse, int32_t T,
+                                  int32_t n_seq, const int32_t *q_offsets, const int32_t *kv_lens,
+                                  const int32_t *block_table, int64_t ld_table, int32_t table_width,
+                                  const lora_kv_t *kv, const lora_attention_t *att, int32_t *err, AttendArgs *a) {
+    KvView view;
+    lora_status_t st;
+    if (T < 0 || n_seq < 0 || n_seq > LORA_MAX_SEQS || table_width < 0 || ld_table < table_width)
+        return LORA_ERR_INVALID_ARG;
+    if ((st = check_kv(kv, &view)) != LORA_OK) return st;
+    if ((st = check_attention(att, view)) != LORA_OK) return st;
+    if (int64_t(att->n_heads) * view.head_dim > INT32_MAX) return LORA_ERR_INVALID_ARG;
+    if ((st = check_rows(q, ldq, T, att->n_heads * view.head_dim)) != LORA_OK) return st;
+    if ((st = check_rows(out, ldo, T, att->n_heads * view.head_dim)) != LORA_OK) return st;
+    if (q_offsets == nullptr || (n_seq > 0 && kv_lens == nullptr)) return LORA_ERR_INVALID_ARG;
+    if (n_seq > 0 && table_width > 0 && block_table == nullptr) return LORA_ERR_INVALID_ARG;
+    // a cap from 1e30 on changes no score below 1e25 by an fp32 rounding: none
+    const float cap = att->softcap < 1e30f ? att->softcap : 0.0f;
+    *a = AttendArgs{static_cast<const uint16_t *>(q), static_cast<uint16_t *>(out), lse, ldq, ldo, ld_table, q_offsets,
+                    kv_lens, block_table, att->slopes, err, view, T, n_seq, table_width, att->n_heads,
+                    att->n_heads / view.n_kv, att->window, att->scale, cap,
+                    cap > 0.0f ? std::min(1.0f / cap, FLT_MAX) : 0.0f};
+    return LORA_OK;
+}
+
+// A bound on a request's rows: without a hint T rows are taken as shared out evenly.
+inline int32_t rows_hint(int32_t hint, int32_t T, int32_t n_seq) {
+    return std::min(hint <= 0 ? (T - 1) / n_seq + 1 : hint, T);
 }
 
 }  // namespace lora

@@ -1,7 +1,6 @@
 // extern "C" entry points of lora_attention.h: argument checks, the rotary
 // frequencies and kernel dispatch.
 #include <algorithm>
-#include <cfloat>
 #include <cmath>
 
 #include "attention.cuh"
@@ -20,6 +19,7 @@ cudaError_t launch_attend_prompt(const AttendArgs &a, bool e4m3, void *ws, cudaS
 }  // namespace lora
 
 using lora::aligned16;
+using lora::check_attention;
 using lora::check_kv;
 using lora::check_rows;
 using lora::KvView;
@@ -27,14 +27,6 @@ using lora::KvView;
 namespace {
 
 lora_status_t from_cuda(cudaError_t e) { return e == cudaSuccess ? LORA_OK : LORA_ERR_CUDA; }
-
-lora_status_t check_attention(const lora_attention_t *att, const KvView &kv) {
-    if (att == nullptr || att->n_heads < 1 || att->n_heads % kv.n_kv != 0) return LORA_ERR_INVALID_ARG;
-    if (!std::isfinite(att->scale) || !(att->softcap >= 0.0f) || !std::isfinite(att->softcap) || att->window < 0)
-        return LORA_ERR_INVALID_ARG;
-    if (kv.head_dim != 64 && kv.head_dim != 128) return LORA_ERR_UNSUPPORTED;
-    return LORA_OK;
-}
 
 }  // namespace
 
@@ -163,31 +155,18 @@ lora_status_t lora_attend(const void *q, int64_t ldq, void *out, int64_t ldo, fl
                           int64_t ld_table, int32_t table_width, const lora_kv_t *kv, const lora_attention_t *att,
                           int32_t max_q_hint, lora_attend_path_t path, void *ws, size_t ws_bytes, int32_t *err,
                           lora_stream_t stream) {
-    KvView view;
+    lora::AttendArgs a;
     lora_status_t st;
-    if (T < 0 || n_seq < 0 || n_seq > LORA_MAX_SEQS || table_width < 0 || ld_table < table_width)
-        return LORA_ERR_INVALID_ARG;
     if (path < LORA_ATTEND_AUTO || path > LORA_ATTEND_PROMPT) return LORA_ERR_INVALID_ARG;
-    if ((st = check_kv(kv, &view)) != LORA_OK) return st;
-    if ((st = check_attention(att, view)) != LORA_OK) return st;
-    if (int64_t(att->n_heads) * view.head_dim > INT32_MAX) return LORA_ERR_INVALID_ARG;
-    if ((st = check_rows(q, ldq, T, att->n_heads * view.head_dim)) != LORA_OK) return st;
-    if ((st = check_rows(out, ldo, T, att->n_heads * view.head_dim)) != LORA_OK) return st;
-    if (q_offsets == nullptr || (n_seq > 0 && kv_lens == nullptr)) return LORA_ERR_INVALID_ARG;
-    if (n_seq > 0 && table_width > 0 && block_table == nullptr) return LORA_ERR_INVALID_ARG;
+    if ((st = lora::check_attend(q, ldq, out, ldo, lse, T, n_seq, q_offsets, kv_lens, block_table, ld_table, table_width,
+                                 kv, att, err, &a)) != LORA_OK)
+        return st;
     size_t need = 0;
     if ((st = lora_attend_workspace_bytes(att, kv, &need)) != LORA_OK) return st;
     if (ws == nullptr || ws_bytes < need) return LORA_ERR_WORKSPACE;
     if (!aligned16(ws)) return LORA_ERR_ALIGNMENT;
     if (T == 0 || n_seq == 0) return LORA_OK;
-    if (max_q_hint <= 0) max_q_hint = (T - 1) / n_seq + 1;
-    if (max_q_hint > T) max_q_hint = T;
-    // a cap from 1e30 on changes no score below 1e25 by an fp32 rounding: none
-    const float cap = att->softcap < 1e30f ? att->softcap : 0.0f;
-    const lora::AttendArgs a{static_cast<const uint16_t *>(q), static_cast<uint16_t *>(out), lse, ldq, ldo, ld_table,
-                             q_offsets, kv_lens, block_table, att->slopes, err, view, T, n_seq, table_width,
-                             att->n_heads, att->n_heads / view.n_kv, att->window, att->scale, cap,
-                             cap > 0.0f ? std::min(1.0f / cap, FLT_MAX) : 0.0f};
+    max_q_hint = lora::rows_hint(max_q_hint, T, n_seq);
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const bool e4m3 = kv->type == LORA_KV_E4M3;
     if (lora_attend_resolve_path(path, att, kv, n_seq, max_q_hint) == LORA_ATTEND_DECODE)

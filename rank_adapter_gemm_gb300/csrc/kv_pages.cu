@@ -1,0 +1,368 @@
+// Block tables of requests that branch, end and move (lora_kv_fork, lora_kv_compact).
+//
+// Both calls ask which pages a set of table rows names, and then for the k-th page
+// in use or free in rising order: a bitmap of the pages and its prefix sums.  The
+// work is 4 bytes an entry, so chains of dependent loads and the steps between them
+// bound it, not bandwidth.  One cluster therefore does all of it in one launch
+// without a workspace: the entries of the rows are spread over its blocks, each of
+// which marks the pages that it meets in a bitmap of its own in shared memory; the
+// bitmaps are joined through distributed shared memory, every block taking one slice
+// of the pages; and the slices' counts, exchanged the same way, give every page its
+// rank.  The cluster's barriers are the only waits.
+#include "attention.cuh"
+
+namespace lora {
+
+namespace {
+
+constexpr int kCtas = 8, kThreads = 1024, kWarps = kThreads / 32;
+constexpr int kSpan = 256;  // entries of a row that a warp takes at a time
+
+struct PagesArgs {
+    const int32_t *src, *lens, *parents, *held;
+    int32_t *dst, *dst_lens, *dst_held, *copies, *n_copies, *free_pages, *n_free, *err;
+    int64_t ld_src, ld_dst;
+    int32_t src_width, dst_width, n_src, n_rows, n_held, n_pages, shift;
+};
+
+__device__ __forceinline__ uint32_t ld_peer(uint32_t addr) {
+    uint32_t v;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ uint4 ld_peer4(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared::cluster.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(addr) : "memory");
+    return v;
+}
+
+// (Threads may arrive one by one: the loops before it end at different times.)
+__device__ __forceinline__ void sync_cluster() {
+    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+
+// Sum over the block's threads before this one; *total gets all of it.
+__device__ __forceinline__ int32_t scan_block(int32_t mine, int32_t *s_warp, int32_t *total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int32_t incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int32_t v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
+    }
+    __syncthreads();
+    if (lane == 31) s_warp[warp] = incl;
+    __syncthreads();
+    int32_t w = s_warp[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int32_t v = __shfl_up_sync(0xffffffffu, w, o);
+        if (lane >= o) w += v;
+    }
+    *total = __shfl_sync(0xffffffffu, w, 31);
+    const int32_t before = __shfl_sync(0xffffffffu, w, (warp + 31) & 31);
+    return (warp > 0 ? before : 0) + incl - mine;
+}
+
+// Words of the bitmap in a block's slice: a multiple of 4, so that slices are read in 16 bytes.
+__host__ __device__ constexpr int32_t slice_words(int32_t n_pages) {
+    return ((n_pages + 32 * kCtas * 4 - 1) / (32 * kCtas * 4)) * 4;
+}
+
+// The bitmap, and the free pages before each word of the own slice; then by row (of
+// the new batch): its source row and its entries; for a fork, each parent's first child and each copy's row.
+__host__ __device__ constexpr size_t pages_smem(int32_t n_pages, int32_t n_src, int32_t n_rows, bool fork) {
+    const size_t rows = static_cast<size_t>((n_rows + 3) & ~3), src = static_cast<size_t>((n_src + 3) & ~3);
+    return size_t(4) * (slice_words(n_pages) * (kCtas + 1) + 2 * rows + (fork ? src + rows : 0));
+}
+
+template <bool FORK>
+__global__ void __launch_bounds__(kThreads, 1) kv_pages_kernel(const PagesArgs a) {
+    extern __shared__ __align__(16) uint32_t smem_words[];
+    __shared__ int32_t s_warp[32];
+    __shared__ int32_t s_free[1];  // free pages of this block's slice
+    __shared__ int32_t s_most;     // entries of the longest row
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const uint32_t rank = cluster_ctarank();
+    const int32_t per = slice_words(a.n_pages), words = per * kCtas;
+    uint32_t *s_map = smem_words;
+    int32_t *s_before = reinterpret_cast<int32_t *>(smem_words + words);
+    int32_t *s_from = s_before + per, *s_have = s_from + ((a.n_rows + 3) & ~3);
+    int32_t *s_first = s_have + ((a.n_rows + 3) & ~3), *s_job = s_first + ((a.n_src + 3) & ~3);
+
+    for (int32_t w = tid; w < words; w += kThreads) s_map[w] = 0u;
+    if (FORK)
+        for (int32_t i = tid; i < a.n_src; i += kThreads) s_first[i] = INT32_MAX;
+    if (tid == 0) s_most = 0;
+    wait_for_previous();
+    __syncthreads();
+
+    // ---- the rows: where they come from, how many entries, which need a copy -------
+    const int32_t in_page = (1 << a.shift) - 1;
+    // a row's length; bad ones (reported by one block) are empty
+    const auto length_of = [&](int32_t p) {
+        const int32_t len = a.lens[p];
+        const int32_t pages = len > 0 ? static_cast<int32_t>((int64_t(len) + in_page) >> a.shift) : 0;
+        if (len < 0 || pages > a.src_width || pages > a.dst_width) {
+            if (rank == 0) report_error(a.err, LORA_ERR_INVALID_ARG);
+            return 0;
+        }
+        return len;
+    };
+    for (int32_t i = tid; i < a.n_rows; i += kThreads) {
+        int32_t p = i;
+        if (FORK) {
+            p = a.parents[i];
+            if (p < -1 || p >= a.n_src) {
+                if (rank == 0) report_error(a.err, LORA_ERR_INVALID_ARG);
+                p = -1;
+            }
+        }
+        const int32_t len = p >= 0 ? length_of(p) : 0;
+        s_from[i] = p;
+        s_have[i] = len;  // until the entries are known
+        if (FORK && p >= 0) atomicMin(&s_first[p], i);
+        if (len > 0) atomicMax(&s_most, static_cast<int32_t>((int64_t(len) + in_page) >> a.shift));
+    }
+    __syncthreads();
+    int32_t jobs = 0;  // copies of the call
+    if (FORK) {
+        for (int32_t base = 0; base < a.n_rows; base += kThreads) {
+            const int32_t i = base + tid;
+            const bool job = i < a.n_rows && (s_have[i] & in_page) != 0 && s_first[s_from[i]] != i;
+            int32_t total;
+            const int32_t at = jobs + scan_block(job, s_warp, &total);
+            if (job) s_job[at] = i;
+            jobs += total;
+            if (i < a.n_rows && rank == 0) {
+                a.dst_lens[i] = s_have[i];
+                if (!job)
+                    for (int e = 0; e < 3; ++e) a.copies[3 * int64_t(i) + e] = e < 2 ? -1 : 0;
+            }
+        }
+    }
+
+    // ---- the entries: copied, and marked in the block's bitmap ---------------------
+    const auto mark = [&](int32_t page) {
+        if (static_cast<uint32_t>(page) < static_cast<uint32_t>(a.n_pages)) {
+            const uint32_t bit = 1u << (page & 31);
+            if ((s_map[page >> 5] & bit) == 0) atomicOr(&s_map[page >> 5], bit);
+            return true;
+        }
+        return false;
+    };
+    // entries of row i that are copied as they are
+    const auto entries = [&](int32_t i) {
+        const int32_t len = s_have[i], pages = static_cast<int32_t>((int64_t(len) + in_page) >> a.shift);
+        return FORK && (len & in_page) != 0 && s_first[s_from[i]] != i ? pages - 1 : pages;
+    };
+    const int32_t spans = (s_most + kSpan - 1) / kSpan;
+    const int64_t items = int64_t(a.n_rows) * spans;
+    // calls f(row of the new batch, first entry, end) for this warp's spans, spread over the cluster
+    const auto each_span = [&](auto f) {
+        for (int64_t x = warp * kCtas + rank; x < items; x += kWarps * kCtas) {
+            const int32_t c = static_cast<int32_t>(x / a.n_rows), i = static_cast<int32_t>(x - int64_t(c) * a.n_rows);
+            const int32_t e0 = c * kSpan, e1 = min(entries(i), e0 + kSpan);
+            if (e0 < e1) f(i, e0, e1);
+        }
+    };
+    each_span([&](int32_t i, int32_t e0, int32_t e1) {
+        const int32_t *from = a.src + s_from[i] * a.ld_src;
+        int32_t *to = a.dst + i * a.ld_dst;
+        int32_t page[kSpan / 32];
+#pragma unroll
+        for (int u = 0; u < kSpan / 32; ++u) page[u] = from[min(e0 + u * 32 + lane, e1 - 1)];
+#pragma unroll
+        for (int u = 0; u < kSpan / 32; ++u) {
+            const int32_t e = e0 + u * 32 + lane;
+            if (e >= e1) break;
+            if (FORK) to[e] = page[u];
+            if (!mark(page[u])) report_error(a.err, LORA_ERR_SLOT_RANGE);
+        }
+    });
+    for (int32_t i = rank * kThreads + tid; i < a.n_held; i += kCtas * kThreads) {
+        const int32_t page = a.held[i];
+        if (page != -1 && !mark(page)) report_error(a.err, LORA_ERR_SLOT_RANGE);
+    }
+    sync_cluster();
+
+    // ---- the bitmaps joined: this block's slice of the pages, free ones as ones ------
+    const int32_t w0 = static_cast<int32_t>(rank) * per;
+    const uint32_t slice = smem_addr(s_map + w0);
+    for (int32_t v = tid; v < per / 4; v += kThreads) {
+        uint4 x = make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int c = 0; c < kCtas; ++c) {
+            const uint4 y = ld_peer4(map_to_rank(slice + v * 16, c));
+            x.x |= y.x, x.y |= y.y, x.z |= y.z, x.w |= y.w;
+        }
+        // (other blocks still read this slice of the bitmap: the joined words go elsewhere)
+        reinterpret_cast<uint4 *>(s_before)[v] = x;
+    }
+    sync_cluster();
+    const int32_t each = (per + kThreads - 1) / kThreads;  // words a thread
+    int32_t mine = 0;
+    for (int32_t j = 0; j < each; ++j) {
+        const int32_t w = tid * each + j;
+        if (w >= per) break;
+        const int64_t left = int64_t(a.n_pages) - int64_t(w0 + w) * 32;  // pages from this word on
+        const uint32_t real = left >= 32 ? 0xffffffffu : left > 0 ? (1u << left) - 1 : 0u;
+        const uint32_t word = ~static_cast<uint32_t>(s_before[w]) & real;
+        s_map[w0 + w] = word;
+        mine += __popc(word);
+    }
+    int32_t slice_free;
+    int32_t at = scan_block(mine, s_warp, &slice_free);
+    if (tid == 0) s_free[0] = slice_free;
+    sync_cluster();
+    int32_t free_before = 0, n_free = 0;  // in the slices before this one; in all
+#pragma unroll
+    for (int c = 0; c < kCtas; ++c) {
+        const int32_t f = static_cast<int32_t>(ld_peer(map_to_rank(smem_addr(s_free), c)));
+        if (c < static_cast<int>(rank)) free_before += f;
+        n_free += f;
+    }
+    at += free_before;
+    for (int32_t j = 0; j < each; ++j) {
+        const int32_t w = tid * each + j;
+        if (w >= per) break;
+        s_before[w] = at;
+        at += __popc(s_map[w0 + w]);
+    }
+    __syncthreads();
+
+    if constexpr (FORK) {
+        // ---- free pages in order: to the copies first, then to the list --------------
+        for (int32_t w = warp; w < per; w += kWarps) {
+            const uint32_t word = s_map[w0 + w];
+            if (!((word >> lane) & 1)) continue;
+            const int32_t f = s_before[w] + __popc(word & ((1u << lane) - 1)), page = (w0 + w) * 32 + lane;
+            if (f >= jobs) {
+                a.free_pages[f - jobs] = page;
+                continue;
+            }
+            const int32_t i = s_job[f], len = s_have[i], last = len >> a.shift;
+            const int32_t from = a.src[s_from[i] * a.ld_src + last];
+            const bool ok = static_cast<uint32_t>(from) < static_cast<uint32_t>(a.n_pages);
+            if (!ok) report_error(a.err, LORA_ERR_SLOT_RANGE);
+            a.dst[i * a.ld_dst + last] = page;
+            a.copies[3 * int64_t(i)] = ok ? from : -1;
+            a.copies[3 * int64_t(i) + 1] = ok ? page : -1;
+            a.copies[3 * int64_t(i) + 2] = ok ? len & in_page : 0;
+        }
+        if (rank == 0) {
+            for (int32_t u = n_free + tid; u < jobs; u += kThreads) {  // copies without a page
+                const int32_t i = s_job[u];
+                report_error(a.err, LORA_ERR_NO_PAGES);
+                a.dst_lens[i] = s_have[i] & ~in_page;
+                for (int e = 0; e < 3; ++e) a.copies[3 * int64_t(i) + e] = e < 2 ? -1 : 0;
+            }
+        }
+        n_free = max(0, n_free - jobs);
+    } else {
+        // ---- pages in use at or past their number: each to the free page of its rank --
+        const int32_t used = a.n_pages - n_free;
+        // free pages before page p of any slice
+        const auto word_of = [&](int32_t w) {
+            return ld_peer(map_to_rank(smem_addr(s_map + w), static_cast<uint32_t>(w / per)));
+        };
+        const auto before_of = [&](int32_t w) {
+            return static_cast<int32_t>(ld_peer(map_to_rank(smem_addr(s_before + w % per),
+                                                            static_cast<uint32_t>(w / per))));
+        };
+        sync_cluster();  // every slice's words and counts are there
+        int32_t n_moves = 0;
+        if (used < a.n_pages) {
+            n_moves = before_of(used >> 5) + __popc(word_of(used >> 5) & ((1u << (used & 31)) - 1));
+        }
+        // a page at or past `used` that is in use: its rank among those
+        const auto rank_of = [&](int32_t p, int32_t free_before_p) { return p - free_before_p - (used - n_moves); };
+        for (int32_t w = warp; w < per; w += kWarps) {
+            const uint32_t word = s_map[w0 + w];
+            const int32_t page = (w0 + w) * 32 + lane, f = s_before[w] + __popc(word & ((1u << lane) - 1));
+            const bool is_free = (word >> lane) & 1;
+            if (page >= a.n_pages) continue;
+            if (page < used && is_free) a.copies[3 * int64_t(f) + 1] = page;
+            if (page >= used && !is_free) {
+                const int64_t r = rank_of(page, f);
+                a.copies[3 * r] = page;
+                a.copies[3 * r + 2] = in_page + 1;
+            }
+        }
+        const int32_t all = static_cast<int32_t>(rank) * kThreads + tid;
+        for (int64_t i = n_moves + all; i < a.n_pages / 2; i += kCtas * kThreads)
+            for (int e = 0; e < 3; ++e) a.copies[3 * i + e] = e < 2 ? -1 : 0;
+        for (int32_t p = all; p < n_free; p += kCtas * kThreads) a.free_pages[p] = used + p;
+        if (all == 0) a.n_copies[0] = n_moves;
+        __threadfence();
+        sync_cluster();  // the moves are written
+        const auto moved = [&](int32_t p) {
+            if (static_cast<uint32_t>(p) >= static_cast<uint32_t>(a.n_pages) || p < used) return p;
+            const uint32_t word = word_of(p >> 5);
+            const int64_t r = rank_of(p, before_of(p >> 5) + __popc(word & ((1u << (p & 31)) - 1)));
+            return __ldcg(a.copies + 3 * r + 1);
+        };
+        each_span([&](int32_t i, int32_t e0, int32_t e1) {
+            const int32_t *from = a.src + s_from[i] * a.ld_src;
+            int32_t *to = a.dst + i * a.ld_dst;
+            for (int32_t e = e0 + lane; e < e1; e += 32) to[e] = moved(from[e]);
+        });
+        for (int32_t i = all; i < a.n_held; i += kCtas * kThreads) {
+            const int32_t p = a.held[i];
+            a.dst_held[i] = p == -1 ? -1 : moved(p);
+        }
+    }
+    for (int32_t p = n_free + static_cast<int32_t>(rank) * kThreads + tid; p < a.n_pages; p += kCtas * kThreads)
+        a.free_pages[p] = -1;
+    if (rank == 0 && tid == 0) a.n_free[0] = n_free;
+    sync_cluster();  // no block's shared memory is read any more
+}
+
+template <bool FORK>
+cudaError_t launch(const PagesArgs &a, cudaStream_t stream) {
+    static std::atomic<uint64_t> seen{0};
+    constexpr size_t kMost = pages_smem(LORA_MAX_PAGES, LORA_MAX_SEQS, LORA_MAX_SEQS, true);
+    static_assert(kMost <= 227 * 1024 - 1024, "shared memory");
+    int sms = 0;
+    const cudaError_t e = prepare_kernel(kv_pages_kernel<FORK>, static_cast<int>(kMost), seen, &sms);
+    if (e != cudaSuccess) return e;
+    cudaLaunchAttribute attr[2] = {};
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = kCtas;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(kCtas);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = pages_smem(a.n_pages, a.n_src, a.n_rows, FORK);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kv_pages_kernel<FORK>, a);
+}
+
+}  // namespace
+
+cudaError_t launch_kv_fork(const int32_t *src, int64_t ld_src, int32_t src_width, const int32_t *lens, int32_t n_src,
+                           const int32_t *parents, int32_t n_dst, int32_t shift, int32_t n_pages, const int32_t *held,
+                           int32_t n_held, int32_t *dst, int64_t ld_dst, int32_t dst_width, int32_t *dst_lens,
+                           int32_t *copies, int32_t *free_pages, int32_t *n_free, int32_t *err, cudaStream_t stream) {
+    return launch<true>(PagesArgs{src, lens, parents, held, dst, dst_lens, nullptr, copies, nullptr, free_pages, n_free,
+                                  err, ld_src, ld_dst, src_width, dst_width, n_src, n_dst, n_held, n_pages, shift},
+                        stream);
+}
+
+cudaError_t launch_kv_compact(const int32_t *src, int64_t ld_src, int32_t width, const int32_t *lens, int32_t n_seq,
+                              int32_t shift, int32_t n_pages, const int32_t *held, int32_t n_held, int32_t *dst,
+                              int64_t ld_dst, int32_t *dst_held, int32_t *moves, int32_t *n_moves, int32_t *free_pages,
+                              int32_t *n_free, int32_t *err, cudaStream_t stream) {
+    return launch<false>(PagesArgs{src, lens, nullptr, held, dst, nullptr, dst_held, moves, n_moves, free_pages, n_free,
+                                   err, ld_src, ld_dst, width, width, n_seq, n_seq, n_held, n_pages, shift},
+                         stream);
+}
+
+}  // namespace lora
