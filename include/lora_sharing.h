@@ -150,8 +150,8 @@ lora_status_t lora_kv_copy(const lora_kv_t *kvs, int32_t n_layers, const int32_t
  * lora_attend for groups of requests that share a prefix.  Requests
  * [group_offsets[g], group_offsets[g + 1]) hold the same keys and values at their
  * positions below prefix_lens[g] (in the same or in different pages): those are
- * read once for all rows of the group, through the table row of its first request, and
- * each request's other positions through its own row.  The result is what
+ * read once for all rows of the group, through the table row of its first request with
+ * rows, and each request's other positions through its own row.  The result is what
  * lora_attend computes, up to rounding.  Where a request of the group with rows has
  * cached less before its own rows, the prefix is cut to that; groups with fewer than
  * two requests, and requests outside every group, share nothing.
@@ -164,8 +164,8 @@ lora_status_t lora_kv_copy(const lora_kv_t *kvs, int32_t n_layers, const int32_t
  *                  zero it again after a call that reports LORA_ERR_TIMEOUT).  Calls that
  *                  may overlap need a workspace each
  * All other arguments, limits and device errors are lora_attend's; LORA_ERR_INVALID_ARG
- * in err also reports group offsets out of order or range and negative prefix
- * lengths (that group shares nothing).  Made for few rows a request (decode,
+ * in err also reports group offsets out of order or range (nothing is shared then)
+ * and negative prefix lengths (that group shares nothing).  Made for few rows a request (decode,
  * speculative decode); any number is computed.
  */
 typedef struct {
