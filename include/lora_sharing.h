@@ -146,6 +146,8 @@ lora_status_t lora_kv_compact(const int32_t *src_table, int64_t ld_src, int32_t 
 lora_status_t lora_kv_copy(const lora_kv_t *kvs, int32_t n_layers, const int32_t *copies, int32_t n_copies,
                            const int32_t *count, int32_t *err, lora_stream_t stream);
 
+typedef enum { LORA_SHARE_AUTO = 0, LORA_SHARE_ALWAYS = 1 } lora_share_t;
+
 /*
  * lora_attend for groups of requests that share a prefix.  Requests
  * [group_offsets[g], group_offsets[g + 1]) hold the same keys and values at their
@@ -163,6 +165,9 @@ lora_status_t lora_kv_copy(const lora_kv_t *kvs, int32_t n_layers, const int32_t
  *                  call leaves it as it found it, up to values that no call reads (but
  *                  zero it again after a call that reports LORA_ERR_TIMEOUT).  Calls that
  *                  may overlap need a workspace each
+ * mode           LORA_SHARE_AUTO: prefixes are read once where that is estimated to
+ *                  save time, which short ones do not (decided on the device, from the
+ *                  lengths); LORA_SHARE_ALWAYS: all of them
  * All other arguments, limits and device errors are lora_attend's; LORA_ERR_INVALID_ARG
  * in err also reports group offsets out of order or range (nothing is shared then)
  * and negative prefix lengths (that group shares nothing).  Made for few rows a request (decode,
@@ -171,6 +176,7 @@ lora_status_t lora_kv_copy(const lora_kv_t *kvs, int32_t n_layers, const int32_t
 typedef struct {
     const int32_t *group_offsets, *prefix_lens;
     int32_t n_groups;
+    int32_t mode; /* lora_share_t */
 } lora_prefix_t;
 
 lora_status_t lora_attend_shared_workspace_bytes(const lora_attention_t *att, const lora_kv_t *kv, int32_t T,

@@ -67,6 +67,7 @@ LORA_MAX_VOCAB = 1 << 24
 LORA_MAX_PAGES = 1 << 20
 LORA_MAX_KV_LAYERS = 128
 LOGITS_TYPES = {"bf16": 0, "fp32": 1}
+SHARE_MODES = {"auto": 0, "always": 1}
 ATTEND_PATHS = {"auto": 0, "decode": 1, "prompt": 2}
 ROPE_KINDS = {"plain": 0, "linear": 1, "ntk": 2, "llama3": 3, "yarn": 4}
 
@@ -107,7 +108,8 @@ class lora_attention_t(ctypes.Structure):
 
 
 class lora_prefix_t(ctypes.Structure):
-    _fields_ = [("group_offsets", ctypes.c_void_p), ("prefix_lens", ctypes.c_void_p), ("n_groups", ctypes.c_int32)]
+    _fields_ = [("group_offsets", ctypes.c_void_p), ("prefix_lens", ctypes.c_void_p), ("n_groups", ctypes.c_int32),
+                ("mode", ctypes.c_int32)]
 
 
 class LoraError(RuntimeError):

@@ -10,7 +10,7 @@ size_t decode_workspace_bytes(int32_t head_dim) {
 }
 
 cudaError_t launch_attend_decode(const AttendArgs &a, bool e4m3, int32_t max_q, void *ws, cudaStream_t stream) {
-    return pick_decode<false>(a, e4m3, max_q, OwnRows{}, ws, stream);
+    return pick_decode<false>(a, e4m3, int64_t(max_q) * a.group, OwnRows{}, ws, stream);
 }
 
 }  // namespace lora

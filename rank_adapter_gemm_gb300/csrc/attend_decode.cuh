@@ -47,6 +47,7 @@
 #include <cuda_fp16.h>
 
 #include "attend.cuh"
+#include "shared_plan.cuh"
 #include "tc.cuh"
 
 namespace lora {
@@ -58,7 +59,7 @@ constexpr int kSmemMax = 227 * 1024;
 constexpr int kWarps = 8;
 constexpr int kPrefixMax = ((LORA_MAX_SEQS + 1) * 4 + 127) & ~127;  // the requests' step prefix
 
-template <int HD, bool E4M3, int ROWS>
+template <int HD, bool E4M3, int ROWS, bool SHARED = false>
 struct Config {
     static constexpr int kRowB = HD * (E4M3 ? 1 : 2);  // bytes of a key
     static constexpr int kChunks = kRowB / 16;         // 16-byte pieces of a key
@@ -71,7 +72,7 @@ struct Config {
     // A warp's query fragments in shared memory: with 32 rows there are no registers for them.
     static constexpr int kQBytes = ROWS == 32 ? (HD / 16) * 2 * 512 : 0;
     // Tiles of a warp's ring: all the memory that the longest prefix leaves.
-    static constexpr int kRoom = (kSmemMax - 1024 - kPrefixMax) / kWarps - kQBytes;
+    static constexpr int kRoom = (kSmemMax - 1024 - (SHARED ? 2 : 1) * kPrefixMax) / kWarps - kQBytes;
     static constexpr int kTiles = kRoom / kTileB < 9 ? kRoom / kTileB : 9;
     static constexpr int kWarpB = kQBytes + kTiles * kTileB;
     static_assert(kTiles >= 2 && kPartial * 4 <= kWarpB, "ring");
@@ -115,25 +116,33 @@ __device__ __forceinline__ uint32_t piece_at(int row, int piece) {
     return row * (CHUNKS * 16) + ((piece ^ (row & 7)) << 4);
 }
 
-// Where a request's keys start, and the partials of its rows (of requests with shared
-// keys): reference and sum of row (head T + token) group + head in group, and its outputs, four
-// dims of all rows together.  started: by token, set where rows have such partials.
+// The groups of requests that share a prefix, and the partials of their rows for the join with
+// it.  Of row (head T + token) group + head in group, by the warp that has its segment's first
+// step: reference, sum, (first of the warps with its other pieces) << 5 | row of the tile, and
+// how many they are; and its outputs, four dims of all rows together.  The other warps leave
+// theirs in the place of their partial: reference and sum of ROWS rows, outputs alike.
 struct OwnRows {
-    const int32_t *shared;
-    float2 *sums;
+    Groups groups;
+    float4 *sums;
     float *outs;
-    int32_t *started;
 };
 
 struct DecodeRows : RequestRows {
     int32_t shared;
 };
 
+// Data that a kernel before wrote, where this kernel does not begin with a wait.
+template <bool PAST, class V>
+__device__ __forceinline__ V load_past_l1(const V *p) {
+    return PAST ? __ldcg(p) : *p;
+}
+
+// shared: by request, the keys that are not this call's.
 template <bool SHARED>
-__device__ __forceinline__ DecodeRows load_request(const AttendArgs &a, const OwnRows &own, int32_t i) {
+__device__ __forceinline__ DecodeRows load_request(const AttendArgs &a, const int32_t *shared, int32_t i) {
     DecodeRows r;
-    static_cast<RequestRows &>(r) = load_rows(a, i);
-    r.shared = SHARED ? own.shared[i] : 0;
+    static_cast<RequestRows &>(r) = SHARED ? load_rows_cg(a, i) : load_rows(a, i);
+    r.shared = SHARED ? shared[i] : 0;
     return r;
 }
 
@@ -182,9 +191,9 @@ __device__ __forceinline__ int64_t cost_of(const AttendArgs &a, const DecodeRows
 
 // The segment of request `seq` that step x of the call belongs to.
 template <int ROWS, int KEYS, bool SHARED>
-__device__ __forceinline__ Segment segment_at(const AttendArgs &a, const OwnRows &own, const int32_t *s_pref, int32_t seq,
+__device__ __forceinline__ Segment segment_at(const AttendArgs &a, const int32_t *shared, const int32_t *s_pref, int32_t seq,
                                               int32_t x, bool whole_blocks) {
-    const DecodeRows r = load_request<SHARED>(a, own, seq);
+    const DecodeRows r = load_request<SHARED>(a, shared, seq);
     Segment s;
     s.seq = seq;
     s.q0 = r.q0;
@@ -202,12 +211,9 @@ __device__ __forceinline__ Segment segment_at(const AttendArgs &a, const OwnRows
     return s;
 }
 
-// A row of a segment among all rows and heads, and where dims d, d + 1 of its partial lie.
+// A row of a segment among all rows and heads.
 __device__ __forceinline__ int64_t own_row(const AttendArgs &a, const Segment &s, int32_t row) {
     return (int64_t(s.head) * a.T + s.q0) * a.group + row;
-}
-__device__ __forceinline__ float *own_out(const AttendArgs &a, const OwnRows &own, int64_t at, int d) {
-    return own.outs + ((d >> 2) * (int64_t(a.T) * a.n_heads) + at) * 4 + (d & 3);
 }
 
 // The request that step x (below the total) belongs to.
@@ -225,8 +231,8 @@ __device__ __forceinline__ int32_t find_seq(const int32_t *s_pref, int32_t n, in
 // part(i) is partial i's address, in shared or global memory; B of them are loaded at
 // a time, the first while the weights are computed (one request of 4,096 tokens: 16 at
 // a time 14.6 us, 4 after the weights 16.1).  Writes rows of `out`, or of the partial `to`.
-template <int HD, int ROWS, int R, int B, bool SHARED, class P>
-__device__ __forceinline__ void join_rows(const AttendArgs &a, const OwnRows &own, P part, int32_t first, int32_t last, const Segment &s,
+template <int HD, int ROWS, int R, int B, class P>
+__device__ __forceinline__ void join_rows(const AttendArgs &a, P part, int32_t first, int32_t last, const Segment &s,
                                           int r0, int rows, float shift, float *to, int lane) {
     constexpr int V = HD / 32;
     float top[R], sum[R], o[R][V];
@@ -309,17 +315,6 @@ __device__ __forceinline__ void join_rows(const AttendArgs &a, const OwnRows &ow
             continue;
         }
         const int32_t row = s.tile + r, t = s.q0 + row / a.group, h = s.head * a.group + row % a.group;
-        if (SHARED && s.shared > 0) {
-            const int64_t at = own_row(a, s, row);
-            if (lane == 0) {
-                own.sums[at] = make_float2(top[q] - shift, sum[q]);
-                own.started[t] = 1;
-            }
-#pragma unroll
-            for (int e = 0; e < V; e += 2)
-                *reinterpret_cast<float2 *>(own_out(a, own, at, lane * V + e)) = make_float2(o[q][e], o[q][e + 1]);
-            continue;
-        }
         const float inv = sum[q] > 0.0f ? a.kv.v_scale / sum[q] : sum[q] == 0.0f ? 0.0f : sum[q];
         uint32_t w[V / 2];
 #pragma unroll
@@ -332,10 +327,17 @@ __device__ __forceinline__ void join_rows(const AttendArgs &a, const OwnRows &ow
     }
 }
 
+// A block that did not wait for the kernel before it does so at its end: the kernel after
+// this one then finds both finished.
+template <bool SHARED>
+__device__ __forceinline__ void end_own() {
+    if (SHARED) asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 template <int HD, bool E4M3, int ROWS, bool SHARED>
 __global__ void __launch_bounds__(kWarps * 32, 1)
 attend_decode_kernel(const AttendArgs a, float *parts, int32_t *counters, int pref_bytes, const OwnRows own) {
-    using C = Config<HD, E4M3, ROWS>;
+    using C = Config<HD, E4M3, ROWS, SHARED>;
     constexpr int kKeys = C::kKeys, NK = kKeys / 32, ST = kKeys / 8, KB = kKeys / 16, kTiles = C::kTiles;
     constexpr int NW = kWarps, NT = NW * 32, MB = ROWS == 32 ? 2 : 1, KK = HD / 16, DT = HD / 8;
     constexpr bool kHalf = ROWS == 8;      // only rows 0..7 of the MMA's 16 hold queries
@@ -346,7 +348,32 @@ attend_decode_kernel(const AttendArgs a, float *parts, int32_t *counters, int pr
     __shared__ int64_t s_warp[NW][2];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c4 = lane & 3;
 
-    wait_for_previous();
+    int32_t grid = gridDim.x;  // blocks that take part
+    const int32_t *s_shared = nullptr;
+    if constexpr (SHARED) {
+        // The prefix kernel lets this one start when all of its blocks run, that is after all
+        // kernels before it: what they wrote may be read (past the first-level cache), and only
+        // the end waits for the prefix kernel.  Its blocks compute on as many SMs as the
+        // plan gives them, this kernel's on the others.
+        asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+        __shared__ int64_t s_sum[4 * NW];
+        bool bad;
+        const GroupPlan plan(reinterpret_cast<int32_t *>(smem + 2 * pref_bytes), own.groups.n_groups, a.n_seq);
+        grid = plan_groups<NT>(a, own.groups, plan, s_sum, grid, false, &bad).own;
+        int32_t *to = reinterpret_cast<int32_t *>(smem + pref_bytes);
+        for (int32_t i = tid; i < a.n_seq; i += NT) {
+            const int32_t g = group_of(plan, own.groups.n_groups, bad, i);
+            to[i] = g >= 0 ? plan.prefix[g] : 0;
+        }
+        s_shared = to;
+        __syncthreads();
+        if (static_cast<int32_t>(blockIdx.x) >= grid) {
+            end_own<SHARED>();
+            return;
+        }
+    } else {
+        wait_for_previous();
+    }
     // steps of every request: exclusive prefix in s_pref[0..n_seq], total behind it
     int32_t total;
     bool whole_blocks;
@@ -354,7 +381,7 @@ attend_decode_kernel(const AttendArgs a, float *parts, int32_t *counters, int pr
         const int32_t per = (a.n_seq + NT - 1) / NT, i0 = min(a.n_seq, tid * per), i1 = min(a.n_seq, i0 + per);
         int64_t mine = 0, padded = 0;
         for (int32_t i = i0; i < i1; ++i) {
-            const DecodeRows r = load_request<SHARED>(a, own, i);
+            const DecodeRows r = load_request<SHARED>(a, s_shared, i);
             if (!r.ok && blockIdx.x == 0) report_error(a.err, LORA_ERR_INVALID_ARG);
             mine += cost_of<ROWS, kKeys>(a, r, false);
             padded += cost_of<ROWS, kKeys>(a, r, true);
@@ -379,14 +406,15 @@ attend_decode_kernel(const AttendArgs a, float *parts, int32_t *counters, int pr
             if (w < warp) run += s_warp[w][0], run2 += s_warp[w][1];
             sum += s_warp[w][0], sum2 += s_warp[w][1];
         }
-        whole_blocks = sum2 <= int64_t(gridDim.x) * NW;
+        whole_blocks = sum2 <= int64_t(grid) * NW;
         if (whole_blocks) run = run2, sum = sum2;
         if (sum > INT32_MAX) {  // the same in every block
             if (blockIdx.x == 0 && tid == 0) report_error(a.err, LORA_ERR_UNSUPPORTED);
+            end_own<SHARED>();
             return;
         }
         for (int32_t i = i0; i < i1; ++i) {
-            const DecodeRows r = load_request<SHARED>(a, own, i);
+            const DecodeRows r = load_request<SHARED>(a, s_shared, i);
             s_pref[i] = static_cast<int32_t>(run);
             run += cost_of<ROWS, kKeys>(a, r, whole_blocks);
         }
@@ -396,9 +424,9 @@ attend_decode_kernel(const AttendArgs a, float *parts, int32_t *counters, int pr
     }
 
     // rows of requests without cached tokens
-    for (int32_t i = blockIdx.x; i < a.n_seq; i += gridDim.x) {
+    for (int32_t i = blockIdx.x; i < a.n_seq; i += grid) {
         if (s_pref[i + 1] != s_pref[i]) continue;
-        const DecodeRows r = load_request<SHARED>(a, own, i);
+        const DecodeRows r = load_request<SHARED>(a, s_shared, i);
         for (int64_t e = tid; e < int64_t(r.n) * a.n_heads; e += NT) {
             const int64_t t = r.q0 + e / a.n_heads, h = e % a.n_heads;
             for (int d = 0; d < HD; d += 8) stg_u4(a.out + t * a.ldo + h * HD + d, make_uint4(0, 0, 0, 0));
@@ -406,7 +434,7 @@ attend_decode_kernel(const AttendArgs a, float *parts, int32_t *counters, int pr
         }
     }
 
-    const int32_t shares = gridDim.x * NW;
+    const int32_t shares = grid * NW;
     const int64_t share = (int64_t(total) + shares - 1) / shares;  // steps a warp
     const int32_t me = blockIdx.x * NW + warp;
     const int32_t x0 = static_cast<int32_t>(min(int64_t(total), me * share));
@@ -414,7 +442,8 @@ attend_decode_kernel(const AttendArgs a, float *parts, int32_t *counters, int pr
 
     // this warp's memory: its query fragments and its ring of k and v tiles; the last
     // partial of its share takes their place in the end
-    unsigned char *const warp_ptr = smem + pref_bytes + warp * C::kWarpB;
+    const int ring_at = (SHARED ? 2 : 1) * pref_bytes;
+    unsigned char *const warp_ptr = smem + ring_at + warp * C::kWarpB;
     const uint32_t ring = tc::smem_u32(warp_ptr) + C::kQBytes;
     uint4 *s_q = reinterpret_cast<uint4 *>(warp_ptr);
 
@@ -428,11 +457,11 @@ attend_decode_kernel(const AttendArgs a, float *parts, int32_t *counters, int pr
         if (lx < x1) {
 #pragma unroll
             for (int i = 0; i < NK; ++i)
-                lpage[i] = has_key(i) ? ltab[(lkey + 32 * i + lane) >> a.kv.page_shift] : -1;
+                lpage[i] = has_key(i) ? load_past_l1<SHARED>(ltab + ((lkey + 32 * i + lane) >> a.kv.page_shift)) : -1;
         }
     };
     const auto open_load = [&](int32_t seq) {
-        ls = segment_at<ROWS, kKeys, SHARED>(a, own, s_pref, seq, lx, whole_blocks);
+        ls = segment_at<ROWS, kKeys, SHARED>(a, s_shared, s_pref, seq, lx, whole_blocks);
         lx = max(lx, ls.begin);
         lkey = ls.base + (lx - ls.begin) * kKeys;
         lend = ls.begin + ls.steps;
@@ -508,7 +537,7 @@ attend_decode_kernel(const AttendArgs a, float *parts, int32_t *counters, int pr
     float m[MB][2], l[MB][2], mult[MB][2], slope[MB][2], acc[MB][DT][4];
 
     const auto open_compute = [&](int32_t seq) {
-        cs = segment_at<ROWS, kKeys, SHARED>(a, own, s_pref, seq, cx, whole_blocks);
+        cs = segment_at<ROWS, kKeys, SHARED>(a, s_shared, s_pref, seq, cx, whole_blocks);
         cx = max(cx, cs.begin);
         cend = cs.begin + cs.steps;
         if (cx >= cend) cx = x1;  // a unit behind the segment's steps
@@ -525,7 +554,7 @@ attend_decode_kernel(const AttendArgs a, float *parts, int32_t *counters, int pr
                 const bool live = r < rows;
                 const int32_t token = row / a.group, h = cs.head * a.group + row % a.group;
                 pos[mb][i] = live ? cs.len - cs.n + token : -1;
-                slope[mb][i] = live && a.slopes != nullptr ? a.slopes[h] * kLog2e : 0.0f;
+                slope[mb][i] = live && a.slopes != nullptr ? load_past_l1<SHARED>(a.slopes + h) * kLog2e : 0.0f;
                 m[mb][i] = -INFINITY;
                 l[mb][i] = 0.0f;
                 mult[mb][i] = a.scale * a.kv.k_scale;
@@ -537,7 +566,7 @@ attend_decode_kernel(const AttendArgs a, float *parts, int32_t *counters, int pr
                     float f[KK][4];
 #pragma unroll
                     for (int kk = 0; kk < KK; ++kk) {
-                        const uint2 u = live ? *reinterpret_cast<const uint2 *>(src + kk * 16 + 4 * c4)
+                        const uint2 u = live ? load_past_l1<SHARED>(reinterpret_cast<const uint2 *>(src + kk * 16 + 4 * c4))
                                              : make_uint2(0, 0);
                         f[kk][0] = bf16lo_to_f32(u.x), f[kk][1] = bf16hi_to_f32(u.x);
                         f[kk][2] = bf16lo_to_f32(u.y), f[kk][3] = bf16hi_to_f32(u.y);
@@ -558,8 +587,8 @@ attend_decode_kernel(const AttendArgs a, float *parts, int32_t *counters, int pr
                 } else {
 #pragma unroll
                     for (int kk = 0; kk < KK; ++kk) {
-                        w[kk][0] = live ? *reinterpret_cast<const uint32_t *>(src + kk * 16 + 2 * c4) : 0u;
-                        w[kk][1] = live ? *reinterpret_cast<const uint32_t *>(src + kk * 16 + 8 + 2 * c4) : 0u;
+                        w[kk][0] = live ? load_past_l1<SHARED>(reinterpret_cast<const uint32_t *>(src + kk * 16 + 2 * c4)) : 0u;
+                        w[kk][1] = live ? load_past_l1<SHARED>(reinterpret_cast<const uint32_t *>(src + kk * 16 + 8 + 2 * c4)) : 0u;
                     }
                 }
 #pragma unroll
@@ -728,6 +757,10 @@ attend_decode_kernel(const AttendArgs a, float *parts, int32_t *counters, int pr
     const auto close = [&]() {
         const int32_t rows = min(ROWS, cs.n * a.group - cs.tile);
         const bool whole = cs.begin >= x0 && cend == cx;
+        // a piece for the join with the prefix: at the rows' place or, of a segment that begins before, at the warp's
+        const bool piece = SHARED && cs.shared > 0, first = cs.begin >= x0;
+        float *const cut = parts + int64_t(me) * C::kPartial;
+        const int64_t all_rows = int64_t(a.T) * a.n_heads;
         float *part = cend + kOpen >= x1 ? reinterpret_cast<float *>(warp_ptr) : parts + int64_t(me) * C::kPartial;
 #pragma unroll
         for (int mb = 0; mb < MB; ++mb)
@@ -739,18 +772,23 @@ attend_decode_kernel(const AttendArgs a, float *parts, int32_t *counters, int pr
                 const int32_t r = mb * 16 + i * 8 + g, row = cs.tile + r;
                 if (r >= rows) continue;
                 const int32_t t = cs.q0 + row / a.group, h = cs.head * a.group + row % a.group;
-                const bool partial = SHARED && whole && cs.shared > 0;  // for the join with the prefix
-                const int64_t at = partial ? own_row(a, cs, row) : 0;
-                const float inv = !whole || partial ? 1.0f : sum > 0.0f ? a.kv.v_scale / sum : sum == 0.0f ? 0.0f : sum;
+                const int64_t at = piece ? own_row(a, cs, row) : 0;
+                float *const to_piece = first ? own.outs + at * 4 : cut + 2 * ROWS + r * 4;
+                const int64_t dims4 = first ? 4 * all_rows : 4 * ROWS;  // from four dims to the next
+                const float inv = !whole || piece ? 1.0f : sum > 0.0f ? a.kv.v_scale / sum : sum == 0.0f ? 0.0f : sum;
                 uint16_t *out = a.out + t * a.ldo + h * HD;
                 float *to = part + 2 * ROWS + r * HD;
                 if (c4 == 0) {
-                    if (!whole) {
+                    if (piece) {
+                        const int32_t others = static_cast<int32_t>((int64_t(cend) - 1) / share - me);
+                        if (first)
+                            own.sums[at] = make_float4(m[mb][i] - kShift, sum, __int_as_float((me + 1) << 5 | r),
+                                                       __int_as_float(others));
+                        else
+                            *reinterpret_cast<float2 *>(cut + 2 * r) = make_float2(m[mb][i] - kShift, sum);
+                    } else if (!whole) {
                         part[r] = m[mb][i];
                         part[ROWS + r] = sum;
-                    } else if (partial) {
-                        own.sums[at] = make_float2(m[mb][i] - kShift, sum);
-                        own.started[t] = 1;
                     } else if (a.lse != nullptr) {
                         a.lse[int64_t(t) * a.n_heads + h] = sum == 0.0f ? -INFINITY
                                                                         : kLn2 * (m[mb][i] - kShift) + logf(sum);
@@ -762,8 +800,8 @@ attend_decode_kernel(const AttendArgs a, float *parts, int32_t *counters, int pr
                         const float4 v = make_float4(acc[mb][c][2 * i] * inv, acc[mb][c + 1][2 * i] * inv,
                                                      acc[mb][c][2 * i + 1] * inv, acc[mb][c + 1][2 * i + 1] * inv);
                         const int d = 8 * c + 4 * c4;
-                        if (partial)
-                            *reinterpret_cast<float4 *>(own_out(a, own, at, d)) = v;
+                        if (piece)
+                            *reinterpret_cast<float4 *>(to_piece + (d >> 2) * dims4) = v;
                         else if (whole)
                             *reinterpret_cast<uint2 *>(out + d) = make_uint2(pack_bf16x2(v.x, v.y),
                                                                              pack_bf16x2(v.z, v.w));
@@ -776,7 +814,8 @@ attend_decode_kernel(const AttendArgs a, float *parts, int32_t *counters, int pr
                         float v0 = acc[mb][d8][2 * i], v1 = acc[mb][d8][2 * i + 1];
                         if (kHalf) v0 += acc[mb][d8][2], v1 += acc[mb][d8][3];
                         const int d = 8 * d8 + 2 * c4;
-                        if (partial) *reinterpret_cast<float2 *>(own_out(a, own, at, d)) = make_float2(v0, v1);
+                        if (piece)
+                            *reinterpret_cast<float2 *>(to_piece + (d >> 2) * dims4 + (d & 3)) = make_float2(v0, v1);
                         else if (whole) *reinterpret_cast<uint32_t *>(out + d) = pack_bf16x2(v0 * inv, v1 * inv);
                         else *reinterpret_cast<float2 *>(to + d) = make_float2(v0, v1);
                     }
@@ -823,17 +862,17 @@ attend_decode_kernel(const AttendArgs a, float *parts, int32_t *counters, int pr
         bool last;
     };
     __shared__ Cut s_cut[NW + 1];
-    float *block_parts = parts + int64_t(gridDim.x) * NW * C::kPartial;
+    float *block_parts = parts + int64_t(grid) * NW * C::kPartial;
     const int64_t block_share = share * NW, b0 = min(int64_t(total), blockIdx.x * block_share);
     const int64_t b1 = min(int64_t(total), b0 + block_share);
     if (tid <= NW) {
         const int64_t x = min(int64_t(total), b0 + tid * share);
         Cut c{};
         if (x > 0 && x < total) {
-            c.s = segment_at<ROWS, kKeys, SHARED>(a, own, s_pref, find_seq(s_pref, a.n_seq, static_cast<int32_t>(x)),
+            c.s = segment_at<ROWS, kKeys, SHARED>(a, s_shared, s_pref, find_seq(s_pref, a.n_seq, static_cast<int32_t>(x)),
                                           static_cast<int32_t>(x), whole_blocks);
             const int64_t end = int64_t(c.s.begin) + c.s.steps;
-            if (c.s.begin < x && x < end && (tid == 0 || c.s.begin >= x - share)) {
+            if (c.s.shared == 0 && c.s.begin < x && x < end && (tid == 0 || c.s.begin >= x - share)) {
                 c.rows = min(ROWS, c.s.n * a.group - c.s.tile);
                 c.w0 = static_cast<int32_t>(max(int64_t(c.s.begin), b0) / share);
                 c.w1 = static_cast<int32_t>((min(end, b1) - 1) / share);
@@ -868,14 +907,17 @@ attend_decode_kernel(const AttendArgs a, float *parts, int32_t *counters, int pr
         // a warp's partial is in its own memory, unless more segments followed in its share
         const auto of_warp = [&](int32_t w) -> const float * {
             if (end + kOpen < min(int64_t(total), (w + 1) * share)) return parts + int64_t(w) * C::kPartial;
-            return reinterpret_cast<const float *>(smem + pref_bytes + (w - blockIdx.x * NW) * C::kWarpB);
+            return reinterpret_cast<const float *>(smem + ring_at + (w - blockIdx.x * NW) * C::kWarpB);
         };
-        join_rows<HD, ROWS, by.value, ROWS == 32 ? 2 : 4, SHARED>(a, own, of_warp, c.w0, c.w1, c.s, r, c.rows, kShift,
+        join_rows<HD, ROWS, by.value, ROWS == 32 ? 2 : 4>(a, of_warp, c.w0, c.w1, c.s, r, c.rows, kShift,
                                                           c.c0 == c.c1 ? nullptr : block_part(c.s, blockIdx.x), lane);
     });
     bool shared_cut = false;
     for (int i = 0; i <= NW; ++i) shared_cut = shared_cut || (s_cut[i].rows > 0 && s_cut[i].c0 != s_cut[i].c1);
-    if (!shared_cut) return;
+    if (!shared_cut) {
+        end_own<SHARED>();
+        return;
+    }
     __threadfence();
     __syncthreads();
     if (tid <= NW && s_cut[tid].rows > 0 && s_cut[tid].c0 != s_cut[tid].c1) {
@@ -887,22 +929,25 @@ attend_decode_kernel(const AttendArgs a, float *parts, int32_t *counters, int pr
     __threadfence();
     each([](const Cut &c) { return c.last; }, [&](const Cut &c, int r, auto by) {
         const auto of_block = [&](int32_t b) -> const float * { return block_part(c.s, b); };
-        join_rows<HD, ROWS, by.value, ROWS == 32 ? 2 : by.value == 1 ? 16 : 4, SHARED>(a, own, of_block, c.c0, c.c1, c.s, r, c.rows,
+        join_rows<HD, ROWS, by.value, ROWS == 32 ? 2 : by.value == 1 ? 16 : 4>(a, of_block, c.c0, c.c1, c.s, r, c.rows,
                                                                                kShift, nullptr, lane);
     });
+    end_own<SHARED>();
 }
 
 template <int HD, bool E4M3, int ROWS, bool SHARED>
 cudaError_t launch_decode(const AttendArgs &a, const OwnRows &own, void *ws, cudaStream_t stream) {
-    using C = Config<HD, E4M3, ROWS>;
+    using C = Config<HD, E4M3, ROWS, SHARED>;
     static std::atomic<uint64_t> seen{0};
     const auto kernel = attend_decode_kernel<HD, E4M3, ROWS, SHARED>;
     int sms = 0;
-    const cudaError_t e = prepare_kernel(kernel, kPrefixMax + kWarps * C::kWarpB, seen, &sms);
+    constexpr int kLists = SHARED ? 2 : 1;  // of the requests: step prefixes; shared keys
+    const cudaError_t e = prepare_kernel(kernel, kLists * kPrefixMax + kWarps * C::kWarpB, seen, &sms);
     if (e != cudaSuccess) return e;
     const int grid = sms < kMaxGrid ? sms : kMaxGrid;
     const int pref = ((a.n_seq + 1) * 4 + 127) & ~127;
-    const int smem = pref + kWarps * C::kWarpB;
+    const int smem = kLists * pref + kWarps * C::kWarpB;
+    static_assert(!SHARED || GroupPlan::bytes(LORA_MAX_SEQS, LORA_MAX_SEQS) <= size_t(kWarps) * C::kWarpB, "the plan's place");
     int32_t *counters = static_cast<int32_t *>(ws);
     float *parts = reinterpret_cast<float *>(static_cast<char *>(ws) + 1024);
     return launch_dependent(kernel, grid, kWarps * 32, smem, stream, a, parts, counters, pref, own);
@@ -916,9 +961,8 @@ cudaError_t pick_rows(const AttendArgs &a, int64_t rows, const OwnRows &own, voi
 }
 
 template <bool SHARED>
-cudaError_t pick_decode(const AttendArgs &a, bool e4m3, int32_t max_q, const OwnRows &own, void *ws,
+cudaError_t pick_decode(const AttendArgs &a, bool e4m3, int64_t rows, const OwnRows &own, void *ws,
                         cudaStream_t stream) {
-    const int64_t rows = int64_t(max_q) * a.group;
     if (a.kv.head_dim == 64)
         return e4m3 ? pick_rows<64, true, SHARED>(a, rows, own, ws, stream)
                     : pick_rows<64, false, SHARED>(a, rows, own, ws, stream);

@@ -3,9 +3,12 @@
 
 namespace lora {
 
-cudaError_t launch_attend_own(const AttendArgs &a, bool e4m3, int32_t max_q, const int32_t *shared, float2 *sums,
-                              float *outs, int32_t *started, void *ws, cudaStream_t stream) {
-    return pick_decode<true>(a, e4m3, max_q, OwnRows{shared, sums, outs, started}, ws, stream);
+// The other pieces of rows are left in ws, behind the counters: see OwnRows.
+cudaError_t launch_attend_own(const AttendArgs &a, bool e4m3, const Groups &groups, float4 *sums, float *outs, void *ws,
+                              cudaStream_t stream) {
+    return pick_decode<true>(a, e4m3, groups.tile_rows, OwnRows{groups, sums, outs}, ws, stream);
 }
+
+const float *own_pieces(const void *ws) { return reinterpret_cast<const float *>(static_cast<const char *>(ws) + 1024); }
 
 }  // namespace lora

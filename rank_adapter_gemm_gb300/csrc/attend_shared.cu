@@ -24,20 +24,20 @@
 // pieces.  Weights are rounded to bf16 over a bf16 cache (the instruction takes one type
 // for both operands; sums use them unrounded), to f16, times 2^7, over an e4m3 cache.
 #include "attend_tc.cuh"
+#include "shared_plan.cuh"
 
 namespace lora {
 
 size_t decode_workspace_bytes(int32_t head_dim);
-cudaError_t launch_attend_own(const AttendArgs &a, bool e4m3, int32_t max_q, const int32_t *shared, float2 *sums,
-                              float *outs, int32_t *started, void *ws, cudaStream_t stream);
+cudaError_t launch_attend_own(const AttendArgs &a, bool e4m3, const Groups &groups, float4 *sums, float *outs, void *ws,
+                              cudaStream_t stream);
+const float *own_pieces(const void *ws);
 
 namespace {
 
 constexpr int kThreads = 16 * 32, kMaxGrid = 160;
 
-// Opening a piece (its queries, its result) costs a block about as much as kOpen steps:
-// every segment counts as so many more, in front of the real ones.
-constexpr int kOpen = 1;
+static_assert(kPrefixRows == 2 * kRows && kPrefixKeys == kKeys, "a step");
 
 // The tensor cores cut off what does not fit when they add to O, about 2^-24 of it with
 // every 16 keys: more steps than these are taken one after the other and added up in fp32.
@@ -58,18 +58,18 @@ struct PrefixConfig {
 };
 
 // What the kernels of a call hand over.  Every block of the prefix kernel writes the same
-// plan (and reads only what it wrote itself, or what is equal to it).
+// lists of groups (and reads what it wrote itself, or what is equal to it).
 struct SharedWork {
-    const int32_t *offsets, *lens;
-    int32_t n_groups;
-    int64_t *units;             // by group: steps (and openings) before it, n_groups + 1
-    int32_t *prefix, *lo, *lead;  // by group: its keys' end and first, the request whose row of the table holds them
-    int32_t *shared, *started;  // by request: keys of the prefix; by token: set where there are own partials
-    float2 *own_sums;           // reference and sum of a row over its own keys
-    float *own_outs;            // its output, four dims of all rows together
-    float4 *heads;              // reference and sum over the prefix, first block with another piece and how many
-    float *outs;                // its output, as above
-    float4 *cut_heads;          // of a block's piece, 256 rows a block
+    Groups groups;
+    int64_t *units;               // by group: steps (and openings) before it, n_groups + 1
+    int32_t *prefix, *lo, *lead;  // by group, of its plan
+    int32_t *live;                // whether anything is shared; then by token, whether its request shares
+    float4 *own_sums;             // of a row over its own keys, see OwnRows
+    float *own_outs;
+    const float *own_cuts;
+    float4 *heads;                // reference and sum over the prefix; place of the row's other pieces and their number
+    float *outs;                  // its output, as above
+    float4 *cut_heads;            // of a block's piece, 256 rows a block
     float *cut_outs;
 };
 
@@ -88,76 +88,13 @@ struct Item {
     bool any;                        // none: the work is done
 };
 
-// Steps of a group's prefix (any row tile and key head).
-__device__ __forceinline__ int32_t steps_of(int32_t lo, int32_t prefix) {
-    return prefix > lo ? (prefix - 1) / kKeys - lo / kKeys + 1 : 0;
-}
-
-// The last entry of n rising ones that is <= x, from 0.
-template <class V>
-__device__ __forceinline__ int32_t last_at_most(const V *rising, int32_t n, int64_t x) {
-    int32_t lo = 0, hi = n - 1;
-    while (lo < hi) {
-        const int32_t mid = (lo + hi + 1) >> 1;
-        if (rising[mid] <= x) lo = mid;
-        else hi = mid - 1;
-    }
-    return lo;
-}
-
-// The groups' prefixes, for the whole block: arrays of n_groups int32 in scratch (which the
-// ring takes over afterwards).  Sets the plan; returns all units.
-__device__ int64_t plan_groups(const AttendArgs &a, const SharedWork &w, int32_t *scratch, int64_t *s_sum) {
+// The lists of the call's groups in global memory, by the whole block; returns all units.
+__device__ int64_t list_groups(const AttendArgs &a, const SharedWork &w, const GroupPlan &p, int64_t *s_sum) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    int32_t *s_ctx = scratch, *s_count = scratch + w.n_groups, *s_lead = s_count + w.n_groups;
-    bool bad = false;
-    for (int32_t g = tid; g < w.n_groups; g += kThreads) {
-        s_ctx[g] = INT32_MAX;
-        s_count[g] = 0;
-        s_lead[g] = INT32_MAX;
-        const int32_t from = w.offsets[g], to = w.offsets[g + 1];
-        bad = bad || from < 0 || to < from || to > a.n_seq;
-        if (w.lens[g] < 0 && blockIdx.x == 0) report_error(a.err, LORA_ERR_INVALID_ARG);
-    }
-    bad = __syncthreads_or(bad);
-    if (bad && blockIdx.x == 0 && tid == 0) report_error(a.err, LORA_ERR_INVALID_ARG);
-    // the group of request i, -1: none
-    const auto group_of = [&](int32_t i) {
-        if (bad || w.n_groups == 0 || i < w.offsets[0] || i >= w.offsets[w.n_groups]) return -1;
-        return last_at_most(w.offsets, w.n_groups, i);
-    };
-    for (int32_t i = tid; i < a.n_seq; i += kThreads) {
-        const RequestRows r = load_rows(a, i);
-        const int32_t g = r.n > 0 ? group_of(i) : -1;
-        if (g < 0) continue;
-        atomicMin(&s_ctx[g], r.len - r.n);
-        atomicMin(&s_lead[g], i);
-        atomicAdd(&s_count[g], 1);
-    }
-    __syncthreads();
-    const int32_t per = (w.n_groups + kThreads - 1) / kThreads;
-    const int32_t g0 = min(w.n_groups, tid * per), g1 = min(w.n_groups, g0 + per);
+    const int32_t n = w.groups.n_groups;
+    const int32_t per = (n + kThreads - 1) / kThreads, g0 = min(n, tid * per), g1 = min(n, g0 + per);
     int64_t mine = 0;
-    const auto units_of = [&](int32_t g) {
-        const int32_t steps = steps_of(w.lo[g], w.prefix[g]);
-        if (steps == 0) return int64_t(0);
-        const int64_t rows = int64_t(a.q_offsets[w.offsets[g + 1]] - a.q_offsets[w.offsets[g]]) * a.group;
-        return (rows + 2 * kRows - 1) / (2 * kRows) * a.kv.n_kv * (steps + kOpen);
-    };
-    for (int32_t g = g0; g < g1; ++g) {
-        int32_t prefix = 0, lo = 0;
-        if (!bad && s_count[g] > 1) {
-            const int32_t q0 = a.q_offsets[w.offsets[g]], q1 = a.q_offsets[w.offsets[g + 1]];
-            if (q0 >= 0 && q1 >= q0 && q1 <= a.T) prefix = max(0, min(w.lens[g], s_ctx[g]));
-            if (a.window > 0) lo = static_cast<int32_t>(max(int64_t(0), int64_t(s_ctx[g]) - a.window + 1));
-            if (lo >= prefix) prefix = lo = 0;  // no row sees any of it
-        }
-        w.prefix[g] = prefix;
-        w.lo[g] = lo;
-        w.lead[g] = s_lead[g];
-        s_ctx[g] = prefix;
-        mine += units_of(g);
-    }
+    for (int32_t g = g0; g < g1; ++g) mine += prefix_units(a, p, g);
     int64_t incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -173,15 +110,12 @@ __device__ int64_t plan_groups(const AttendArgs &a, const SharedWork &w, int32_t
     }
     for (int32_t g = g0; g < g1; ++g) {
         w.units[g] = run;
-        run += units_of(g);
+        w.prefix[g] = p.prefix[g];
+        w.lo[g] = p.lo[g];
+        w.lead[g] = p.lead[g];
+        run += prefix_units(a, p, g);
     }
-    if (tid == 0) w.units[w.n_groups] = total;
-    // what the next kernels read: this block's part
-    for (int32_t i = blockIdx.x * kThreads + tid; i < a.n_seq; i += gridDim.x * kThreads) {
-        const int32_t g = group_of(i);
-        w.shared[i] = g >= 0 ? s_ctx[g] : 0;
-    }
-    for (int32_t t = blockIdx.x * kThreads + tid; t < a.T; t += gridDim.x * kThreads) w.started[t] = 0;
+    if (tid == 0) w.units[n] = total;
     return total;
 }
 
@@ -236,7 +170,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefix_kernel(const Attend
     extern __shared__ unsigned char smem_raw[];
     __shared__ Barriers bar;
     __shared__ Item s_item[2];
-    __shared__ int64_t s_sum[kThreads / 32];
+    __shared__ int64_t s_sum[4 * kThreads / 32];
     __shared__ uint32_t s_tmem;
     __shared__ volatile int32_t s_abort;
     __shared__ int8_t s_qexp[2][E4M3 ? 2 * kRows : 1];  // of this and the next piece: q rows' powers of two
@@ -245,10 +179,19 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefix_kernel(const Attend
     const uint32_t ring = q_base + 2 * C::kQ * C::kTileB;
 
     wait_for_previous();
-    const int64_t total = plan_groups(a, w, reinterpret_cast<int32_t *>(smem_raw), s_sum);
-    const int64_t share = (total + gridDim.x - 1) / gridDim.x;
+    int32_t blocks;
+    int64_t total;
+    {
+        const GroupPlan plan(reinterpret_cast<int32_t *>(smem_raw), w.groups.n_groups, a.n_seq);  // (the ring's place)
+        bool bad;
+        blocks = plan_groups<kThreads>(a, w.groups, plan, s_sum, gridDim.x, blockIdx.x == 0, &bad).prefix;
+        if (blockIdx.x == 0 && tid == 0) w.live[0] = blocks > 0;
+        // blocks without a share leave their SM to the next kernel (whole blocks: nothing is allocated yet)
+        if (static_cast<int32_t>(blockIdx.x) >= blocks) return;
+        total = list_groups(a, w, plan, s_sum);
+    }
+    const int64_t share = (total + blocks - 1) / blocks;
     const int64_t x0 = min(total, blockIdx.x * share), x1 = min(total, x0 + share);
-    if (x0 >= x1) return;  // (the whole block: nothing is allocated yet)
     if (tid == 0) {
         s_abort = 0;
         for (int i = 0; i < C::kQ; ++i) {
@@ -569,13 +512,13 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefix_kernel(const Attend
                 } else {
                     it.any = false;
                     while (x < x1) {
-                        if (k == 0 || w.units[g + 1] <= x) g = last_at_most(w.units, w.n_groups + 1, x);
+                        if (k == 0 || w.units[g + 1] <= x) g = last_at_most(w.units, w.groups.n_groups + 1, x);
                         // (of groups that begin at x the last is the one with units)
-                        const int32_t lo = w.lo[g], end = w.prefix[g], steps = steps_of(lo, end);
-                        const int32_t q0 = a.q_offsets[w.offsets[g]], q1 = a.q_offsets[w.offsets[g + 1]];
+                        const int32_t lo = w.lo[g], end = w.prefix[g], steps = prefix_steps(lo, end);
+                        const int32_t q0 = a.q_offsets[w.groups.offsets[g]], q1 = a.q_offsets[w.groups.offsets[g + 1]];
                         const int64_t rows = int64_t(q1 - q0) * a.group, tiles = (rows + 2 * kRows - 1) / (2 * kRows);
-                        const int64_t i = (x - w.units[g]) / (steps + kOpen), head = i / tiles, tile = i - head * tiles;
-                        const int64_t begin = w.units[g] + i * (steps + kOpen) + kOpen;  // its first step
+                        const int64_t i = (x - w.units[g]) / (steps + kPrefixOpen), head = i / tiles, tile = i - head * tiles;
+                        const int64_t begin = w.units[g] + i * (steps + kPrefixOpen) + kPrefixOpen;  // its first step
                         const int64_t from = max(x, begin), to = min(x1, begin + steps);
                         x = begin + steps;
                         if (from >= to) continue;  // only the opening lies in this share
@@ -608,6 +551,15 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefix_kernel(const Attend
                 }
                 __syncwarp();
                 if (!it.any) break;
+            }
+        } else {
+            // ---- the tokens whose rows are to be joined: the two warps left -------------------
+            const int32_t n = w.groups.n_groups;
+            for (int64_t t = blockIdx.x * 64 + (warp - 14) * 32 + lane; t < a.T; t += int64_t(blocks) * 64) {
+                const int32_t i = last_at_most(a.q_offsets, a.n_seq, t);
+                const RequestRows r = load_rows(a, i);
+                const bool in = t >= r.q0 && t < r.q0 + r.n && i >= w.groups.offsets[0] && i < w.groups.offsets[n];
+                w.live[1 + t] = in && w.prefix[last_at_most(w.groups.offsets, n, i)] > 0;
             }
         }
     } else {
@@ -788,19 +740,27 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefix_kernel(const Attend
 template <int HD>
 __global__ void __launch_bounds__(256) attend_join_kernel(const AttendArgs a, const SharedWork w) {
     wait_for_previous();
-    const int64_t rows = int64_t(a.T) * a.n_heads, row = int64_t(blockIdx.x) * 32 + (threadIdx.x & 31);
-    if (row >= rows) return;
+    const int64_t rows = int64_t(a.T) * a.n_heads, row = min(int64_t(blockIdx.x) * 32 + (threadIdx.x & 31), rows - 1);
     const int64_t per = int64_t(a.T) * a.group, head = row / per, at = row - head * per;
     const int32_t t = static_cast<int32_t>(at / a.group), h = static_cast<int32_t>(head * a.group + at % a.group);
-    if (w.started[t] == 0) return;
-    const float2 own = w.own_sums[row];
-    const float4 first = ldg_cg_f4(reinterpret_cast<const float *>(w.heads + row));
-    // where the other pieces' results of this row lie
-    const int32_t place = __float_as_int(first.z), c0 = place >> 8, c1 = c0 + __float_as_int(first.w), r = place & 255;
+    // (of a row that is not joined these are of another call)
+    const float4 first = __ldcg(w.heads + row), own = __ldcg(w.own_sums + row);
+    const bool live = w.live[1 + t] != 0 && int64_t(blockIdx.x) * 32 + (threadIdx.x & 31) < rows;
+    if (w.live[0] == 0 || !live) return;
+    // where the row's other pieces lie: prefix pieces by block, own ones by warp of the decode path
+    constexpr int kDim4s = HD / 4;
+    const int32_t tile = w.groups.tile_rows, own_size = tile * (HD + 2);
+    const int32_t c0 = __float_as_int(first.z) >> 8, c1 = c0 + __float_as_int(first.w), r = __float_as_int(first.z) & 255;
+    const int32_t w0 = __float_as_int(own.z) >> 5, w1 = w0 + __float_as_int(own.w), r1 = __float_as_int(own.z) & 31;
+    const float2 *cuts = reinterpret_cast<const float2 *>(w.cut_heads + r);
+    const float *owns = w.own_cuts + 2 * r1;
     float top = fmaxf(own.x, first.x);
-    for (int32_t c = c0; c < c1; ++c) top = fmaxf(top, ldg_cg_f4(reinterpret_cast<const float *>(w.cut_heads + c * 2 * kRows + r)).x);
+#pragma unroll 8
+    for (int32_t c = c0; c < c1; ++c) top = fmaxf(top, __ldcg(cuts + c * 4 * kRows).x);
+#pragma unroll 8
+    for (int32_t c = w0; c < w1; ++c) top = fmaxf(top, __ldcg(owns + int64_t(c) * own_size));
     const float ref = top == -INFINITY ? 0.0f : top;
-    constexpr int kGroups = HD / 64;  // of 8 dims, a warp
+    constexpr int kGroups = kDim4s / 16;  // of 8 dims, a warp
     const int warp = threadIdx.x >> 5;
     float o[kGroups][8], sum = 0.0f;
 #pragma unroll
@@ -815,7 +775,7 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const AttendArgs a, co
         for (int g = 0; g < kGroups; ++g)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const float4 v = ldg_cg_f4(from + (2 * (g * 8 + warp) + e) * stride);
+                const float4 v = __ldcg(reinterpret_cast<const float4 *>(from + (2 * (g * 8 + warp) + e) * stride));
                 o[g][4 * e] = fmaf(f, v.x, o[g][4 * e]);
                 o[g][4 * e + 1] = fmaf(f, v.y, o[g][4 * e + 1]);
                 o[g][4 * e + 2] = fmaf(f, v.z, o[g][4 * e + 2]);
@@ -825,10 +785,15 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const AttendArgs a, co
     add(first.x, first.y, w.outs + row * 4, 4 * rows);
 #pragma unroll 4
     for (int32_t c = c0; c < c1; ++c) {
-        const float4 head_c = ldg_cg_f4(reinterpret_cast<const float *>(w.cut_heads + c * 2 * kRows + r));
-        add(head_c.x, head_c.y, w.cut_outs + c * int64_t(2 * kRows * HD) + r * 4, 8 * kRows);
+        const float2 part = __ldcg(cuts + c * 4 * kRows);
+        add(part.x, part.y, w.cut_outs + c * int64_t(2 * kRows * HD) + r * 4, 8 * kRows);
     }
     add(own.x, own.y, w.own_outs + row * 4, 4 * rows);
+#pragma unroll 4
+    for (int32_t c = w0; c < w1; ++c) {
+        const float2 part = __ldcg(reinterpret_cast<const float2 *>(owns + int64_t(c) * own_size));
+        add(part.x, part.y, w.own_cuts + int64_t(c) * own_size + 2 * tile + r1 * 4, 4 * tile);
+    }
     const float inv = sum > 0.0f ? a.kv.v_scale / sum : sum == 0.0f ? 0.0f : sum;
 #pragma unroll
     for (int g = 0; g < kGroups; ++g) {
@@ -845,7 +810,7 @@ size_t up128(size_t b) { return (b + 127) & ~size_t(127); }
 
 // The parts of a call's workspace behind the decode path's.  Nothing in them outlives a call.
 struct Layout {
-    size_t units, prefix, lo, lead, shared, started, own_sums, own_outs, heads, outs, cut_heads, cut_outs, end;
+    size_t units, prefix, lo, lead, live, own_sums, own_outs, heads, outs, cut_heads, cut_outs, end;
     Layout(int32_t head_dim, int32_t n_heads, int32_t T) {
         const size_t rows = size_t(T) * n_heads;
         size_t at = up128(decode_workspace_bytes(head_dim));
@@ -858,9 +823,8 @@ struct Layout {
         prefix = take(LORA_MAX_SEQS * 4);
         lo = take(LORA_MAX_SEQS * 4);
         lead = take(LORA_MAX_SEQS * 4);
-        shared = take(LORA_MAX_SEQS * 4);
-        started = take(size_t(T) * 4);
-        own_sums = take(rows * 8);
+        live = take((size_t(T) + 1) * 4);
+        own_sums = take(rows * 16);
         own_outs = take(rows * head_dim * 4);
         heads = take(rows * 16);
         outs = take(rows * head_dim * 4);
@@ -871,7 +835,7 @@ struct Layout {
 };
 
 template <int HD, bool E4M3>
-cudaError_t launch(const AttendArgs &a, const SharedWork &w, int32_t max_q, void *ws, cudaStream_t stream) {
+cudaError_t launch(const AttendArgs &a, const SharedWork &w, void *ws, cudaStream_t stream) {
     static std::atomic<uint64_t> seen{0};
     int sms = 0;
     cudaError_t e = prepare_kernel(attend_prefix_kernel<HD, E4M3>, PrefixConfig<HD>::kSmem, seen, &sms);
@@ -879,10 +843,20 @@ cudaError_t launch(const AttendArgs &a, const SharedWork &w, int32_t max_q, void
     e = launch_dependent(attend_prefix_kernel<HD, E4M3>, sms < kMaxGrid ? sms : kMaxGrid, kThreads,
                          PrefixConfig<HD>::kSmem, stream, a, w);
     if (e != cudaSuccess) return e;
-    if ((e = launch_attend_own(a, E4M3, max_q, w.shared, w.own_sums, w.own_outs, w.started, ws, stream)) != cudaSuccess)
+    if ((e = launch_attend_own(a, E4M3, w.groups, w.own_sums, w.own_outs, ws, stream)) != cudaSuccess)
         return e;
     return launch_dependent(attend_join_kernel<HD>, static_cast<unsigned>((int64_t(a.T) * a.n_heads + 31) / 32), 256, 0,
                             stream, a, w);
+}
+
+// Costs of the two ways, ns of one SM (measured in long calls; a cap, a bias or a window lengthen the softmax).
+Groups costs(const lora_prefix_t &prefix, int32_t tile_rows, const AttendArgs &a, bool e4m3) {
+    const bool plain = a.softcap == 0.0f && a.slopes == nullptr;
+    const int32_t two = (a.kv.head_dim == 128 ? 1750 : 1500) + (plain ? 0 : 800);
+    const int32_t bytes = a.kv.head_dim * (e4m3 ? 1 : 2);  // of k or v, a key
+    const int32_t stream = 2 * kKeys * bytes * 10 / 448;   // at 44.8 GB/s an SM
+    const int32_t own = tile_rows == 32 ? 2 * stream : tile_rows == 16 && e4m3 ? 2 * stream : stream;
+    return {prefix.group_offsets, prefix.prefix_lens, prefix.n_groups, tile_rows, prefix.mode == LORA_SHARE_ALWAYS, two * 2 / 3, two, own};
 }
 
 }  // namespace
@@ -897,14 +871,16 @@ cudaError_t launch_attend_shared(const AttendArgs &a, bool e4m3, int32_t max_q, 
     char *base = static_cast<char *>(ws);
     const auto ints = [&](size_t o) { return reinterpret_cast<int32_t *>(base + o); };
     const auto floats = [&](size_t o) { return reinterpret_cast<float *>(base + o); };
-    const SharedWork w{prefix.group_offsets, prefix.prefix_lens, prefix.n_groups,
-                       reinterpret_cast<int64_t *>(base + at.units), ints(at.prefix), ints(at.lo), ints(at.lead),
-                       ints(at.shared), ints(at.started), reinterpret_cast<float2 *>(base + at.own_sums),
-                       floats(at.own_outs), reinterpret_cast<float4 *>(base + at.heads), floats(at.outs),
+    const int64_t rows = int64_t(max_q) * a.group;
+    const int32_t tile_rows = rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
+    const Groups groups = costs(prefix, tile_rows, a, e4m3);
+    const SharedWork w{groups, reinterpret_cast<int64_t *>(base + at.units), ints(at.prefix), ints(at.lo), ints(at.lead),
+                       ints(at.live), reinterpret_cast<float4 *>(base + at.own_sums), floats(at.own_outs), own_pieces(ws),
+                       reinterpret_cast<float4 *>(base + at.heads), floats(at.outs),
                        reinterpret_cast<float4 *>(base + at.cut_heads), floats(at.cut_outs)};
     if (a.kv.head_dim == 64)
-        return e4m3 ? launch<64, true>(a, w, max_q, ws, stream) : launch<64, false>(a, w, max_q, ws, stream);
-    return e4m3 ? launch<128, true>(a, w, max_q, ws, stream) : launch<128, false>(a, w, max_q, ws, stream);
+        return e4m3 ? launch<64, true>(a, w, ws, stream) : launch<64, false>(a, w, ws, stream);
+    return e4m3 ? launch<128, true>(a, w, ws, stream) : launch<128, false>(a, w, ws, stream);
 }
 
 }  // namespace lora

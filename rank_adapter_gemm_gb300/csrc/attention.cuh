@@ -42,11 +42,19 @@ struct RequestRows {
     bool ok;
 };
 
-__device__ __forceinline__ RequestRows load_rows(const AttendArgs &a, int32_t i) {
-    const int32_t q0 = a.q_offsets[i], q1 = a.q_offsets[i + 1], len = a.kv_lens[i];
+__device__ __forceinline__ RequestRows check_request(const AttendArgs &a, int32_t q0, int32_t q1, int32_t len) {
     const bool ok = q0 >= 0 && q1 >= q0 && q1 <= a.T && len >= 0 && len <= LORA_MAX_KV_LEN &&
                     len <= (int64_t(a.width) << a.kv.page_shift);
     return {q0, ok ? q1 - q0 : 0, ok ? len : 0, ok};
+}
+
+__device__ __forceinline__ RequestRows load_rows(const AttendArgs &a, int32_t i) {
+    return check_request(a, a.q_offsets[i], a.q_offsets[i + 1], a.kv_lens[i]);
+}
+
+// Past the first-level cache, for kernels that do not begin with a wait.
+__device__ __forceinline__ RequestRows load_rows_cg(const AttendArgs &a, int32_t i) {
+    return check_request(a, __ldcg(a.q_offsets + i), __ldcg(a.q_offsets + i + 1), __ldcg(a.kv_lens + i));
 }
 
 // The kernels of this file's users are launched as programmatic dependents of the

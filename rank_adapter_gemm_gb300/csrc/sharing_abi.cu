@@ -163,6 +163,7 @@ lora_status_t lora_attend_shared(const void *q, int64_t ldq, void *out, int64_t 
                                  kv, att, err, &a)) != LORA_OK)
         return st;
     if (prefix == nullptr || prefix->n_groups < 0 || prefix->n_groups > LORA_MAX_SEQS) return LORA_ERR_INVALID_ARG;
+    if (prefix->mode != LORA_SHARE_AUTO && prefix->mode != LORA_SHARE_ALWAYS) return LORA_ERR_INVALID_ARG;
     if (prefix->n_groups > 0 && (prefix->group_offsets == nullptr || prefix->prefix_lens == nullptr))
         return LORA_ERR_INVALID_ARG;
     if (ws == nullptr || ws_bytes < lora::shared_workspace_bytes(a.kv.head_dim, a.n_heads, T, n_seq))

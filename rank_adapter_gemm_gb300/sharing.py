@@ -15,7 +15,7 @@ from typing import Optional, Sequence
 
 from . import _dev, _torch
 from . import attention as _att
-from ._lib import (LOGITS_TYPES, LORA_MAX_KV_LAYERS, LORA_MAX_SEQS, check, load, lora_attention_t, lora_kv_t,
+from ._lib import (LOGITS_TYPES, LORA_MAX_KV_LAYERS, LORA_MAX_SEQS, SHARE_MODES, check, load, lora_attention_t, lora_kv_t,
                    lora_prefix_t)
 from .attention import PagedKV, _flat, _matrix, _on, _table
 
@@ -136,7 +136,8 @@ def lora_attend_shared_workspace_bytes(att: lora_attention_t, kv: lora_kv_t, T: 
 
 
 def lora_attend_shared(q, out, q_offsets, kv_lens, block_table, group_offsets, prefix_lens, kv: lora_kv_t,
-                       att: lora_attention_t, ws, err, max_q_hint: int = 0, lse=None, stream=None) -> None:
+                       att: lora_attention_t, ws, err, max_q_hint: int = 0, lse=None, share: str = "auto",
+                       stream=None) -> None:
     A = _ready()
     n, groups = kv_lens.numel(), prefix_lens.numel()
     x, ldq, T, q_cols = _matrix(q, "q")
@@ -149,7 +150,7 @@ def lora_attend_shared(q, out, q_offsets, kv_lens, block_table, group_offsets, p
         _dev(ws, "ws")
         raise ValueError("ws must be contiguous")
     prefix = lora_prefix_t(_flat(group_offsets, "group_offsets", A._I32, groups + 1),
-                           _flat(prefix_lens, "prefix_lens", A._I32), groups)
+                           _flat(prefix_lens, "prefix_lens", A._I32), groups, SHARE_MODES[share])
     status = load().lora_attend_shared(
         x, ldq, o, ldo, _opt(lse, "lse", A._F32, T * att.n_heads), T, n, _flat(q_offsets, "q_offsets", A._I32, n + 1),
         _flat(kv_lens, "kv_lens", A._I32), table, ld, width, prefix, kv, att, max_q_hint, ws.data_ptr(),
@@ -270,8 +271,9 @@ class SharedAttention:
         self.err = torch.zeros(1, dtype=torch.int32, device=device)
 
     def run(self, q, out, q_offsets, kv_lens, block_table, group_offsets, prefix_lens, max_q_hint: int = 0,
-            kv: Optional[PagedKV] = None, lse=None, stream=None) -> None:
+            kv: Optional[PagedKV] = None, lse=None, share: str = "auto", stream=None) -> None:
         """out = attention of q's rows; requests group_offsets[g] .. group_offsets[g + 1] - 1 hold the same keys and
-        values below prefix_lens[g]; max_q_hint is an upper bound on a request's rows (0: taken as T / n_seq)."""
+        values below prefix_lens[g]; max_q_hint is an upper bound on a request's rows (0: taken as T / n_seq).
+        share: "auto" reads prefixes once where that saves time, "always" all of them."""
         lora_attend_shared(q, out, q_offsets, kv_lens, block_table, group_offsets, prefix_lens, (kv or self.kv).c,
-                           self.c, self.ws, self.err, max_q_hint, lse, stream)
+                           self.c, self.ws, self.err, max_q_hint, lse, share, stream)

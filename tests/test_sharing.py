@@ -150,7 +150,7 @@ def test_shared_refusals(L):
     att = lora_attention_t(8, 0.1, 0.0, 0, None)
     need = L.lora_attend_shared_workspace_bytes(att, kv, 4, 2)
     good = dict(q=P, ldq=1024, out=P, ldo=1024, lse=None, T=4, n=2, off=P, lens=P, table=P, ld=4, width=4,
-                prefix=lora_prefix_t(P, P, 1), kv=kv, att=att, hint=1, ws=P, bytes=need)
+                prefix=lora_prefix_t(P, P, 1, 0), kv=kv, att=att, hint=1, ws=P, bytes=need)
 
     def call(**kw):
         return lib.lora_attend_shared(*{**good, **kw}.values(), None, None)
@@ -158,8 +158,8 @@ def test_shared_refusals(L):
     for bad, status in [(dict(T=-1), 1), (dict(n=-1), 1), (dict(n=4097), 1), (dict(width=5), 1), (dict(q=None), 1),
                         (dict(out=None), 1), (dict(off=None), 1), (dict(lens=None), 1), (dict(table=None), 1),
                         (dict(ldq=1016), 1), (dict(q=P + 8), 2), (dict(ldo=1028), 2), (dict(prefix=None), 1),
-                        (dict(prefix=lora_prefix_t(None, P, 1)), 1), (dict(prefix=lora_prefix_t(P, None, 1)), 1),
-                        (dict(prefix=lora_prefix_t(P, P, -1)), 1), (dict(prefix=lora_prefix_t(P, P, 4097)), 1),
+                        (dict(prefix=lora_prefix_t(None, P, 1, 0)), 1), (dict(prefix=lora_prefix_t(P, None, 1, 0)), 1),
+                        (dict(prefix=lora_prefix_t(P, P, -1, 0)), 1), (dict(prefix=lora_prefix_t(P, P, 4097, 0)), 1), (dict(prefix=lora_prefix_t(P, P, 1, 2)), 1),
                         (dict(kv=_kv(n_pages=0)), 1), (dict(kv=_kv(head_dim=96)), 9),
                         (dict(att=lora_attention_t(7, 0.1, 0.0, 0, None)), 1),
                         (dict(att=lora_attention_t(8, math.nan, 0.0, 0, None)), 1),
@@ -723,7 +723,7 @@ class Batch:
             self.v[self.table[i, j // self.ps], j % self.ps] = vv[j]
 
     def run(self, L, softcap=0.0, window=0, slopes=None, scale=None, hint=0, prefix=None, starts=None, att=None, lens=None,
-            repeat=1):
+            repeat=1, share="always"):
         torch = _torch()
         kv = L.PagedKV(self.dk, self.dv, *self.scales)
         s = None if slopes is None else dev(slopes, torch.float32)
@@ -734,7 +734,7 @@ class Batch:
         for _ in range(repeat):
             att.run(self.dq, out, dev(off), dev(self.lens if lens is None else lens), dev(self.table),
                     dev(self.starts if starts is None else starts), dev(self.prefix if prefix is None else prefix),
-                    hint, kv=kv, lse=lse)
+                    hint, kv=kv, lse=lse, share=share)
         torch.cuda.synchronize()
         self.err = int(att.err)
         return out, lse
@@ -802,9 +802,10 @@ GROUPS = {
 def test_shared_prefix(L, groups, H, KV, hd, ps, fp8):
     b = Batch(GROUPS[groups], H, KV, hd, ps, fp8, order="head" if H == 8 else "token", alone=[(20, 1), (0, 2)],
               rows_after=3, seed=len(groups) + H)
-    out, lse = b.run(L, repeat=2)
-    b.check(out, lse)
-    assert b.err == 0
+    for share in ("always", "auto"):
+        out, lse = b.run(L, repeat=2, share=share)
+        b.check(out, lse)
+        assert b.err == 0
 
 
 @gpu
@@ -896,7 +897,7 @@ def test_shared_prefix_long_cache_and_repeats(L):
     kv = L.PagedKV(b.dk, b.dv, *b.scales)
     att = L.SharedAttention(b.n, b.rows, b.H, kv)
     args = [b.dq, torch.zeros_like(out), dev(np.concatenate([[0], np.cumsum(b.new)])), dev(b.lens), dev(b.table),
-            dev(b.starts), dev(b.prefix)]
+            dev(b.starts), dev(b.prefix), 0, None, None, "always"]
     att.run(*args)
     torch.cuda.synchronize()
     g = torch.cuda.CUDAGraph()
@@ -962,7 +963,8 @@ def test_beams_over_a_paged_cache(L, fp8):
             q = torch.empty(T, H * hd, dtype=torch.bfloat16, device="cuda")
             rope.append(x[:, i].contiguous(), q, H, kv, st.positions, st.slot_map, st.err)
             att = L.SharedAttention(len(m), T, H, kv)
-            att.run(q, out, st.q_offsets, st.kv_lens, st.block_table, dev(groups), dev(prefix), max(m))
+            att.run(q, out, st.q_offsets, st.kv_lens, st.block_table, dev(groups), dev(prefix), max(m),
+                    share="always" if i else "auto")
             torch.cuda.synchronize()
             assert int(att.err) == 0 and int(st.err) == 0
         tables.lens.copy_(st.kv_lens)
