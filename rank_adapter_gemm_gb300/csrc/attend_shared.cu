@@ -741,58 +741,88 @@ template <int HD>
 __global__ void __launch_bounds__(256) attend_join_kernel(const AttendArgs a, const SharedWork w) {
     wait_for_previous();
     const int64_t rows = int64_t(a.T) * a.n_heads, row = min(int64_t(blockIdx.x) * 32 + (threadIdx.x & 31), rows - 1);
-    const int64_t per = int64_t(a.T) * a.group, head = row / per, at = row - head * per;
-    const int32_t t = static_cast<int32_t>(at / a.group), h = static_cast<int32_t>(head * a.group + at % a.group);
+    const int64_t per = int64_t(a.T) * a.group, kv_head = row / per;
+    const int32_t of_head = static_cast<int32_t>(row - kv_head * per), t = of_head / a.group;
+    const int32_t h = static_cast<int32_t>(kv_head) * a.group + of_head % a.group;
     // (of a row that is not joined these are of another call)
     const float4 first = __ldcg(w.heads + row), own = __ldcg(w.own_sums + row);
     const bool live = w.live[1 + t] != 0 && int64_t(blockIdx.x) * 32 + (threadIdx.x & 31) < rows;
     if (w.live[0] == 0 || !live) return;
-    // where the row's other pieces lie: prefix pieces by block, own ones by warp of the decode path
-    constexpr int kDim4s = HD / 4;
+    // The row's pieces, in the order of the keys: of the prefix the first and the others, by block;
+    // its own first one and the others, by warp of the decode path.
     const int32_t tile = w.groups.tile_rows, own_size = tile * (HD + 2);
-    const int32_t c0 = __float_as_int(first.z) >> 8, c1 = c0 + __float_as_int(first.w), r = __float_as_int(first.z) & 255;
-    const int32_t w0 = __float_as_int(own.z) >> 5, w1 = w0 + __float_as_int(own.w), r1 = __float_as_int(own.z) & 31;
-    const float2 *cuts = reinterpret_cast<const float2 *>(w.cut_heads + r);
-    const float *owns = w.own_cuts + 2 * r1;
-    float top = fmaxf(own.x, first.x);
-#pragma unroll 8
-    for (int32_t c = c0; c < c1; ++c) top = fmaxf(top, __ldcg(cuts + c * 4 * kRows).x);
-#pragma unroll 8
-    for (int32_t c = w0; c < w1; ++c) top = fmaxf(top, __ldcg(owns + int64_t(c) * own_size));
-    const float ref = top == -INFINITY ? 0.0f : top;
-    constexpr int kGroups = kDim4s / 16;  // of 8 dims, a warp
+    const int32_t c0 = __float_as_int(first.z) >> 8, n0 = 1 + __float_as_int(first.w), r = __float_as_int(first.z) & 255;
+    const int32_t w0 = __float_as_int(own.z) >> 5, n = n0 + 1 + __float_as_int(own.w), r1 = __float_as_int(own.z) & 31;
+    constexpr int kBatch = 4;         // pieces whose loads are under way together
+    constexpr int kGroups = HD / 64;  // of 8 dims, a warp
     const int warp = threadIdx.x >> 5;
-    float o[kGroups][8], sum = 0.0f;
+    float o[kGroups][8], top = -INFINITY, sum = 0.0f;
 #pragma unroll
     for (int g = 0; g < kGroups; ++g)
 #pragma unroll
         for (int e = 0; e < 8; ++e) o[g][e] = 0.0f;
-    // adds a partial result whose dims 4 i lie at from + i * stride
-    const auto add = [&](float m, float l, const float *from, int64_t stride) {
-        const float f = ex2(m - ref);
-        sum = fmaf(f, l, sum);
+    for (int32_t p0 = 0; p0 < n; p0 += kBatch) {
+        float2 head[kBatch];
+        float4 x[kBatch][kGroups][2];
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+            const int32_t i = p0 + b;
+            if (i >= n) {
+                head[b] = make_float2(-INFINITY, 0.0f);
+#pragma unroll
+                for (int g = 0; g < kGroups; ++g) x[b][g][0] = x[b][g][1] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                continue;
+            }
+            const bool pre = i < n0;
+            const int32_t c = pre ? c0 + i - 1 : w0 + i - n0 - 1;
+            const float *from, *at;  // reference and sum; dims 4 i at from + i * stride
+            int64_t stride = 4 * rows;
+            if (i == 0) {
+                at = reinterpret_cast<const float *>(w.heads + row);
+                from = w.outs + row * 4;
+            } else if (i == n0) {
+                at = reinterpret_cast<const float *>(w.own_sums + row);
+                from = w.own_outs + row * 4;
+            } else if (pre) {
+                at = reinterpret_cast<const float *>(w.cut_heads + int64_t(c) * 2 * kRows + r);
+                from = w.cut_outs + int64_t(c) * 2 * kRows * HD + r * 4;
+                stride = 8 * kRows;
+            } else {
+                at = w.own_cuts + int64_t(c) * own_size + 2 * r1;
+                from = w.own_cuts + int64_t(c) * own_size + 2 * tile + r1 * 4;
+                stride = 4 * tile;
+            }
+            head[b] = __ldcg(reinterpret_cast<const float2 *>(at));
+#pragma unroll
+            for (int g = 0; g < kGroups; ++g)
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    x[b][g][e] = __ldcg(reinterpret_cast<const float4 *>(from + (2 * (g * 8 + warp) + e) * stride));
+        }
+        float now = top;
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) now = fmaxf(now, head[b].x);
+        const float ref = now == -INFINITY ? 0.0f : now, f = ex2(top - ref);
+        top = now;
+        sum *= f;
 #pragma unroll
         for (int g = 0; g < kGroups; ++g)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const float4 v = __ldcg(reinterpret_cast<const float4 *>(from + (2 * (g * 8 + warp) + e) * stride));
-                o[g][4 * e] = fmaf(f, v.x, o[g][4 * e]);
-                o[g][4 * e + 1] = fmaf(f, v.y, o[g][4 * e + 1]);
-                o[g][4 * e + 2] = fmaf(f, v.z, o[g][4 * e + 2]);
-                o[g][4 * e + 3] = fmaf(f, v.w, o[g][4 * e + 3]);
-            }
-    };
-    add(first.x, first.y, w.outs + row * 4, 4 * rows);
-#pragma unroll 4
-    for (int32_t c = c0; c < c1; ++c) {
-        const float2 part = __ldcg(cuts + c * 4 * kRows);
-        add(part.x, part.y, w.cut_outs + c * int64_t(2 * kRows * HD) + r * 4, 8 * kRows);
-    }
-    add(own.x, own.y, w.own_outs + row * 4, 4 * rows);
-#pragma unroll 4
-    for (int32_t c = w0; c < w1; ++c) {
-        const float2 part = __ldcg(reinterpret_cast<const float2 *>(owns + int64_t(c) * own_size));
-        add(part.x, part.y, w.own_cuts + int64_t(c) * own_size + 2 * tile + r1 * 4, 4 * tile);
+            for (int e = 0; e < 8; ++e) o[g][e] *= f;
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+            const float v = ex2(head[b].x - ref);
+            sum = fmaf(v, head[b].y, sum);
+#pragma unroll
+            for (int g = 0; g < kGroups; ++g)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    o[g][4 * e] = fmaf(v, x[b][g][e].x, o[g][4 * e]);
+                    o[g][4 * e + 1] = fmaf(v, x[b][g][e].y, o[g][4 * e + 1]);
+                    o[g][4 * e + 2] = fmaf(v, x[b][g][e].z, o[g][4 * e + 2]);
+                    o[g][4 * e + 3] = fmaf(v, x[b][g][e].w, o[g][4 * e + 3]);
+                }
+        }
     }
     const float inv = sum > 0.0f ? a.kv.v_scale / sum : sum == 0.0f ? 0.0f : sum;
 #pragma unroll

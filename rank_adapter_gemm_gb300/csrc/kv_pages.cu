@@ -15,7 +15,7 @@ namespace lora {
 
 namespace {
 
-constexpr int kCtas = 8, kThreads = 1024, kWarps = kThreads / 32;
+constexpr int kCtas = 16, kThreads = 1024, kWarps = kThreads / 32;
 constexpr int kSpan = 256;  // entries of a row that a warp takes at a time
 
 struct PagesArgs {
@@ -158,24 +158,23 @@ __global__ void __launch_bounds__(kThreads, 1) kv_pages_kernel(const PagesArgs a
         const int32_t len = s_have[i], pages = static_cast<int32_t>((int64_t(len) + in_page) >> a.shift);
         return FORK && (len & in_page) != 0 && s_first[s_from[i]] != i ? pages - 1 : pages;
     };
-    const int32_t spans = (s_most + kSpan - 1) / kSpan;
-    const int64_t items = int64_t(a.n_rows) * spans;
     // calls f(row of the new batch, first entry, end) for this warp's spans, spread over the cluster
     const auto each_span = [&](auto f) {
-        for (int64_t x = warp * kCtas + rank; x < items; x += kWarps * kCtas) {
-            const int32_t c = static_cast<int32_t>(x / a.n_rows), i = static_cast<int32_t>(x - int64_t(c) * a.n_rows);
-            const int32_t e0 = c * kSpan, e1 = min(entries(i), e0 + kSpan);
-            if (e0 < e1) f(i, e0, e1);
-        }
+        for (int32_t c = 0; c < s_most; c += kSpan)
+            for (int32_t i = warp * kCtas + rank; i < a.n_rows; i += kWarps * kCtas) {
+                const int32_t end = min(entries(i), c + kSpan);
+                if (c < end) f(i, c, end);
+            }
     };
+    constexpr int kEach = kSpan / 32;  // entries a lane, all of whose loads are under way together
     each_span([&](int32_t i, int32_t e0, int32_t e1) {
         const int32_t *from = a.src + s_from[i] * a.ld_src;
         int32_t *to = a.dst + i * a.ld_dst;
-        int32_t page[kSpan / 32];
+        int32_t page[kEach];
 #pragma unroll
-        for (int u = 0; u < kSpan / 32; ++u) page[u] = from[min(e0 + u * 32 + lane, e1 - 1)];
+        for (int u = 0; u < kEach; ++u) page[u] = from[min(e0 + u * 32 + lane, e1 - 1)];
 #pragma unroll
-        for (int u = 0; u < kSpan / 32; ++u) {
+        for (int u = 0; u < kEach; ++u) {
             const int32_t e = e0 + u * 32 + lane;
             if (e >= e1) break;
             if (FORK) to[e] = page[u];
@@ -193,7 +192,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_pages_kernel(const PagesArgs a
     const uint32_t slice = smem_addr(s_map + w0);
     for (int32_t v = tid; v < per / 4; v += kThreads) {
         uint4 x = make_uint4(0, 0, 0, 0);
-#pragma unroll
+#pragma unroll 8
         for (int c = 0; c < kCtas; ++c) {
             const uint4 y = ld_peer4(map_to_rank(slice + v * 16, c));
             x.x |= y.x, x.y |= y.y, x.z |= y.z, x.w |= y.w;
@@ -299,15 +298,23 @@ __global__ void __launch_bounds__(kThreads, 1) kv_pages_kernel(const PagesArgs a
         __threadfence();
         sync_cluster();  // the moves are written
         const auto moved = [&](int32_t p) {
-            if (static_cast<uint32_t>(p) >= static_cast<uint32_t>(a.n_pages) || p < used) return p;
-            const uint32_t word = word_of(p >> 5);
-            const int64_t r = rank_of(p, before_of(p >> 5) + __popc(word & ((1u << (p & 31)) - 1)));
-            return __ldcg(a.copies + 3 * r + 1);
+            const bool move = p >= used && p < a.n_pages;
+            const int32_t at = move ? p : used < a.n_pages ? used : 0;  // (no branch around the loads)
+            const uint32_t word = word_of(at >> 5);
+            const int64_t r = rank_of(at, before_of(at >> 5) + __popc(word & ((1u << (at & 31)) - 1)));
+            return move ? __ldcg(a.copies + 3 * r + 1) : p;
         };
         each_span([&](int32_t i, int32_t e0, int32_t e1) {
             const int32_t *from = a.src + s_from[i] * a.ld_src;
             int32_t *to = a.dst + i * a.ld_dst;
-            for (int32_t e = e0 + lane; e < e1; e += 32) to[e] = moved(from[e]);
+            int32_t page[kEach];
+#pragma unroll
+            for (int u = 0; u < kEach; ++u) page[u] = from[min(e0 + u * 32 + lane, e1 - 1)];
+#pragma unroll
+            for (int u = 0; u < kEach; ++u) page[u] = moved(page[u]);
+#pragma unroll
+            for (int u = 0; u < kEach; ++u)
+                if (e0 + u * 32 + lane < e1) to[e0 + u * 32 + lane] = page[u];
         });
         for (int32_t i = all; i < a.n_held; i += kCtas * kThreads) {
             const int32_t p = a.held[i];
@@ -326,7 +333,9 @@ cudaError_t launch(const PagesArgs &a, cudaStream_t stream) {
     constexpr size_t kMost = pages_smem(LORA_MAX_PAGES, LORA_MAX_SEQS, LORA_MAX_SEQS, true);
     static_assert(kMost <= 227 * 1024 - 1024, "shared memory");
     int sms = 0;
-    const cudaError_t e = prepare_kernel(kv_pages_kernel<FORK>, static_cast<int>(kMost), seen, &sms);
+    cudaError_t e = prepare_kernel(kv_pages_kernel<FORK>, static_cast<int>(kMost), seen, &sms);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(kv_pages_kernel<FORK>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute attr[2] = {};
     attr[0].id = cudaLaunchAttributeClusterDimension;

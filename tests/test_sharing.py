@@ -297,6 +297,16 @@ def test_select_equal_logits_lowest_token_first(L, keep, fp32):
 
 
 @gpu
+@pytest.mark.parametrize("keep", [5, 64])
+def test_select_equal_beams(L, keep):
+    """64 beams of the same logits and scores: more candidates reach the bound than are gathered."""
+    torch = _torch()
+    sel, y, s = run_select(L, np.zeros((2, 64, 70)), np.zeros((2, 64)), keep, torch.bfloat16)
+    assert sel.parents.tolist() == [0] * keep + [64] * keep
+    assert sel.tokens.tolist() == 2 * list(range(keep))
+
+
+@gpu
 @pytest.mark.parametrize("fp32", [False, True])
 def test_select_masks_and_numbers_out_of_range(L, fp32):
     torch = _torch()
