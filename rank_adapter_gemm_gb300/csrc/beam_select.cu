@@ -1,28 +1,30 @@
 // Selection of beam search (lora_beam_select).
 //
 // What it must read is the logits, once: HBM bounds it, with one exponential an
-// element.  A block takes kChunk neighbouring logits of a row into registers and
-// leaves what a selection can need of them: maximum, sum of exponentials, and the
-// `keep` largest.  The block that arrives last at a request joins them: the rows'
-// logarithms, then the `keep` best of all lists.
+// element.  A block takes a part of a row, in chunks that its threads hold in
+// registers, the next one loading meanwhile, and leaves what a selection can need of it:
+// maximum, sum of exponentials, and the `keep` largest.  The block that arrives last at
+// a request joins them: the rows' logarithms, then the `keep` best of all lists.
 //
-// The largest of a set are found through a bound: of 64 groups of elements, the
-// keep-th largest of the groups' maxima is one that at least `keep` elements
-// reach.  The elements that reach it, usually little more than `keep`, in few threads,
-// are gathered and ranked by counting; where many are equal they are taken one by one.
-// All keys of a chunk differ (value, then the lower token first), so order never
-// depends on timing.
+// The largest of a part are found through a bound: of 64 groups of threads, the keep-th
+// largest of the groups' maxima over the first chunk is one that at least `keep` elements
+// reach.  The elements that reach it, of all chunks a few times `keep`, in few threads,
+// are gathered and ranked by counting; where there are too many (equal or rising ones)
+// they are taken one by one.  All keys differ (value, then the lower token first), so order
+// never depends on timing.  Between the first chunk and the last no thread waits for another.
 //
-// A chunk's sum is taken in fp32 (32 terms a thread, then a tree); a row's, and all
+// A thread's sum is taken in fp32 against its own running maximum; a row's, and all
 // comparisons of candidates, in 64 bits: scores of different beams meet there, and a
 // rounding to fp32 would decide between candidates.
+#include <algorithm>
+
 #include "attend.cuh"
 
 namespace lora {
 
 namespace {
 
-constexpr int kThreads = 256, kEach = 32, kChunk = kThreads * kEach;
+constexpr int kThreads = 256;
 constexpr int kGroups = 64;   // groups of 4 neighbouring threads
 constexpr int kGather = 1024;  // gathered keys at most; more take the slow way
 
@@ -34,10 +36,10 @@ struct SelectArgs {
     int32_t *parents, *tokens, *out_ended;
     float *out_scores;
     int32_t *counters;   // a request
-    float2 *sums;        // maximum and sum of each row's chunks
-    float *values;       // the largest of each chunk
+    float2 *sums;        // maximum and sum of each row's parts
+    float *values;       // the largest of each part, by request and rank
     int32_t *ids;        // and their tokens
-    int32_t beams, vocab, keep, eos, chunks;
+    int32_t beams, vocab, keep, eos, parts, part_chunks;
 };
 
 // Order of fp32 values as unsigned numbers; -0 counts as 0.
@@ -53,51 +55,44 @@ __device__ __forceinline__ uint64_t ordered(double x) {
     return (u >> 63) ? ~u : u | (uint64_t(1) << 63);
 }
 
-// A thread's elements in registers.  Keys of elements: the value, then the lower index first; 0 is
-// below all.  Indexes within a chunk are below 2^16.
+// A thread's elements of a chunk in 16 registers.
 struct Bf16Logits {
-    using Key = uint32_t;
-    static constexpr int kVec = 8, kWords = kEach / 2;
+    static constexpr int kVec = 8, kEach = 32;
     static constexpr uint32_t kNone = 0xff80ff80u;  // -inf
-    __device__ static float value(const uint32_t (&w)[kWords], int e) {
+    __device__ static float value(const uint32_t (&w)[16], int e) {
         return (e & 1) ? bf16hi_to_f32(w[e / 2]) : bf16lo_to_f32(w[e / 2]);
     }
     __device__ static uint32_t element(const void *p, int64_t i) { return static_cast<const uint16_t *>(p)[i]; }
-    // the elements of a vector that are there, one by one
+    // element e of a vector
     __device__ static void put(uint32_t *w, int e, uint32_t v) {
         w[e / 2] = __byte_perm(w[e / 2], v, (e & 1) ? 0x5410 : 0x3254);
     }
-    __device__ static float top(const uint32_t (&w)[kWords]) {
+    __device__ static float top(const uint32_t (&w)[16]) {
         uint32_t m = w[0];
 #pragma unroll
-        for (int i = 1; i < kWords; ++i) asm("max.bf16x2 %0, %1, %2;" : "=r"(m) : "r"(m), "r"(w[i]));
+        for (int i = 1; i < 16; ++i) asm("max.bf16x2 %0, %1, %2;" : "=r"(m) : "r"(m), "r"(w[i]));
         return fmaxf(bf16lo_to_f32(m), bf16hi_to_f32(m));
     }
-    __device__ static Key key(float x, int32_t i) {
-        return (ordered(x) & 0xffff0000u) | static_cast<uint32_t>(0xffff - i);
-    }
-    // (a negative value's ordered form is its complement: the low half was ones)
-    __device__ static float of_key(Key k) { return from_ordered((k & 0x80000000u) ? k & 0xffff0000u : k | 0xffffu); }
 };
 
 struct Fp32Logits {
-    using Key = uint64_t;
-    static constexpr int kVec = 4, kWords = kEach;
+    static constexpr int kVec = 4, kEach = 16;
     static constexpr uint32_t kNone = 0xff800000u;
-    __device__ static float value(const uint32_t (&w)[kWords], int e) { return __uint_as_float(w[e]); }
+    __device__ static float value(const uint32_t (&w)[16], int e) { return __uint_as_float(w[e]); }
     __device__ static uint32_t element(const void *p, int64_t i) { return static_cast<const uint32_t *>(p)[i]; }
     __device__ static void put(uint32_t *w, int e, uint32_t v) { w[e] = v; }
-    __device__ static float top(const uint32_t (&w)[kWords]) {
+    __device__ static float top(const uint32_t (&w)[16]) {
         float m = __uint_as_float(w[0]);
 #pragma unroll
-        for (int i = 1; i < kWords; ++i) m = fmaxf(m, __uint_as_float(w[i]));
+        for (int i = 1; i < 16; ++i) m = fmaxf(m, __uint_as_float(w[i]));
         return m;
     }
-    __device__ static Key key(float x, int32_t i) {
-        return (static_cast<uint64_t>(ordered(x)) << 32) | static_cast<uint32_t>(0xffff - i);
-    }
-    __device__ static float of_key(Key k) { return from_ordered(static_cast<uint32_t>(k >> 32)); }
 };
+
+// An element's key: the value, then the lower token first; 0 is below all.
+__device__ __forceinline__ uint64_t key_of(float x, int32_t token) {
+    return (static_cast<uint64_t>(ordered(x)) << 32) | ~static_cast<uint32_t>(token);
+}
 
 template <class K>
 __device__ __forceinline__ K shfl_max(K v, int o) {
@@ -105,18 +100,19 @@ __device__ __forceinline__ K shfl_max(K v, int o) {
     return u > v ? u : v;
 }
 
-// The keep-th largest of 64 group values (s_group), by counting; by the whole block, with a
-// barrier in front and behind.  Groups without elements hold the least value.
-template <class K>
-__device__ __forceinline__ K bound_of(const K *s_group, K *s_bound, int32_t keep) {
+// The keep-th largest of 64 group values (s_group, 16-byte aligned), by counting; by the whole
+// block, with a barrier in front and behind.  Groups without elements hold the least value.
+__device__ __forceinline__ uint32_t bound_of(const uint32_t *s_group, uint32_t *s_bound, int32_t keep) {
     __syncthreads();
     if (threadIdx.x < kGroups) {
-        const K me = s_group[threadIdx.x];
+        const int tid = threadIdx.x;
+        const uint32_t me = s_group[tid];
         int above = 0;
-#pragma unroll 16
-        for (int j = 0; j < kGroups; ++j) {
-            const K other = s_group[j];
-            above += other > me || (other == me && j < static_cast<int>(threadIdx.x));
+#pragma unroll
+        for (int j = 0; j < kGroups; j += 4) {
+            const uint4 v = *reinterpret_cast<const uint4 *>(s_group + j);
+            above += (v.x > me || (v.x == me && j < tid)) + (v.y > me || (v.y == me && j + 1 < tid)) +
+                     (v.z > me || (v.z == me && j + 2 < tid)) + (v.w > me || (v.w == me && j + 3 < tid));
         }
         if (above == keep - 1) *s_bound = me;
     }
@@ -131,64 +127,88 @@ struct Candidate {
     __device__ bool before(const Candidate &o) const { return key > o.key || (key == o.key && id < o.id); }
 };
 
+// top + ln sum, in 64 bits but for the logarithm of a number near 1 (2^-25).
+__device__ __forceinline__ double log_sum(float top, float sum) {
+    const int32_t bits = __float_as_int(sum), e = ((bits - 0x3f400000) >> 23);  // sum / 2^e in [3/4, 3/2)
+    if (!(sum > 0.0f && sum < INFINITY)) return top + logf(sum);  // (a sum of terms up to 1 is 0, NaN or at least 1)
+    return top + (e * 0.693147180559945309417 + static_cast<double>(logf(__int_as_float(bits - (e << 23)))));
+}
+
 // The keep best of the request's lists, in order, to the outputs.
 __device__ void join_request(const SelectArgs &a, int32_t r) {
+    constexpr int kHeld = 4;                   // candidates a thread holds
     __shared__ double s_base[LORA_MAX_BEAMS];  // score minus the logarithm; NaN: no candidates
     __shared__ bool s_ended[LORA_MAX_BEAMS];   // (outputs may take the inputs' place)
-    __shared__ uint64_t s_group[kGroups], s_bound;
+    __shared__ __align__(16) uint32_t s_group[kGroups];
+    __shared__ uint32_t s_bound;
     __shared__ Candidate s_found[kGather], s_best[kThreads / 32];
     __shared__ int32_t s_n;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int32_t lists = a.beams * a.chunks;
-    const int64_t list0 = int64_t(r) * lists;
+    const int32_t lists = a.beams * a.parts, all = lists * a.keep;
+    const int64_t list0 = int64_t(r) * all;
+    // the first candidates, loaded beside what makes values of them
+    float value[kHeld];
+    int32_t token[kHeld];
+#pragma unroll
+    for (int h = 0; h < kHeld; ++h) {
+        const int32_t i = tid + h * kThreads;
+        value[h] = i < all ? __ldcg(a.values + list0 + i) : -INFINITY;
+        token[h] = i < all ? __ldcg(a.ids + list0 + i) : -1;
+    }
     if (tid == 0) s_n = 0;
     for (int32_t b = warp; b < a.beams; b += kThreads / 32) {
         const int32_t row = r * a.beams + b;
-        const float2 *sums = a.sums + int64_t(row) * a.chunks;
-        float2 mine = lane < a.chunks ? __ldcg(sums + lane) : make_float2(-INFINITY, 0.0f);
+        const float2 *sums = a.sums + int64_t(row) * a.parts;
+        float2 mine = lane < a.parts ? __ldcg(sums + lane) : make_float2(-INFINITY, 0.0f);
         const float score = lane == 0 ? a.scores[row] : 0.0f;
         const bool ended = lane == 0 && a.ended != nullptr && a.ended[row] != 0;
         float top = mine.x;
-        for (int32_t c = lane + 32; c < a.chunks; c += 32) top = fmaxf(top, __ldcg(sums + c).x);
+        for (int32_t c = lane + 32; c < a.parts; c += 32) top = fmaxf(top, __ldcg(sums + c).x);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        double sum = 0.0;
-        for (int32_t c = lane; c < a.chunks; c += 32) {
+        float sum = 0.0f;
+        for (int32_t c = lane; c < a.parts; c += 32) {
             if (c != lane) mine = __ldcg(sums + c);
-            // (a chunk without a number above -inf has sum 0; a NaN or +inf makes the sum NaN)
-            if (mine.y != 0.0f) sum += mine.y * exp(static_cast<double>(mine.x) - top);
+            // (a part without a number above -inf has sum 0; a NaN or +inf makes the sum NaN)
+            if (mine.y != 0.0f) sum += mine.y * ex2((mine.x - top) * kLog2e);
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
         if (lane == 0) {
-            double base = ended ? score : score - (top + log(sum));
+            double base = ended ? score : score - log_sum(top, sum);
             if (!(base > -INFINITY && base < INFINITY)) base = NAN;
             s_base[b] = base;
             s_ended[b] = ended;
         }
     }
     __syncthreads();
-    // candidate k of a list; key 0: none
-    const auto candidate = [&](int32_t list, int32_t k) {
-        const int64_t at = (list0 + list) * a.keep + k;
-        const int32_t b = list / a.chunks, token = __ldcg(a.ids + at);
-        const double v = s_base[b] + __ldcg(a.values + at);
-        return Candidate{token >= 0 && v > -INFINITY ? ordered(v) : 0, static_cast<uint32_t>(b) * a.vocab + token};
+    // candidate i of the request; key 0: none
+    const auto made = [&](int32_t i, float x, int32_t id) {
+        const int32_t b = i < all ? i % lists / a.parts : 0;
+        const double v = s_base[b] + x;
+        return Candidate{id >= 0 && v > -INFINITY ? ordered(v) : 0, static_cast<uint32_t>(b) * a.vocab + id};
     };
-    // a bound that `keep` candidates reach: of 64 groups of lists, their firsts
+    const auto loaded = [&](int32_t i) { return made(i, __ldcg(a.values + list0 + i), __ldcg(a.ids + list0 + i)); };
+    Candidate held[kHeld];
     uint64_t best = 0;
-    for (int32_t l = tid; l < lists; l += kThreads) best = max(best, candidate(l, 0).key);
-    best = shfl_max(shfl_max(best, 1), 2);
-    if ((lane & 3) == 0) s_group[tid >> 2] = best;
-    const uint64_t bound = max(bound_of(s_group, &s_bound, a.keep), uint64_t(1));
-    for (int32_t l = tid; l < lists; l += kThreads) {
-        for (int32_t k = 0; k < a.keep; ++k) {
-            const Candidate c = candidate(l, k);
-            if (c.key < bound) break;  // the list falls
-            const int32_t at = atomicAdd(&s_n, 1);
-            if (at < kGather) s_found[at] = c;
-        }
+#pragma unroll
+    for (int h = 0; h < kHeld; ++h) {
+        held[h] = made(tid + h * kThreads, value[h], token[h]);
+        best = max(best, held[h].key);
     }
+    for (int32_t i = tid + kHeld * kThreads; i < all; i += kThreads) best = max(best, loaded(i).key);
+    // a bound that `keep` candidates reach: of 64 groups of threads, their best (its upper half)
+    const uint32_t group = shfl_max(shfl_max(static_cast<uint32_t>(best >> 32), 1), 2);
+    if ((lane & 3) == 0) s_group[tid >> 2] = group;
+    const uint64_t bound = max(uint64_t(bound_of(s_group, &s_bound, a.keep)) << 32, uint64_t(1));
+    const auto gather = [&](const Candidate &c) {
+        if (c.key < bound) return;
+        const int32_t at = atomicAdd(&s_n, 1);
+        if (at < kGather) s_found[at] = c;
+    };
+#pragma unroll
+    for (int h = 0; h < kHeld; ++h) gather(held[h]);
+    for (int32_t i = tid + kHeld * kThreads; i < all; i += kThreads) gather(loaded(i));
     __syncthreads();
     const int32_t found = s_n;
     const auto put = [&](int32_t k, const Candidate &c) {
@@ -217,12 +237,10 @@ __device__ void join_request(const SelectArgs &a, int32_t r) {
     Candidate last{~uint64_t(0), 0};
     for (int32_t k = 0; k < a.keep; ++k) {
         Candidate now{0, 0xffffffffu};
-        for (int32_t l = tid; l < lists; l += kThreads)
-            for (int32_t j = 0; j < a.keep; ++j) {
-                const Candidate c = candidate(l, j);
-                if (c.key < bound) break;
-                if (last.before(c) && c.before(now)) now = c;
-            }
+        for (int32_t i = tid; i < all; i += kThreads) {
+            const Candidate c = loaded(i);
+            if (c.key >= bound && last.before(c) && c.before(now)) now = c;
+        }
         const auto better = [&](uint64_t key, uint32_t id) {
             const Candidate c{key, id};
             if (c.before(now)) now = c;
@@ -241,148 +259,163 @@ __device__ void join_request(const SelectArgs &a, int32_t r) {
 
 template <class T>
 __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const SelectArgs a) {
-    using Key = typename T::Key;
-    constexpr int kVec = T::kVec, kVecs = kEach / kVec, kSize = 16 / kVec;
-    __shared__ uint32_t s_top[kThreads / 32], s_group[kGroups], s_bound;
+    constexpr int kVec = T::kVec, kEach = T::kEach, kVecs = kEach / kVec, kSize = 16 / kVec, kChunk = kThreads * kEach;
+    __shared__ __align__(16) uint32_t s_group[kGroups];
+    __shared__ uint32_t s_top[kThreads / 32], s_bound;
     __shared__ float s_sum[kThreads / 32];
-    __shared__ Key s_keys[kGather], s_best[kThreads / 32];
+    __shared__ uint64_t s_keys[kGather], s_best[kThreads / 32];
     __shared__ int32_t s_n;
     __shared__ bool s_last;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int32_t row = static_cast<int32_t>(blockIdx.x / a.chunks), chunk = static_cast<int32_t>(blockIdx.x % a.chunks);
+    const int32_t row = static_cast<int32_t>(blockIdx.x / a.parts), part = static_cast<int32_t>(blockIdx.x % a.parts);
     const int32_t r = row / a.beams;
     if (tid == 0) s_n = 0;
     wait_for_previous();
     const bool ended = a.ended != nullptr && a.ended[row] != 0;
-    const int64_t list = (int64_t(row) * a.chunks + chunk) * a.keep;
+    // where this part's k-th largest goes: lists stand side by side, so that neighbours are of one rank
+    const int32_t lists = a.beams * a.parts;
+    const int64_t list = int64_t(r) * lists * a.keep + (row - r * a.beams) * a.parts + part;
+    const auto place = [&](int32_t k) { return list + int64_t(k) * lists; };
     if (ended) {
         for (int32_t k = tid; k < a.keep; k += kThreads) {
-            const bool here = chunk == 0 && k == 0;
-            a.values[list + k] = here ? 0.0f : -INFINITY;
-            a.ids[list + k] = here ? a.eos : -1;
+            const bool here = part == 0 && k == 0;
+            a.values[place(k)] = here ? 0.0f : -INFINITY;
+            a.ids[place(k)] = here ? a.eos : -1;
         }
-        if (tid == 0) a.sums[int64_t(row) * a.chunks + chunk] = make_float2(0.0f, 1.0f);
+        if (tid == 0) a.sums[int64_t(row) * a.parts + part] = make_float2(0.0f, 1.0f);
     } else {
-        const int32_t v0 = chunk * kChunk, n = min(kChunk, a.vocab - v0);
-        const unsigned char *base = static_cast<const unsigned char *>(a.logits) + (row * a.ld + v0) * kSize;
-        // thread t's vector u holds elements (u * 256 + t) * kVec - skew ..: whole vectors lie on 16
-        // bytes.  A skewed chunk's last elements go one each to the first threads' last places, which
-        // hold elements before the chunk or none (u = 0, t = 0: `skew` elements of 8 or 4).
+        // Vectors lie on 16 bytes: the row's elements are counted from `skew` elements before it.
+        // Thread t's vector u of chunk c holds tokens (c kChunk + (u 256 + t) kVec - skew) ..
+        const unsigned char *base = static_cast<const unsigned char *>(a.logits) + row * a.ld * kSize;
         const int skew = static_cast<int>((reinterpret_cast<uintptr_t>(base) & 15) / kSize);
-        uint32_t w[T::kWords];
+        const int32_t c0 = part * a.part_chunks;
+        const int32_t c1 = min(c0 + a.part_chunks, static_cast<int32_t>((int64_t(a.vocab) + skew + kChunk - 1) / kChunk));
+        const auto load = [&](int32_t c, uint32_t (&w)[16]) {
 #pragma unroll
-        for (int u = 0; u < kVecs; ++u) {
-            const int32_t i = (u * kThreads + tid) * kVec - skew;
-            uint32_t *to = w + u * (T::kWords / kVecs);
-            if (i >= 0 && i + kVec <= n) {
-                const uint4 v = ldg_cg(base + int64_t(i) * kSize);
-                to[0] = v.x, to[1] = v.y, to[2] = v.z, to[3] = v.w;
-            } else {
-                to[0] = to[1] = to[2] = to[3] = T::kNone;
-                if (i + kVec > 0 && i < n) {
+            for (int u = 0; u < kVecs; ++u) {
+                const int32_t i = c * kChunk + (u * kThreads + tid) * kVec - skew;
+                uint32_t *to = w + 4 * u;
+                if (i >= 0 && i + kVec <= a.vocab) {
+                    const uint4 v = ldg_cg(base + int64_t(i) * kSize);
+                    to[0] = v.x, to[1] = v.y, to[2] = v.z, to[3] = v.w;
+                } else {
+                    to[0] = to[1] = to[2] = to[3] = T::kNone;
+                    if (i + kVec > 0 && i < a.vocab) {
 #pragma unroll
-                    for (int e = 0; e < kVec; ++e)
-                        if (i + e >= 0 && i + e < n) T::put(to, e, T::element(base, i + e));
+                        for (int e = 0; e < kVec; ++e)
+                            if (i + e >= 0 && i + e < a.vocab) T::put(to, e, T::element(base, i + e));
+                    }
                 }
             }
-        }
-        // thread 0's first vector has room for the elements that the skew pushes out at the end
-        const int32_t tail = kChunk - skew;  // their first index
-        if (tid == 0 && tail < n) {
-#pragma unroll
-            for (int e = 0; e < kVec; ++e)
-                if (e < skew && tail + e < n) T::put(w, e, T::element(base, tail + e));
-        }
-        const auto index_of = [&](int e) {
-            const int32_t i = (e / kVec * kThreads + tid) * kVec - skew + e % kVec;
-            return i < 0 ? i + kChunk : i;
         };
-        const float mine = T::top(w);
-        const uint32_t order = ordered(mine);
-        uint32_t best = shfl_max(shfl_max(order, 1), 2);
-        if ((lane & 3) == 0) s_group[tid >> 2] = best;
-        best = __reduce_max_sync(0xffffffffu, best);
-        if (lane == 0) s_top[warp] = best;
-        const float bound = from_ordered(bound_of(s_group, &s_bound, a.keep));
-        best = s_top[0];
+        const auto token_of = [&](int32_t c, int e) {
+            return c * kChunk + (e / kVec * kThreads + tid) * kVec - skew + e % kVec;
+        };
+        uint32_t w[16], next[16];
+        if (c0 < c1) load(c0, w);
+        float m = -INFINITY, sum = 0.0f, bound = INFINITY;  // of this thread: its maximum, its terms against that
+        for (int32_t c = c0; c < c1; ++c) {
+            if (c + 1 < c1) load(c + 1, next);
+            const float top = T::top(w);
+            if (c == c0) {
+                const uint32_t best = shfl_max(shfl_max(ordered(top), 1), 2);
+                if ((lane & 3) == 0) s_group[tid >> 2] = best;
+                bound = from_ordered(bound_of(s_group, &s_bound, a.keep));
+            }
+            if (top > m) {
+                if (m > -INFINITY) sum *= ex2((m - top) * kLog2e);
+                m = top;
+            }
+            const float ref = m == -INFINITY ? 0.0f : m;
+            const uint64_t by2 = pack2(kLog2e, kLog2e), ref2 = pack2(-ref, -ref);
+            uint64_t sums[2] = {0, 0};
 #pragma unroll
-        for (int i = 1; i < kThreads / 32; ++i) best = max(best, s_top[i]);
-        const float top = from_ordered(best), ref = top == -INFINITY ? 0.0f : top;
-        const uint64_t by2 = pack2(kLog2e, kLog2e), ref2 = pack2(-ref, -ref);
-        uint64_t sums[2] = {0, 0};
+            for (int e = 0; e < kEach; e += 2) {
+                // the difference first: it is exact near the maximum, where the terms count
+                float d0, d1;
+                unpack2(mul2(add2(pack2(T::value(w, e), T::value(w, e + 1)), ref2), by2), d0, d1);
+                sums[e / 2 & 1] = add2(sums[e / 2 & 1], pack2(ex2(d0), ex2(d1)));
+            }
+            float even, odd;
+            unpack2(add2(sums[0], sums[1]), even, odd);
+            sum += even + odd;
+            // few threads have an element that reaches the bound
+            if (top >= bound && top > -INFINITY) {
 #pragma unroll
-        for (int e = 0; e < kEach; e += 2) {
-            // the difference first: it is exact near the maximum, where the terms count
-            float d0, d1;
-            unpack2(mul2(add2(pack2(T::value(w, e), T::value(w, e + 1)), ref2), by2), d0, d1);
-            sums[e / 2 & 1] = add2(sums[e / 2 & 1], pack2(ex2(d0), ex2(d1)));
+                for (int e = 0; e < kEach; ++e) {
+                    const float x = T::value(w, e);
+                    if (x >= bound && x > -INFINITY) {
+                        const int32_t at = atomicAdd(&s_n, 1);
+                        if (at < kGather) s_keys[at] = key_of(x, token_of(c, e));
+                    }
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 16; ++i) w[i] = next[i];
         }
-        float sum, odd;
-        unpack2(add2(sums[0], sums[1]), sum, odd);
-        sum += odd;
+        // the block's maximum and sum
+        uint32_t best = __reduce_max_sync(0xffffffffu, ordered(m));
+        if (lane == 0) s_top[warp] = best;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kThreads / 32; ++i) best = max(best, s_top[i]);
+        const float all_top = from_ordered(best);
+        if (m > -INFINITY) sum *= ex2((m - all_top) * kLog2e);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
         if (lane == 0) s_sum[warp] = sum;
-        // few threads have an element that reaches the bound
-        if (mine >= bound && mine > -INFINITY) {
-#pragma unroll
-            for (int e = 0; e < kEach; ++e) {
-                const float x = T::value(w, e);
-                if (x >= bound && x > -INFINITY) {
-                    const int32_t at = atomicAdd(&s_n, 1);
-                    if (at < kGather) s_keys[at] = T::key(x, index_of(e));
-                }
-            }
-        }
         __syncthreads();
         if (tid == 0) {
             float all = 0.0f;
             for (int i = 0; i < kThreads / 32; ++i) all += s_sum[i];
-            a.sums[int64_t(row) * a.chunks + chunk] = make_float2(top, all);
+            a.sums[int64_t(row) * a.parts + part] = make_float2(all_top, all);
         }
         const int32_t found = s_n;
-        const auto put = [&](int32_t k, Key key) {
-            a.values[list + k] = T::of_key(key);
-            a.ids[list + k] = v0 + 0xffff - static_cast<int32_t>(key & 0xffffu);
+        const auto put = [&](int32_t k, uint64_t key) {
+            a.values[place(k)] = from_ordered(static_cast<uint32_t>(key >> 32));
+            a.ids[place(k)] = static_cast<int32_t>(~static_cast<uint32_t>(key));
         };
         if (found <= kGather) {
             for (int32_t i = tid; i < found; i += kThreads) {
-                const Key me = s_keys[i];
+                const uint64_t me = s_keys[i];
                 int32_t above = 0;
                 for (int32_t j = 0; j < found; ++j) above += s_keys[j] > me;
                 if (above < a.keep) put(above, me);
             }
         } else {
             // one after the other: the largest below the last one
-            Key last = ~Key(0);
+            uint64_t last = ~uint64_t(0);
             for (int32_t k = 0; k < a.keep; ++k) {
-                Key now = 0;
+                uint64_t now = 0;
+                for (int32_t c = c0; c < c1; ++c) {
+                    load(c, w);
 #pragma unroll
-                for (int e = 0; e < kEach; ++e) {
-                    const float x = T::value(w, e);
-                    const Key key = x > -INFINITY ? T::key(x, index_of(e)) : 0;
-                    if (key < last && key > now) now = key;
+                    for (int e = 0; e < kEach; ++e) {
+                        const float x = T::value(w, e);
+                        const uint64_t key = x > -INFINITY ? key_of(x, token_of(c, e)) : 0;
+                        if (key < last && key > now) now = key;
+                    }
                 }
 #pragma unroll
                 for (int o = 16; o > 0; o >>= 1) now = shfl_max(now, o);
                 __syncthreads();
                 if (lane == 0) s_best[warp] = now;
                 __syncthreads();
-                for (int i = 0; i < kThreads / 32; ++i) now = s_best[i] > now ? s_best[i] : now;
+                for (int i = 0; i < kThreads / 32; ++i) now = max(now, s_best[i]);
                 last = now;
                 if (tid == 0) put(k, now);
             }
         }
         for (int32_t k = min(found, a.keep) + tid; k < a.keep; k += kThreads) {
-            a.values[list + k] = -INFINITY;
-            a.ids[list + k] = -1;
+            a.values[place(k)] = -INFINITY;
+            a.ids[place(k)] = -1;
         }
     }
     // the last block of the request joins its lists
     __threadfence();
     __syncthreads();
     if (tid == 0) {
-        const int32_t all = a.beams * a.chunks;
+        const int32_t all = a.beams * a.parts;
         s_last = atomicAdd(a.counters + r, 1) == all - 1;
         if (s_last) a.counters[r] = 0;
     }
@@ -392,7 +425,17 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const SelectAr
     join_request(a, r);
 }
 
-int32_t chunks_of(int32_t vocab) { return (vocab + kChunk - 1) / kChunk; }
+// Chunks of a row, at any alignment.
+int32_t chunks_of(int32_t vocab, bool fp32) {
+    const int32_t chunk = kThreads * (fp32 ? Fp32Logits::kEach : Bf16Logits::kEach);
+    return static_cast<int32_t>((int64_t(vocab) + 7 + chunk - 1) / chunk);
+}
+// Parts of a row: as many as fill the GPU's places for blocks once (4 an SM), a chunk at least.
+constexpr int32_t kPlaces = 4 * 152;
+int32_t parts_of(int32_t rows, int32_t chunks) {
+    const int32_t parts = std::max(1, std::min(chunks, kPlaces / rows)), each = (chunks + parts - 1) / parts;
+    return (chunks + each - 1) / each;
+}
 size_t up128(size_t b) { return (b + 127) & ~size_t(127); }
 
 // Their place does not depend on the call, so calls of other sizes find them as they were.
@@ -400,20 +443,22 @@ constexpr size_t kCounters = size_t(LORA_MAX_SEQS) * 4;
 
 }  // namespace
 
-// Counters (a request), then sums (a chunk of a row), values and tokens (`keep` a chunk).
+// Counters (a request), then sums (a part of a row), values and tokens (`keep` a part).
 size_t beam_select_workspace_bytes(int32_t n_req, int32_t beams, int32_t keep, int32_t vocab) {
-    const size_t lists = size_t(n_req) * beams * chunks_of(vocab);
+    const int32_t rows = std::max(1, n_req * beams);
+    const size_t lists = size_t(n_req) * beams * parts_of(rows, chunks_of(vocab, true));
     return kCounters + up128(lists * 8) + 2 * up128(lists * keep * 4);
 }
 
 cudaError_t launch_beam_select(const void *logits, int64_t ld, bool fp32, int32_t n_req, int32_t beams, int32_t vocab,
                                int32_t keep, const float *scores, const int32_t *ended, int32_t eos, int32_t *parents,
                                int32_t *tokens, float *out_scores, int32_t *out_ended, void *ws, cudaStream_t stream) {
-    const int32_t chunks = chunks_of(vocab);
-    const size_t lists = size_t(n_req) * beams * chunks;
+    const int32_t chunks = chunks_of(vocab, fp32), parts = parts_of(n_req * beams, chunks);
+    const int32_t part_chunks = (chunks + parts - 1) / parts;
+    const size_t lists = size_t(n_req) * beams * parts;
     char *at = static_cast<char *>(ws);
     SelectArgs a{logits, ld, scores, ended, parents, tokens, out_ended, out_scores, reinterpret_cast<int32_t *>(at),
-                 nullptr, nullptr, nullptr, beams, vocab, keep, eos, chunks};
+                 nullptr, nullptr, nullptr, beams, vocab, keep, eos, parts, part_chunks};
     at += kCounters;
     a.sums = reinterpret_cast<float2 *>(at);
     at += up128(lists * 8);

@@ -31,13 +31,6 @@ __device__ __forceinline__ uint32_t ld_peer(uint32_t addr) {
     return v;
 }
 
-__device__ __forceinline__ uint4 ld_peer4(uint32_t addr) {
-    uint4 v;
-    asm volatile("ld.shared::cluster.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "r"(addr) : "memory");
-    return v;
-}
-
 // (Threads may arrive one by one: the loops before it end at different times.)
 __device__ __forceinline__ void sync_cluster() {
     asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
@@ -159,9 +152,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv_pages_kernel(const PagesArgs a
         return FORK && (len & in_page) != 0 && s_first[s_from[i]] != i ? pages - 1 : pages;
     };
     // calls f(row of the new batch, first entry, end) for this warp's spans, spread over the cluster
+    constexpr int32_t kTakers = kWarps * kCtas;
+    const int32_t id = warp * kCtas + rank;
     const auto each_span = [&](auto f) {
         for (int32_t c = 0; c < s_most; c += kSpan)
-            for (int32_t i = warp * kCtas + rank; i < a.n_rows; i += kWarps * kCtas) {
+            // (spans of neighbouring rows, then of their next entries, go round the warps)
+            for (int32_t i = ((id - c / kSpan * (a.n_rows % kTakers)) % kTakers + kTakers) % kTakers; i < a.n_rows;
+                 i += kTakers) {
                 const int32_t end = min(entries(i), c + kSpan);
                 if (c < end) f(i, c, end);
             }
@@ -189,16 +186,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv_pages_kernel(const PagesArgs a
 
     // ---- the bitmaps joined: this block's slice of the pages, free ones as ones ------
     const int32_t w0 = static_cast<int32_t>(rank) * per;
-    const uint32_t slice = smem_addr(s_map + w0);
-    for (int32_t v = tid; v < per / 4; v += kThreads) {
-        uint4 x = make_uint4(0, 0, 0, 0);
-#pragma unroll 8
-        for (int c = 0; c < kCtas; ++c) {
-            const uint4 y = ld_peer4(map_to_rank(slice + v * 16, c));
-            x.x |= y.x, x.y |= y.y, x.z |= y.z, x.w |= y.w;
-        }
+    for (int32_t v = tid; v < per; v += kThreads) {
+        const uint32_t at = smem_addr(s_map + w0 + v);
+        uint32_t x[kCtas], all = 0;
+#pragma unroll
+        for (int c = 0; c < kCtas; ++c) x[c] = ld_peer(map_to_rank(at, c));
+#pragma unroll
+        for (int c = 0; c < kCtas; ++c) all |= x[c];
         // (other blocks still read this slice of the bitmap: the joined words go elsewhere)
-        reinterpret_cast<uint4 *>(s_before)[v] = x;
+        s_before[v] = static_cast<int32_t>(all);
     }
     sync_cluster();
     const int32_t each = (per + kThreads - 1) / kThreads;  // words a thread
@@ -216,13 +212,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_pages_kernel(const PagesArgs a
     int32_t at = scan_block(mine, s_warp, &slice_free);
     if (tid == 0) s_free[0] = slice_free;
     sync_cluster();
-    int32_t free_before = 0, n_free = 0;  // in the slices before this one; in all
-#pragma unroll
-    for (int c = 0; c < kCtas; ++c) {
-        const int32_t f = static_cast<int32_t>(ld_peer(map_to_rank(smem_addr(s_free), c)));
-        if (c < static_cast<int>(rank)) free_before += f;
-        n_free += f;
-    }
+    // free pages in the slices before this one, and in all: a lane a block
+    const int32_t theirs = lane < kCtas ? static_cast<int32_t>(ld_peer(map_to_rank(smem_addr(s_free), lane))) : 0;
+    const int32_t free_before = __reduce_add_sync(0xffffffffu, lane < static_cast<int>(rank) ? theirs : 0);
+    int32_t n_free = __reduce_add_sync(0xffffffffu, theirs);
     at += free_before;
     for (int32_t j = 0; j < each; ++j) {
         const int32_t w = tid * each + j;
@@ -262,48 +255,46 @@ __global__ void __launch_bounds__(kThreads, 1) kv_pages_kernel(const PagesArgs a
         n_free = max(0, n_free - jobs);
     } else {
         // ---- pages in use at or past their number: each to the free page of its rank --
+        // The list of free pages, written last, holds on the way: in front, by rank, the pages that
+        // are moved to (fewer than are in use); at page p >= used, where it moves.
         const int32_t used = a.n_pages - n_free;
-        // free pages before page p of any slice
-        const auto word_of = [&](int32_t w) {
-            return ld_peer(map_to_rank(smem_addr(s_map + w), static_cast<uint32_t>(w / per)));
-        };
-        const auto before_of = [&](int32_t w) {
-            return static_cast<int32_t>(ld_peer(map_to_rank(smem_addr(s_before + w % per),
-                                                            static_cast<uint32_t>(w / per))));
-        };
         sync_cluster();  // every slice's words and counts are there
-        int32_t n_moves = 0;
-        if (used < a.n_pages) {
-            n_moves = before_of(used >> 5) + __popc(word_of(used >> 5) & ((1u << (used & 31)) - 1));
-        }
-        // a page at or past `used` that is in use: its rank among those
-        const auto rank_of = [&](int32_t p, int32_t free_before_p) { return p - free_before_p - (used - n_moves); };
-        for (int32_t w = warp; w < per; w += kWarps) {
-            const uint32_t word = s_map[w0 + w];
-            const int32_t page = (w0 + w) * 32 + lane, f = s_before[w] + __popc(word & ((1u << lane) - 1));
-            const bool is_free = (word >> lane) & 1;
-            if (page >= a.n_pages) continue;
-            if (page < used && is_free) a.copies[3 * int64_t(f) + 1] = page;
-            if (page >= used && !is_free) {
-                const int64_t r = rank_of(page, f);
-                a.copies[3 * r] = page;
-                a.copies[3 * r + 2] = in_page + 1;
-            }
+        int32_t n_moves = 0;  // free pages below `used`
+        if (n_free > 0) {
+            const int32_t w = used >> 5, owner = w / per;
+            const uint32_t word = ld_peer(map_to_rank(smem_addr(s_map + w), owner));
+            n_moves = static_cast<int32_t>(ld_peer(map_to_rank(smem_addr(s_before + w % per), owner))) +
+                      __popc(word & ((1u << (used & 31)) - 1));
         }
         const int32_t all = static_cast<int32_t>(rank) * kThreads + tid;
-        for (int64_t i = n_moves + all; i < a.n_pages / 2; i += kCtas * kThreads)
-            for (int e = 0; e < 3; ++e) a.copies[3 * i + e] = e < 2 ? -1 : 0;
-        for (int32_t p = all; p < n_free; p += kCtas * kThreads) a.free_pages[p] = used + p;
+        // calls f(page, free, free pages before it) for the pages of this slice
+        const auto each_page = [&](auto f) {
+            for (int32_t w = warp; w < per; w += kWarps) {
+                const uint32_t word = s_map[w0 + w];
+                const int32_t page = (w0 + w) * 32 + lane;
+                if (page < a.n_pages) f(page, (word >> lane) & 1, s_before[w] + __popc(word & ((1u << lane) - 1)));
+            }
+        };
+        each_page([&](int32_t page, bool is_free, int32_t f) {
+            if (page < used && is_free) a.free_pages[f] = page;
+        });
+        for (int64_t i = 3 * int64_t(n_moves) + all; i < 3 * int64_t(a.n_pages / 2); i += kCtas * kThreads)
+            a.copies[i] = i % 3 < 2 ? -1 : 0;
         if (all == 0) a.n_copies[0] = n_moves;
         __threadfence();
-        sync_cluster();  // the moves are written
-        const auto moved = [&](int32_t p) {
-            const bool move = p >= used && p < a.n_pages;
-            const int32_t at = move ? p : used < a.n_pages ? used : 0;  // (no branch around the loads)
-            const uint32_t word = word_of(at >> 5);
-            const int64_t r = rank_of(at, before_of(at >> 5) + __popc(word & ((1u << (at & 31)) - 1)));
-            return move ? __ldcg(a.copies + 3 * r + 1) : p;
-        };
+        sync_cluster();
+        each_page([&](int32_t page, bool is_free, int32_t f) {
+            if (page < used || is_free) return;
+            const int64_t i = page - f - (used - n_moves);  // its rank among those
+            const int32_t to = __ldcg(a.free_pages + i);
+            a.free_pages[page] = to;
+            a.copies[3 * i] = page;
+            a.copies[3 * i + 1] = to;
+            a.copies[3 * i + 2] = in_page + 1;
+        });
+        __threadfence();
+        sync_cluster();
+        const auto moved = [&](int32_t p) { return p >= used && p < a.n_pages ? __ldcg(a.free_pages + p) : p; };
         each_span([&](int32_t i, int32_t e0, int32_t e1) {
             const int32_t *from = a.src + s_from[i] * a.ld_src;
             int32_t *to = a.dst + i * a.ld_dst;
@@ -320,6 +311,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_pages_kernel(const PagesArgs a
             const int32_t p = a.held[i];
             a.dst_held[i] = p == -1 ? -1 : moved(p);
         }
+        sync_cluster();  // the ways have been read
+        for (int32_t p = all; p < n_free; p += kCtas * kThreads) a.free_pages[p] = used + p;
     }
     for (int32_t p = n_free + static_cast<int32_t>(rank) * kThreads + tid; p < a.n_pages; p += kCtas * kThreads)
         a.free_pages[p] = -1;
