@@ -39,7 +39,7 @@ struct SelectArgs {
     float2 *sums;        // maximum and sum of each row's parts
     float *values;       // the largest of each part, by request and rank
     int32_t *ids;        // and their tokens
-    int32_t beams, vocab, keep, eos, parts, part_chunks;
+    int32_t beams, vocab, keep, eos, parts, part_vecs;
 };
 
 // Order of fp32 values as unsigned numbers; -0 counts as 0.
@@ -51,8 +51,9 @@ __device__ __forceinline__ float from_ordered(uint32_t u) {
     return __uint_as_float((u & 0x80000000u) ? u ^ 0x80000000u : ~u);
 }
 __device__ __forceinline__ uint64_t ordered(double x) {
-    const uint64_t u = static_cast<uint64_t>(__double_as_longlong(x + 0.0));
-    return (u >> 63) ? ~u : u | (uint64_t(1) << 63);
+    constexpr uint64_t kSign = uint64_t(1) << 63;
+    const uint64_t u = static_cast<uint64_t>(__double_as_longlong(x));  // (64-bit arithmetic is slow here)
+    return u <= kSign ? u | kSign : ~u;
 }
 
 // A thread's elements of a chunk in 16 registers.
@@ -136,8 +137,9 @@ __device__ __forceinline__ double log_sum(float top, float sum) {
 
 // The keep best of the request's lists, in order, to the outputs.
 __device__ void join_request(const SelectArgs &a, int32_t r) {
-    constexpr int kHeld = 4;                   // candidates a thread holds
-    __shared__ double s_base[LORA_MAX_BEAMS];  // score minus the logarithm; NaN: no candidates
+    constexpr long long kNoBase = 0x7ff8000000000000;
+    constexpr int kHeld = 8;                   // candidates a thread holds
+    __shared__ double s_base[LORA_MAX_BEAMS];  // score minus the logarithm; kNoBase: no candidates
     __shared__ bool s_ended[LORA_MAX_BEAMS];   // (outputs may take the inputs' place)
     __shared__ __align__(16) uint32_t s_group[kGroups];
     __shared__ uint32_t s_bound;
@@ -176,7 +178,7 @@ __device__ void join_request(const SelectArgs &a, int32_t r) {
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
         if (lane == 0) {
             double base = ended ? score : score - log_sum(top, sum);
-            if (!(base > -INFINITY && base < INFINITY)) base = NAN;
+            if (!(base > -INFINITY && base < INFINITY)) base = __longlong_as_double(kNoBase);
             s_base[b] = base;
             s_ended[b] = ended;
         }
@@ -184,18 +186,22 @@ __device__ void join_request(const SelectArgs &a, int32_t r) {
     __syncthreads();
     // candidate i of the request; key 0: none
     const auto made = [&](int32_t i, float x, int32_t id) {
-        const int32_t b = i < all ? i % lists / a.parts : 0;
-        const double v = s_base[b] + x;
-        return Candidate{id >= 0 && v > -INFINITY ? ordered(v) : 0, static_cast<uint32_t>(b) * a.vocab + id};
+        const int32_t b = i % lists / a.parts;
+        const double base = s_base[b];
+        const bool there = id >= 0 && x > -INFINITY && __double_as_longlong(base) != kNoBase;
+        return Candidate{there ? ordered(base + x) : 0, static_cast<uint32_t>(b) * a.vocab + id};
     };
     const auto loaded = [&](int32_t i) { return made(i, __ldcg(a.values + list0 + i), __ldcg(a.ids + list0 + i)); };
     Candidate held[kHeld];
     uint64_t best = 0;
 #pragma unroll
     for (int h = 0; h < kHeld; ++h) {
+        held[h].key = 0;
+        if (h * kThreads >= all) continue;
         held[h] = made(tid + h * kThreads, value[h], token[h]);
         best = max(best, held[h].key);
     }
+#pragma unroll 4
     for (int32_t i = tid + kHeld * kThreads; i < all; i += kThreads) best = max(best, loaded(i).key);
     // a bound that `keep` candidates reach: of 64 groups of threads, their best (its upper half)
     const uint32_t group = shfl_max(shfl_max(static_cast<uint32_t>(best >> 32), 1), 2);
@@ -207,7 +213,9 @@ __device__ void join_request(const SelectArgs &a, int32_t r) {
         if (at < kGather) s_found[at] = c;
     };
 #pragma unroll
-    for (int h = 0; h < kHeld; ++h) gather(held[h]);
+    for (int h = 0; h < kHeld; ++h)
+        if (h * kThreads < all) gather(held[h]);
+#pragma unroll 4
     for (int32_t i = tid + kHeld * kThreads; i < all; i += kThreads) gather(loaded(i));
     __syncthreads();
     const int32_t found = s_n;
@@ -259,7 +267,7 @@ __device__ void join_request(const SelectArgs &a, int32_t r) {
 
 template <class T>
 __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const SelectArgs a) {
-    constexpr int kVec = T::kVec, kEach = T::kEach, kVecs = kEach / kVec, kSize = 16 / kVec, kChunk = kThreads * kEach;
+    constexpr int kVec = T::kVec, kEach = T::kEach, kVecs = kEach / kVec, kSize = 16 / kVec;
     __shared__ __align__(16) uint32_t s_group[kGroups];
     __shared__ uint32_t s_top[kThreads / 32], s_bound;
     __shared__ float s_sum[kThreads / 32];
@@ -284,23 +292,24 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const SelectAr
         }
         if (tid == 0) a.sums[int64_t(row) * a.parts + part] = make_float2(0.0f, 1.0f);
     } else {
-        // Vectors lie on 16 bytes: the row's elements are counted from `skew` elements before it.
-        // Thread t's vector u of chunk c holds tokens (c kChunk + (u 256 + t) kVec - skew) ..
+        // Vectors lie on 16 bytes: the row's elements are counted from `skew` elements before it.  The
+        // part's vectors start at v0; thread t's vector u of chunk c is v0 + c kChunkVecs + u 256 + t.
         const unsigned char *base = static_cast<const unsigned char *>(a.logits) + row * a.ld * kSize;
         const int skew = static_cast<int>((reinterpret_cast<uintptr_t>(base) & 15) / kSize);
-        const int32_t c0 = part * a.part_chunks;
-        const int32_t c1 = min(c0 + a.part_chunks, static_cast<int32_t>((int64_t(a.vocab) + skew + kChunk - 1) / kChunk));
+        constexpr int kChunkVecs = kThreads * kVecs;
+        const int32_t v0 = part * a.part_vecs, v1 = min(v0 + a.part_vecs, (a.vocab + skew + kVec - 1) / kVec);
+        const int32_t chunks = (v1 - v0 + kChunkVecs - 1) / kChunkVecs;
         const auto load = [&](int32_t c, uint32_t (&w)[16]) {
 #pragma unroll
             for (int u = 0; u < kVecs; ++u) {
-                const int32_t i = c * kChunk + (u * kThreads + tid) * kVec - skew;
+                const int32_t v = v0 + c * kChunkVecs + u * kThreads + tid, i = v * kVec - skew;
                 uint32_t *to = w + 4 * u;
-                if (i >= 0 && i + kVec <= a.vocab) {
-                    const uint4 v = ldg_cg(base + int64_t(i) * kSize);
-                    to[0] = v.x, to[1] = v.y, to[2] = v.z, to[3] = v.w;
+                if (v < v1 && i >= 0 && i + kVec <= a.vocab) {
+                    const uint4 x = ldg_cg(base + int64_t(i) * kSize);
+                    to[0] = x.x, to[1] = x.y, to[2] = x.z, to[3] = x.w;
                 } else {
                     to[0] = to[1] = to[2] = to[3] = T::kNone;
-                    if (i + kVec > 0 && i < a.vocab) {
+                    if (v < v1) {
 #pragma unroll
                         for (int e = 0; e < kVec; ++e)
                             if (i + e >= 0 && i + e < a.vocab) T::put(to, e, T::element(base, i + e));
@@ -309,15 +318,15 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const SelectAr
             }
         };
         const auto token_of = [&](int32_t c, int e) {
-            return c * kChunk + (e / kVec * kThreads + tid) * kVec - skew + e % kVec;
+            return (v0 + c * kChunkVecs + e / kVec * kThreads + tid) * kVec - skew + e % kVec;
         };
         uint32_t w[16], next[16];
-        if (c0 < c1) load(c0, w);
+        if (chunks > 0) load(0, w);
         float m = -INFINITY, sum = 0.0f, bound = INFINITY;  // of this thread: its maximum, its terms against that
-        for (int32_t c = c0; c < c1; ++c) {
-            if (c + 1 < c1) load(c + 1, next);
+        for (int32_t c = 0; c < chunks; ++c) {
+            if (c + 1 < chunks) load(c + 1, next);
             const float top = T::top(w);
-            if (c == c0) {
+            if (c == 0) {
                 const uint32_t best = shfl_max(shfl_max(ordered(top), 1), 2);
                 if ((lane & 3) == 0) s_group[tid >> 2] = best;
                 bound = from_ordered(bound_of(s_group, &s_bound, a.keep));
@@ -387,7 +396,7 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const SelectAr
             uint64_t last = ~uint64_t(0);
             for (int32_t k = 0; k < a.keep; ++k) {
                 uint64_t now = 0;
-                for (int32_t c = c0; c < c1; ++c) {
+                for (int32_t c = 0; c < chunks; ++c) {
                     load(c, w);
 #pragma unroll
                     for (int e = 0; e < kEach; ++e) {
@@ -425,16 +434,19 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const SelectAr
     join_request(a, r);
 }
 
-// Chunks of a row, at any alignment.
-int32_t chunks_of(int32_t vocab, bool fp32) {
-    const int32_t chunk = kThreads * (fp32 ? Fp32Logits::kEach : Bf16Logits::kEach);
-    return static_cast<int32_t>((int64_t(vocab) + 7 + chunk - 1) / chunk);
-}
-// Parts of a row: as many as fill the GPU's places for blocks once (4 an SM), a chunk at least.
+// Vectors of a row, at any alignment, and its parts: as many as fill the GPU's places for
+// blocks once (4 an SM), of equal size, a chunk at least.  32 x 4 rows of 128,256: 4 parts 19.5
+// us, 2 23.0, 8 20.5, 16 (a chunk each) 23.9; 4 x 16 fp32 rows of 131,072: 9 parts 26.3, 4 26.5, 38 52.
 constexpr int32_t kPlaces = 4 * 152;
-int32_t parts_of(int32_t rows, int32_t chunks) {
-    const int32_t parts = std::max(1, std::min(chunks, kPlaces / rows)), each = (chunks + parts - 1) / parts;
-    return (chunks + each - 1) / each;
+struct Parts {
+    int32_t parts, vecs;
+};
+Parts parts_of(int32_t rows, int32_t vocab, bool fp32) {
+    const int32_t vec = fp32 ? Fp32Logits::kVec : Bf16Logits::kVec;
+    const int32_t chunk = kThreads * (fp32 ? Fp32Logits::kEach : Bf16Logits::kEach) / vec;
+    const int32_t vecs = (vocab + 2 * vec - 2) / vec, chunks = (vecs + chunk - 1) / chunk;
+    const int32_t parts = std::max(1, std::min(chunks, kPlaces / rows));
+    return {parts, (vecs + parts - 1) / parts};
 }
 size_t up128(size_t b) { return (b + 127) & ~size_t(127); }
 
@@ -446,19 +458,18 @@ constexpr size_t kCounters = size_t(LORA_MAX_SEQS) * 4;
 // Counters (a request), then sums (a part of a row), values and tokens (`keep` a part).
 size_t beam_select_workspace_bytes(int32_t n_req, int32_t beams, int32_t keep, int32_t vocab) {
     const int32_t rows = std::max(1, n_req * beams);
-    const size_t lists = size_t(n_req) * beams * parts_of(rows, chunks_of(vocab, true));
+    const size_t lists = size_t(n_req) * beams * parts_of(rows, vocab, true).parts;  // (bf16 rows have no more)
     return kCounters + up128(lists * 8) + 2 * up128(lists * keep * 4);
 }
 
 cudaError_t launch_beam_select(const void *logits, int64_t ld, bool fp32, int32_t n_req, int32_t beams, int32_t vocab,
                                int32_t keep, const float *scores, const int32_t *ended, int32_t eos, int32_t *parents,
                                int32_t *tokens, float *out_scores, int32_t *out_ended, void *ws, cudaStream_t stream) {
-    const int32_t chunks = chunks_of(vocab, fp32), parts = parts_of(n_req * beams, chunks);
-    const int32_t part_chunks = (chunks + parts - 1) / parts;
-    const size_t lists = size_t(n_req) * beams * parts;
+    const Parts p = parts_of(n_req * beams, vocab, fp32);
+    const size_t lists = size_t(n_req) * beams * p.parts;
     char *at = static_cast<char *>(ws);
     SelectArgs a{logits, ld, scores, ended, parents, tokens, out_ended, out_scores, reinterpret_cast<int32_t *>(at),
-                 nullptr, nullptr, nullptr, beams, vocab, keep, eos, parts, part_chunks};
+                 nullptr, nullptr, nullptr, beams, vocab, keep, eos, p.parts, p.vecs};
     at += kCounters;
     a.sums = reinterpret_cast<float2 *>(at);
     at += up128(lists * 8);
