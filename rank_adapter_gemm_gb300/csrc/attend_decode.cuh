@@ -125,6 +125,7 @@ struct OwnRows {
     Groups groups;
     float4 *sums;
     float *outs;
+    const int32_t *blocks;  // the prefix kernel's word on how many blocks take part, 0 until it is there
 };
 
 struct DecodeRows : RequestRows {
@@ -357,6 +358,12 @@ attend_decode_kernel(const AttendArgs a, float *parts, int32_t *counters, int pr
         // plan gives them, this kernel's on the others.
         asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
         __shared__ int64_t s_sum[4 * NW];
+        // (blocks without a part, which start when the prefix kernel's end, leave at once)
+        const int32_t known = __ldcg(own.blocks);
+        if (__syncthreads_and(known > 0 && static_cast<int32_t>(blockIdx.x) >= known)) {
+            end_own<SHARED>();
+            return;
+        }
         bool bad;
         const GroupPlan plan(reinterpret_cast<int32_t *>(smem + 2 * pref_bytes), own.groups.n_groups, a.n_seq);
         grid = plan_groups<NT>(a, own.groups, plan, s_sum, grid, false, &bad).own;

@@ -4,9 +4,9 @@
 namespace lora {
 
 // The other pieces of rows are left in ws, behind the counters: see OwnRows.
-cudaError_t launch_attend_own(const AttendArgs &a, bool e4m3, const Groups &groups, float4 *sums, float *outs, void *ws,
-                              cudaStream_t stream) {
-    return pick_decode<true>(a, e4m3, groups.tile_rows, OwnRows{groups, sums, outs}, ws, stream);
+cudaError_t launch_attend_own(const AttendArgs &a, bool e4m3, const Groups &groups, float4 *sums, float *outs,
+                              const int32_t *blocks, void *ws, cudaStream_t stream) {
+    return pick_decode<true>(a, e4m3, groups.tile_rows, OwnRows{groups, sums, outs, blocks}, ws, stream);
 }
 
 const float *own_pieces(const void *ws) { return reinterpret_cast<const float *>(static_cast<const char *>(ws) + 1024); }

@@ -29,8 +29,8 @@
 namespace lora {
 
 size_t decode_workspace_bytes(int32_t head_dim);
-cudaError_t launch_attend_own(const AttendArgs &a, bool e4m3, const Groups &groups, float4 *sums, float *outs, void *ws,
-                              cudaStream_t stream);
+cudaError_t launch_attend_own(const AttendArgs &a, bool e4m3, const Groups &groups, float4 *sums, float *outs,
+                              const int32_t *blocks, void *ws, cudaStream_t stream);
 const float *own_pieces(const void *ws);
 
 namespace {
@@ -63,6 +63,7 @@ struct SharedWork {
     Groups groups;
     int64_t *units;               // by group: steps (and openings) before it, n_groups + 1
     int32_t *prefix, *lo, *lead;  // by group, of its plan
+    int32_t *own_blocks;          // that take part in the own keys; 0 between calls
     int32_t *live;                // whether anything is shared; then by token, whether its request shares
     float4 *own_sums;             // of a row over its own keys, see OwnRows
     float *own_outs;
@@ -88,8 +89,16 @@ struct Item {
     bool any;                        // none: the work is done
 };
 
-// The lists of the call's groups in global memory, by the whole block; returns all units.
-__device__ int64_t list_groups(const AttendArgs &a, const SharedWork &w, const GroupPlan &p, int64_t *s_sum) {
+// The group that a block's share begins in, and the units before it.
+struct First {
+    int64_t before;
+    int32_t group;
+};
+
+// The lists of the call's groups in global memory, by the whole block, and where its share (of
+// all units over `blocks`) begins; returns all units.
+__device__ int64_t list_groups(const AttendArgs &a, const SharedWork &w, const GroupPlan &p, int64_t *s_sum,
+                               int32_t blocks, First *s_first) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int32_t n = w.groups.n_groups;
     const int32_t per = (n + kThreads - 1) / kThreads, g0 = min(n, tid * per), g1 = min(n, g0 + per);
@@ -108,12 +117,15 @@ __device__ int64_t list_groups(const AttendArgs &a, const SharedWork &w, const G
         if (i < warp) run += s_sum[i];
         total += s_sum[i];
     }
+    const int64_t share = (total + blocks - 1) / blocks, x0 = blockIdx.x * share;
     for (int32_t g = g0; g < g1; ++g) {
+        const int64_t units = prefix_units(a, p, g);
+        if (run <= x0 && x0 < run + units) *s_first = {run, g};
         w.units[g] = run;
         w.prefix[g] = p.prefix[g];
         w.lo[g] = p.lo[g];
         w.lead[g] = p.lead[g];
-        run += prefix_units(a, p, g);
+        run += units;
     }
     if (tid == 0) w.units[n] = total;
     return total;
@@ -178,18 +190,25 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefix_kernel(const Attend
     const uint32_t q_base = (tc::smem_u32(smem_raw) + 1023) & ~1023u;  // q tiles of kQ pieces, then the ring
     const uint32_t ring = q_base + 2 * C::kQ * C::kTileB;
 
+    __shared__ First s_first;
     wait_for_previous();
-    int32_t blocks;
-    int64_t total;
-    {
-        const GroupPlan plan(reinterpret_cast<int32_t *>(smem_raw), w.groups.n_groups, a.n_seq);  // (the ring's place)
-        bool bad;
-        blocks = plan_groups<kThreads>(a, w.groups, plan, s_sum, gridDim.x, blockIdx.x == 0, &bad).prefix;
-        if (blockIdx.x == 0 && tid == 0) w.live[0] = blocks > 0;
-        // blocks without a share leave their SM to the next kernel (whole blocks: nothing is allocated yet)
-        if (static_cast<int32_t>(blockIdx.x) >= blocks) return;
-        total = list_groups(a, w, plan, s_sum);
+    if (warp == 12) tc::tmem_alloc(&s_tmem, 512);
+    const GroupPlan plan(reinterpret_cast<int32_t *>(smem_raw), w.groups.n_groups, a.n_seq);  // (the ring's place)
+    bool bad;
+    const Blocks counts = plan_groups<kThreads>(a, w.groups, plan, s_sum, gridDim.x, blockIdx.x == 0, &bad);
+    const int32_t blocks = counts.prefix;
+    if (blockIdx.x == 0 && tid == 0) {
+        w.live[0] = blocks > 0;
+        w.own_blocks[0] = counts.own;
     }
+    // blocks without a share leave their SM to the next kernel
+    if (static_cast<int32_t>(blockIdx.x) >= blocks) {
+        __syncthreads();
+        tc::fence_after_sync();
+        if (warp == 12) tc::tmem_dealloc(s_tmem, 512);
+        return;
+    }
+    const int64_t total = list_groups(a, w, plan, s_sum, blocks, &s_first);
     const int64_t share = (total + blocks - 1) / blocks;
     const int64_t x0 = min(total, blockIdx.x * share), x1 = min(total, x0 + share);
     if (tid == 0) {
@@ -215,7 +234,6 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefix_kernel(const Attend
         tc::mbar_init(&bar.done, 1);
         tc::mbar_init_fence();
     }
-    if (warp == 12) tc::tmem_alloc(&s_tmem, 512);
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
@@ -504,6 +522,32 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefix_kernel(const Attend
             int64_t x = x0;
             int32_t g = 0, rest = 0;  // rest: steps of the last piece still to be handed out
             Item it{};
+            // the piece of group g (whose units begin at `before`) that x lies in; x goes on to the next
+            const auto open = [&](int64_t before, int32_t lo, int32_t end, int32_t lead, int32_t q0, int32_t q1) {
+                const int32_t steps = prefix_steps(lo, end);
+                const int64_t rows = int64_t(q1 - q0) * a.group, tiles = (rows + 2 * kRows - 1) / (2 * kRows);
+                const int64_t i = (x - before) / (steps + kPrefixOpen), head = i / tiles, tile = i - head * tiles;
+                const int64_t begin = before + i * (steps + kPrefixOpen) + kPrefixOpen;  // its first step
+                const int64_t from = max(x, begin), to = min(x1, begin + steps);
+                x = begin + steps;
+                if (from >= to) return;  // only the opening lies in this share
+                it.lead = lead;
+                it.head = static_cast<int32_t>(head);
+                it.q0 = q0;
+                it.row0 = static_cast<int32_t>(tile * 2 * kRows);
+                it.rows = static_cast<int32_t>(min(int64_t(2 * kRows), rows - tile * 2 * kRows));
+                it.lo = lo;
+                it.end = end;
+                rest = static_cast<int32_t>(to - from);
+                it.key0 = (lo & ~(kKeys - 1)) + static_cast<int32_t>(from - begin) * kKeys;
+                it.cut = from == begin ? 0 : 1;
+                it.first_cut = static_cast<int32_t>(blockIdx.x) + 1;
+                it.cuts = static_cast<int32_t>((begin + steps - 1) / share - from / share);
+                it.first = true;
+                it.any = true;
+                it.steps = min(rest, kSegment);
+                it.key0 += (rest - it.steps) * kKeys;
+            };
             for (int32_t k = 0;; ++k) {
                 if (rest > 0) {
                     it.steps = min(rest, kSegment);
@@ -511,35 +555,17 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefix_kernel(const Attend
                     it.first = false;
                 } else {
                     it.any = false;
-                    while (x < x1) {
-                        if (k == 0 || w.units[g + 1] <= x) g = last_at_most(w.units, w.groups.n_groups + 1, x);
+                    if (k == 0 && x < x1) {
+                        // the first one from the plan, in shared memory until its copies begin
+                        g = s_first.group;
+                        open(s_first.before, plan.lo[g], plan.prefix[g], plan.lead[g], plan.rows[plan.offsets[g]],
+                             plan.rows[plan.offsets[g + 1]]);
+                    }
+                    while (!it.any && x < x1) {
                         // (of groups that begin at x the last is the one with units)
-                        const int32_t lo = w.lo[g], end = w.prefix[g], steps = prefix_steps(lo, end);
-                        const int32_t q0 = a.q_offsets[w.groups.offsets[g]], q1 = a.q_offsets[w.groups.offsets[g + 1]];
-                        const int64_t rows = int64_t(q1 - q0) * a.group, tiles = (rows + 2 * kRows - 1) / (2 * kRows);
-                        const int64_t i = (x - w.units[g]) / (steps + kPrefixOpen), head = i / tiles, tile = i - head * tiles;
-                        const int64_t begin = w.units[g] + i * (steps + kPrefixOpen) + kPrefixOpen;  // its first step
-                        const int64_t from = max(x, begin), to = min(x1, begin + steps);
-                        x = begin + steps;
-                        if (from >= to) continue;  // only the opening lies in this share
-                        it.lead = w.lead[g];
-                        it.head = static_cast<int32_t>(head);
-                        it.q0 = q0;
-                        it.row0 = static_cast<int32_t>(tile * 2 * kRows);
-                        it.rows = static_cast<int32_t>(min(int64_t(2 * kRows), rows - tile * 2 * kRows));
-                        it.lo = lo;
-                        it.end = end;
-                        // steps count from the segment's last keys: neighbouring pieces are neighbouring keys
-                        rest = static_cast<int32_t>(to - from);
-                        it.key0 = (lo & ~(kKeys - 1)) + static_cast<int32_t>(from - begin) * kKeys;
-                        it.cut = from == begin ? 0 : 1;
-                        it.first_cut = static_cast<int32_t>(blockIdx.x) + 1;
-                        it.cuts = static_cast<int32_t>((begin + steps - 1) / share - from / share);
-                        it.first = true;
-                        it.any = true;
-                        it.steps = min(rest, kSegment);
-                        it.key0 += (rest - it.steps) * kKeys;
-                        break;
+                        if (w.units[g + 1] <= x) g = last_at_most(w.units, w.groups.n_groups + 1, x);
+                        open(w.units[g], w.lo[g], w.prefix[g], w.lead[g], a.q_offsets[w.groups.offsets[g]],
+                             a.q_offsets[w.groups.offsets[g + 1]]);
                     }
                 }
                 rest -= it.any ? it.steps : 0;
@@ -747,7 +773,9 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const AttendArgs a, co
     // (of a row that is not joined these are of another call)
     const float4 first = __ldcg(w.heads + row), own = __ldcg(w.own_sums + row);
     const bool live = w.live[1 + t] != 0 && int64_t(blockIdx.x) * 32 + (threadIdx.x & 31) < rows;
-    if (w.live[0] == 0 || !live) return;
+    const bool any = w.live[0] != 0;
+    if (blockIdx.x == 0 && threadIdx.x == 0) w.own_blocks[0] = 0;
+    if (!any || !live) return;
     // The row's pieces, in the order of the keys: of the prefix the first and the others, by block;
     // its own first one and the others, by warp of the decode path.
     const int32_t tile = w.groups.tile_rows, own_size = tile * (HD + 2);
@@ -838,6 +866,10 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const AttendArgs a, co
 
 size_t up128(size_t b) { return (b + 127) & ~size_t(127); }
 
+// The word that has to be 0 when a call begins: behind the decode path's counters, at a place
+// that does not depend on the call.
+constexpr size_t kOwnBlocks = 1020;
+
 // The parts of a call's workspace behind the decode path's.  Nothing in them outlives a call.
 struct Layout {
     size_t units, prefix, lo, lead, live, own_sums, own_outs, heads, outs, cut_heads, cut_outs, end;
@@ -873,20 +905,28 @@ cudaError_t launch(const AttendArgs &a, const SharedWork &w, void *ws, cudaStrea
     e = launch_dependent(attend_prefix_kernel<HD, E4M3>, sms < kMaxGrid ? sms : kMaxGrid, kThreads,
                          PrefixConfig<HD>::kSmem, stream, a, w);
     if (e != cudaSuccess) return e;
-    if ((e = launch_attend_own(a, E4M3, w.groups, w.own_sums, w.own_outs, ws, stream)) != cudaSuccess)
+    if ((e = launch_attend_own(a, E4M3, w.groups, w.own_sums, w.own_outs, w.own_blocks, ws, stream)) != cudaSuccess)
         return e;
     return launch_dependent(attend_join_kernel<HD>, static_cast<unsigned>((int64_t(a.T) * a.n_heads + 31) / 32), 256, 0,
                             stream, a, w);
 }
 
-// Costs of the two ways, ns of one SM (measured in long calls; a cap, a bias or a window lengthen the softmax).
+// Costs of the two ways, ns of one SM, from calls long enough to show them; a cap or a bias
+// lengthens the softmax of both.  Shared always / never, us, 32/8 heads of 128 over bf16, one row a
+// request: 4 requests behind 2,000 tokens 24.8 / 23.5, behind 30,000 51 / 74; 64 behind 500 26 / 35; 8
+// groups of 4 behind 8,000 75 / 127; 64 of 2 behind 1,000 110 / 90, behind 4,000 220 / 325; over e4m3
+// 32 of 4 behind 2,000 111 / 109, 8 of 16 53 / 98.
 Groups costs(const lora_prefix_t &prefix, int32_t tile_rows, const AttendArgs &a, bool e4m3) {
-    const bool plain = a.softcap == 0.0f && a.slopes == nullptr;
-    const int32_t two = (a.kv.head_dim == 128 ? 1750 : 1500) + (plain ? 0 : 800);
-    const int32_t bytes = a.kv.head_dim * (e4m3 ? 1 : 2);  // of k or v, a key
-    const int32_t stream = 2 * kKeys * bytes * 10 / 448;   // at 44.8 GB/s an SM
-    const int32_t own = tile_rows == 32 ? 2 * stream : tile_rows == 16 && e4m3 ? 2 * stream : stream;
-    return {prefix.group_offsets, prefix.prefix_lens, prefix.n_groups, tile_rows, prefix.mode == LORA_SHARE_ALWAYS, two * 2 / 3, two, own};
+    const bool wide = a.kv.head_dim == 128;
+    const int32_t more = a.softcap == 0.0f && a.slopes == nullptr ? 0 : 800;
+    const int32_t one = (e4m3 ? wide ? 2300 : 1650 : wide ? 1650 : 1400) + more;
+    const int32_t two = one + (wide ? 550 : 400) + more;
+    int32_t own = e4m3 ? wide ? 800 : 450 : wide ? 700 : 400;
+    const int32_t first = e4m3 ? 0 : wide ? 750 : 350;
+    if (tile_rows == 16) own = own * 5 / 4;
+    if (tile_rows == 32) own = own * 5 / 2;
+    return {prefix.group_offsets, prefix.prefix_lens, prefix.n_groups, tile_rows, prefix.mode == LORA_SHARE_ALWAYS,
+            one, two, own + more / 4, first, e4m3 ? 128 : 64};
 }
 
 }  // namespace
@@ -905,7 +945,7 @@ cudaError_t launch_attend_shared(const AttendArgs &a, bool e4m3, int32_t max_q, 
     const int32_t tile_rows = rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
     const Groups groups = costs(prefix, tile_rows, a, e4m3);
     const SharedWork w{groups, reinterpret_cast<int64_t *>(base + at.units), ints(at.prefix), ints(at.lo), ints(at.lead),
-                       ints(at.live), reinterpret_cast<float4 *>(base + at.own_sums), floats(at.own_outs), own_pieces(ws),
+                       ints(kOwnBlocks), ints(at.live), reinterpret_cast<float4 *>(base + at.own_sums), floats(at.own_outs), own_pieces(ws),
                        reinterpret_cast<float4 *>(base + at.heads), floats(at.outs),
                        reinterpret_cast<float4 *>(base + at.cut_heads), floats(at.cut_outs)};
     if (a.kv.head_dim == 64)

@@ -10,21 +10,25 @@ constexpr int kPrefixRows = 256, kPrefixKeys = 128;  // of a step of the prefix 
 
 // Opening a piece (its queries, its result) costs a block of the prefix kernel about as
 // much as kPrefixOpen steps: every segment counts as so many more, in front of the real ones.
-constexpr int kPrefixOpen = 3;
+constexpr int kPrefixOpen = 6;
 
 // What sharing must save, of each SM, to be worth the prefix kernel and the join.
-constexpr int32_t kSharedFixedNs = 6000;
+constexpr int32_t kSharedFixedNs = 3000;
 
 // Calls that take an SM up to kSharedLongNs compute prefixes on some SMs and own keys on the
 // others, so that one starts up beside the other; longer ones take all SMs for each in turn.
-constexpr int32_t kSharedLongNs = 100000;
+// (Measured, 32 groups of 4 requests behind 2,000 tokens: 97 us in turn, 107 beside each other; 8
+// of 4 behind 8,000 80 and 74; 64 requests behind 8,000 73 and 54.)
+constexpr int32_t kSharedLongNs = 50000, kSharedLateNs = 6000;
 
 // The call's groups, and the costs that decide what is shared (ns, of one SM).
 struct Groups {
     const int32_t *offsets, *lens;
     int32_t n_groups, tile_rows;       // rows a tile of the decode path
     bool always;                       // whatever they are
-    int32_t step_one, step_two, own;   // a step of the prefix kernel with up to 128 rows, with more; 128 keys of a tile of the decode path
+    int32_t step_one, step_two;        // a step of the prefix kernel with up to 128 rows, with more
+    int32_t own, first;                // 128 keys of a tile of the decode path; and where no other tile reads them
+    int32_t own_open;                  // keys that a tile of it counts more
 };
 
 // In shared memory: by request its first row; by group the rest.
@@ -112,7 +116,7 @@ __device__ Blocks plan_groups(const AttendArgs &a, const Groups &w, const GroupP
         len = len_at(i + NT);
         if (r.n == 0) continue;
         const int64_t tiles = tiles_of(r.n);
-        own += tiles * (a.window > 0 ? min(int64_t(r.len), int64_t(a.window) + r.n) : r.len);
+        own += tiles * (w.own_open + (a.window > 0 ? min(int64_t(r.len), int64_t(a.window) + r.n) : r.len));
         const int32_t g = group_of(p, w.n_groups, bad, i);
         if (g < 0) continue;
         atomicMin(&p.prefix[g], r.len - r.n);
@@ -134,7 +138,8 @@ __device__ Blocks plan_groups(const AttendArgs &a, const Groups &w, const GroupP
                 const int64_t rows = int64_t(q1 - q0) * a.group, steps = prefix_steps(lo, prefix);
                 const int64_t here = (rows + kPrefixRows - 1) / kPrefixRows * (steps + kPrefixOpen) *
                                      (rows > kPrefixRows / 2 ? w.step_two : w.step_one);
-                const int64_t keys = int64_t(p.tiles[g]) * (prefix - lo), there = keys * w.own / kPrefixKeys;
+                const int64_t keys = int64_t(p.tiles[g]) * (prefix - lo);
+                const int64_t there = (keys * w.own + int64_t(prefix - lo) * w.first) / kPrefixKeys;
                 if (here < there || w.always) {
                     sums[0] += there - here;
                     sums[1] += here;
@@ -166,9 +171,11 @@ __device__ Blocks plan_groups(const AttendArgs &a, const Groups &w, const GroupP
         __syncthreads();
         return {0, grid};
     }
-    const int64_t rest = max(int64_t(1), (sums[3] - sums[2]) * w.own / kPrefixKeys), all = sums[1] + rest;
+    const int64_t rest = max(int64_t(1), (sums[3] - sums[2]) * (w.own + w.first) / kPrefixKeys), all = sums[1] + rest;
     if (all * a.kv.n_kv > int64_t(kSharedLongNs) * grid) return {grid, grid};
-    const int32_t blocks = max(1, min(grid - 1, static_cast<int32_t>((grid * sums[1] + all / 2) / all)));
+    // (the prefix kernel's first scores come kSharedLateNs later than the other kernel's)
+    const int64_t late = min(sums[1], rest) * kSharedLateNs / (all * a.kv.n_kv) * grid, cost = sums[1] + late;
+    const int32_t blocks = max(1, min(grid - 1, static_cast<int32_t>((grid * cost + (cost + rest) / 2) / (cost + rest))));
     return {blocks, grid - blocks};
 }
 
