@@ -278,7 +278,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_pages_kernel(const PagesArgs a
         each_page([&](int32_t page, bool is_free, int32_t f) {
             if (page < used && is_free) a.free_pages[f] = page;
         });
-        for (int64_t i = 3 * int64_t(n_moves) + all; i < 3 * int64_t(a.n_pages / 2); i += kCtas * kThreads)
+        for (uint32_t i = 3 * n_moves + all; i < 3u * (a.n_pages / 2); i += kCtas * kThreads)
             a.copies[i] = i % 3 < 2 ? -1 : 0;
         if (all == 0) a.n_copies[0] = n_moves;
         __threadfence();
@@ -314,6 +314,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_pages_kernel(const PagesArgs a
         sync_cluster();  // the ways have been read
         for (int32_t p = all; p < n_free; p += kCtas * kThreads) a.free_pages[p] = used + p;
     }
+#pragma unroll 4
     for (int32_t p = n_free + static_cast<int32_t>(rank) * kThreads + tid; p < a.n_pages; p += kCtas * kThreads)
         a.free_pages[p] = -1;
     if (rank == 0 && tid == 0) a.n_free[0] = n_free;
@@ -327,9 +328,15 @@ cudaError_t launch(const PagesArgs &a, cudaStream_t stream) {
     static_assert(kMost <= 227 * 1024 - 1024, "shared memory");
     int sms = 0;
     cudaError_t e = prepare_kernel(kv_pages_kernel<FORK>, static_cast<int>(kMost), seen, &sms);
-    if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(kv_pages_kernel<FORK>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
+    static std::atomic<uint64_t> wide{0};  // a bit a device: clusters beyond 8 blocks allowed
+    int device = 0;
+    if ((e = cudaGetDevice(&device)) != cudaSuccess) return e;
+    if (device >= 64 || ((wide.load(std::memory_order_acquire) >> device) & 1) == 0) {
+        e = cudaFuncSetAttribute(kv_pages_kernel<FORK>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e != cudaSuccess) return e;
+        if (device < 64) wide.fetch_or(uint64_t(1) << device, std::memory_order_release);
+    }
     cudaLaunchAttribute attr[2] = {};
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = kCtas;
