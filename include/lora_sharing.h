@@ -168,7 +168,8 @@ typedef enum { LORA_SHARE_AUTO = 0, LORA_SHARE_ALWAYS = 1 } lora_share_t;
  * mode           LORA_SHARE_AUTO: prefixes are read once where that is estimated to
  *                  save time, which short ones do not (decided on the device, from the
  *                  lengths); LORA_SHARE_ALWAYS: all of them
- * All other arguments, limits and device errors are lora_attend's; LORA_ERR_INVALID_ARG
+ * A NaN or infinity in a value of the prefix that some row of the group sees can reach
+ * the group's other rows.  All other arguments, limits and device errors are lora_attend's; LORA_ERR_INVALID_ARG
  * in err also reports group offsets out of order or range (nothing is shared then)
  * and negative prefix lengths (that group shares nothing).  Made for few rows a request (decode,
  * speculative decode); any number is computed.

@@ -16,6 +16,12 @@
 // A thread's sum is taken in fp32 against its own running maximum; a row's, and all
 // comparisons of candidates, in 64 bits: scores of different beams meet there, and a
 // rounding to fp32 would decide between candidates.
+//
+// Measured, graph replay: 32 requests of 4 beams over 128,256 tokens (29 MB are read: a tenth of
+// the beams has ended) 18.4 us, 1.6 TB/s over all: about 12 us pass until the last part is done
+// (SMs with four blocks take longer than those with three, and exponentials 4 us), 5 in the
+// request's join, a chain of loads, barriers and rankings.  One request of 4 beams over 32,000 fp32 logits
+// 8.0 us.  A chunk a block instead of parts: 23.9.
 #include <algorithm>
 
 #include "attend.cuh"

@@ -9,6 +9,13 @@
 // bitmaps are joined through distributed shared memory, every block taking one slice
 // of the pages; and the slices' counts, exchanged the same way, give every page its
 // rank.  The cluster's barriers are the only waits.
+//
+// Measured, graph replay: 128 rows of up to 4,000 tokens (pages of 16) forked in 7.5 us, 1,024 rows
+// with 102,000 entries in 14.1 (8 blocks a cluster 19), 16 rows compacted in 10.4, 1,024 in 29.5.
+// A barrier of the cluster and what it waits for take about 1 us each; 5 of them, and one
+// chain of loads (parents, lengths, entries), are the small fork.  The large ones spend the
+// rest on entries and lists, 16 SMs' loads and stores; the compaction asks for every entry where
+// its page moves (a load that depends on one).
 #include "attention.cuh"
 
 namespace lora {

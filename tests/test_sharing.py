@@ -935,6 +935,52 @@ def test_shared_workspace_over_calls_of_other_sizes(L):
         assert b.err == 0
 
 
+@gpu
+@pytest.mark.parametrize("share", ["always", "auto"])
+def test_shared_prefix_reads_what_the_kernels_before_wrote(L, share):
+    """Queries, lengths, tables and caches written on the stream right before each call, without a wait; two streams
+    with a workspace each at once.  Every call must give what it gives alone."""
+    torch = _torch()
+    steps = [Batch([(300 + 40 * i, [(c, 1) for c in (i, 9, 40, 3 * i)]), (64, [(i, 1), (0, 1)])], 8, 2, 128, 16, seed=i)
+             for i in range(6)]
+    pages, width = max(b.dk.shape[0] for b in steps), max(b.table.shape[1] for b in steps)
+    alone = [b.run(L, share=share) for b in steps]
+
+    def room():
+        k, v = (torch.zeros(pages, 16, 2, 128, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+        n, T = steps[0].n, steps[0].rows
+        i32 = dict(dtype=torch.int32, device="cuda")
+        kv = L.PagedKV(k, v)
+        return dict(kv=kv, k=k, v=v, q=torch.zeros(T, 1024, dtype=torch.bfloat16, device="cuda"), lens=torch.zeros(n, **i32),
+                    table=torch.zeros(n, width, **i32), prefix=torch.zeros(2, **i32), starts=dev(steps[0].starts),
+                    off=dev(np.arange(n + 1)), att=L.SharedAttention(n, T, 8, kv), stream=torch.cuda.Stream())
+
+    rooms = [room(), room()]
+    inputs = [(b.dk, b.dv, b.dq, dev(b.lens), dev(np.pad(b.table, ((0, 0), (0, width - b.table.shape[1])))), dev(b.prefix))
+              for b in steps]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for turn in range(5):
+        for s, r in enumerate(rooms):
+            with torch.cuda.stream(r["stream"]):
+                for i, (k, v, q, lens, table, prefix) in enumerate(inputs):
+                    r["k"].zero_()
+                    r["k"][:k.shape[0]].copy_(k)
+                    r["v"][:v.shape[0]].copy_(v)
+                    r["table"].copy_(table)
+                    r["prefix"].copy_(prefix)
+                    r["lens"].copy_(lens)
+                    r["q"].copy_(q)
+                    out = torch.zeros_like(q)
+                    r["att"].run(r["q"], out, r["off"], r["lens"], r["table"], r["starts"], r["prefix"], share=share)
+                    got[s].append((i, out))
+    torch.cuda.synchronize()
+    for s, r in enumerate(rooms):
+        assert int(r["att"].err) == 0
+        for i, out in got[s]:
+            assert torch.equal(out, alone[i][0]), (s, i)
+
+
 # ---------------------------------------------------------------------------
 # A run of them together
 # ---------------------------------------------------------------------------
