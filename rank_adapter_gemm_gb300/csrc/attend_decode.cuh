@@ -125,7 +125,8 @@ struct OwnRows {
     Groups groups;
     float4 *sums;
     float *outs;
-    const int32_t *blocks;  // the prefix kernel's word on how many blocks take part, 0 until it is there
+    const int32_t *blocks;  // the prefix kernel's word on how many blocks take part, 0 until it is there; null:
+                            // that kernel does not run, nothing is shared
 };
 
 struct DecodeRows : RequestRows {
@@ -352,25 +353,35 @@ attend_decode_kernel(const AttendArgs a, float *parts, int32_t *counters, int pr
     int32_t grid = gridDim.x;  // blocks that take part
     const int32_t *s_shared = nullptr;
     if constexpr (SHARED) {
-        // The prefix kernel lets this one start when all of its blocks run, that is after all
-        // kernels before it: what they wrote may be read (past the first-level cache), and only
-        // the end waits for the prefix kernel.  Its blocks compute on as many SMs as the
-        // plan gives them, this kernel's on the others.
-        asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-        __shared__ int64_t s_sum[4 * NW];
-        // (blocks without a part, which start when the prefix kernel's end, leave at once)
-        const int32_t known = __ldcg(own.blocks);
-        if (__syncthreads_and(known > 0 && static_cast<int32_t>(blockIdx.x) >= known)) {
-            end_own<SHARED>();
-            return;
-        }
-        bool bad;
-        const GroupPlan plan(reinterpret_cast<int32_t *>(smem + 2 * pref_bytes), own.groups.n_groups, a.n_seq);
-        grid = plan_groups<NT>(a, own.groups, plan, s_sum, grid, false, &bad).own;
         int32_t *to = reinterpret_cast<int32_t *>(smem + pref_bytes);
-        for (int32_t i = tid; i < a.n_seq; i += NT) {
-            const int32_t g = group_of(plan, own.groups.n_groups, bad, i);
-            to[i] = g >= 0 ? plan.prefix[g] : 0;
+        if (own.blocks == nullptr) {
+            wait_for_previous();
+            const Groups &w = own.groups;
+            if (blockIdx.x == 0)
+                for (int32_t g = tid; g < w.n_groups; g += NT)
+                    if (w.offsets[g] < 0 || w.offsets[g + 1] < w.offsets[g] || w.offsets[g + 1] > a.n_seq || w.lens[g] < 0)
+                        report_error(a.err, LORA_ERR_INVALID_ARG);
+            for (int32_t i = tid; i < a.n_seq; i += NT) to[i] = 0;
+        } else {
+            // The prefix kernel lets this one start when all of its blocks run, that is after all
+            // kernels before it: what they wrote may be read (past the first-level cache), and only
+            // the end waits for the prefix kernel.  Its blocks compute on as many SMs as the
+            // plan gives them, this kernel's on the others.
+            asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+            __shared__ int64_t s_sum[4 * NW];
+            // (blocks without a part, which start when the prefix kernel's end, leave at once)
+            const int32_t known = __ldcg(own.blocks);
+            if (__syncthreads_and(known > 0 && static_cast<int32_t>(blockIdx.x) >= known)) {
+                end_own<SHARED>();
+                return;
+            }
+            bool bad;
+            const GroupPlan plan(reinterpret_cast<int32_t *>(smem + 2 * pref_bytes), own.groups.n_groups, a.n_seq);
+            grid = plan_groups<NT>(a, own.groups, plan, s_sum, grid, false, &bad).own;
+            for (int32_t i = tid; i < a.n_seq; i += NT) {
+                const int32_t g = group_of(plan, own.groups.n_groups, bad, i);
+                to[i] = g >= 0 ? plan.prefix[g] : 0;
+            }
         }
         s_shared = to;
         __syncthreads();

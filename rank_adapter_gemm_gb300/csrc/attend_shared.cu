@@ -876,6 +876,8 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const AttendArgs a, co
         a.lse[int64_t(t) * a.n_heads + h] = sum == 0.0f ? -INFINITY : kLn2 * top + logf(sum);
 }
 
+constexpr int kSms = 152;  // a GB300's
+
 size_t up128(size_t b) { return (b + 127) & ~size_t(127); }
 
 // The word that has to be 0 when a call begins: behind the decode path's counters, at a place
@@ -956,6 +958,12 @@ cudaError_t launch_attend_shared(const AttendArgs &a, bool e4m3, int32_t max_q, 
     const int64_t rows = int64_t(max_q) * a.group;
     const int32_t tile_rows = rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
     const Groups groups = costs(prefix, tile_rows, a, e4m3);
+    // Short tables cannot hold prefixes worth sharing, whatever the lengths: one group of all requests,
+    // its prefix as long as a row of the table, would save most.  The own keys' kernel then does it all.
+    const int64_t keys = int64_t(a.width) << a.kv.page_shift, tiles = int64_t(a.T) * a.group / tile_rows + a.n_seq;
+    const int64_t most = (tiles * groups.own + groups.first - groups.step_one) * (keys / kKeys + 1) * a.kv.n_kv;
+    if (!groups.always && most < int64_t(kSharedFixedNs) * kSms)
+        return launch_attend_own(a, e4m3, groups, nullptr, nullptr, nullptr, ws, stream);
     const SharedWork w{groups, reinterpret_cast<int64_t *>(base + at.units), ints(at.prefix), ints(at.lo), ints(at.lead),
                        ints(kOwnBlocks), ints(at.live), reinterpret_cast<float4 *>(base + at.own_sums), floats(at.own_outs), own_pieces(ws),
                        reinterpret_cast<float4 *>(base + at.heads), floats(at.outs),
