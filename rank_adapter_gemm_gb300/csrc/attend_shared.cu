@@ -24,12 +24,12 @@
 // keys' kernel starts as soon as all blocks of the prefix kernel run, without a wait.
 //
 // Measured, 32/8 heads of 128 over bf16, one row a request, graph replay: 16 prompts of 20,000 to
-// 30,000 tokens with 16 samples each 351 us, 5.8 TB/s of what has to be read (each prefix for each
+// 30,000 tokens with 16 samples each 343 us, 5.9 TB/s of what has to be read (each prefix for each
 // request: 3,361); the prefixes' part reads 1.64 GB in 263 us, 6.2 TB/s.  64 requests of 100 to 1,000
-// own tokens behind one prompt of 8,000 56 us (each on its own 178), of which HBM needs 20: 11 us pass
+// own tokens behind one prompt of 8,000 54 us (each on its own 178), of which HBM needs 20: 11 us pass
 // until the first scores (lengths, plan, queries, first keys), 8 to 10 at the end (results left,
 // pieces joined, one launch), and a step takes 2.2 us where blocks start together, 1.6 later on.
-// 4 requests behind 30,000 tokens 49 us (72), behind 500 22 us, not shared (the decode path alone 13.5).
+// 4 requests behind 30,000 tokens 49 us (72).
 //
 // Blocks are organised like those of the prompt path: warps 0-3 and 4-7 softmax of a
 // tile's rows, a row a thread; 8-11 copy; 12 issues the products; 13 hands out the
@@ -88,7 +88,7 @@ struct SharedWork {
 
 struct Barriers {
     uint64_t q_full[2], q_empty[2], full[8], empty[8], s_full[2], p_full[2][2], o_full[2], o_empty[2], item_full[2],
-        item_empty[2], exp_full[2], done;
+        item_empty[2], exp_full[2], half_full, done;
 };
 
 // A piece: up to 256 rows of a group and key head, and the keys [lo, end) of its steps.
@@ -99,7 +99,21 @@ struct Item {
     int32_t cut, first_cut, cuts;    // cut: the block's own place; of a segment's first piece, the other pieces
     bool first, last;                // of the piece's runs of kSegment steps
     bool any;                        // none: the work is done
+
+    // With up to 128 rows the block's two halves share them, taking turns at the steps: one's softmax
+    // runs beside the other's products.  64 groups of 2 requests behind 4,000 tokens 210 us, else 220;
+    // 32 of 4 behind 2,000 90 and 96.  Not over e4m3, where widening the codes bounds a step and the ring, with
+    // k a step ahead, has less room for it: 32 of 4 behind 2,000 126 us so, else 108.
+    template <bool E4M3>
+    __device__ bool split() const { return !E4M3 && rows <= kRows && steps > 1; }
 };
+
+// Tiles of a piece in the ring's order: k and v in turn; where halves take turns, k is a step
+// ahead: k0 k1 v0 k2 v1 .. k(n-1) v(n-2) v(n-1).
+__device__ __forceinline__ int32_t k_place(int32_t j, bool split) { return split ? max(0, 2 * j - 1) : 2 * j; }
+__device__ __forceinline__ int32_t v_place(int32_t j, int32_t n, bool split) {
+    return split ? min(2 * j + 2, 2 * n - 1) : 2 * j + 1;
+}
 
 // The group that a block's share begins in, and the units before it.
 struct First {
@@ -194,9 +208,11 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefix_kernel(const Attend
     extern __shared__ unsigned char smem_raw[];
     __shared__ Barriers bar;
     __shared__ Item s_item[2];
-    __shared__ int64_t s_sum[4 * kThreads / 32];
     __shared__ uint32_t s_tmem;
     __shared__ volatile int32_t s_abort;
+    __shared__ float2 s_half[kRows];  // references and sums of the second half's rows; before, the plan's sums
+    int64_t *const s_sum = reinterpret_cast<int64_t *>(s_half);
+    static_assert(sizeof(s_half) >= 4 * kThreads / 32 * sizeof(int64_t), "sums");
     __shared__ int8_t s_qexp[2][E4M3 ? 2 * kRows : 1];  // of this and the next piece: q rows' powers of two
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t q_base = (tc::smem_u32(smem_raw) + 1023) & ~1023u;  // q tiles of kQ pieces, then the ring
@@ -243,6 +259,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefix_kernel(const Attend
             tc::mbar_init(&bar.exp_full[i], 4);
             tc::mbar_init(&bar.item_empty[i], 13);  // the copying, multiplying and softmax warps
         }
+        tc::mbar_init(&bar.half_full, 4);
         tc::mbar_init(&bar.done, 1);
         tc::mbar_init_fence();
     }
@@ -293,6 +310,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefix_kernel(const Attend
             if (!go_on() || !s_item[k & 1].any) break;
             const Item &it = s_item[k & 1];
             const int32_t steps = it.steps, lo = it.lo, end = it.end;
+            const bool split = it.template split<E4M3>();
             const int32_t *table = a.table + it.lead * a.ld_table;
             const int64_t head = it.head * a.kv.head_b;
             // this lane's key of the step to copy (the last keys first) and, ahead of it, its page
@@ -355,15 +373,28 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefix_kernel(const Attend
             }
             release(k);  // nothing below reads the piece
 
-            int64_t at = -1;      // byte offset of this lane's key, -1: none
-            bool smooth = false;  // all keys there, and 16 neighbours always in one page
+            // byte offset of this lane's key, -1: none; of the last k tile's, and of the one before it
+            int64_t at = -1, new_at = -1, old_at = -1;
+            // all keys there, and 16 neighbours always in one page
+            bool smooth = false, new_smooth = false, old_smooth = false;
             const auto next_keys = [&]() {
+                old_at = new_at;
+                old_smooth = new_smooth;
                 const bool ok = page >= 0 && page < a.kv.n_pages, has = has_key();
                 if (has && !ok) report_error(a.err, LORA_ERR_SLOT_RANGE);
-                at = has && ok ? page * a.kv.page_b + (key & a.kv.page_mask) * a.kv.token_b + head : -1;
-                smooth = __all_sync(0xffffffffu, at >= 0) && a.kv.page_shift >= 4;
+                new_at = has && ok ? page * a.kv.page_b + (key & a.kv.page_mask) * a.kv.token_b + head : -1;
+                new_smooth = __all_sync(0xffffffffu, new_at >= 0) && a.kv.page_shift >= 4;
                 key -= kKeys;
                 if (has_key()) page = table[key >> a.kv.page_shift];
+            };
+            // the t-th tile: whether it is v, and its keys
+            const auto tile_is_v = [&](int32_t t) {
+                const bool v = split ? t > 1 && ((t & 1) == 0 || t == 2 * steps - 1) : t & 1;
+                if (!v) next_keys();
+                const bool old = v && split && t < 2 * steps - 1;
+                at = old ? old_at : new_at;
+                smooth = old ? old_smooth : new_smooth;
+                return v;
             };
             // calls f(instruction, address or null) for this warp's 32 keys of k or v
             const auto each = [&](const unsigned char *from, auto f) {
@@ -393,8 +424,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefix_kernel(const Attend
             if constexpr (E4M3) {
                 uint4 v[kKvPieces];
                 const auto load = [&](int32_t t) {
-                    if ((t & 1) == 0) next_keys();
-                    each((t & 1) ? a.kv.v : a.kv.k, [&](int i, const unsigned char *src) {
+                    const bool is_v = tile_is_v(t);
+                    each(is_v ? a.kv.v : a.kv.k, [&](int i, const unsigned char *src) {
                         v[i] = src != nullptr ? ldg_cg(src) : make_uint4(0, 0, 0, 0);
                     });
                 };
@@ -415,10 +446,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefix_kernel(const Attend
                 }
             } else {
                 for (int32_t t = 0; t < tiles; ++t, ++u) {
-                    if ((t & 1) == 0) next_keys();
+                    const bool is_v = tile_is_v(t);
                     if (!slot_free()) break;
                     const uint32_t dst = ring + (u % C::kSlots) * C::kTileB;
-                    each((t & 1) ? a.kv.v : a.kv.k, [&](int i, const unsigned char *src) {
+                    each(is_v ? a.kv.v : a.kv.k, [&](int i, const unsigned char *src) {
                         tc::cp16(dst + tile_at(cw * 32 + i * kKvStep + kv_row, kv_piece), src != nullptr ? src : a.kv.k,
                                  src != nullptr);
                     });
@@ -450,8 +481,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefix_kernel(const Attend
                 if (elect_one()) tc::mma_commit(b);
                 __syncwarp();
             };
-            const auto scores = [&](int qb, int i, int32_t u) {
-                const uint64_t q = q_desc + (((2 * qb + i) * C::kTileB) >> 4), k = k_desc + (((u % C::kSlots) * C::kTileB) >> 4);
+            const auto scores = [&](int q_tile, int i, int32_t u) {
+                const uint64_t q = q_desc + ((q_tile * C::kTileB) >> 4), k = k_desc + (((u % C::kSlots) * C::kTileB) >> 4);
                 if (elect_one()) {
 #pragma unroll
                     for (int kk = 0; kk < HD / 16; ++kk) {
@@ -482,16 +513,56 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefix_kernel(const Attend
                 if (!go_on() || !s_item[k & 1].any) break;
                 const int32_t steps = s_item[k & 1].steps;
                 const int n_tiles = s_item[k & 1].rows > kRows ? 2 : 1;
+                const bool split = s_item[k & 1].template split<E4M3>();
                 release(k);
                 const int qb = q_round % C::kQ;
                 follow(&bar.q_full[qb], (q_round / C::kQ) & 1);
                 full(u);
                 ++q_round;
                 tc::fence_after_sync();
-                for (int i = 0; i < n_tiles; ++i) scores(qb, i, u);
+                for (int i = 0; i < n_tiles; ++i) scores(2 * qb + i, i, u);
                 commit(&bar.empty[u % C::kSlots]);
                 if (steps == 1) commit(&bar.q_empty[qb]);
                 int32_t j = 0;
+                if (split) {
+                    full(u + 1);
+                    tc::fence_after_sync();
+                    scores(2 * qb, 1, u + 1);
+                    commit(&bar.empty[(u + 1) % C::kSlots]);
+                    if (steps == 2) commit(&bar.q_empty[qb]);
+                    for (int32_t stop = min(steps, kVote); j < steps && go_on(); stop = min(steps, stop + kVote)) {
+                        for (; j < stop; ++j) {
+                            const int i = j & 1;
+                            const int32_t v = u + v_place(j, steps, true);
+                            full(v);
+                            // the last piece's output has been read
+                            if (j < 2 && ((o_used >> i) & 1)) follow(&bar.o_empty[i], ((o_parity >> i) & 1) ^ 1);
+                            follow(&bar.p_full[i][0], (p_parity >> i) & 1);
+                            tc::fence_after_sync();
+                            outputs(i, v, 0, j < 2);
+                            follow(&bar.p_full[i][1], (p_parity >> i) & 1);
+                            tc::fence_after_sync();
+                            outputs(i, v, 1, j < 2);
+                            p_parity ^= 1u << i;
+                            if (j + 2 >= steps) {
+                                commit(&bar.o_full[i]);
+                                o_parity ^= 1u << i;
+                                o_used |= 1u << i;
+                            }
+                            commit(&bar.empty[v % C::kSlots]);
+                            if (j + 2 < steps) {
+                                const int32_t kt = u + k_place(j + 2, true);
+                                full(kt);
+                                tc::fence_after_sync();
+                                scores(2 * qb, i, kt);
+                                commit(&bar.empty[kt % C::kSlots]);
+                                if (j + 3 == steps) commit(&bar.q_empty[qb]);
+                            }
+                        }
+                    }
+                    u += 2 * steps;
+                    continue;
+                }
                 for (int32_t stop = min(steps, kVote); j < steps && go_on(); stop = min(steps, stop + kVote)) {
                     for (; j < stop; ++j, u += 2) {
                         const bool more = j + 1 < steps;
@@ -516,7 +587,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefix_kernel(const Attend
                             if (more) {
                                 if (i == 0) full(u + 2);
                                 tc::fence_after_sync();
-                                scores(qb, i, u + 2);
+                                scores(2 * qb + i, i, u + 2);
                                 if (last) {
                                     commit(&bar.empty[(u + 2) % C::kSlots]);
                                     if (j + 2 == steps) commit(&bar.q_empty[qb]);
@@ -603,19 +674,21 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefix_kernel(const Attend
     } else {
         set_registers<C::kSoftmaxRegs, true>();
         // ---- softmax --------------------------------------------------------------------
-        const int i = warp >> 2, r = i * kRows + (warp & 3) * 32 + lane;
+        const int i = warp >> 2;
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t s_at = tmem + lanes + i * kKeys, o_at = tmem + lanes + 2 * kKeys + i * 128;
         const bool plain = a.softcap == 0.0f && a.slopes == nullptr && a.scale > 0.0f;
-        int32_t round = 0, o_round = 0;
+        int32_t round = 0, o_round = 0, half_round = 0;
         for (int32_t k = 0;; ++k) {
             follow(&bar.item_full[k & 1], (k >> 1) & 1);
             if (!go_on() || !s_item[k & 1].any) break;
             // the piece stays in shared memory: registers are scarce in the loop below
             const Item &it = s_item[k & 1];
             const int32_t steps = it.steps, key0 = it.key0, end = it.end;
+            const bool split = it.template split<E4M3>();
+            const int r = (split ? 0 : i * kRows) + (warp & 3) * 32 + lane;
             const bool live = r < it.rows;
-            if (it.rows <= i * kRows) {  // this tile has no rows
+            if (it.rows <= i * kRows && !split) {  // this tile has no rows
                 release(k);
                 continue;
             }
@@ -635,7 +708,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefix_kernel(const Attend
             }
             const float by0 = mult * kLog2e;
             float m = -INFINITY, l = 0.0f;  // the reference of the row's weights, and their sum
-            for (int32_t j = 0; j < steps; ++j, ++round) {
+            const int32_t j0 = split ? i : 0, j_step = split ? 2 : 1;
+            for (int32_t j = j0; j < steps; j += j_step, ++round) {
                 if (!wait(&bar.s_full[i], round & 1)) break;
                 tc::fence_after_sync();
                 const int32_t key = key0 + (steps - 1 - j) * kKeys;
@@ -710,7 +784,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefix_kernel(const Attend
                     const float now = fmaxf(m, top), f = now == -INFINITY ? 1.0f : ex2(m - now);
                     m = now;
                     l *= f;
-                    if (j > 0) rescale_output<HD>(o_at, f);
+                    if (j > j0) rescale_output<HD>(o_at, f);
                 }
                 const float ref = kShift - (m == -INFINITY ? 0.0f : m);
                 const uint64_t by2 = pack2(by, by), ref2 = pack2(ref, ref);
@@ -743,6 +817,41 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefix_kernel(const Attend
             follow(&bar.o_full[i], o_round & 1);
             if (!go_on()) break;
             tc::fence_after_sync();
+            if (split && i == 1) {
+                // this half's references and sums; the first half goes on with both
+                s_half[r] = make_float2(m, l);
+                tc::fence_before_sync();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(&bar.half_full);
+                ++o_round;
+                release(k);
+                continue;
+            }
+            if (split) {
+                follow(&bar.half_full, half_round & 1);
+                ++half_round;
+                if (!go_on()) break;
+                tc::fence_after_sync();
+                const float2 other = s_half[r];
+                const float top = fmaxf(m, other.x), ref = top == -INFINITY ? 0.0f : top;
+                const float w0 = ex2(m - ref), w1 = ex2(other.x - ref);
+                m = top;
+                l = fmaf(w1, other.y, w0 * l);
+#pragma unroll 1
+                for (int c = 0; c < HD / 16; ++c) {
+                    uint32_t x[16], y[16];
+                    tc::tmem_ld16(o_at + 16 * c, x);
+                    tc::tmem_ld16(o_at + 128 + 16 * c, y);
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        x[e] = __float_as_uint(fmaf(w1, __uint_as_float(y[e]), w0 * __uint_as_float(x[e])));
+                    tmem_st16(o_at + 16 * c, x);
+                }
+                tmem_wait_st();
+                tc::fence_before_sync();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(&bar.o_empty[1]);
+            }
             // the rows' own place, or the block's
             const int64_t at = it.cut ? int64_t(blockIdx.x) * 2 * kRows + r
                                       : (int64_t(it.head) * a.T + it.q0) * a.group + it.row0 + r;
@@ -927,9 +1036,9 @@ cudaError_t launch(const AttendArgs &a, const SharedWork &w, void *ws, cudaStrea
 
 // Costs of the two ways, ns of one SM, from calls long enough to show them; a cap or a bias
 // lengthens the softmax of both.  Shared always / never, us, 32/8 heads of 128 over bf16, one row a
-// request: 4 requests behind 2,000 tokens 24.8 / 23.5, behind 30,000 51 / 74; 64 behind 500 26 / 35; 8
-// groups of 4 behind 8,000 75 / 127; 64 of 2 behind 1,000 110 / 90, behind 4,000 220 / 325; over e4m3
-// 32 of 4 behind 2,000 111 / 109, 8 of 16 53 / 98.
+// request: 4 requests behind 2,000 tokens 25 / 16, behind 30,000 49 / 74; 64 behind 500 27 / 35; 8
+// groups of 4 behind 8,000 73 / 127; 64 of 2 behind 1,000 103 / 89, behind 4,000 210 / 324; over e4m3
+// 32 of 4 behind 2,000 108 / 109, 8 of 16 63 / 98.
 Groups costs(const lora_prefix_t &prefix, int32_t tile_rows, const AttendArgs &a, bool e4m3) {
     const bool wide = a.kv.head_dim == 128;
     const int32_t more = a.softcap == 0.0f && a.slopes == nullptr ? 0 : 800;
