@@ -18,7 +18,8 @@
  * checks return a status before anything is enqueued, errors found in device
  * data go to the caller's word `err` (first error wins, never cleared here; it may
  * be null).  Values read from device memory never send an access out of the
- * buffers described by the arguments.
+ * buffers described by the arguments.  Outputs must not overlap inputs, unless said
+ * otherwise.
  */
 #ifndef LORA_SHARING_H
 #define LORA_SHARING_H

@@ -802,6 +802,7 @@ GROUPS = {
     "spec": [(200, [(5, 4), (60, 2), (0, 4)]), (77, [(1, 3), (0, 1)])],
     "large": [(700, [(i % 11, 1) for i in range(130)])],
     "rows": [(260, [(10, 70), (0, 33), (300, 1), (5, 0)])],
+    "idle": [(150, [(3, 0), (0, 1), (5, 2), (0, 0), (40, 1)]), (90, [(7, 0), (8, 0)]), (200, [(0, 1), (0, 0)])],
 }
 
 
@@ -933,6 +934,49 @@ def test_shared_workspace_over_calls_of_other_sizes(L):
     for b in batches * 2:
         b.check(*b.run(L, att=att))
         assert b.err == 0
+
+
+def check_against_each(L, b, out, lse):
+    """What lora_attend gives, every request on its own: roundings of both outputs, 2^-8 each, and of the prefix's weights,
+    2^-8 of max |v| < 6."""
+    torch = _torch()
+    kv = L.PagedKV(b.dk, b.dv, *b.scales)
+    att = L.Attention(b.n, b.rows, b.H, kv)
+    ref, ref_lse = torch.full_like(out, 7.0), torch.full_like(lse, 7.0)
+    att.run(b.dq, ref, dev(np.concatenate([[0], np.cumsum(b.new)])), dev(b.lens), dev(b.table), max(b.new), lse=ref_lse)
+    torch.cuda.synchronize()
+    assert (out.float() - ref.float()).abs().max() <= 3 * 6 * 2.0 ** -8
+    # sums of a few thousand terms in another order
+    assert (lse - ref_lse).abs().max() <= 2.0 ** -16 * ref_lse.abs().max()
+
+
+@gpu
+@pytest.mark.parametrize("fp8", [False, True])
+def test_shared_prefix_of_many_groups(L, fp8):
+    """1,200 requests in 300 groups, many pieces a block; groups of one and of no rows between them."""
+    rng = np.random.default_rng(7)
+    groups = [(int(rng.integers(0, 300)), [(int(rng.integers(0, 9)), int(rng.integers(0, 3))) for _ in range(g % 8)])
+              for g in range(300)]
+    b = Batch(groups, 4, 2, 64, 16, fp8, seed=1)
+    out, lse = b.run(L)
+    assert b.err == 0
+    check_against_each(L, b, out, lse)
+
+
+@gpu
+@pytest.mark.parametrize("groups", [[(9000, [(c, 1) for c in range(0, 320, 5)])], [(9000, [(3, 1)] * 3), (40, [(5, 1)] * 60)],
+                                    [(2500, [(c, 1) for c in range(4)])] * 16])
+def test_shared_prefix_decided_on_the_device(L, groups):
+    """Tables long enough for prefixes worth sharing: shared beside the own keys, some of it, in turn."""
+    b = Batch(groups, 16, 4, 64, 64, seed=3)
+    out, lse = b.run(L, share="auto", repeat=2)
+    assert b.err == 0
+    check_against_each(L, b, out, lse)
+    again = b.run(L, share="auto")
+    assert _torch().equal(out, again[0]) and _torch().equal(lse, again[1])
+    b.starts[-1] = b.n + 1  # groups out of range are reported on this way too
+    b.run(L, share="auto")
+    assert b.err == 1
 
 
 @gpu
