@@ -1025,6 +1025,44 @@ def test_shared_prefix_reads_what_the_kernels_before_wrote(L, share):
             assert torch.equal(out, alone[i][0]), (s, i)
 
 
+@gpu
+@pytest.mark.parametrize("fp8", [False, True])
+def test_shared_prefix_of_many_million_keys(L, fp8):
+    """A prefix of 2^24 keys whose table names one page over and over: pieces of more than 512 steps, added up in fp32.
+    Products on tensor cores lose 2^-24 of what they add to with every 16 keys, below 2^-11 of 65,536 keys."""
+    torch = _torch()
+    rng = np.random.default_rng(8)
+    H, hd, ps, repeats = 4, 64, 1024, 1 << 14
+    dtype, scales = (torch.float8_e4m3fn, (0.5, 0.25)) if fp8 else (torch.bfloat16, (1.0, 1.0))
+    k, v = (torch.from_numpy(rng.standard_normal((3, ps, 1, hd))).float().to(dtype).cuda() for _ in range(2))
+    kv = L.PagedKV(k, v, *scales)
+    q = torch.from_numpy(rng.standard_normal((3, H * hd))).cuda().bfloat16()
+    table = np.zeros((2, repeats + 1), np.int32)
+    table[:, -1] = [1, 2]
+    prefix, own = repeats * ps, [7, 1000]
+    att = L.SharedAttention(2, 3, H, kv)
+    out, lse = torch.empty_like(q), torch.empty(3, H, device="cuda")
+    att.run(q, out, dev([0, 1, 3]), dev([prefix + n for n in own]), dev(table), dev([0, 2]), dev([prefix]), 2, lse=lse,
+            share="always")
+    torch.cuda.synchronize()
+    assert int(att.err) == 0
+    kk, vv, x = k.double().cpu().numpy() * scales[0], v.double().cpu().numpy() * scales[1], q.double().cpu().numpy()
+    for t, (i, seen) in enumerate([(0, 7), (1, 999), (1, 1000)]):
+        for h in range(H):
+            one = x[t, h * hd:(h + 1) * hd]
+            s0, s1 = kk[0, :, 0] @ one * hd ** -0.5, kk[1 + i, :seen, 0] @ one * hd ** -0.5
+            top = max(s0.max(), s1.max())
+            e0, e1 = repeats * np.exp(s0 - top), np.exp(s1 - top)
+            total = e0.sum() + e1.sum()
+            ref = (e0 @ vv[0, :, 0] + e1 @ vv[1 + i, :seen, 0]) / total
+            A = (e0 @ np.abs(vv[0, :, 0]) + e1 @ np.abs(vv[1 + i, :seen, 0])) / total
+            eps = 2.0 ** -18 * (1 + np.abs(s0).max())
+            got = out[t, h * hd:(h + 1) * hd].double().cpu().numpy()
+            assert (np.abs(got - ref) <= 2.0 ** -8 * np.abs(ref) + (2.0 ** -8 + 2.0 ** -11 + 2 * eps) * A).all(), (t, h)
+            want = top + math.log(total)
+            assert abs(float(lse[t, h]) - want) <= 2.0 ** -18 * (1 + abs(want)) + 2.0 ** -16
+
+
 # ---------------------------------------------------------------------------
 # A run of them together
 # ---------------------------------------------------------------------------
