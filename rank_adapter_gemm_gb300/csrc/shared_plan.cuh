@@ -73,7 +73,7 @@ __device__ __forceinline__ int64_t prefix_units(const AttendArgs &a, const Group
     return (rows + kPrefixRows - 1) / kPrefixRows * a.kv.n_kv * (steps + kPrefixOpen);
 }
 
-// The request's group, -1: none.  (bad: the offsets are out of order or range.)
+// The request's group, -1: none.  (bad: the groups' or the rows' offsets are out of order or range.)
 __device__ __forceinline__ int32_t group_of(const GroupPlan &p, int32_t n_groups, bool bad, int32_t i) {
     if (bad || n_groups == 0 || i < p.offsets[0] || i >= p.offsets[n_groups]) return -1;
     return last_at_most(p.offsets, n_groups, i);
@@ -107,11 +107,14 @@ __device__ Blocks plan_groups(const AttendArgs &a, const Groups &w, const GroupP
         bad = bad || p.offsets[g] < 0 || p.offsets[g + 1] < p.offsets[g] || p.offsets[g + 1] > a.n_seq;
     bad = __syncthreads_or(bad);
     if (bad && report && tid == 0) report_error(a.err, LORA_ERR_INVALID_ARG);
-    *bad_out = bad;
     // requests: what each has cached before its rows, its tiles; and the cost of all own keys
     const auto tiles_of = [&](int32_t n) { return (int64_t(n) * a.group + w.tile_rows - 1) / w.tile_rows; };
     int64_t own = 0;  // tiles x keys of the decode path, all requests on their own
+    // A group's rows are those between its ends, and a token's request is found by a search in the
+    // offsets: both need them to rise all over the call, or nothing is shared.
+    bool falls = false;
     for (int32_t i = tid; i < a.n_seq; i += NT) {
+        falls = falls || p.rows[i] < 0 || p.rows[i + 1] < p.rows[i] || p.rows[i + 1] > a.T;
         const RequestRows r = check_request(a, p.rows[i], p.rows[i + 1], len);
         len = len_at(i + NT);
         if (r.n == 0) continue;
@@ -123,7 +126,8 @@ __device__ Blocks plan_groups(const AttendArgs &a, const Groups &w, const GroupP
         atomicMin(&p.lead[g], i);
         atomicAdd(&p.tiles[g], static_cast<int32_t>(min(tiles, int64_t(1) << 18)));
     }
-    __syncthreads();
+    bad = __syncthreads_or(falls) || bad;
+    *bad_out = bad;
     // groups: the prefix, and what sharing it saves
     int64_t sums[4] = {0, 0, 0, own};  // ns saved, ns of prefixes, tiles x keys that are not own any more
     for (int32_t g = tid; g < w.n_groups; g += NT) {
@@ -131,7 +135,7 @@ __device__ Blocks plan_groups(const AttendArgs &a, const Groups &w, const GroupP
         int32_t prefix = 0, lo = 0;
         if (!bad && p.lead[g] != INT32_MAX) {
             const int32_t q0 = p.rows[p.offsets[g]], q1 = p.rows[p.offsets[g + 1]];
-            if (q0 >= 0 && q1 >= q0 && q1 <= a.T) prefix = max(0, min(given, ctx));
+            prefix = max(0, min(given, ctx));
             if (a.window > 0) lo = static_cast<int32_t>(max(int64_t(0), int64_t(ctx) - a.window + 1));
             if (lo >= prefix) prefix = lo = 0;  // no row sees any of it
             if (prefix > 0) {

@@ -1,0 +1,95 @@
+"""Requests that share what they have cached, at the edges of the calls' range: device data that does not fit
+together, sums over many tokens.  Batches and tolerances are those of test_sharing.py.
+"""
+import numpy as np
+import pytest
+
+from test_sharing import Batch, L, _torch, dev  # noqa: F401  (L: a fixture)
+
+gpu = pytest.mark.gpu
+
+
+# ---------------------------------------------------------------------------
+# Attention: row offsets out of order or range
+# ---------------------------------------------------------------------------
+def definition(b, i, q0, q1):
+    """(out, tolerance, lse, tolerance) of request i's rows [q0, q1), its last positions, as Batch.check has them."""
+    k, v = (x.double().cpu().numpy() * s for x, s in zip((b.dk, b.dv), b.scales))
+    q = b.dq.double().cpu().numpy().reshape(b.rows, b.H, b.hd)
+    n, m, G = b.lens[i], q1 - q0, b.H // b.KV
+    j = np.arange(n)
+    kk, vv = (x[b.table[i, j // b.ps], j % b.ps] for x in (k, v))
+    seen = j[None] <= np.arange(n - m, n)[:, None]
+    out, tol = np.zeros((m, b.H, b.hd)), np.zeros((m, b.H, b.hd))
+    lse, lse_tol = np.zeros((m, b.H)), np.zeros((m, b.H))
+    for h in range(b.H):
+        s = b.hd ** -0.5 * q[q0:q1, h] @ kk[:, h // G].T
+        eps = 2.0 ** -18 * (1 + np.abs(np.where(seen, s, 0.0)).max(1, initial=0.0))
+        s = np.where(seen, s, -np.inf)
+        top = s.max(1, keepdims=True)
+        e = np.exp(s - top)
+        total = e.sum(1, keepdims=True)
+        out[:, h], A = e / total @ vv[:, h // G], e / total @ np.abs(vv[:, h // G])
+        tol[:, h] = 2.0 ** -8 * np.abs(out[:, h]) + (2.0 ** -8 + 2 * eps[:, None]) * A + 2.0 ** -20
+        lse[:, h], lse_tol[:, h] = (top + np.log(total))[:, 0], eps
+    return out, tol, lse, lse_tol
+
+
+def check_offsets(L, b, off, att, share):  # noqa: F811
+    """Requests whose offsets fit have their rows by definition where no other has them too; rows of none stay."""
+    torch = _torch()
+    out = torch.full((b.rows, b.H * b.hd), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((b.rows, b.H), 7.0, device="cuda")
+    att.err.zero_()
+    att.run(b.dq, out, dev(off), dev(b.lens), dev(b.table), dev(b.starts), dev(b.prefix), kv=L.PagedKV(b.dk, b.dv, *b.scales),
+            lse=lse, share=share)
+    torch.cuda.synchronize()
+    assert int(att.err) == 1
+    out, lse = out.double().cpu().numpy().reshape(b.rows, b.H, b.hd), lse.double().cpu().numpy()
+    good = [(i, off[i], off[i + 1]) for i in range(b.n) if 0 <= off[i] <= off[i + 1] <= b.rows]
+    owners = np.zeros(b.rows, int)
+    for _, q0, q1 in good:
+        owners[q0:q1] += 1
+    for i, q0, q1 in good:
+        ref, tol, ref_lse, lse_tol = definition(b, i, q0, q1)
+        one = owners[q0:q1] == 1
+        assert (np.abs(out[q0:q1] - ref) <= tol)[one].all(), (off, i)
+        assert (np.abs(lse[q0:q1] - ref_lse) <= lse_tol)[one].all(), (off, i)
+    assert (out[owners == 0] == 7.0).all() and (lse[owners == 0] == 7.0).all()
+
+
+OFFSETS = [[0, 4, 2, 7, 10, 12], [4, 2, 6, 7, 10, 12], [-3, 4, 6, 7, 10, 12], [0, 4, 6, 7, 10, 9], [0, 4, 6, 7, 10, 99],
+           [0, 4, 6, 99, 10, 12], [8, 12, 0, 1, 4, 6], [0, 4, 6, -1, 10, 12], [0, 0, 0, 0, 2 ** 31 - 1, 12]]
+
+
+@gpu
+@pytest.mark.parametrize("used", [False, True], ids=["zeroed", "used"])
+@pytest.mark.parametrize("share", ["always", "auto"])
+@pytest.mark.parametrize("hd,fp8", [(128, False), (64, True)])
+def test_shared_prefix_row_offsets_out_of_order(L, hd, fp8, share, used):  # noqa: F811
+    """Offsets that fall inside a group, at its ends and between groups, that are negative or beyond T; with a workspace
+    fresh or last used for more rows, so that its parts lay elsewhere."""
+    b = Batch([(300, [(10, 4), (5, 2), (0, 1)]), (130, [(20, 3), (4, 2)])], 8, 2, hd, 16, fp8, rows_after=5)
+    c = Batch([(90, [(i, 3) for i in range(20)])], 8, 2, hd, 16, fp8)
+    kv = L.PagedKV(b.dk, b.dv, *b.scales)
+    for off in OFFSETS:
+        att = L.SharedAttention(c.n, c.rows, 8, kv)
+        if used:
+            c.run(L, att=att)
+        check_offsets(L, b, off, att, share)
+        # the workspace serves calls whose offsets fit
+        att.err.zero_()
+        b.check(*b.run(L, att=att, share=share))
+        assert b.err == 0
+
+
+@gpu
+@pytest.mark.parametrize("used", [False, True], ids=["zeroed", "used"])
+def test_shared_prefix_rows_of_a_request_past_its_group(L, used):  # noqa: F811
+    """Two requests, offsets 0, 100, 2: the first one's rows lie beyond the group's last."""
+    b = Batch([(200, [(120, 100), (5, 2)])], 8, 2, 128, 16)
+    c = Batch([(90, [(i, 3) for i in range(60)])], 8, 2, 128, 16)
+    att = L.SharedAttention(c.n, c.rows, 8, L.PagedKV(b.dk, b.dv))
+    if used:
+        c.run(L, att=att)
+    check_offsets(L, b, [0, 100, 2], att, "always")
