@@ -127,6 +127,7 @@ struct OwnRows {
     float *outs;
     const int32_t *blocks;  // the prefix kernel's word on how many blocks take part, 0 until it is there; null:
                             // that kernel does not run, nothing is shared
+    int32_t *live;          // the join's word on whether there is anything to join; written where this kernel refuses
 };
 
 struct DecodeRows : RequestRows {
@@ -429,6 +430,8 @@ attend_decode_kernel(const AttendArgs a, float *parts, int32_t *counters, int pr
         if (sum > INT32_MAX) {  // the same in every block
             if (blockIdx.x == 0 && tid == 0) report_error(a.err, LORA_ERR_UNSUPPORTED);
             end_own<SHARED>();
+            // (behind the prefix kernel, which has set the word)
+            if (SHARED && own.blocks != nullptr && blockIdx.x == 0 && tid == 0) own.live[0] = 0;
             return;
         }
         for (int32_t i = i0; i < i1; ++i) {

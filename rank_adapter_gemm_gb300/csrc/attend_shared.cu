@@ -42,7 +42,7 @@ namespace lora {
 
 size_t decode_workspace_bytes(int32_t head_dim);
 cudaError_t launch_attend_own(const AttendArgs &a, bool e4m3, const Groups &groups, float4 *sums, float *outs,
-                              const int32_t *blocks, void *ws, cudaStream_t stream);
+                              const int32_t *blocks, int32_t *live, void *ws, cudaStream_t stream);
 const float *own_pieces(const void *ws);
 
 namespace {
@@ -76,7 +76,7 @@ struct SharedWork {
     int64_t *units;               // by group: steps (and openings) before it, n_groups + 1
     int32_t *prefix, *lo, *lead;  // by group, of its plan
     int32_t *own_blocks;          // that take part in the own keys; 0 between calls
-    int32_t *live;                // whether anything is shared; then by token, whether its request shares
+    int32_t *live;                // whether there is anything to join; then by token, whether its request shares
     float4 *own_sums;             // of a row over its own keys, see OwnRows
     float *own_outs;
     const float *own_cuts;
@@ -1028,8 +1028,8 @@ cudaError_t launch(const AttendArgs &a, const SharedWork &w, void *ws, cudaStrea
     e = launch_dependent(attend_prefix_kernel<HD, E4M3>, sms < kMaxGrid ? sms : kMaxGrid, kThreads,
                          PrefixConfig<HD>::kSmem, stream, a, w);
     if (e != cudaSuccess) return e;
-    if ((e = launch_attend_own(a, E4M3, w.groups, w.own_sums, w.own_outs, w.own_blocks, ws, stream)) != cudaSuccess)
-        return e;
+    e = launch_attend_own(a, E4M3, w.groups, w.own_sums, w.own_outs, w.own_blocks, w.live, ws, stream);
+    if (e != cudaSuccess) return e;
     return launch_dependent(attend_join_kernel<HD>, static_cast<unsigned>((int64_t(a.T) * a.n_heads + 31) / 32), 256, 0,
                             stream, a, w);
 }
@@ -1073,7 +1073,7 @@ cudaError_t launch_attend_shared(const AttendArgs &a, bool e4m3, int32_t max_q, 
     const int64_t keys = int64_t(a.width) << a.kv.page_shift, tiles = int64_t(a.T) * a.group / tile_rows + a.n_seq;
     const int64_t most = (tiles * groups.own + groups.first - groups.step_one) * (keys / kKeys + 1) * a.kv.n_kv;
     if (prefix.n_groups == 0 || a.n_seq < 2 || (!groups.always && most < int64_t(kSharedFixedNs) * kSms))
-        return launch_attend_own(a, e4m3, groups, nullptr, nullptr, nullptr, ws, stream);
+        return launch_attend_own(a, e4m3, groups, nullptr, nullptr, nullptr, nullptr, ws, stream);
     const SharedWork w{groups, reinterpret_cast<int64_t *>(base + at.units), ints(at.prefix), ints(at.lo), ints(at.lead),
                        ints(kOwnBlocks), ints(at.live), reinterpret_cast<float4 *>(base + at.own_sums), floats(at.own_outs), own_pieces(ws),
                        reinterpret_cast<float4 *>(base + at.heads), floats(at.outs),

@@ -93,3 +93,40 @@ def test_shared_prefix_rows_of_a_request_past_its_group(L, used):  # noqa: F811
     if used:
         c.run(L, att=att)
     check_offsets(L, b, [0, 100, 2], att, "always")
+
+
+# ---------------------------------------------------------------------------
+# Attention: calls that are refused on the device
+# ---------------------------------------------------------------------------
+@gpu
+@pytest.mark.parametrize("share", ["always", "auto"])
+def test_shared_prefix_more_own_steps_than_32_bits_count(L, share):  # noqa: F811
+    """4,096 requests of 2^25 tokens in two groups, a short prefix in common, one page over and over: 2^32 steps of own
+    keys.  The call reports it and writes nothing, with a workspace last used for more rows; the same call with shorter
+    requests is served in it."""
+    torch = _torch()
+    n = L.LORA_MAX_SEQS
+    kv = L.PagedKV.empty(1, 1024, 1, 128)
+    kv.k.zero_(), kv.v.fill_(0.5)
+    table = torch.zeros(n, 2 ** 15, dtype=torch.int32, device="cuda")
+    att = L.SharedAttention(n, 2 * n, 1, kv)
+    q = torch.zeros(2 * n, 128, dtype=torch.bfloat16, device="cuda")
+    groups, prefix = dev([0, n // 2, n]), dev([2048, 3000])
+
+    def run(rows, length):
+        out, lse = torch.full((rows * n, 128), 7.0, dtype=torch.bfloat16, device="cuda"), torch.full((rows * n, 1), 7.0, device="cuda")
+        lens = torch.full((n,), length, dtype=torch.int32, device="cuda")
+        off = rows * torch.arange(n + 1, dtype=torch.int32, device="cuda")
+        att.run(q[:rows * n], out, off, lens, table, groups, prefix, rows, lse=lse, share=share)
+        torch.cuda.synchronize()
+        return out, lse
+
+    out, _ = run(2, 5000)
+    assert att.err.item() == 0 and bool((out == 0.5).all())
+    out, lse = run(1, 2 ** 25)
+    assert att.err.item() == 9 and bool((out == 7.0).all()) and bool((lse == 7.0).all())
+    att.err.zero_()
+    out, lse = run(1, 4096)
+    # equal scores of 0: weights 1 of 4,096 keys, sums of powers of two
+    assert att.err.item() == 0 and bool((out == 0.5).all())
+    assert bool(((lse - 12 * np.log(2.0)).abs() <= 2.0 ** -18 * 13).all())
