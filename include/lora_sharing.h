@@ -164,8 +164,10 @@ typedef enum { LORA_SHARE_AUTO = 0, LORA_SHARE_ALWAYS = 1 } lora_share_t;
  *   ws             lora_attend_shared_workspace_bytes() bytes for at least this T and
  *                  n_seq, 16-byte aligned, zeroed once before the first call; every
  *                  call leaves it as it found it, up to values that no call reads (but
- *                  zero it again after a call that reports LORA_ERR_TIMEOUT).  Calls that
- *                  may overlap need a workspace each
+ *                  zero it again after a call that reports LORA_ERR_TIMEOUT, which joins
+ *                  nothing: rows of requests that share are not written, and calls
+ *                  that share report it too until then).  Calls that may overlap need a
+ *                  workspace each (LORA_ERR_WORKSPACE in err where that is noticed)
  * mode           LORA_SHARE_AUTO: prefixes are read once where that is estimated to
  *                  save time, which short ones do not (decided on the device, from the
  *                  lengths); LORA_SHARE_ALWAYS: all of them

@@ -57,6 +57,7 @@ namespace {
 constexpr int kMaxGrid = 160;
 constexpr int kSmemMax = 227 * 1024;
 constexpr int kWarps = 8;
+static_assert(kMaxGrid * kWarps == kOwnWarps, "the join's bound");
 constexpr int kPrefixMax = ((LORA_MAX_SEQS + 1) * 4 + 127) & ~127;  // the requests' step prefix
 
 template <int HD, bool E4M3, int ROWS, bool SHARED = false>

@@ -47,7 +47,7 @@ const float *own_pieces(const void *ws);
 
 namespace {
 
-constexpr int kThreads = 16 * 32, kMaxGrid = 160;
+constexpr int kThreads = 16 * 32, kMaxGrid = kPrefixBlocks;
 
 static_assert(kPrefixRows == 2 * kRows && kPrefixKeys == kKeys, "a step");
 
@@ -76,6 +76,7 @@ struct SharedWork {
     int64_t *units;               // by group: steps (and openings) before it, n_groups + 1
     int32_t *prefix, *lo, *lead;  // by group, of its plan
     int32_t *own_blocks;          // that take part in the own keys; 0 between calls
+    int32_t *gave_up;             // whether a wait did: pieces are missing; stays until the workspace is zeroed again
     int32_t *live;                // whether there is anything to join; then by token, whether its request shares
     float4 *own_sums;             // of a row over its own keys, see OwnRows
     float *own_outs;
@@ -871,6 +872,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefix_kernel(const Attend
     // the tensor memory goes
     if (!__all_sync(0xffffffffu, fine)) {
         s_abort = 1;
+        *w.gave_up = 1;
         report_error(a.err, LORA_ERR_TIMEOUT);
         __nanosleep(1000000);
     }
@@ -894,14 +896,26 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const AttendArgs a, co
     // (of a row that is not joined these are of another call)
     const float4 first = __ldcg(w.heads + row), own = __ldcg(w.own_sums + row);
     const bool live = w.live[1 + t] != 0 && int64_t(blockIdx.x) * 32 + (threadIdx.x & 31) < rows;
-    const bool any = w.live[0] != 0;
-    if (blockIdx.x == 0 && threadIdx.x == 0) w.own_blocks[0] = 0;
-    if (!any || !live) return;
+    const bool any = w.live[0] != 0, gave_up = *w.gave_up != 0;
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+        w.own_blocks[0] = 0;
+        if (gave_up) report_error(a.err, LORA_ERR_TIMEOUT);  // (of an earlier call, the workspace not zeroed since)
+    }
+    if (!any || !live || gave_up) return;
     // The row's pieces, in the order of the keys: of the prefix the first and the others, by block;
     // its own first one and the others, by warp of the decode path.
     const int32_t tile = w.groups.tile_rows, own_size = tile * (HD + 2);
     const int32_t c0 = __float_as_int(first.z) >> 8, n0 = 1 + __float_as_int(first.w), r = __float_as_int(first.z) & 255;
-    const int32_t w0 = __float_as_int(own.z) >> 5, n = n0 + 1 + __float_as_int(own.w), r1 = __float_as_int(own.z) & 31;
+    const int32_t w0 = __float_as_int(own.z) >> 5, n1 = 1 + __float_as_int(own.w), r1 = __float_as_int(own.z) & 31;
+    const int32_t n = n0 + n1;
+    // (what another call writes into this one's workspace at the same time sends no access out of it)
+    const auto within = [](int32_t from, int32_t pieces, int32_t most) {
+        return pieces >= 1 && pieces <= most && from >= 0 && from <= most - (pieces - 1);
+    };
+    if (!within(c0, n0, kMaxGrid) || !within(w0, n1, kOwnWarps)) {
+        report_error(a.err, LORA_ERR_WORKSPACE);
+        return;
+    }
     constexpr int kBatch = 4;         // pieces whose loads are under way together
     constexpr int kGroups = HD / 64;  // of 8 dims, a warp
     const int warp = threadIdx.x >> 5;
@@ -990,8 +1004,8 @@ constexpr int kSms = 152;  // a GB300's
 size_t up128(size_t b) { return (b + 127) & ~size_t(127); }
 
 // The word that has to be 0 when a call begins: behind the decode path's counters, at a place
-// that does not depend on the call.
-constexpr size_t kOwnBlocks = 1020;
+// that does not depend on the call; and the one that says that a wait gave up.
+constexpr size_t kOwnBlocks = 1020, kGaveUp = 1016;
 
 // The parts of a call's workspace behind the decode path's.  Nothing in them outlives a call.
 struct Layout {
@@ -1075,7 +1089,8 @@ cudaError_t launch_attend_shared(const AttendArgs &a, bool e4m3, int32_t max_q, 
     if (prefix.n_groups == 0 || a.n_seq < 2 || (!groups.always && most < int64_t(kSharedFixedNs) * kSms))
         return launch_attend_own(a, e4m3, groups, nullptr, nullptr, nullptr, nullptr, ws, stream);
     const SharedWork w{groups, reinterpret_cast<int64_t *>(base + at.units), ints(at.prefix), ints(at.lo), ints(at.lead),
-                       ints(kOwnBlocks), ints(at.live), reinterpret_cast<float4 *>(base + at.own_sums), floats(at.own_outs), own_pieces(ws),
+                       ints(kOwnBlocks), ints(kGaveUp), ints(at.live), reinterpret_cast<float4 *>(base + at.own_sums),
+                       floats(at.own_outs), own_pieces(ws),
                        reinterpret_cast<float4 *>(base + at.heads), floats(at.outs),
                        reinterpret_cast<float4 *>(base + at.cut_heads), floats(at.cut_outs)};
     if (a.kv.head_dim == 64)

@@ -7,6 +7,7 @@
 namespace lora {
 
 constexpr int kPrefixRows = 256, kPrefixKeys = 128;  // of a step of the prefix kernel
+constexpr int kPrefixBlocks = 160, kOwnWarps = 8 * 160;  // at most: of the prefix kernel, of the own keys' kernel
 
 // Opening a piece (its queries, its result) costs a block of the prefix kernel about as
 // much as kPrefixOpen steps: every segment counts as so many more, in front of the real ones.

@@ -130,3 +130,27 @@ def test_shared_prefix_more_own_steps_than_32_bits_count(L, share):  # noqa: F81
     # equal scores of 0: weights 1 of 4,096 keys, sums of powers of two
     assert att.err.item() == 0 and bool((out == 0.5).all())
     assert bool(((lse - 12 * np.log(2.0)).abs() <= 2.0 ** -18 * 13).all())
+
+
+@gpu
+@pytest.mark.parametrize("fp8", [False, True])
+def test_shared_prefix_pieces_of_a_call_that_gave_up(L, fp8):  # noqa: F811
+    """A wait that gave up leaves a word in the workspace (a word of the counters' KB) because pieces are missing: nothing
+    is joined, the call reports it, requests that share nothing have their rows, and the rest stays as it was.  The
+    zeroed workspace serves again."""
+    torch = _torch()
+    b = Batch([(300, [(10, 1), (5, 2), (0, 1)])], 8, 2, 128, 16, fp8, alone=[(40, 2), (7, 1)], rows_after=2)
+    att = L.SharedAttention(b.n, b.rows, 8, L.PagedKV(b.dk, b.dv, *b.scales))
+    b.check(*b.run(L, att=att))
+    words = att.ws[:1024].view(torch.int32)
+    assert not bool(words.any())
+    words[1016 // 4] = 1
+    for _ in range(2):
+        att.err.zero_()
+        out, lse = b.run(L, att=att)
+        assert b.err == 7
+        b.check(out, lse, skip=[0, 1, 2])
+    att.ws.zero_()
+    att.err.zero_()
+    b.check(*b.run(L, att=att))
+    assert b.err == 0 and not bool(words.any())
