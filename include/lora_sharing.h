@@ -157,7 +157,7 @@ typedef enum { LORA_SHARE_AUTO = 0, LORA_SHARE_ALWAYS = 1 } lora_share_t;
  * rows, and each request's other positions through its own row.  The result is what
  * lora_attend computes, up to rounding.  Where a request of the group with rows has
  * cached less before its own rows, the prefix is cut to that; groups with fewer than
- * two requests, and requests outside every group, share nothing.
+ * two requests with rows, and requests outside every group, share nothing.
  *   group_offsets  int32 [n_groups + 1], non-decreasing, within [0, n_seq]
  *   prefix_lens    int32 [n_groups]
  *   n_groups       0 .. LORA_MAX_SEQS

@@ -154,3 +154,27 @@ def test_shared_prefix_pieces_of_a_call_that_gave_up(L, fp8):  # noqa: F811
     att.err.zero_()
     b.check(*b.run(L, att=att))
     assert b.err == 0 and not bool(words.any())
+
+
+# ---------------------------------------------------------------------------
+# Attention: groups of one
+# ---------------------------------------------------------------------------
+@gpu
+@pytest.mark.parametrize("share", ["always", "auto"])
+@pytest.mark.parametrize("hd,fp8", [(128, False), (64, True)])
+def test_a_group_of_one_request_shares_nothing(L, hd, fp8, share):  # noqa: F811
+    """A request that is alone in its group, or alone there with rows, gives the bits of the call without groups (a
+    prefix read apart would round weights on the way)."""
+    torch = _torch()
+    b = Batch([(4000, [(10, 3)]), (9000, [(0, 0), (700, 5), (3, 0)]), (300, [(0, 0)])], 8, 2, hd, 64, fp8, alone=[(40, 2)])
+    want = b.run(L, starts=[0], prefix=[], hint=5)
+    assert b.err == 0
+    b.check(*want)
+    got = b.run(L, hint=5, share=share)
+    assert b.err == 0
+    assert all(torch.equal(x, y) for x, y in zip(got, want))
+    # with company the prefix is shared: other bits
+    c = Batch([(4000, [(10, 3), (0, 1)])], 8, 2, hd, 64, fp8)
+    alone, shared = c.run(L, starts=[0], prefix=[], hint=3), c.run(L, hint=3)
+    assert not all(torch.equal(x, y) for x, y in zip(alone, shared))
+    c.check(*shared)
