@@ -50,8 +50,8 @@ extern "C" {
  * Candidates of -inf are not taken (masked tokens, beams with a score of -inf);
  * places that are left get parent -1, token -1, score -inf, ended 0.  A beam with a
  * NaN or +inf among its logits, a score that is NaN or +inf, or no logit above -inf
- * has no candidates.  Candidates are compared in 64 bits; the logarithm's sum
- * carries 2^-22.
+ * has no candidates.  Candidates are compared in 64 bits; the sum in the logarithm
+ * is taken in fp32, within 2^-17 of itself whatever the vocabulary (about 2^-21 as measured).
  *   logits  bf16 or fp32 [n_req beams, ld], `vocab` columns used; aligned to
  *           its elements, any ld >= vocab
  *   scores  fp32 [n_req beams]; ended int32 [n_req beams], or null: none has

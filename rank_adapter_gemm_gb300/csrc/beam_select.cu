@@ -13,9 +13,13 @@
 // they are taken one by one.  All keys differ (value, then the lower token first), so order
 // never depends on timing.  Between the first chunk and the last no thread waits for another.
 //
-// A thread's sum is taken in fp32 against its own running maximum; a row's, and all
-// comparisons of candidates, in 64 bits: scores of different beams meet there, and a
-// rounding to fp32 would decide between candidates.
+// A thread's sum is two fp32 numbers (the second holds what adding up the chunks rounds off),
+// against a reference that follows its maximum at a distance (kMove): neither the additions'
+// roundings nor those of moving the reference pile up over a long row, and so for the parts of a
+// row.  In one number against the maximum itself, equal logits below 512 larger ones were off by
+// up to 2^-15 over 2^22 tokens and 2^-13 over 2^24; so they are within 2^-21 at every length, in the same
+// time.  Candidates are compared in 64 bits: scores of different beams meet there, and a
+// rounding to fp32 would decide between them.
 //
 // Measured, graph replay: 32 requests of 4 beams over 128,256 tokens (29 MB are read: a tenth of
 // the beams has ended) 18.4 us, 1.6 TB/s over all: about 12 us pass until the last part is done
@@ -33,6 +37,9 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kGroups = 64;   // groups of 4 neighbouring threads
 constexpr int kGather = 1024;  // gathered keys at most; more take the slow way
+// How far a thread's maximum may grow above its reference: terms stay below 2^6, and terms that a
+// reference has moved k times for weigh at most e^(-k kMove), so few roundings count.
+constexpr float kMove = 4.0f;
 
 struct SelectArgs {
     const void *logits;
@@ -42,7 +49,7 @@ struct SelectArgs {
     int32_t *parents, *tokens, *out_ended;
     float *out_scores;
     int32_t *counters;   // a request
-    float2 *sums;        // maximum and sum of each row's parts
+    float2 *sums;        // reference and sum of each row's parts
     float *values;       // the largest of each part, by request and rank
     int32_t *ids;        // and their tokens
     int32_t beams, vocab, keep, eos, parts, part_vecs;
@@ -134,10 +141,18 @@ struct Candidate {
     __device__ bool before(const Candidate &o) const { return key > o.key || (key == o.key && id < o.id); }
 };
 
+// A number >= 0 added to sum + low: low takes what sum rounds off.  (Exactly where the number is the
+// smaller one; else it is off by half a unit of it, and the sum has at least doubled.)
+__device__ __forceinline__ void add_to(float &sum, float &low, float x) {
+    const float now = __fadd_rn(sum, x);
+    low += __fsub_rn(x, __fsub_rn(now, sum));
+    sum = now;
+}
+
 // top + ln sum, in 64 bits but for the logarithm of a number near 1 (2^-25).
 __device__ __forceinline__ double log_sum(float top, float sum) {
     const int32_t bits = __float_as_int(sum), e = ((bits - 0x3f400000) >> 23);  // sum / 2^e in [3/4, 3/2)
-    if (!(sum > 0.0f && sum < INFINITY)) return top + logf(sum);  // (a sum of terms up to 1 is 0, NaN or at least 1)
+    if (!(sum > 0.0f && sum < INFINITY)) return top + logf(sum);  // (a sum with a term of 1 is 0, NaN or at least 1)
     return top + (e * 0.693147180559945309417 + static_cast<double>(logf(__int_as_float(bits - (e << 23)))));
 }
 
@@ -174,12 +189,13 @@ __device__ void join_request(const SelectArgs &a, int32_t r) {
         for (int32_t c = lane + 32; c < a.parts; c += 32) top = fmaxf(top, __ldcg(sums + c).x);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        float sum = 0.0f;
+        float sum = 0.0f, low = 0.0f;
         for (int32_t c = lane; c < a.parts; c += 32) {
             if (c != lane) mine = __ldcg(sums + c);
             // (a part without a number above -inf has sum 0; a NaN or +inf makes the sum NaN)
-            if (mine.y != 0.0f) sum += mine.y * ex2((mine.x - top) * kLog2e);
+            if (mine.y != 0.0f) add_to(sum, low, mine.y * ex2((mine.x - top) * kLog2e));
         }
+        sum += low;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
         if (lane == 0) {
@@ -328,7 +344,7 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const SelectAr
         };
         uint32_t w[16], next[16];
         if (chunks > 0) load(0, w);
-        float m = -INFINITY, sum = 0.0f, bound = INFINITY;  // of this thread: its maximum, its terms against that
+        float m = -INFINITY, sum = 0.0f, low = 0.0f, bound = INFINITY;  // of this thread: its reference, its terms' sum
         for (int32_t c = 0; c < chunks; ++c) {
             if (c + 1 < chunks) load(c + 1, next);
             const float top = T::top(w);
@@ -337,8 +353,10 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const SelectAr
                 if ((lane & 3) == 0) s_group[tid >> 2] = best;
                 bound = from_ordered(bound_of(s_group, &s_bound, a.keep));
             }
-            if (top > m) {
-                if (m > -INFINITY) sum *= ex2((m - top) * kLog2e);
+            if (top > m + kMove) {
+                const float f = m > -INFINITY ? ex2((m - top) * kLog2e) : 0.0f;
+                sum *= f;
+                low *= f;
                 m = top;
             }
             const float ref = m == -INFINITY ? 0.0f : m;
@@ -353,7 +371,7 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const SelectAr
             }
             float even, odd;
             unpack2(add2(sums[0], sums[1]), even, odd);
-            sum += even + odd;
+            add_to(sum, low, even + odd);
             // few threads have an element that reaches the bound
             if (top >= bound && top > -INFINITY) {
 #pragma unroll
@@ -368,7 +386,8 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const SelectAr
 #pragma unroll
             for (int i = 0; i < 16; ++i) w[i] = next[i];
         }
-        // the block's maximum and sum
+        // the block's reference and sum
+        sum += low;
         uint32_t best = __reduce_max_sync(0xffffffffu, ordered(m));
         if (lane == 0) s_top[warp] = best;
         __syncthreads();
@@ -382,7 +401,8 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const SelectAr
         __syncthreads();
         if (tid == 0) {
             float all = 0.0f;
-            for (int i = 0; i < kThreads / 32; ++i) all += s_sum[i];
+#pragma unroll
+            for (int i = 0; i < kThreads / 32; i += 4) all += (s_sum[i] + s_sum[i + 1]) + (s_sum[i + 2] + s_sum[i + 3]);
             a.sums[int64_t(row) * a.parts + part] = make_float2(all_top, all);
         }
         const int32_t found = s_n;

@@ -178,3 +178,58 @@ def test_a_group_of_one_request_shares_nothing(L, hd, fp8, share):  # noqa: F811
     alone, shared = c.run(L, starts=[0], prefix=[], hint=3), c.run(L, hint=3)
     assert not all(torch.equal(x, y) for x, y in zip(alone, shared))
     c.check(*shared)
+
+
+# ---------------------------------------------------------------------------
+# Selection: sums over many tokens
+# ---------------------------------------------------------------------------
+# A term's exponent carries two roundings and that of log2 e, 2.25 2^-24 of its distance from the largest logit (of which the
+# weighted mean is below 13 up to 2^24 tokens; references lie up to 4 below, twice); an exponential 2^-22, and each of four moves
+# of a reference another; additions 25 2^-24.  (2.25 (13 + 8) + 5 * 4 + 25) 2^-24 < 2^-17: what the header states.  In the rows
+# below the mean distance is below 8, one of the references lies below, and a term's weight counts for two moves:
+# (2.25 (8 + 4) + 3 * 4 + 25) 2^-24 = 2^-18.  Scores that meet the sum half way leave candidates near 0, whose own
+# rounding to fp32 is nothing beside that.
+def select_values(L, x, top, total, keep):  # noqa: F811
+    """The selection of rows x, a beam each, with `total` the logarithm of their sums and `top` their largest logits (64
+    bits): the best candidates' logits as the scores give them back."""
+    torch = _torch()
+    rows, V = x.shape
+    scores = torch.full((rows,), total - top, dtype=torch.float32, device="cuda")
+    sel = L.BeamSelect(rows, 1, keep, V, dtype=x.dtype)
+    sel.run(x, scores)
+    return sel, sel.scores.double().reshape(rows, keep) - (scores.double() - (total - top))[:, None] + top
+
+
+@gpu
+@pytest.mark.parametrize("fp32", [False, True])
+@pytest.mark.parametrize("rows,V", [(305, 131072), (305, 1 << 20), (305, 1 << 22), (1, 1 << 20), (1, 1 << 24), (40, 1 << 21)])
+def test_select_sums_of_equal_logits_below_some(L, rows, V, fp32):  # noqa: F811
+    """Rows of equal logits behind 512 larger ones, a few for every thread that adds: additions that all round the same
+    way, where one part takes the row and where hundreds do."""
+    torch = _torch()
+    for tail in (-0.6953125, -2.296875, -5.125, -9.6875, -12.1875, -14.125):
+        x = torch.full((rows, V), tail, dtype=torch.float32 if fp32 else torch.bfloat16, device="cuda")
+        x[:, :2048:4] = 0.0
+        sel, got = select_values(L, x, 0.0, np.log(512 + (V - 512) * np.exp(tail)), 2)
+        assert float(got.abs().max()) <= 2.0 ** -18, tail
+        assert sel.tokens.reshape(rows, 2).tolist() == [[0, 4]] * rows
+
+
+@gpu
+@pytest.mark.parametrize("fp32", [False, True])
+@pytest.mark.parametrize("rows,V", [(305, 131072), (305, 1 << 20), (305, 1 << 22), (2, 1 << 22)])
+@pytest.mark.parametrize("kind", ["rising", "slowly", "falling", "waves", "normal"])
+def test_select_sums_of_rows_that_move_their_reference(L, kind, rows, V, fp32):  # noqa: F811
+    torch = _torch()
+    at = torch.arange(V, dtype=torch.float64, device="cuda") / V
+    gen = torch.Generator(device="cuda").manual_seed(V)
+    row = {"rising": 20.0 * at, "slowly": at, "falling": -20.0 * at, "waves": 15.0 * at + torch.sin(300.0 * at),
+           "normal": 2.0 * torch.randn(V, generator=gen, device="cuda", dtype=torch.float64)}[kind]
+    row = row.to(torch.float32 if fp32 else torch.bfloat16)
+    order = torch.sort(row.double(), descending=True, stable=True)
+    total = float(torch.logsumexp(row.double(), 0))
+    sel, got = select_values(L, row.expand(rows, V).contiguous(), float(order.values[0]), total, 4)
+    want = order.values[:4]
+    # (scores: distances from the largest logit, rounded to fp32)
+    assert bool(((got - want).abs() <= 2.0 ** -18 + 2.0 ** -24 * (want - want[0]).abs()).all()), float((got - want).abs().max())
+    assert sel.tokens.reshape(rows, 4).tolist() == [order.indices[:4].tolist()] * rows
