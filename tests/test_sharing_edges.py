@@ -4,7 +4,8 @@ together, sums over many tokens.  Batches and tolerances are those of test_shari
 import numpy as np
 import pytest
 
-from test_sharing import Batch, L, _torch, dev  # noqa: F401  (L: a fixture)
+from test_sharing import (Batch, L, _torch, check_against_each, check_compact, check_fork, dev, random_tables,  # noqa: F401
+                          ref_compact, ref_fork, run_compact, run_fork)  # (L: a fixture)
 
 gpu = pytest.mark.gpu
 
@@ -233,3 +234,77 @@ def test_select_sums_of_rows_that_move_their_reference(L, kind, rows, V, fp32): 
     # (scores: distances from the largest logit, rounded to fp32)
     assert bool(((got - want).abs() <= 2.0 ** -18 + 2.0 ** -24 * (want - want[0]).abs()).all()), float((got - want).abs().max())
     assert sel.tokens.reshape(rows, 4).tolist() == [order.indices[:4].tolist()] * rows
+
+
+# ---------------------------------------------------------------------------
+# The largest calls
+# ---------------------------------------------------------------------------
+@gpu
+def test_tables_of_the_most_rows_and_pages(L):  # noqa: F811
+    """4,096 rows and 2^20 pages at once: the table kernels' shared memory is full."""
+    rng = np.random.default_rng(1)
+    n, ps, n_pages = L.LORA_MAX_SEQS, 16, 1 << 20
+    src, lens, _ = random_tables(rng, n, ps, 300, 20, n_pages, 3)
+    held = rng.integers(0, n_pages, 5000).astype(np.int32)
+    parents = rng.integers(-1, n, n)
+    dst = rng.integers(-9, 9, (n, 20)).astype(np.int32)
+    check_fork(run_fork(L, src, lens, parents, ps, n_pages, dst, held), ref_fork(src, lens, parents, ps, n_pages, dst, held))
+    check_compact(run_compact(L, src, lens, ps, n_pages, dst, held), ref_compact(src, lens, ps, n_pages, dst, held))
+
+
+@gpu
+@pytest.mark.parametrize("n,beams,keep,V", [(4096, 64, 64, 5), (4096, 3, 64, 40), (9, 64, 64, 3000)])
+def test_select_of_the_most_rows(L, n, beams, keep, V):  # noqa: F811
+    torch = _torch()
+    rng = np.random.default_rng(V)
+    x = torch.from_numpy(rng.standard_normal((n * beams, V))).cuda().bfloat16()
+    scores = torch.from_numpy(-rng.random(n * beams)).float().cuda()
+    sel = L.BeamSelect(n, beams, keep, V)
+    sel.run(x, scores)
+    c = (torch.log_softmax(x.double(), 1) + scores.double()[:, None]).view(n, beams * V)
+    k = min(keep, beams * V)
+    best = c.topk(k, 1).values
+    got = sel.scores.double().view(n, keep)
+    assert bool(((got[:, :k] - best).abs() <= 2.0 ** -18 + 2.0 ** -24 * best.abs()).all())
+    assert bool((got[:, k:] == -np.inf).all()) and bool((sel.parents.view(n, keep)[:, k:] == -1).all())
+    # the candidates named have these scores, none of them twice, in falling order
+    at = ((sel.parents.view(n, keep)[:, :k].long() - beams * torch.arange(n, device="cuda")[:, None]) * V +
+          sel.tokens.view(n, keep)[:, :k])
+    assert bool((c.gather(1, at) - got[:, :k]).abs().max() <= 2.0 ** -18 + 2.0 ** -24 * 20)
+    assert bool((at.sort(1).values.diff(dim=1) > 0).all()) and bool((got.diff(dim=1)[:, :k - 1] <= 0).all())
+
+
+@gpu
+@pytest.mark.parametrize("share", ["always", "auto"])
+def test_shared_prefix_of_the_most_requests_and_groups(L, share):  # noqa: F811
+    """4,096 requests in 4,096 groups, a third of them without requests, with one, with two."""
+    rng = np.random.default_rng(2)
+    groups = [(int(rng.integers(0, 200)), [(int(rng.integers(0, 5)), int(rng.random() < 0.9))] * (0, 1, 2)[g % 3])
+              for g in range(L.LORA_MAX_SEQS)]
+    b = Batch(groups, 2, 1, 64, 16, seed=1)
+    assert b.n == 1365 + 2 * 1365 and len(b.prefix) == 4096
+    out, lse = b.run(L, share=share)
+    assert b.err == 0
+    check_against_each(L, b, out, lse)
+
+
+# ---------------------------------------------------------------------------
+# Attention: scores far from 1
+# ---------------------------------------------------------------------------
+SLOPES = [2.0 ** -(h + 1) for h in range(8)]
+
+
+@gpu
+@pytest.mark.parametrize("hd,fp8", [(128, False), (64, True)])
+@pytest.mark.parametrize("kw", [dict(slopes=SLOPES), dict(softcap=30.0, slopes=SLOPES), dict(softcap=1e-5), dict(softcap=3e38),
+                                dict(softcap=30.0, window=130)], ids=str)
+@pytest.mark.parametrize("power", [90, 40, -40, -90])
+def test_shared_prefix_at_query_magnitudes(L, power, kw, hd, fp8):  # noqa: F811
+    """Queries times a power of two and the scale divided by it; groups of few and of many rows."""
+    b = Batch([(600, [(c, 1) for c in (0, 1, 90, 300)]), (130, [(200, 3), (0, 2)]), (400, [(i, 1) for i in range(40)])], 8, 2,
+              hd, 16, fp8, alone=[(40, 2)])
+    b.dq.mul_(2.0 ** power)
+    for scale in (hd ** -0.5 * 2.0 ** -power, -hd ** -0.5 * 2.0 ** -power):
+        out, lse = b.run(L, scale=scale, **kw)
+        b.check(out, lse, scale=scale, **kw)
+        assert b.err == 0
