@@ -38,11 +38,10 @@ struct GroupPlan {
     int32_t *offsets;         // n_groups + 1
     int32_t *prefix, *lo, *lead;  // its keys' end (0: shares nothing) and first, the request whose table row holds them
     int32_t *tiles;           // of the decode path, over its requests
-    int32_t *members;         // requests with rows
     __device__ GroupPlan(int32_t *scratch, int32_t n, int32_t n_seq)
         : rows(scratch), offsets(rows + n_seq + 1), prefix(offsets + n + 1), lo(prefix + n), lead(lo + n),
-          tiles(lead + n), members(tiles + n) {}
-    __host__ __device__ static constexpr size_t bytes(int32_t n, int32_t n_seq) { return (size_t(6) * n + n_seq + 2) * 4; }
+          tiles(lead + n) {}
+    __host__ __device__ static constexpr size_t bytes(int32_t n, int32_t n_seq) { return (size_t(5) * n + n_seq + 2) * 4; }
 };
 
 // How many blocks compute prefixes (0: nothing is shared) and own keys.
@@ -94,7 +93,7 @@ __device__ Blocks plan_groups(const AttendArgs &a, const Groups &w, const GroupP
     for (int32_t g = tid; g < w.n_groups; g += NT) {
         p.prefix[g] = INT32_MAX;
         p.lead[g] = INT32_MAX;
-        p.tiles[g] = p.members[g] = 0;
+        p.tiles[g] = 0;
         const int32_t given = __ldcg(w.lens + g);
         p.lo[g] = given;  // for now
         if (given < 0 && report) report_error(a.err, LORA_ERR_INVALID_ARG);
@@ -126,7 +125,6 @@ __device__ Blocks plan_groups(const AttendArgs &a, const Groups &w, const GroupP
         if (g < 0) continue;
         atomicMin(&p.prefix[g], r.len - r.n);
         atomicMin(&p.lead[g], i);
-        atomicAdd(&p.members[g], 1);
         atomicAdd(&p.tiles[g], static_cast<int32_t>(min(tiles, int64_t(1) << 18)));
     }
     bad = __syncthreads_or(falls) || bad;
@@ -136,13 +134,14 @@ __device__ Blocks plan_groups(const AttendArgs &a, const Groups &w, const GroupP
     for (int32_t g = tid; g < w.n_groups; g += NT) {
         const int32_t ctx = p.prefix[g], given = p.lo[g];
         int32_t prefix = 0, lo = 0;
-        if (!bad && p.members[g] >= 2) {
-            const int32_t q0 = p.rows[p.offsets[g]], q1 = p.rows[p.offsets[g + 1]];
+        const int32_t lead = p.lead[g], rows_of_group = bad ? 0 : p.rows[p.offsets[g + 1]] - p.rows[p.offsets[g]];
+        // more rows than one request has (seen from the offsets: counting requests costs a call of 64 in a group 1 us)
+        if (lead != INT32_MAX && rows_of_group > p.rows[lead + 1] - p.rows[lead]) {
             prefix = max(0, min(given, ctx));
             if (a.window > 0) lo = static_cast<int32_t>(max(int64_t(0), int64_t(ctx) - a.window + 1));
             if (lo >= prefix) prefix = lo = 0;  // no row sees any of it
             if (prefix > 0) {
-                const int64_t rows = int64_t(q1 - q0) * a.group, steps = prefix_steps(lo, prefix);
+                const int64_t rows = int64_t(rows_of_group) * a.group, steps = prefix_steps(lo, prefix);
                 const int64_t here = (rows + kPrefixRows - 1) / kPrefixRows * (steps + kPrefixOpen) *
                                      (rows > kPrefixRows / 2 ? w.step_two : w.step_one);
                 const int64_t keys = int64_t(p.tiles[g]) * (prefix - lo);
