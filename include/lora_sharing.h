@@ -154,10 +154,13 @@ typedef enum { LORA_SHARE_AUTO = 0, LORA_SHARE_ALWAYS = 1 } lora_share_t;
  * [group_offsets[g], group_offsets[g + 1]) hold the same keys and values at their
  * positions below prefix_lens[g] (in the same or in different pages): those are
  * read once for all rows of the group, through the table row of its first request with
- * rows, and each request's other positions through its own row.  The result is what
- * lora_attend computes, up to rounding.  Where a request of the group with rows has
- * cached less before its own rows, the prefix is cut to that; groups with fewer than
- * two requests with rows, and requests outside every group, share nothing.
+ * rows, and each request's other positions through its own row, by the decode path
+ * whatever the number of rows.  The result is what lora_attend computes, up to rounding:
+ * weights of a shared prefix are rounded to bf16 (over LORA_KV_E4M3 to f16, times 2^7)
+ * before the product with v, as on lora_attend's prompt path, so that how a row's
+ * weights are rounded depends on whether its group shares.  Where a request of the group
+ * with rows has cached less before its own rows, the prefix is cut to that; groups with
+ * fewer than two requests with rows, and requests outside every group, share nothing.
  *   group_offsets  int32 [n_groups + 1], non-decreasing, within [0, n_seq]
  *   prefix_lens    int32 [n_groups]
  *   n_groups       0 .. LORA_MAX_SEQS
@@ -168,14 +171,17 @@ typedef enum { LORA_SHARE_AUTO = 0, LORA_SHARE_ALWAYS = 1 } lora_share_t;
  *                  nothing: rows of requests that share are not written, and calls
  *                  that share report it too until then).  Calls that may overlap need a
  *                  workspace each (LORA_ERR_WORKSPACE in err where that is noticed)
- * mode           LORA_SHARE_AUTO: prefixes are read once where that is estimated to
+ *   mode           LORA_SHARE_AUTO: prefixes are read once where that is estimated to
  *                  save time, which short ones do not (decided on the device, from the
- *                  lengths); LORA_SHARE_ALWAYS: all of them
+ *                  lengths; a call that turns out to share nothing takes longer than
+ *                  lora_attend, 1 us with short tables and 11 with long ones as
+ *                  measured); LORA_SHARE_ALWAYS: all of them
  * A NaN or infinity in a value of the prefix that some row of the group sees can reach
- * the group's other rows.  All other arguments, limits and device errors are lora_attend's; LORA_ERR_INVALID_ARG
- * in err also reports group offsets out of order or range (nothing is shared then)
- * and negative prefix lengths (that group shares nothing).  Made for few rows a request (decode,
- * speculative decode); any number is computed.
+ * the group's other rows.  All other arguments, limits and device errors are lora_attend's;
+ * LORA_ERR_INVALID_ARG in err also reports group offsets out of order or range and negative
+ * prefix lengths (that group shares nothing).  Nothing is shared where offsets of groups or
+ * of rows are out of order or range.  Made for few rows a request (decode, speculative
+ * decode); any number is computed.
  */
 typedef struct {
     const int32_t *group_offsets, *prefix_lens;

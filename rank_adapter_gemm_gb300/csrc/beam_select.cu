@@ -9,8 +9,9 @@
 // The largest of a part are found through a bound: of 64 groups of threads, the keep-th
 // largest of the groups' maxima over the first chunk is one that at least `keep` elements
 // reach.  The elements that reach it, of all chunks a few times `keep`, in few threads,
-// are gathered and ranked by counting; where there are too many (equal or rising ones)
-// they are taken one by one.  All keys differ (value, then the lower token first), so order
+// are gathered and ranked by counting; where there are too many (equal or rising ones, a first
+// chunk full of a mask's finite value) they are taken one by one, a pass over the part each (the call
+// below with all but 1 in 10,000 logits at the type's lowest value 131 us; with 99 in 100 as without).  All keys differ (value, then the lower token first), so order
 // never depends on timing.  Between the first chunk and the last no thread waits for another.
 //
 // A thread's sum is two fp32 numbers (the second holds what adding up the chunks rounds off),
