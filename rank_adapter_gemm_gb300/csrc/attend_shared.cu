@@ -35,9 +35,10 @@
 // tile's rows, a row a thread; 8-11 copy; 12 issues the products; 13 hands out the
 // pieces.  Weights are rounded to bf16 over a bf16 cache (the instruction takes one type
 // for both operands; sums use them unrounded), to f16, times 2^7, over an e4m3 cache: as on the
-// prompt path, and fewer bits than the decode path gives the own keys (16, f16 times 2^12).  A second
-// product for the remainder would be half as much again on the tensor cores.  Outputs of 64 requests behind
-// 8,000 tokens lie 0.0017 (rms, relative) from 64 bits so, 0.0016 with one rounding at the end.
+// prompt path, and fewer bits than the decode path gives the own keys (16, f16 times 2^12).  With a
+// second product for the weights' remainders the 64 requests above take 60.7 us in place of 53.9 and the 16
+// prompts 351 in place of 341, and outputs lie 0.0016 and 0.0015 (rms, relative) from 64 bits in place of
+// 0.0017 and 0.0016: the output's own rounding is 0.0016.
 #include "attend_tc.cuh"
 #include "shared_plan.cuh"
 
